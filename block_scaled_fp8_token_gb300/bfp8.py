@@ -64,6 +64,36 @@ class bfp8_members(ctypes.Structure):
     _fields_ = [("n_members", ctypes.c_int32), ("member_rows", ctypes.POINTER(ctypes.c_int64))]
 
 
+class bfp8_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_e4m3", ctypes.c_void_p), ("v_e4m3", ctypes.c_void_p),
+        ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("k_stride_page", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("k_stride_token", ctypes.c_int64),
+        ("v_stride_page", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+        ("v_stride_token", ctypes.c_int64),
+        ("exp_stride_page", ctypes.c_int64), ("exp_stride_head", ctypes.c_int64),
+    ]
+
+
+class bfp8_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+        ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+        ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("w_dtype", ctypes.c_int32),
+        ("weight_offset", ctypes.c_float), ("residual_scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("residual_out", ctypes.c_void_p), ("ld_residual_out", ctypes.c_int64),
+        ("norm_out", ctypes.c_void_p), ("ld_norm_out", ctypes.c_int64),
+        ("q_e4m3", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("scales", ctypes.c_void_p), ("s_stride_m", ctypes.c_int64),
+        ("s_stride_kb", ctypes.c_int64),
+    ]
+
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {
     "bfp8_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -103,6 +133,11 @@ _SIGS = {
                                                  _i64, _i64, _vp]),
     "bfp8_moe_combine": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i64,
                                         _vp]),
+    "bfp8_kv_plan": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp,
+                                    _vp, _vp, _i64, _vp, _vp]),
+    "bfp8_kv_append": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
+                                      ctypes.POINTER(bfp8_kv_cache), _vp]),
+    "bfp8_residual_norm": (ctypes.c_int, [ctypes.POINTER(bfp8_norm_args), _i64, _i64, _vp]),
     "bfp8_device_status": (ctypes.c_int, [_vp]),
     "bfp8_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _vp]),
 }
@@ -297,7 +332,8 @@ def _layout(t, name: str, shape, pitch: int | None = None) -> None:
 
 
 _KINDS = {"bf16": (torch.bfloat16,), "e4m3": (torch.uint8, torch.float8_e4m3fn),
-          "f32": (torch.float32,), "i32": (torch.int32,)}
+          "f32": (torch.float32,), "i32": (torch.int32,), "i64": (torch.int64,),
+          "u8": (torch.uint8,)}
 
 
 def _dtypes(**args) -> None:
@@ -646,6 +682,137 @@ def bfp8_moe_combine(y, token_rows, token_weights, out, stream=None) -> None:
                                  _ptr(token_weights), T, topk, _ptr(out), out.stride(0),
                                  _stream(stream)),
            "bfp8_moe_combine")
+
+
+def bfp8_kv_plan(ctx_len, q_len, free_pages, block_table, page_size: int, q_offsets, kv_len, slots,
+                 positions, counts, stream=None) -> None:
+    """The block plan of one step: pages for each request's new tokens from the
+    front of free_pages, and every new token's slot and position."""
+    B, width = block_table.shape
+    T = slots.shape[0]
+    _dtypes(ctx_len=(ctx_len, "i32"), q_len=(q_len, "i32"), free_pages=(free_pages, "i32"),
+            block_table=(block_table, "i32"), q_offsets=(q_offsets, "i32"), kv_len=(kv_len, "i32"),
+            slots=(slots, "i64"), positions=(positions, "i32"), counts=(counts, "i32"))
+    for name, t, n in [("ctx_len", ctx_len, B), ("q_len", q_len, B),
+                       ("free_pages", free_pages, free_pages.shape[0]),
+                       ("q_offsets", q_offsets, B + 1), ("kv_len", kv_len, B), ("slots", slots, T),
+                       ("positions", positions, T), ("counts", counts, 3)]:
+        _layout(t, name, (n,))
+    _rows(block_table, "block_table")
+    _check(_lib.bfp8_kv_plan(_ptr(ctx_len), _ptr(q_len), B, _ptr(free_pages), free_pages.shape[0],
+                             _ptr(block_table), _pitch(block_table), width, int(page_size),
+                             _ptr(q_offsets), _ptr(kv_len), _ptr(slots), _ptr(positions), T,
+                             _ptr(counts), _stream(stream)),
+           "bfp8_kv_plan")
+
+
+def _pitch(t) -> int:
+    """Row stride of a matrix; what a one-row tensor reports there means nothing."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _kv_cache(k_cache, v_cache, k_exp, v_exp) -> bfp8_kv_cache:
+    """The cache [pages, kv heads, page size, 128] as the library takes it: any
+    strides of pages, heads and tokens, contiguous codes."""
+    _dtypes(k_cache=(k_cache, "e4m3"), v_cache=(v_cache, "e4m3"), k_exp=(k_exp, "u8"),
+            v_exp=(v_exp, "u8"))
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("bfp8: k_cache and v_cache must be [pages, heads, page size, head dim], "
+                         f"got {list(k_cache.shape)} and {list(v_cache.shape)}")
+    P, H, page, D = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if D > 1 and t.stride(3) != 1:
+            raise ValueError(f"bfp8: {name} must have contiguous codes, got strides "
+                             f"{list(t.stride())}")
+    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+        if tuple(t.shape) != (P, H):
+            raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[P, H]}")
+
+    def strides(t):   # a dimension of one element is never stepped along
+        return [s if n > 1 else 128 * page * H for s, n in zip(t.stride(), t.shape)]
+
+    es, es_v = strides(k_exp), strides(v_exp)
+    if es != es_v:
+        raise ValueError(f"bfp8: k_exp and v_exp must have the same strides, got "
+                         f"{list(k_exp.stride())} and {list(v_exp.stride())}")
+    return bfp8_kv_cache(_ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp), P, page, H, D,
+                         *strides(k_cache)[:3], *strides(v_cache)[:3], *es)
+
+
+def _head_rows(t, name: str, T: int, H: int, D: int) -> tuple[int, int]:
+    """Token and head strides of a [T, H, D] tensor with contiguous head rows."""
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[T, H, D]}")
+    if D > 1 and t.stride(2) != 1:
+        raise ValueError(f"bfp8: {name} must have contiguous head rows, got strides "
+                         f"{list(t.stride())}")
+    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+
+
+def bfp8_kv_append(k, v, slots, k_cache, v_cache, k_exp, v_exp, stream=None) -> None:
+    """Quantize new keys and values [T, kv heads, 128] into their slots of the cache."""
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    T = slots.shape[0]
+    _dtypes(k=(k, "bf16"), v=(v, "bf16"), slots=(slots, "i64"))
+    _layout(slots, "slots", (T,))
+    ks = _head_rows(k, "k", T, cache.n_kv_heads, cache.head_dim)
+    vs = _head_rows(v, "v", T, cache.n_kv_heads, cache.head_dim)
+    _check(_lib.bfp8_kv_append(_ptr(k), *ks, _ptr(v), *vs, _ptr(slots), T, ctypes.byref(cache),
+                               _stream(stream)),
+           "bfp8_kv_append")
+
+
+def bfp8_residual_norm(y, residual, residual_out=None, *, q=None, scales=None, norm_out=None,
+                       w_post=None, w_pre=None, gate=None, residual_scale: float = 1.0,
+                       eps: float = 1e-6, weight_offset: float = 0.0, s_stride_m=None,
+                       s_stride_kb=None, stream=None) -> None:
+    """The post-norm of y, its gate, the residual sum, the pre-norm of the next
+    block and its 1x128 quantization. gate is [H] (every token) or [T, H]."""
+    T, H = residual.shape
+    a = bfp8_norm_args(residual_scale=residual_scale, eps=eps, weight_offset=weight_offset,
+                       w_dtype=BFP8_DT_BF16)
+    for name, ld, t in (("y", "ldy", y), ("residual", "ld_residual", residual)):
+        if t is None:
+            continue
+        _dtypes(**{name: (t, "bf16")})
+        if tuple(t.shape) != (T, H):
+            raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[T, H]}")
+        _rows(t, name)
+        setattr(a, name, _ptr(t))
+        setattr(a, ld, _pitch(t))
+    if gate is not None:
+        _dtypes(gate=(gate, "bf16"))
+        if tuple(gate.shape) not in ((H,), (T, H)):
+            raise ValueError(f"bfp8: gate has shape {list(gate.shape)}, expected {[H]} or {[T, H]}")
+        if H > 1 and gate.stride(-1) != 1:
+            raise ValueError("bfp8: gate must have contiguous columns")
+        a.gate, a.ld_gate = _ptr(gate), 0 if gate.dim() == 1 else _pitch(gate)
+    weights = [(n, w) for n, w in (("w_post", w_post), ("w_pre", w_pre)) if w is not None]
+    for name, w in weights:
+        _layout(w, name, (H,))
+        if w.dtype != weights[0][1].dtype:
+            raise ValueError("bfp8: w_post and w_pre must have the same dtype")
+        setattr(a, name, _ptr(w))
+        a.w_dtype = _scale_dtype(w) & 0xFF
+    for name, ld, t, kind, eb in (("residual_out", "ld_residual_out", residual_out, "bf16", 2),
+                                  ("norm_out", "ld_norm_out", norm_out, "bf16", 2),
+                                  ("q_e4m3", "ldq", q, "e4m3", 1)):
+        if t is None:
+            continue
+        _dtypes(**{name: (t, kind)})
+        _out(t, name, T, H, eb)
+        setattr(a, name, _ptr(t))
+        setattr(a, ld, _pitch(t))
+    if q is not None:
+        if scales is None:
+            raise ValueError("bfp8: q needs scales")
+        _dtypes(scales=(scales, "f32"))
+        a.s_stride_m = scales.stride(0) if s_stride_m is None else s_stride_m
+        a.s_stride_kb = scales.stride(1) if s_stride_kb is None else s_stride_kb
+        _scales_out(scales, "scales", T, -(-H // 128), a.s_stride_m, a.s_stride_kb,
+                    s_stride_m is not None or s_stride_kb is not None)
+        a.scales = _ptr(scales)
+    _check(_lib.bfp8_residual_norm(ctypes.byref(a), T, H, _stream(stream)), "bfp8_residual_norm")
 
 
 def bfp8_device_status(stream=None) -> int:

@@ -515,6 +515,28 @@ int bfp8_grouped_linear_silu_quant(const void* q_a, const float* s_a, int64_t s_
                                     sh_stride_m, sh_stride_kb, workspace, ws_bytes, stream);
 }
 
+int bfp8_kv_plan(const int32_t* ctx_len, const int32_t* q_len, int64_t B,
+                 const int32_t* free_pages, int64_t n_free, int32_t* block_table,
+                 int64_t ld_table, int64_t max_blocks, int32_t page_size, int32_t* q_offsets,
+                 int32_t* kv_len, int64_t* slots, int32_t* positions, int64_t T, int32_t* counts,
+                 void* stream) {
+  return launch_kv_plan(ctx_len, q_len, B, free_pages, n_free, block_table, ld_table, max_blocks,
+                        page_size, q_offsets, kv_len, slots, positions, T, counts, stream);
+}
+
+int bfp8_kv_append(const void* k_bf16, int64_t k_stride_token, int64_t k_stride_head,
+                   const void* v_bf16, int64_t v_stride_token, int64_t v_stride_head,
+                   const int64_t* slots, int64_t T, const bfp8_kv_cache* cache, void* stream) {
+  if (!cache) return BFP8_ERR_INVALID_ARG;
+  return launch_kv_append(k_bf16, k_stride_token, k_stride_head, v_bf16, v_stride_token,
+                          v_stride_head, slots, T, *cache, stream);
+}
+
+int bfp8_residual_norm(const bfp8_norm_args* args, int64_t T, int64_t H, void* stream) {
+  if (!args) return BFP8_ERR_INVALID_ARG;
+  return launch_residual_norm(*args, T, H, stream);
+}
+
 int bfp8_selftest_wait_timeout(uint64_t limit_ns, void* stream) {
   return launch_wait_selftest(limit_ns, stream);
 }

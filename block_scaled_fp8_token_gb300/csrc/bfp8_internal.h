@@ -122,6 +122,16 @@ int launch_decode_ffn(int32_t arith, const void* x, int64_t ldx, const void* w_g
                       int64_t M, int64_t H, int64_t I, void* y, int64_t ldy, void* workspace,
                       size_t ws_bytes, void* stream);
 
+// The paged KV cache and the residual stream between blocks.
+int launch_kv_plan(const int32_t* ctx, const int32_t* q_len, int64_t B, const int32_t* free_pages,
+                   int64_t n_free, int32_t* table, int64_t ld_table, int64_t max_blocks,
+                   int32_t page_size, int32_t* q_offsets, int32_t* kv_len, int64_t* slots,
+                   int32_t* positions, int64_t T, int32_t* counts, void* stream);
+int launch_kv_append(const void* k, int64_t k_ldt, int64_t k_ldh, const void* v, int64_t v_ldt,
+                     int64_t v_ldh, const int64_t* slots, int64_t T, const bfp8_kv_cache& cache,
+                     void* stream);
+int launch_residual_norm(const bfp8_norm_args& args, int64_t T, int64_t H, void* stream);
+
 // Device error words, one per translation unit with bounded waits: read and
 // clear. Return BFP8_OK, BFP8_ERR_TIMEOUT or BFP8_ERR_CUDA.
 int gemm_read_clear_error();

@@ -517,6 +517,126 @@ int bfp8_moe_combine(const void* y_bf16, int64_t R, int64_t H, int64_t ldy,
                      const int32_t* token_rows, const float* token_weights, int64_t T,
                      int32_t topk, void* out_bf16, int64_t ldo, void* stream);
 
+/* ---- the attention layer around the projections: a paged 8-bit KV cache ---- */
+/*
+ * The cache holds keys and values as E4M3 codes in pages of `page_size`
+ * tokens, with one power-of-two scale per page and head, stored as one byte:
+ *   value = e4m3(code) * 2^(byte - 127),  byte in [87, 167].
+ * A request's tokens are found through its row of a block table: token i is
+ * at offset i % page_size of page table[i / page_size]; its slot is
+ * page * page_size + offset. The layout of pages, heads and tokens is the
+ * caller's (strides in bytes); the 128 codes of a token and head are contiguous.
+ */
+typedef struct {
+  void* k_e4m3;               /* codes of the keys, (page, head, token) at the strides below */
+  void* v_e4m3;               /* codes of the values                                        */
+  uint8_t* k_exp;             /* scale bytes of the keys, (page, head)                      */
+  uint8_t* v_exp;             /* scale bytes of the values                                  */
+  int64_t n_pages;
+  int32_t page_size;          /* 16, 32, 64 or 128                                          */
+  int32_t n_kv_heads;
+  int32_t head_dim;           /* 128                                                        */
+  int64_t k_stride_page, k_stride_head, k_stride_token;   /* bytes, multiples of 16         */
+  int64_t v_stride_page, v_stride_head, v_stride_token;
+  int64_t exp_stride_page, exp_stride_head;               /* of both byte arrays            */
+} bfp8_kv_cache;
+
+/*
+ * bfp8_kv_plan -- the block plan of one step, from lengths alone: pages for
+ * the new tokens of every request, and where each new token goes.
+ *   ctx_len, q_len  device int32 [B]: tokens in the cache, and new tokens (a
+ *               negative length counts as 0)
+ *   free_pages  device int32 [n_free]: page numbers; request by request, each
+ *               new page takes the next one. The call does not change the list:
+ *               the caller drops counts[0] pages from its front.
+ *   block_table device int32 [B, max_blocks], row stride ld_table. Entries below
+ *               ceil(ctx_len / page_size) are read; the new pages' entries
+ *               behind them are written, and no others.
+ *   q_offsets   int32 [B + 1] out: first row of each request among the new tokens
+ *   kv_len      int32 [B] out: ctx_len + q_len
+ *   slots       int64 [T] out: the slot of each new token, -1 where it has none
+ *               (past the last token, no free page left, past max_blocks, or
+ *               a negative page number in the table)
+ *   positions   int32 [T] out: a token's place in its request, -1 past the last
+ *   counts      int32 [3] out: pages taken, pages that were wanted and not
+ *               there (their table entries are -1), and tokens with no page
+ * T is the caller's capacity (a captured step keeps it fixed); rows past the
+ * step's tokens are written -1. Repeating a call gives the same result. One
+ * launch, no host synchronisation. Errors: INVALID_ARG (null pointers, negative
+ * sizes, ld_table < max_blocks), UNSUPPORTED (page_size, B > 16384).
+ */
+int bfp8_kv_plan(const int32_t* ctx_len, const int32_t* q_len, int64_t B,
+                 const int32_t* free_pages, int64_t n_free, int32_t* block_table,
+                 int64_t ld_table, int64_t max_blocks, int32_t page_size, int32_t* q_offsets,
+                 int32_t* kv_len, int64_t* slots, int32_t* positions, int64_t T, int32_t* counts,
+                 void* stream);
+
+/*
+ * bfp8_kv_append -- quantize the step's new keys and values into their slots.
+ *   k_bf16, v_bf16  [T, n_kv_heads, 128] BF16, token and head strides in elements
+ *               (multiples of 8; 16-byte aligned), for example columns of the
+ *               QKV projection's output
+ *   slots       device int64 [T], as bfp8_kv_plan writes them; a slot outside
+ *               [0, n_pages * page_size) skips its row. Rows of one page must
+ *               follow one another in consecutive slots.
+ * Per page and head, over the page's new rows (finite values):
+ *   e = the least integer with max|x| <= 448 * 2^e, clamped to [-40, 40]
+ * A page whose first new row is not at offset 0 already holds the rows before
+ * it: it keeps the larger of e and its present exponent, and when e is the
+ * larger, the codes of those rows are multiplied by the power of two between
+ * (rounded to nearest even; exact above E4M3's subnormals). Then
+ *   code = RNE_satfinite_e4m3(x * 2^-e).
+ * NaN gives the NaN code and does not enter the maximum; infinities saturate.
+ * Rows of a page behind the new ones hold nothing afterwards that is defined.
+ * T == 0 is a no-op. Errors: INVALID_ARG, UNSUPPORTED (page size, head width,
+ * alignment).
+ */
+int bfp8_kv_append(const void* k_bf16, int64_t k_stride_token, int64_t k_stride_head,
+                   const void* v_bf16, int64_t v_stride_token, int64_t v_stride_head,
+                   const int64_t* slots, int64_t T, const bfp8_kv_cache* cache, void* stream);
+
+/* ---- the residual stream between two blocks -------------------------------- */
+/*
+ * bfp8_residual_norm -- the norm after a block, its gate, the scaled residual
+ * sum, the norm before the next block and the 1x128 quantization for its
+ * projection, in one pass:
+ *   u = w_post ? y * rsqrt(mean(y^2) + eps) * (w_post + weight_offset) : y
+ *   h = residual_scale * residual + gate * u          (h = that residual if y is NULL)
+ *   residual_out = bf16_rn(h)
+ *   n = h * rsqrt(mean(h^2) + eps) * (w_pre + weight_offset)
+ *   norm_out = bf16_rn(n); per 128 columns s = max(max|n|, 1e-10f) / 448,
+ *   q = RNE_satfinite_e4m3(n / s)
+ * in float32 throughout: the second norm takes h, and the quantizer n, before
+ * either is rounded to BF16.
+ */
+typedef struct {
+  const void* y;              /* [T, H] BF16, the block's output; NULL: none               */
+  int64_t ldy;
+  const void* residual;       /* [T, H] BF16                                               */
+  int64_t ld_residual;
+  const void* gate;           /* BF16: [T, H] with row stride ld_gate, or [H] with 0; NULL: 1 */
+  int64_t ld_gate;
+  const void* w_post;         /* [H]; NULL: y is not normed                                */
+  const void* w_pre;          /* [H]; needed when norm_out or q_e4m3 is given              */
+  int32_t w_dtype;            /* BFP8_DT_BF16 or BFP8_DT_F32, of both                      */
+  float weight_offset;        /* 1 for weights stored around zero, else 0                  */
+  float residual_scale;
+  float eps;
+  void* residual_out;         /* [T, H] BF16, may be `residual` itself; NULL: not written  */
+  int64_t ld_residual_out;
+  void* norm_out;             /* [T, H] BF16, may be `y` itself; NULL: not written         */
+  int64_t ld_norm_out;
+  void* q_e4m3;               /* [T, H] E4M3, row stride ldq bytes; NULL: not written      */
+  int64_t ldq;
+  float* scales;              /* (m, g) at scales[m*s_stride_m + g*s_stride_kb]            */
+  int64_t s_stride_m, s_stride_kb;
+} bfp8_norm_args;
+
+/* T == 0 or H == 0 is a no-op. Errors: INVALID_ARG (null residual, no output at
+ * all, gate or w_post without y, w_pre missing, strides below H, eps < 0),
+ * SCALE_DTYPE (w_dtype), UNSUPPORTED (H > 16384). */
+int bfp8_residual_norm(const bfp8_norm_args* args, int64_t T, int64_t H, void* stream);
+
 /* ---- diagnostics ---------------------------------------------------------- */
 /*
  * bfp8_device_status -- synchronise `stream`, then read and clear the library's
