@@ -78,6 +78,23 @@ class bfp8_kv_cache(ctypes.Structure):
     ]
 
 
+class bfp8_kv_attention_args(ctypes.Structure):
+    _fields_ = [
+        ("q_bf16", ctypes.c_void_p), ("q_stride_token", ctypes.c_int64),
+        ("q_stride_head", ctypes.c_int64),
+        ("out_bf16", ctypes.c_void_p), ("out_stride_token", ctypes.c_int64),
+        ("out_stride_head", ctypes.c_int64),
+        ("lse", ctypes.c_void_p), ("lse_stride_token", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+        ("max_blocks", ctypes.c_int64),
+        ("q_offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_q_len", ctypes.c_int64),
+        ("n_heads", ctypes.c_int64),
+        ("softmax_scale", ctypes.c_float), ("window", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
 class bfp8_norm_args(ctypes.Structure):
     _fields_ = [
         ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
@@ -137,6 +154,9 @@ _SIGS = {
                                     _vp, _vp, _i64, _vp, _vp]),
     "bfp8_kv_append": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
                                       ctypes.POINTER(bfp8_kv_cache), _vp]),
+    "bfp8_kv_attention": (ctypes.c_int, [ctypes.POINTER(bfp8_kv_attention_args),
+                                         ctypes.POINTER(bfp8_kv_cache), _vp]),
+    "bfp8_kv_attention_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "bfp8_residual_norm": (ctypes.c_int, [ctypes.POINTER(bfp8_norm_args), _i64, _i64, _vp]),
     "bfp8_device_status": (ctypes.c_int, [_vp]),
     "bfp8_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _vp]),
@@ -760,6 +780,42 @@ def bfp8_kv_append(k, v, slots, k_cache, v_cache, k_exp, v_exp, stream=None) -> 
     _check(_lib.bfp8_kv_append(_ptr(k), *ks, _ptr(v), *vs, _ptr(slots), T, ctypes.byref(cache),
                                _stream(stream)),
            "bfp8_kv_append")
+
+
+def bfp8_kv_attention_workspace(batch: int, tokens: int, max_q_len: int, n_heads: int,
+                                n_kv_heads: int) -> int:
+    return int(_lib.bfp8_kv_attention_workspace(batch, tokens, max_q_len, n_heads, n_kv_heads))
+
+
+def bfp8_kv_attention(q, k_cache, v_cache, k_exp, v_exp, block_table, q_offsets, kv_len, out,
+                      max_q_len: int, softmax_scale=None, window: int = -1, lse=None,
+                      workspace=None, stream=None) -> None:
+    """Causal attention of q [T, heads, 128] over the paged cache; softmax_scale
+    defaults to 1 / sqrt(128)."""
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    T, heads, D = q.shape
+    B, width = block_table.shape
+    _dtypes(q=(q, "bf16"), out=(out, "bf16"), block_table=(block_table, "i32"),
+            q_offsets=(q_offsets, "i32"), kv_len=(kv_len, "i32"), lse=(lse, "f32"))
+    _rows(block_table, "block_table")
+    _layout(q_offsets, "q_offsets", (B + 1,))
+    _layout(kv_len, "kv_len", (B,))
+    a = bfp8_kv_attention_args(batch=B, tokens=T, max_q_len=int(max_q_len), n_heads=heads,
+                               window=int(window), max_blocks=width)
+    a.q_bf16, (a.q_stride_token, a.q_stride_head) = _ptr(q), _head_rows(q, "q", T, heads, cache.head_dim)
+    a.out_bf16 = _ptr(out)
+    a.out_stride_token, a.out_stride_head = _head_rows(out, "out", T, heads, cache.head_dim)
+    if lse is not None:
+        if tuple(lse.shape) != (T, heads):
+            raise ValueError(f"bfp8: lse has shape {list(lse.shape)}, expected {[T, heads]}")
+        _rows(lse, "lse")
+        a.lse, a.lse_stride_token = _ptr(lse), _pitch(lse)
+    a.block_table, a.ld_table = _ptr(block_table), _pitch(block_table)
+    a.q_offsets, a.kv_len = _ptr(q_offsets), _ptr(kv_len)
+    a.softmax_scale = D ** -0.5 if softmax_scale is None else softmax_scale
+    a.workspace, a.ws_bytes = _ws(workspace)
+    _check(_lib.bfp8_kv_attention(ctypes.byref(a), ctypes.byref(cache), _stream(stream)),
+           "bfp8_kv_attention")
 
 
 def bfp8_residual_norm(y, residual, residual_out=None, *, q=None, scales=None, norm_out=None,

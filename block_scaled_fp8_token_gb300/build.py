@@ -22,7 +22,8 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = PKG / "libbfp8.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["api.cpp", "quant.cu", "gemm_sm103.cu", "gemv_decode.cu", "kv_cache.cu", "norm.cu"]
+SOURCES = ["api.cpp", "quant.cu", "gemm_sm103.cu", "gemv_decode.cu", "kv_cache.cu",
+           "kv_attention.cu", "norm.cu"]
 
 
 def _nvcc() -> str:

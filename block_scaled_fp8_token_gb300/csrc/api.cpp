@@ -51,7 +51,7 @@ int encode(CUtensorMap* map, CUtensorMapDataType dt, cuuint32_t rank, const void
            CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return BFP8_ERR_CUDA;
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, dt, rank, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -127,6 +127,16 @@ int make_tmap_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uin
   const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
   const cuuint32_t box[3] = {box0, box1, box2};
   return encode(map, dt, 3, base, dims, strides, box, swizzle);
+}
+
+int make_tmap_4d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t dim0,
+                 uint64_t dim1, uint64_t dim2, uint64_t dim3, uint64_t stride1_bytes,
+                 uint64_t stride2_bytes, uint64_t stride3_bytes, uint32_t box0, uint32_t box1,
+                 uint32_t box2, uint32_t box3, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[4] = {dim0, dim1, dim2, dim3};
+  const cuuint64_t strides[3] = {stride1_bytes, stride2_bytes, stride3_bytes};
+  const cuuint32_t box[4] = {box0, box1, box2, box3};
+  return encode(map, dt, 4, base, dims, strides, box, swizzle);
 }
 
 int resolve_members(int64_t N, const bfp8_members* members, MemberTable* out) {
@@ -532,6 +542,21 @@ int bfp8_kv_append(const void* k_bf16, int64_t k_stride_token, int64_t k_stride_
                           v_stride_head, slots, T, *cache, stream);
 }
 
+size_t bfp8_kv_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q_len,
+                                   int64_t n_heads, int64_t n_kv_heads) {
+  int sms = 0;
+  if (batch <= 0 || tokens <= 0 || max_q_len <= 0 || n_heads <= 0 || n_kv_heads <= 0 ||
+      n_heads % n_kv_heads || sm_count(&sms) != BFP8_OK)
+    return 0;
+  return kv_attention_workspace_bytes(batch, tokens, max_q_len, n_heads, n_kv_heads, sms);
+}
+
+int bfp8_kv_attention(const bfp8_kv_attention_args* args, const bfp8_kv_cache* cache,
+                      void* stream) {
+  if (!args || !cache) return BFP8_ERR_INVALID_ARG;
+  return launch_kv_attention(*args, *cache, stream);
+}
+
 int bfp8_residual_norm(const bfp8_norm_args* args, int64_t T, int64_t H, void* stream) {
   if (!args) return BFP8_ERR_INVALID_ARG;
   return launch_residual_norm(*args, T, H, stream);
@@ -546,9 +571,10 @@ int bfp8_device_status(void* stream) {
     return BFP8_ERR_CUDA;
   const int a = gemm_read_clear_error();
   const int b = gemv_read_clear_error();
-  if (a == BFP8_ERR_CUDA || b == BFP8_ERR_CUDA) return BFP8_ERR_CUDA;
+  const int c = kv_read_clear_error();
+  if (a == BFP8_ERR_CUDA || b == BFP8_ERR_CUDA || c == BFP8_ERR_CUDA) return BFP8_ERR_CUDA;
   if (a != BFP8_OK) return a;
-  return b;
+  return b != BFP8_OK ? b : c;
 }
 
 }  // extern "C"

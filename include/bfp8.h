@@ -595,6 +595,53 @@ int bfp8_kv_append(const void* k_bf16, int64_t k_stride_token, int64_t k_stride_
                    const void* v_bf16, int64_t v_stride_token, int64_t v_stride_head,
                    const int64_t* slots, int64_t T, const bfp8_kv_cache* cache, void* stream);
 
+/*
+ * bfp8_kv_attention -- attention of the step's queries over the cache:
+ *   out[t, h] = sum_i w_i v[i, g],  w = softmax_i( softmax_scale * q[t, h] . k[i, g] ),
+ * g = h / (n_heads / n_kv_heads), over the positions i that the query sees. Row
+ * i of a request's new rows sits at position kv_len - (its rows) + i and sees
+ * the positions up to its own, at most `window` before it when window >= 0.
+ * Scores, softmax statistics and sums are float32; out is rounded to BF16 once.
+ *   q_bf16, out_bf16  [tokens, n_heads, 128] BF16, 16-byte aligned, token and
+ *               head strides in elements, multiples of 8. They must not overlap.
+ *   lse         float32 [tokens, n_heads] or NULL: ln(sum_i exp(score_i))
+ *   block_table, q_offsets, kv_len  as bfp8_kv_plan leaves them, on the device.
+ *               The new tokens' keys and values are in the cache already.
+ *   max_q_len   at least the most new rows of a request; rows past it are not written
+ * A row that sees nothing (its request is empty, or its position is below 0)
+ * gives 0 and -inf. A table entry outside [0, n_pages) hides its tokens. Rows of
+ * a page at or behind kv_len are never used, whatever they hold.  A NaN among
+ * the values a request does see may reach every row of that request.
+ *   workspace   at least bfp8_kv_attention_workspace() bytes, 256-byte aligned,
+ *               contents free; calls sharing it must not overlap.
+ * Nothing synchronises with the host: the schedule comes from the lengths on
+ * the device, so a step can be captured in a CUDA graph and replayed as lengths
+ * grow. Results do not depend on what else runs. Errors: INVALID_ARG (null
+ * pointers, negative sizes, n_heads not a multiple of n_kv_heads, workspace
+ * missing or too small), UNSUPPORTED (page size, head width, alignment).
+ */
+typedef struct {
+  const void* q_bf16;
+  int64_t q_stride_token, q_stride_head;
+  void* out_bf16;
+  int64_t out_stride_token, out_stride_head;
+  float* lse;                    /* may be NULL                                  */
+  int64_t lse_stride_token;      /* heads are contiguous                         */
+  const int32_t* block_table;    /* [batch, max_blocks], row stride ld_table     */
+  int64_t ld_table, max_blocks;
+  const int32_t* q_offsets;      /* [batch + 1]                                  */
+  const int32_t* kv_len;         /* [batch]                                      */
+  int64_t batch, tokens, max_q_len, n_heads;
+  float softmax_scale;
+  int32_t window;                /* -1: none                                     */
+  void* workspace;
+  size_t ws_bytes;
+} bfp8_kv_attention_args;
+
+size_t bfp8_kv_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q_len,
+                                   int64_t n_heads, int64_t n_kv_heads);
+int bfp8_kv_attention(const bfp8_kv_attention_args* args, const bfp8_kv_cache* cache, void* stream);
+
 /* ---- the residual stream between two blocks -------------------------------- */
 /*
  * bfp8_residual_norm -- the norm after a block, its gate, the scaled residual
