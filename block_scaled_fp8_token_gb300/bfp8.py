@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from pathlib import Path
 
 import torch
@@ -152,12 +153,11 @@ _SIGS = {
                                         _vp]),
     "bfp8_kv_plan": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp,
                                     _vp, _vp, _i64, _vp, _vp]),
-    "bfp8_kv_append": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
-                                      ctypes.POINTER(bfp8_kv_cache), _vp]),
-    "bfp8_kv_attention": (ctypes.c_int, [ctypes.POINTER(bfp8_kv_attention_args),
-                                         ctypes.POINTER(bfp8_kv_cache), _vp]),
+    # (their structs come packed as bytes, or by reference)
+    "bfp8_kv_append": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "bfp8_kv_attention": (ctypes.c_int, [_vp, _vp, _vp]),
     "bfp8_kv_attention_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
-    "bfp8_residual_norm": (ctypes.c_int, [ctypes.POINTER(bfp8_norm_args), _i64, _i64, _vp]),
+    "bfp8_residual_norm": (ctypes.c_int, [_vp, _i64, _i64, _vp]),
     "bfp8_device_status": (ctypes.c_int, [_vp]),
     "bfp8_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _vp]),
 }
@@ -704,81 +704,137 @@ def bfp8_moe_combine(y, token_rows, token_weights, out, stream=None) -> None:
            "bfp8_moe_combine")
 
 
-def bfp8_kv_plan(ctx_len, q_len, free_pages, block_table, page_size: int, q_offsets, kv_len, slots,
-                 positions, counts, stream=None) -> None:
-    """The block plan of one step: pages for each request's new tokens from the
-    front of free_pages, and every new token's slot and position."""
-    B, width = block_table.shape
-    T = slots.shape[0]
-    _dtypes(ctx_len=(ctx_len, "i32"), q_len=(q_len, "i32"), free_pages=(free_pages, "i32"),
-            block_table=(block_table, "i32"), q_offsets=(q_offsets, "i32"), kv_len=(kv_len, "i32"),
-            slots=(slots, "i64"), positions=(positions, "i32"), counts=(counts, "i32"))
-    for name, t, n in [("ctx_len", ctx_len, B), ("q_len", q_len, B),
-                       ("free_pages", free_pages, free_pages.shape[0]),
-                       ("q_offsets", q_offsets, B + 1), ("kv_len", kv_len, B), ("slots", slots, T),
-                       ("positions", positions, T), ("counts", counts, 3)]:
-        _layout(t, name, (n,))
-    _rows(block_table, "block_table")
-    _check(_lib.bfp8_kv_plan(_ptr(ctx_len), _ptr(q_len), B, _ptr(free_pages), free_pages.shape[0],
-                             _ptr(block_table), _pitch(block_table), width, int(page_size),
-                             _ptr(q_offsets), _ptr(kv_len), _ptr(slots), _ptr(positions), T,
-                             _ptr(counts), _stream(stream)),
-           "bfp8_kv_plan")
+# The calls below run once a layer and step, some of them for a few microseconds
+# on the GPU, so their checks are one comparison a property; what one of them
+# refuses goes to the helpers above, which say why.
+_PLAIN = {"i32": torch.int32, "i64": torch.int64, "f32": torch.float32, "bf16": torch.bfloat16}
+_KV_CACHE = struct.Struct("4Pq3i8q")         # bfp8_kv_cache
+_KV_ATTENTION = struct.Struct("P2qP2qPqP2q2P4qfiPN")   # bfp8_kv_attention_args
+_NORM = struct.Struct("PqPqPqPPifffPqPqPqP2q")         # bfp8_norm_args
 
 
-def _pitch(t) -> int:
-    """Row stride of a matrix; what a one-row tensor reports there means nothing."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+_WEIGHT_CODES = {None: BFP8_DT_BF16, torch.bfloat16: BFP8_DT_BF16, torch.float32: BFP8_DT_F32,
+                 torch.float16: BFP8_DT_F16}
 
 
-def _kv_cache(k_cache, v_cache, k_exp, v_exp) -> bfp8_kv_cache:
-    """The cache [pages, kv heads, page size, 128] as the library takes it: any
-    strides of pages, heads and tokens, contiguous codes."""
-    _dtypes(k_cache=(k_cache, "e4m3"), v_cache=(v_cache, "e4m3"), k_exp=(k_exp, "u8"),
-            v_exp=(v_exp, "u8"))
+def _device() -> int:
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _vec(t, name: str, kind: str, n: int, dev: int) -> int:
+    """The address of a dense vector of n elements on the current device."""
+    if t.dtype is _PLAIN[kind] and t.shape == (n,) and t.get_device() == dev and (
+            n < 2 or t.stride(0) == 1):
+        return t.data_ptr()
+    _dtypes(**{name: (t, kind)})
+    _layout(t, name, (n,))
+    return _ptr(t)
+
+
+def _matrix(t, name: str, kind: str, shape, dev: int) -> tuple[int, int]:
+    """The address and row stride of a matrix with contiguous rows. (A matrix
+    of one row has no row stride: its width stands in.)"""
+    if t.shape != shape:
+        raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {list(shape)}")
+    if t.dtype not in _KINDS[kind] or t.get_device() != dev or (shape[1] > 1 and t.stride(1) != 1):
+        _dtypes(**{name: (t, kind)})
+        _ptr(t)
+        raise ValueError(f"bfp8: {name} must have contiguous columns, got strides "
+                         f"{list(t.stride())}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _out_matrix(t, name: str, kind: str, rows: int, cols: int, elem_bytes: int,
+                dev: int) -> tuple[int, int]:
+    """The same for an output, which may be larger than what is written."""
+    if t.dtype not in _KINDS[kind] or t.get_device() != dev or t.shape != (rows, cols):
+        _dtypes(**{name: (t, kind)})
+        _out(t, name, rows, cols, elem_bytes)
+        _ptr(t)
+    elif cols > 1 and t.stride(1) != 1:
+        _rows(t, name)
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _head_rows(t, name: str, T: int, H: int, D: int, dev: int) -> tuple[int, int, int]:
+    """Address, token stride and head stride of [T, H, D] BF16 with contiguous head rows."""
+    if t.shape != (T, H, D):
+        raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[T, H, D]}")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _dtypes(**{name: (t, "bf16")})
+        _ptr(t)
+    st, sh, sd = t.stride()
+    if D > 1 and sd != 1:
+        raise ValueError(f"bfp8: {name} must have contiguous head rows, got strides {[st, sh, sd]}")
+    return t.data_ptr(), st if T > 1 else H * D, sh if H > 1 else D
+
+
+def _kv_cache(k_cache, v_cache, k_exp, v_exp, dev: int) -> tuple[bytes, int, int]:
+    """The cache [pages, kv heads, page size, 128] as the library takes it (any
+    strides of pages, heads and tokens, contiguous codes), its heads and width."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("bfp8: k_cache and v_cache must be [pages, heads, page size, head dim], "
                          f"got {list(k_cache.shape)} and {list(v_cache.shape)}")
     P, H, page, D = k_cache.shape
+    lone = 128 * page * H   # the stride of a dimension of one element, which is never stepped along
+    flat = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if D > 1 and t.stride(3) != 1:
+        if t.dtype not in _KINDS["e4m3"] or t.get_device() != dev:
+            _dtypes(**{name: (t, "e4m3")})
+            _ptr(t)
+        sp, sh, st, sd = t.stride()
+        if D > 1 and sd != 1:
             raise ValueError(f"bfp8: {name} must have contiguous codes, got strides "
                              f"{list(t.stride())}")
+        flat += [sp if P > 1 else lone, sh if H > 1 else lone, st if page > 1 else lone]
+    exps = []
     for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-        if tuple(t.shape) != (P, H):
+        if t.shape != (P, H):
             raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[P, H]}")
-
-    def strides(t):   # a dimension of one element is never stepped along
-        return [s if n > 1 else 128 * page * H for s, n in zip(t.stride(), t.shape)]
-
-    es, es_v = strides(k_exp), strides(v_exp)
-    if es != es_v:
+        if t.dtype is not torch.uint8 or t.get_device() != dev:
+            _dtypes(**{name: (t, "u8")})
+            _ptr(t)
+        sp, sh = t.stride()
+        exps.append((sp if P > 1 else H, sh if H > 1 else 1))
+    if exps[0] != exps[1]:
         raise ValueError(f"bfp8: k_exp and v_exp must have the same strides, got "
                          f"{list(k_exp.stride())} and {list(v_exp.stride())}")
-    return bfp8_kv_cache(_ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp), P, page, H, D,
-                         *strides(k_cache)[:3], *strides(v_cache)[:3], *es)
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
+                          v_exp.data_ptr(), P, page, H, D, *flat, *exps[0]), H, D
 
 
-def _head_rows(t, name: str, T: int, H: int, D: int) -> tuple[int, int]:
-    """Token and head strides of a [T, H, D] tensor with contiguous head rows."""
-    if tuple(t.shape) != (T, H, D):
-        raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[T, H, D]}")
-    if D > 1 and t.stride(2) != 1:
-        raise ValueError(f"bfp8: {name} must have contiguous head rows, got strides "
-                         f"{list(t.stride())}")
-    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+def bfp8_kv_plan(ctx_len, q_len, free_pages, block_table, page_size: int, q_offsets, kv_len, slots,
+                 positions, counts, stream=None) -> None:
+    """The block plan of one step: pages for each request's new tokens from the
+    front of free_pages, and every new token's slot and position."""
+    dev = _device()
+    B, width = block_table.shape
+    T, n_free = slots.shape[0], free_pages.shape[0]
+    table, pitch = _matrix(block_table, "block_table", "i32", (B, width), dev)
+    _check(_lib.bfp8_kv_plan(_vec(ctx_len, "ctx_len", "i32", B, dev),
+                             _vec(q_len, "q_len", "i32", B, dev), B,
+                             _vec(free_pages, "free_pages", "i32", n_free, dev), n_free, table,
+                             pitch, width, page_size,
+                             _vec(q_offsets, "q_offsets", "i32", B + 1, dev),
+                             _vec(kv_len, "kv_len", "i32", B, dev),
+                             _vec(slots, "slots", "i64", T, dev),
+                             _vec(positions, "positions", "i32", T, dev), T,
+                             _vec(counts, "counts", "i32", 3, dev), _raw_stream(stream, dev)),
+           "bfp8_kv_plan")
 
 
 def bfp8_kv_append(k, v, slots, k_cache, v_cache, k_exp, v_exp, stream=None) -> None:
     """Quantize new keys and values [T, kv heads, 128] into their slots of the cache."""
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    dev = _device()
+    cache, H, D = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
     T = slots.shape[0]
-    _dtypes(k=(k, "bf16"), v=(v, "bf16"), slots=(slots, "i64"))
-    _layout(slots, "slots", (T,))
-    ks = _head_rows(k, "k", T, cache.n_kv_heads, cache.head_dim)
-    vs = _head_rows(v, "v", T, cache.n_kv_heads, cache.head_dim)
-    _check(_lib.bfp8_kv_append(_ptr(k), *ks, _ptr(v), *vs, _ptr(slots), T, ctypes.byref(cache),
-                               _stream(stream)),
+    _check(_lib.bfp8_kv_append(*_head_rows(k, "k", T, H, D, dev), *_head_rows(v, "v", T, H, D, dev),
+                               _vec(slots, "slots", "i64", T, dev), T, cache,
+                               _raw_stream(stream, dev)),
            "bfp8_kv_append")
 
 
@@ -792,30 +848,18 @@ def bfp8_kv_attention(q, k_cache, v_cache, k_exp, v_exp, block_table, q_offsets,
                       workspace=None, stream=None) -> None:
     """Causal attention of q [T, heads, 128] over the paged cache; softmax_scale
     defaults to 1 / sqrt(128)."""
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
-    T, heads, D = q.shape
+    dev = _device()
+    cache, H, D = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    T, heads, _ = q.shape
     B, width = block_table.shape
-    _dtypes(q=(q, "bf16"), out=(out, "bf16"), block_table=(block_table, "i32"),
-            q_offsets=(q_offsets, "i32"), kv_len=(kv_len, "i32"), lse=(lse, "f32"))
-    _rows(block_table, "block_table")
-    _layout(q_offsets, "q_offsets", (B + 1,))
-    _layout(kv_len, "kv_len", (B,))
-    a = bfp8_kv_attention_args(batch=B, tokens=T, max_q_len=int(max_q_len), n_heads=heads,
-                               window=int(window), max_blocks=width)
-    a.q_bf16, (a.q_stride_token, a.q_stride_head) = _ptr(q), _head_rows(q, "q", T, heads, cache.head_dim)
-    a.out_bf16 = _ptr(out)
-    a.out_stride_token, a.out_stride_head = _head_rows(out, "out", T, heads, cache.head_dim)
-    if lse is not None:
-        if tuple(lse.shape) != (T, heads):
-            raise ValueError(f"bfp8: lse has shape {list(lse.shape)}, expected {[T, heads]}")
-        _rows(lse, "lse")
-        a.lse, a.lse_stride_token = _ptr(lse), _pitch(lse)
-    a.block_table, a.ld_table = _ptr(block_table), _pitch(block_table)
-    a.q_offsets, a.kv_len = _ptr(q_offsets), _ptr(kv_len)
-    a.softmax_scale = D ** -0.5 if softmax_scale is None else softmax_scale
-    a.workspace, a.ws_bytes = _ws(workspace)
-    _check(_lib.bfp8_kv_attention(ctypes.byref(a), ctypes.byref(cache), _stream(stream)),
-           "bfp8_kv_attention")
+    args = _KV_ATTENTION.pack(
+        *_head_rows(q, "q", T, heads, D, dev), *_head_rows(out, "out", T, heads, D, dev),
+        *((0, 0) if lse is None else _matrix(lse, "lse", "f32", (T, heads), dev)),
+        *_matrix(block_table, "block_table", "i32", (B, width), dev), width,
+        _vec(q_offsets, "q_offsets", "i32", B + 1, dev), _vec(kv_len, "kv_len", "i32", B, dev),
+        B, T, max_q_len, heads, D ** -0.5 if softmax_scale is None else softmax_scale, window,
+        *((0, 0) if workspace is None else _ws(workspace)))
+    _check(_lib.bfp8_kv_attention(args, cache, _raw_stream(stream, dev)), "bfp8_kv_attention")
 
 
 def bfp8_residual_norm(y, residual, residual_out=None, *, q=None, scales=None, norm_out=None,
@@ -824,51 +868,48 @@ def bfp8_residual_norm(y, residual, residual_out=None, *, q=None, scales=None, n
                        s_stride_kb=None, stream=None) -> None:
     """The post-norm of y, its gate, the residual sum, the pre-norm of the next
     block and its 1x128 quantization. gate is [H] (every token) or [T, H]."""
-    T, H = residual.shape
-    a = bfp8_norm_args(residual_scale=residual_scale, eps=eps, weight_offset=weight_offset,
-                       w_dtype=BFP8_DT_BF16)
-    for name, ld, t in (("y", "ldy", y), ("residual", "ld_residual", residual)):
-        if t is None:
+    dev = _device()
+    T, H = shape = residual.shape
+    none = (0, 0)
+    if gate is None:
+        gate_at = none
+    elif gate.dim() == 1:
+        gate_at = (_vec(gate, "gate", "bf16", H, dev), 0)
+    else:
+        gate_at = _matrix(gate, "gate", "bf16", shape, dev)
+    weights, w_dtype = [0, 0], None
+    for i, w in enumerate((w_post, w_pre)):
+        if w is None:
             continue
-        _dtypes(**{name: (t, "bf16")})
-        if tuple(t.shape) != (T, H):
-            raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {[T, H]}")
-        _rows(t, name)
-        setattr(a, name, _ptr(t))
-        setattr(a, ld, _pitch(t))
-    if gate is not None:
-        _dtypes(gate=(gate, "bf16"))
-        if tuple(gate.shape) not in ((H,), (T, H)):
-            raise ValueError(f"bfp8: gate has shape {list(gate.shape)}, expected {[H]} or {[T, H]}")
-        if H > 1 and gate.stride(-1) != 1:
-            raise ValueError("bfp8: gate must have contiguous columns")
-        a.gate, a.ld_gate = _ptr(gate), 0 if gate.dim() == 1 else _pitch(gate)
-    weights = [(n, w) for n, w in (("w_post", w_post), ("w_pre", w_pre)) if w is not None]
-    for name, w in weights:
-        _layout(w, name, (H,))
-        if w.dtype != weights[0][1].dtype:
+        if w.shape != shape[1:] or w.get_device() != dev or (H > 1 and w.stride(0) != 1):
+            _layout(w, ("w_post", "w_pre")[i], (H,))
+        weights[i] = _ptr(w) if w.get_device() != dev else w.data_ptr()
+        if w_dtype not in (None, w.dtype):
             raise ValueError("bfp8: w_post and w_pre must have the same dtype")
-        setattr(a, name, _ptr(w))
-        a.w_dtype = _scale_dtype(w) & 0xFF
-    for name, ld, t, kind, eb in (("residual_out", "ld_residual_out", residual_out, "bf16", 2),
-                                  ("norm_out", "ld_norm_out", norm_out, "bf16", 2),
-                                  ("q_e4m3", "ldq", q, "e4m3", 1)):
-        if t is None:
-            continue
-        _dtypes(**{name: (t, kind)})
-        _out(t, name, T, H, eb)
-        setattr(a, name, _ptr(t))
-        setattr(a, ld, _pitch(t))
+        w_dtype = w.dtype
+    scales_at = (0, 0, 0)
     if q is not None:
         if scales is None:
             raise ValueError("bfp8: q needs scales")
-        _dtypes(scales=(scales, "f32"))
-        a.s_stride_m = scales.stride(0) if s_stride_m is None else s_stride_m
-        a.s_stride_kb = scales.stride(1) if s_stride_kb is None else s_stride_kb
-        _scales_out(scales, "scales", T, -(-H // 128), a.s_stride_m, a.s_stride_kb,
-                    s_stride_m is not None or s_stride_kb is not None)
-        a.scales = _ptr(scales)
-    _check(_lib.bfp8_residual_norm(ctypes.byref(a), T, H, _stream(stream)), "bfp8_residual_norm")
+        plain = s_stride_m is None and s_stride_kb is None
+        ssm = scales.stride(0) if s_stride_m is None else s_stride_m
+        sskb = scales.stride(1) if s_stride_kb is None else s_stride_kb
+        if not plain or scales.dtype is not torch.float32 or scales.get_device() != dev or \
+                scales.shape != (T, -(-H // 128)):
+            _dtypes(scales=(scales, "f32"))
+            _scales_out(scales, "scales", T, -(-H // 128), ssm, sskb, not plain)
+            _ptr(scales)
+        scales_at = (scales.data_ptr(), ssm, sskb)
+    args = _NORM.pack(
+        *(none if y is None else _matrix(y, "y", "bf16", shape, dev)),
+        *_matrix(residual, "residual", "bf16", shape, dev), *gate_at, *weights,
+        _WEIGHT_CODES.get(w_dtype, BFP8_DT_NONE),
+        weight_offset, residual_scale, eps,
+        *(none if residual_out is None else
+          _out_matrix(residual_out, "residual_out", "bf16", T, H, 2, dev)),
+        *(none if norm_out is None else _out_matrix(norm_out, "norm_out", "bf16", T, H, 2, dev)),
+        *(none if q is None else _out_matrix(q, "q", "e4m3", T, H, 1, dev)), *scales_at)
+    _check(_lib.bfp8_residual_norm(args, T, H, _raw_stream(stream, dev)), "bfp8_residual_norm")
 
 
 def bfp8_device_status(stream=None) -> int:

@@ -371,9 +371,11 @@ int launch_kv_plan(const int32_t* ctx, const int32_t* q_len, int64_t B, const in
   p.max_blocks = static_cast<int32_t>(max_blocks);
   p.shift = kv_page_shift(page_size);
   const size_t smem = static_cast<size_t>(B) * 8;
-  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_plan_kernel),
-                            static_cast<int>(kPlanMaxBatch * 8));
-  if (rc != BFP8_OK) return rc;
+  if (smem > 48 * 1024) {
+    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_plan_kernel),
+                              static_cast<int>(kPlanMaxBatch * 8));
+    if (rc != BFP8_OK) return rc;
+  }
   const int64_t items = T > B ? T : B;
   const int64_t want = (items + kPlanThreads - 1) / kPlanThreads;
   const unsigned blocks = static_cast<unsigned>(want < 1 ? 1 : want < sms ? want : sms);

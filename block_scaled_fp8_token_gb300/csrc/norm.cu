@@ -163,22 +163,24 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) residual_norm_kernel(co
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[i][e] *= p.res_scale;
       if (p.y) {
-        float y[8];
+        // y times weight times gate is exact in FP32 when all are BF16 (8
+        // significant bits each), so the row's factor and the sum round once
+        float y[8], f[8];
         widen8(yr[i], y);
         if (p.w_post) {
-          float w[8];
-          load_weight8<VEC>(p.w_post, p.w_f32, p.w_offset, c, H, w);
+          load_weight8<VEC>(p.w_post, p.w_f32, p.w_offset, c, H, f);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * ry * w[e];
+          for (int e = 0; e < 8; ++e) f[e] = 1.0f;
         }
         if (p.gate) {
           float g[8];
           widen8(gr[i], g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] *= g[e];
+          for (int e = 0; e < 8; ++e) f[e] *= g[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] += y[e];
+        for (int e = 0; e < 8; ++e) h[i][e] = fmaf(y[e] * f[e], ry, h[i][e]);
       }
       if (p.res_out) store8<VEC>(p.res_out + row * p.ldro, c, H, h[i]);
 #pragma unroll
@@ -195,17 +197,25 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) residual_norm_kernel(co
       float am = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[i][e] = h[i][e] * rh * w[e];
+        h[i][e] *= w[e];   // n = h * rh
         am = fmaxf(am, fabsf(h[i][e]));
       }
-      if (p.norm_out) store8<VEC>(p.norm_out + row * p.ldn, c, H, h[i]);
+      if (p.norm_out) {
+        float n[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] = h[i][e] * rh;
+        store8<VEC>(p.norm_out + row * p.ldn, c, H, n);
+      }
       if (!p.q) continue;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-      const float sc = __fdiv_rn(fmaxf(am, 1e-10f), 448.0f);
+      // n / s with the row's factor cancelled: h / (max|h| / 448), unless the floor holds
+      const float an = am * rh;
+      const float sc = __fdiv_rn(fmaxf(an, 1e-10f), 448.0f);
+      const float dv = an >= 1e-10f ? __fdiv_rn(am, 448.0f) : __fdiv_rn(sc, rh);
       if ((tid & 15) == 0 && c < H) p.s[row * p.ssm + static_cast<int64_t>(c >> 7) * p.sskb] = sc;
-      const float rc = __frcp_rn(sc);
-      const float2 y2 = make_float2(rc, rc), ns2 = make_float2(-sc, -sc);
+      const float rc = __frcp_rn(dv);
+      const float2 y2 = make_float2(rc, rc), ns2 = make_float2(-dv, -dv);
       uint32_t cw[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
