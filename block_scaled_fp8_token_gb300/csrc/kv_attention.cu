@@ -26,6 +26,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
 
+// Waits for copies or products in flight before a block ends, whatever else
+// went wrong; bounded like every wait.
+BFP8_DEV void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > kWaitLimitNs) break;
+}
+
 struct AttnParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
@@ -36,10 +44,14 @@ struct AttnParams {
   const int32_t* q_offsets;
   const int32_t* kv_len;
   float* partial;            // split rows' partial sums
-  uint64_t* schedule;        // [B + 1]: units before each request, and in all
+  uint64_t* schedule;        // [B + 1]: the rows kernel's units before each request, and in all
+  uint32_t* item_base;       // [B]: the tiles kernel's items before each request
   int64_t q_ldt, q_ldh, o_ldt, o_ldh, l_ldt, ld_table, exp_page, exp_head;
   int64_t T, n_pages;
   int32_t B, H, G, page_shift, max_blocks, window;
+  int32_t few_rows;          // requests of at most this many rows of a KV head go to the rows kernel
+  int32_t splits;            // parts that the tiles kernel cuts an item's tokens into
+  float* tile_partial;       // [items * splits] of kTilePartialFloats
   float scale_log2;          // softmax scale * log2(e)
 };
 
@@ -85,6 +97,7 @@ BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   r.nt = r.n > 0 && hi > r.lo ? static_cast<uint32_t>(hi - r.lo) : 0u;
   const int64_t rows = static_cast<int64_t>(r.n) * p.G;
   r.nseg = static_cast<uint32_t>((rows + kRows - 1) / kRows) * p.H;
+  if (rows > p.few_rows) r.nt = 0;   // the tiles kernel's
   return r;
 }
 BFP8_DEV uint64_t units_of(const AttnParams& p, int b) {
@@ -600,11 +613,581 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok && lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
   // no copy may still be landing in shared memory when the block exits
   for (int s = 0; s < kStages; ++s)
-    if ((armed >> s) & 1u) {
-      const uint64_t t_start = globaltimer();
-      while (!mbar_try_wait(bar0 + 8 * s, (phase_bits >> s) & 1u))
-        if (globaltimer() - t_start > kWaitLimitNs) break;
+    if ((armed >> s) & 1u) drain(bar0 + 8 * s, (phase_bits >> s) & 1u);
+}
+
+// ============================================================ many query rows
+// An item is 256 query rows (two tiles of 128; the heads of a group times
+// consecutive tokens) of one request and KV head, against its tokens in tiles
+// of 128. S = Q K^T runs on the FP8 tensor cores with the codes of the keys as
+// they lie in memory: a query row goes in as two terms, hi in E5M2 (3 of a
+// BF16's 8 significant bits, and the range) and lo in E4M3 (the rest, exactly),
+// at the cost of one BF16 product and half its operand bytes. O += P V runs on the F16 ones, P rounded to 11 significant
+// bits and the codes of V widened exactly.
+//   warp 0       loads pages by TMA into a ring of keys and one of values
+//   warp 1       issues the products
+//   warps 2, 3   widen the values' codes to F16, MN-major, in two buffers
+//   warps 4..7   softmax of tile 0, one thread a row; warps 8..11 of tile 1
+// While one tile's softmax runs, the tensor cores work on the other's. S is
+// FP32 in tensor memory; P replaces it there and is the PV product's A
+// operand, so weights never touch shared memory. O stays in tensor memory and
+// is scaled down only when a row's maximum has outgrown the kept one by 2^10.
+constexpr int kTileRows = 128, kTileTokens = 128;
+constexpr int kItemRows = 2 * kTileRows;
+constexpr int kTileThreads = 384;
+constexpr int kTileStages = 3;
+constexpr int kInfos = kTileStages + 1;                  // see TileShared
+constexpr int kQBytes = kTileRows * kHeadDim;            // one term of one query tile
+constexpr int kKvBytes = kTileTokens * kHeadDim;
+constexpr int kV16Bytes = 2 * kKvBytes;
+constexpr int kTileSmem = 4 * kQBytes + kTileStages * 2 * kKvBytes + 2 * kV16Bytes + 1024;
+constexpr int kTilePartialFloats = kItemRows * kHeadDim + 2 * kItemRows;
+constexpr int kTileLaunchRegs = 168, kTileCtrlRegs = 72, kTileSoftRegs = 216;
+static_assert(kTileCtrlRegs + 2 * kTileSoftRegs == 3 * kTileLaunchRegs, "register split");
+constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w, O at 256 + 128 w
+
+struct TileItem {
+  int32_t b, h, q0, n, kv, held;
+  int32_t row0;          // first row of the item in its request
+  int32_t lo, hi;        // tiles of tokens, this part's
+};
+
+// Item `it` of request b (heaviest first: the last rows of a prompt see the most).
+BFP8_DEV TileItem tile_item(const AttnParams& p, int b, uint32_t it, int part) {
+  TileItem x;
+  x.b = b;
+  x.q0 = max(__ldg(p.q_offsets + b), 0);
+  x.n = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T) - x.q0);
+  x.kv = max(__ldg(p.kv_len + b), 0);
+  x.held = static_cast<int32_t>(min(static_cast<int64_t>(x.kv),
+                                    static_cast<int64_t>(p.max_blocks) << p.page_shift));
+  const uint32_t rows = static_cast<uint32_t>(x.n) * p.G;
+  const uint32_t pairs = (rows + kItemRows - 1) / kItemRows;
+  const uint32_t back = it / p.H;
+  x.h = it - back * p.H;
+  x.row0 = (pairs - 1 - back) * kItemRows;
+  const uint32_t last = min(rows, static_cast<uint32_t>(x.row0 + kItemRows)) - 1;
+  const int pos0 = x.kv - x.n + static_cast<int>(static_cast<uint32_t>(x.row0) / p.G);
+  const int pos1 = x.kv - x.n + static_cast<int>(last / p.G);
+  const int end = min(pos1 + 1, x.held);
+  const int begin = p.window >= 0 ? max(pos0 - p.window, 0) : 0;
+  const int lo = begin / kTileTokens;
+  const int hi = end > begin ? (end + kTileTokens - 1) / kTileTokens : lo;
+  const int64_t tiles = hi - lo;
+  x.lo = lo + static_cast<int>(tiles * part / p.splits);
+  x.hi = lo + static_cast<int>(tiles * (part + 1) / p.splits);
+  return x;
+}
+BFP8_DEV uint32_t tile_items_of(const AttnParams& p, int b) {
+  const int64_t q0 = max(__ldg(p.q_offsets + b), 0);
+  const int64_t n = min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T) - q0;
+  const int64_t rows = n * p.G;
+  if (n <= 0 || rows <= p.few_rows) return 0;
+  return static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows) * p.H;
+}
+
+// Three-way maximum, one instruction.
+BFP8_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+BFP8_DEV uint32_t join16(uint16_t lo, uint16_t hi) {
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+struct TileShared {
+  uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
+  uint64_t w_full[2], w_empty[2];      // the widened values' buffers
+  uint64_t info_full[kInfos];
+  uint64_t q_full, s_full[2], p_full[2], o_done[2], drained;
+  // What softmax needs of a tile. One slot more than there are stages: tile m's
+  // keys are loaded once S of tile m - 3 is complete for both query tiles, which
+  // follows their P of tile m - 4.
+  float4 scale[kInfos][8];             // per 16 tokens: 2^ek, ev, 2^-ev
+  uint16_t valid[kInfos][8];           // per 16 tokens: a bit for each that exists
+  uint32_t tmem;
+  uint32_t scan[kTileThreads / 32];
+  uint32_t found_it;
+  int found_b;
+  int abort_flag;
+};
+
+__global__ void __launch_bounds__(kTileThreads, 1)
+    kv_attention_tiles_kernel(const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ CUtensorMap tv, const AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TileShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = base;                         // [tile][hi, lo]
+  const uint32_t sK = base + 4 * kQBytes;
+  const uint32_t sV = sK + kTileStages * kKvBytes;
+  const uint32_t sW = sV + kTileStages * kKvBytes;  // [buffer][64 columns][token]
+  if (tid == 0) {
+    for (int s = 0; s < kTileStages; ++s) {
+      mbar_init(smem_u32(&sh.k_full[s]), 1);
+      mbar_init(smem_u32(&sh.k_empty[s]), 1);
+      mbar_init(smem_u32(&sh.v_full[s]), 1);
+      mbar_init(smem_u32(&sh.v_empty[s]), 2);
     }
+    for (int s = 0; s < kInfos; ++s) mbar_init(smem_u32(&sh.info_full[s]), 1);
+    mbar_init(smem_u32(&sh.q_full), 8);
+    mbar_init(smem_u32(&sh.drained), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&sh.w_full[w]), 2);
+      mbar_init(smem_u32(&sh.w_empty[w]), 1);
+      mbar_init(smem_u32(&sh.s_full[w]), 1);
+      mbar_init(smem_u32(&sh.p_full[w]), 4);
+      mbar_init(smem_u32(&sh.o_done[w]), 1);
+    }
+    sh.abort_flag = 0;
+    sh.found_b = -1;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- which item: block index = item * splits + part, items request by request
+  {
+    const uint32_t item = blockIdx.x / p.splits;
+    uint32_t run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kTileThreads) {
+      const uint32_t mine = b0 + tid < p.B ? tile_items_of(p, b0 + tid) : 0;
+      uint32_t inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = inc;
+      __syncthreads();
+      uint32_t total = 0, off = 0;
+#pragma unroll
+      for (int w = 0; w < kTileThreads / 32; ++w) {
+        if (w == warp) off = total;
+        total += sh.scan[w];
+      }
+      const uint32_t at = run + off + inc - mine;
+      if (mine && item >= at && item < at + mine) sh.found_b = b0 + tid, sh.found_it = item - at;
+      if (blockIdx.x == 0 && b0 + tid < p.B) p.item_base[b0 + tid] = at;
+      run += total;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int part = blockIdx.x % p.splits;
+  const volatile int* abort_flag = &sh.abort_flag;
+  const bool some = sh.found_b >= 0;
+  TileItem x{};
+  if (some) x = tile_item(p, sh.found_b, sh.found_it, part);
+  const int nt = x.hi - x.lo;
+
+  if (warp < 4) {
+    warpgroup_reg_dealloc<kTileCtrlRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer
+      const int page = 1 << p.page_shift;
+      const uint32_t box_bytes = page * kHeadDim;
+      bool ok = true;
+      uint32_t armed = 0, phases = 0;   // stages loaded, and the parity of each one's last load
+      const int32_t* row = p.table + x.b * p.ld_table;
+      auto page_id = [&](int j) {   // lane l < 8: the page of tokens 16 l .. of tile j
+        const int t = (x.lo + j) * kTileTokens + 16 * lane;
+        return j < nt && lane < 8 && t < x.held ? __ldg(row + (t >> p.page_shift)) : -1;
+      };
+      int32_t id = page_id(0);
+      for (int j = 0; j < nt; ++j) {
+        const int s = j % kTileStages;
+        const uint32_t ph = (j / kTileStages) & 1;
+        const uint32_t kf = smem_u32(&sh.k_full[s]), vf = smem_u32(&sh.v_full[s]);
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_sleep(smem_u32(&sh.k_empty[s]), ph ^ 1u, abort_flag) &&
+                            mbar_wait_sleep(smem_u32(&sh.v_empty[s]), ph ^ 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const int t = (x.lo + j) * kTileTokens + 16 * lane;
+        const bool there = lane < 8 && id >= 0 && id < p.n_pages;
+        const bool leads = there && (t & (page - 1)) == 0;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, leads));
+        if (lane == 0) {
+          mbar_expect_tx(kf, boxes * box_bytes);
+          mbar_expect_tx(vf, boxes * box_bytes);
+        }
+        __syncwarp();
+        if (leads) {
+          const uint32_t at = s * kKvBytes + 16 * lane * kHeadDim;
+          tma_load_4d(sK + at, &tk, 0, 0, x.h, id, kf);
+          tma_load_4d(sV + at, &tv, 0, 0, x.h, id, vf);
+        }
+        int ek = 127, ev = 127;
+        if (there) {
+          const int64_t at = id * p.exp_page + x.h * p.exp_head;
+          ek = __ldg(p.k_exp + at);
+          ev = __ldg(p.v_exp + at);
+        }
+        id = page_id(j + 1);
+        if (lane < 8) {
+          const int left = there ? min(x.held - t, 16) : 0;
+          sh.scale[j % kInfos][lane] = make_float4(exp2_int(ek - 127), static_cast<float>(ev - 127),
+                                                   exp2_int(127 - ev), 0.0f);
+          sh.valid[j % kInfos][lane] = static_cast<uint16_t>((1u << left) - 1u);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kf);
+          mbar_arrive(vf);
+          mbar_arrive(smem_u32(&sh.info_full[j % kInfos]));
+        }
+        armed |= 1u << s;
+        phases = (phases & ~(1u << s)) | (ph << s);
+      }
+      if (!ok) sh.abort_flag = 1;
+      // every stage's last load has landed before the block may end
+      for (int s = 0; s < kTileStages; ++s)
+        if ((armed >> s) & 1u) {
+          drain(smem_u32(&sh.k_full[s]), (phases >> s) & 1u);
+          drain(smem_u32(&sh.v_full[s]), (phases >> s) & 1u);
+        }
+      if (!ok && lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t kQk[2] = {idesc_e5m2_e4m3(kTileRows, kTileTokens),
+                                   idesc_e4m3(kTileRows, kTileTokens)};
+      constexpr uint32_t kPv = idesc_f16_bmn(kTileRows, kHeadDim);
+      bool ok = true;
+      auto wait = [&](uint64_t& bar, uint32_t parity) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&bar), parity, abort_flag))) ok = false;
+      };
+      auto qk = [&](int j, int w) {
+        const int s = j % kTileStages;
+        if (elect_one()) {
+          const uint64_t db = smem_desc_sw128(sK + s * kKvBytes);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint64_t da = smem_desc_sw128(sQ + (2 * w + t) * kQBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)   // 32 columns a step: 32 bytes
+              umma_e4m3(tmem + kColS + 128 * w, da + 2 * k, db + 2 * k, kQk[t], t || k);
+          }
+          umma_commit(smem_u32(&sh.s_full[w]));
+          if (w == 1) umma_commit(smem_u32(&sh.k_empty[s]));
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int j, int w) {
+        if (elect_one()) {
+          const uint64_t db = smem_desc_sw128_mn(sW + (j & 1) * kV16Bytes, kKvBytes);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)   // 16 tokens a step: 16 rows of 128 bytes
+            umma_f16_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 8 * k, db + 128 * k, kPv,
+                        j > 0 || k);
+          umma_commit(smem_u32(&sh.o_done[w]));
+          if (w == 1) umma_commit(smem_u32(&sh.w_empty[j & 1]));
+        }
+        __syncwarp();
+      };
+      if (nt > 0) {
+        wait(sh.q_full, 0);
+        wait(sh.k_full[0], 0);
+        tc_fence_after();
+        if (ok) qk(0, 0);
+        if (ok) qk(0, 1);
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+        wait(sh.w_full[j & 1], (j >> 1) & 1);
+        for (int w = 0; w < 2; ++w) {
+          wait(sh.p_full[w], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          pv(j, w);
+          if (j + 1 == nt) continue;
+          if (w == 0) wait(sh.k_full[(j + 1) % kTileStages], ((j + 1) / kTileStages) & 1);
+          if (!ok) break;
+          qk(j + 1, w);
+        }
+      }
+      if (!ok) {
+        sh.abort_flag = 1;
+        if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
+        // products in flight end before tensor memory is given back
+        if (elect_one()) umma_commit(smem_u32(&sh.drained));
+        __syncwarp();
+        drain(smem_u32(&sh.drained), 0);
+      }
+    } else {
+      // ------------------------------------------- values' codes widened to F16
+      // A lane takes 16 columns (chunk c) of a row a step; its 32 bytes go to
+      // columns 64 (c / 4) .. of that half's tile. Values of tokens that do not
+      // exist become zeros: what lies there may be NaN codes, and a weight of 0
+      // does not silence those.
+      const int c = lane & 7, r0 = 4 * (warp - 2) + (lane >> 3);
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        const int s = j % kTileStages;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_sleep(smem_u32(&sh.w_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag) &&
+                            mbar_wait_sleep(smem_u32(&sh.v_full[s]), (j / kTileStages) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint32_t src = sV + s * kKvBytes;
+        const uint32_t dst = sW + (j & 1) * kV16Bytes + (c >> 2) * kKvBytes;
+        const uint16_t* valid = sh.valid[j % kInfos];
+#pragma unroll 4
+        for (int i = 0; i < kTileTokens; i += 8) {
+          const int r = i + r0;
+          const bool there = (valid[r >> 4] >> (r & 15)) & 1u;
+          const uint4 v = lds128(src + r * kHeadDim + ((c ^ (r & 7)) << 4));
+          uint4 o[2];
+          o[0] = make_uint4(f16_pair(v.x, 0), f16_pair(v.x, 1), f16_pair(v.y, 0), f16_pair(v.y, 1));
+          o[1] = make_uint4(f16_pair(v.z, 0), f16_pair(v.z, 1), f16_pair(v.w, 0), f16_pair(v.w, 1));
+          if (!there) o[0] = o[1] = make_uint4(0u, 0u, 0u, 0u);
+          // the two halves' lanes store their two chunks in opposite order: no bank conflicts
+          const int first = c >> 2;
+          const uint32_t row = dst + r * 128;
+          const int k0 = 2 * (c & 3) + first, k1 = k0 ^ 1;
+          sts128(row + ((k0 ^ (r & 7)) << 4), first ? o[1] : o[0]);
+          sts128(row + ((k1 ^ (r & 7)) << 4), first ? o[0] : o[1]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh.v_empty[s]));
+          mbar_arrive(smem_u32(&sh.w_full[j & 1]));
+        }
+      }
+      if (!ok) {
+        sh.abort_flag = 1;
+        if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
+      }
+    }
+  } else {
+    // ------------------------------------------------- softmax, one thread a row
+    warpgroup_reg_alloc<kTileSoftRegs>();
+    const int w = (warp >> 2) - 1;                 // query tile
+    const int r = tid & 127;                       // row of the tile = TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 (warp mod 4)
+    const uint32_t i = x.row0 + w * kTileRows + r;
+    const uint32_t tok = some ? i / p.G : 0;
+    const bool real = some && tok < static_cast<uint32_t>(x.n);
+    const int64_t token = x.q0 + static_cast<int64_t>(real ? tok : 0);
+    const int head = x.h * p.G + (some ? i - tok * p.G : 0);
+    const int pos = x.kv - x.n + static_cast<int>(tok);
+    bool ok = true;
+
+    // The row's queries as two terms at a power of two that puts the largest
+    // entry in [2^11, 2^12). An entry of 2^e .. 2^(e+1) is a multiple of 2^(e-7);
+    // hi keeps 3 bits of it, so the rest is at most 16 of those steps, which
+    // E4M3's 4 bits hold, and 2^8 at most. Exact for entries down to 2^-13 of the
+    // largest; below, within 2^-21 of it.
+    float fac = 0.0f;
+    if (nt > 0) {
+      uint4 raw[16];
+      const __nv_bfloat16* src = p.q + token * p.q_ldt + head * p.q_ldh;
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        raw[c] = real ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max(m, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+      }
+      const int e = m ? min(max(11 - (static_cast<int>(m >> 7) - 127), -110), 110) : 0;
+      // a negative scale turns the queries round, so that the factor is positive
+      const float up = p.scale_log2 < 0.0f ? -exp2_int(e) : exp2_int(e);
+      fac = exp2_int(-e) * fabsf(p.scale_log2);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint4 q4 = raw[2 * c + (d >> 1)];
+          const uint32_t a = d & 1 ? q4.z : q4.x, b = d & 1 ? q4.w : q4.y;
+          const float f[4] = {__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up,
+                              __uint_as_float(b << 16) * up, __uint_as_float(b & 0xFFFF0000u) * up};
+          const uint16_t h0 = f32x2_to_e5m2x2(f[0], f[1]), h1 = f32x2_to_e5m2x2(f[2], f[3]);
+          const uint32_t b0 = e5m2x2_to_f16x2(h0), b1 = e5m2x2_to_f16x2(h1);
+          const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+          const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+          hi[d] = join16(h0, h1);
+          lo[d] = join16(f32x2_to_e4m3x2(f[0] - g0.x, f[1] - g0.y),
+                         f32x2_to_e4m3x2(f[2] - g1.x, f[3] - g1.y));
+        }
+        const uint32_t at = sQ + 2 * w * kQBytes + r * kHeadDim + ((c ^ (r & 7)) << 4);
+        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(at + kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+    }
+
+    // rows that do not exist never ask for a mask; what they compute is not stored
+    const int lim = real ? pos + 1 : 0x7FFFFFFF;
+    const int win = real && p.window >= 0 ? max(pos - p.window, 0) : 0;
+    const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+    const int win_warp = __reduce_max_sync(0xffffffffu, win);
+
+    float M = kNegInf, Z = 0.0f;
+    for (int j = 0; j < nt; ++j) {
+      const int t0 = (x.lo + j) * kTileTokens;
+      ok = mbar_wait(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
+           mbar_wait(smem_u32(&sh.s_full[w]), j & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float z[128];
+      {
+        float half[64];
+        tmem_ld64(lane_base + kColS + 128 * w, half);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) z[c] = half[c];
+        tmem_ld64(lane_base + kColS + 128 * w + 64, half);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) z[64 + c] = half[c];
+      }
+      const uint4 vw = *reinterpret_cast<const uint4*>(&sh.valid[j % kInfos][0]);
+      if ((vw.x & vw.y & vw.z & vw.w) != 0xffffffffu || t0 + kTileTokens > lim_warp || t0 < win_warp) {
+        const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int top = min(max(lim - t0 - 32 * k, 0), 32), low = min(max(win - t0 - 32 * k, 0), 32);
+          const uint32_t below = top == 32 ? 0xffffffffu : (1u << top) - 1u;
+          const uint32_t under = low == 32 ? 0xffffffffu : (1u << low) - 1u;
+          const uint32_t see = words[k] & below & ~under;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((see >> c) & 1u)) z[32 * k + c] = kNegInf;
+        }
+      }
+      // x = z * fac * 2^ek + ev per group of 16 tokens; the row's maximum of x
+      float top = kNegInf;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float4 sc = sh.scale[j % kInfos][g];
+        float m = max3(z[16 * g], z[16 * g + 1], z[16 * g + 2]);
+#pragma unroll
+        for (int c = 3; c < 15; c += 2) m = max3(m, z[16 * g + c], z[16 * g + c + 1]);
+        m = fmaxf(m, z[16 * g + 15]);
+        top = fmaxf(top, fmaf(m, fmaxf(fac * sc.x, 1e-37f), sc.y));
+      }
+      const bool grow = top > M + kLazy;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = !grow ? 1.0f : M == kNegInf ? 0.0f : ex2_approx(M - top);
+        if (grow) M = top;
+        if (j > 0) {
+          ok = mbar_wait(smem_u32(&sh.o_done[w]), (j - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          Z *= f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            uint32_t u[32];
+            tmem_ld32(lane_base + kColO + 128 * w + 32 * c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * f);
+            tmem_st32(lane_base + kColO + 128 * w + 32 * c, u);
+          }
+        }
+      }
+      const float sub = M == kNegInf ? 0.0f : M - kPBase;
+      float2 zsum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pw[32];
+#pragma unroll
+        for (int g = 4 * q; g < 4 * q + 4; ++g) {
+          const float4 sc = sh.scale[j % kInfos][g];
+          const float ck = fmaxf(fac * sc.x, 1e-37f), cb = sc.y - sub;
+          const float2 ck2 = make_float2(ck, ck), cb2 = make_float2(cb, cb);
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 y = __ffma2_rn(make_float2(z[16 * g + 2 * c], z[16 * g + 2 * c + 1]), ck2, cb2);
+            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            sum = __fadd2_rn(sum, e);
+            pw[8 * (g - 4 * q) + c] = pack_f16x2(e.x, e.y);
+          }
+          zsum = __ffma2_rn(sum, make_float2(sc.z, sc.z), zsum);
+        }
+        tmem_st32(lane_base + kColS + 128 * w + 32 * q, pw);
+      }
+      Z += zsum.x + zsum.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
+    }
+    if (ok && nt > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w]), (nt - 1) & 1, abort_flag));
+      tc_fence_after();
+    }
+    if (!ok) {
+      sh.abort_flag = 1;
+      if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
+    }
+    if (Z != Z && M == kNegInf) M = 0.0f;   // nothing but NaN scores: the row is NaN
+    if (some && ok) {
+      const bool split = p.splits > 1;
+      float* part_at = p.tile_partial + static_cast<int64_t>(blockIdx.x) * kTilePartialFloats;
+      const int row = w * kTileRows + r;
+      if (split) {
+        part_at[kItemRows * kHeadDim + row] = nt > 0 ? M : kNegInf;
+        part_at[kItemRows * kHeadDim + kItemRows + row] = Z;
+      } else if (real && p.lse) {
+        p.lse[token * p.l_ldt + head] = Z == 0.0f ? kNegInf : kLn2 * (M - kPBase + log2f(Z));
+      }
+      const float f = row_factor(Z);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        if (nt > 0) {
+          tmem_ld32(lane_base + kColO + 128 * w + 32 * c, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+        }
+        if (split) {
+          float4* dst = reinterpret_cast<float4*>(part_at + row * kHeadDim + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (real) {
+          __nv_bfloat16* dst = p.out + token * p.o_ldt + head * p.o_ldh + 32 * c;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = o[16 * k + e];
+            store_row16(dst + 16 * k, v, f);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // Joins the partial sums of segments that several blocks shared, in block
@@ -622,14 +1205,32 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   const uint32_t nrb = r.nseg / p.H;
   if (rb >= nrb) return;
   const uint32_t seg = h * nrb + rb;
-  const uint64_t U = __ldg(p.schedule + p.B);
-  const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.nt, e = a + r.nt;
-  uint32_t c0 = 0, c1 = 0, C = 1;
-  if (r.nt) {
-    C = used_blocks(U, grid);
-    c0 = owner_of(a, U, C);
-    c1 = owner_of(e - 1, U, C);
+  const int64_t rows = static_cast<int64_t>(r.n) * p.G;
+  // partial sums: `count` of them, `step` floats apart; M and Z behind the rows
+  const float* first = nullptr;
+  int64_t step = 0;
+  uint32_t count = 0, part_rows = kRows, row0 = 0;
+  if (rows > p.few_rows) {
+    if (p.splits == 1) return;
+    const uint32_t pairs = static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows);
+    const uint32_t pair = rb / (kItemRows / kRows);
+    const uint32_t item = __ldg(p.item_base + b) + (pairs - 1 - pair) * p.H + h;
+    first = p.tile_partial + static_cast<int64_t>(item) * p.splits * kTilePartialFloats;
+    step = kTilePartialFloats;
+    count = p.splits;
+    part_rows = kItemRows;
+    row0 = (rb % (kItemRows / kRows)) * kRows;
+  } else if (r.nt) {
+    const uint64_t U = __ldg(p.schedule + p.B);
+    const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.nt, e = a + r.nt;
+    const uint32_t C = used_blocks(U, grid);
+    const uint32_t c0 = owner_of(a, U, C), c1 = owner_of(e - 1, U, C);
     if (c0 == c1) return;
+    // the first block's slot is its second if the segment begins inside its
+    // range (it always does, or begins exactly with it); the others' the first
+    first = p.partial + static_cast<int64_t>(2 * c0 + 1) * kPartialFloats;
+    step = 2 * kPartialFloats;
+    count = c1 - c0 + 1;
   }
   const int row = threadIdx.x >> 3, ch = threadIdx.x & 7;   // 16 columns of a row per thread
   const RowAt at = row_at(p, r, seg, row);
@@ -637,25 +1238,24 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   float m = kNegInf, z = 0.0f, v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  if (r.nt) {
-    auto slot_of = [&](uint32_t c) {
-      return p.partial + static_cast<int64_t>(2 * c + (a >= range_begin(U, c, C) ? 1 : 0)) * kPartialFloats;
-    };
-    for (uint32_t c = c0; c <= c1; ++c) m = fmaxf(m, slot_of(c)[kRows * kHeadDim + row]);
-    for (uint32_t c = c0; c <= c1; ++c) {
-      const float* part = slot_of(c);
-      const float mc = part[kRows * kHeadDim + row];
-      if (mc == kNegInf) continue;
-      const float f = ex2_approx(mc - m);
-      z = fmaf(part[kRows * kHeadDim + kRows + row], f, z);
+  auto part_at = [&](uint32_t c) {   // blocks after the first begin inside the segment: first slot
+    return first + c * step - (part_rows == kRows && c ? kPartialFloats : 0);
+  };
+  const int64_t m_at = static_cast<int64_t>(part_rows) * kHeadDim + row0 + row;
+  for (uint32_t c = 0; c < count; ++c) m = fmaxf(m, part_at(c)[m_at]);
+  for (uint32_t c = 0; c < count; ++c) {
+    const float* part = part_at(c);
+    const float mc = part[m_at];
+    if (mc == kNegInf) continue;
+    const float f = ex2_approx(mc - m);
+    z = fmaf(part[m_at + part_rows], f, z);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(part + row * kHeadDim + 16 * ch + 4 * i);
-        v[4 * i] = fmaf(x.x, f, v[4 * i]);
-        v[4 * i + 1] = fmaf(x.y, f, v[4 * i + 1]);
-        v[4 * i + 2] = fmaf(x.z, f, v[4 * i + 2]);
-        v[4 * i + 3] = fmaf(x.w, f, v[4 * i + 3]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(part + (row0 + row) * kHeadDim + 16 * ch + 4 * i);
+      v[4 * i] = fmaf(x.x, f, v[4 * i]);
+      v[4 * i + 1] = fmaf(x.y, f, v[4 * i + 1]);
+      v[4 * i + 2] = fmaf(x.z, f, v[4 * i + 2]);
+      v[4 * i + 3] = fmaf(x.w, f, v[4 * i + 3]);
     }
   }
   store_row16(p.out + at.token * p.o_ldt + at.head * p.o_ldh + 16 * ch, v, row_factor(z));
@@ -680,15 +1280,46 @@ int launch_dependent(Kernel kernel, unsigned blocks, unsigned threads, size_t sm
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Requests whose rows of a KV head (new tokens times the group) are at most
+// this many go to the rows kernel: at 64 rows, four passes over the request's
+// tokens (from L2) still beat a tile that is a quarter full.
+constexpr int32_t kFewRows = 64;
+
+// What the host knows of a call's shape, from upper bounds alone.
+struct Shape {
+  bool tiles;          // some request may have more than kFewRows rows
+  int64_t items;       // at most so many items of the tiles kernel
+  int64_t splits;      // parts of each, before the tokens are looked at
+};
+Shape shape_of(int64_t B, int64_t T, int64_t max_q, int64_t G, int64_t H, int sms) {
+  Shape s{};
+  s.tiles = max_q * G > kFewRows;
+  if (!s.tiles) return s;
+  const int64_t rows = (max_q < T ? max_q * (B < T ? B : T) < T ? max_q * B : T : T) * G;
+  const int64_t big = B < rows / (kFewRows + 1) + 1 ? B : rows / (kFewRows + 1) + 1;
+  s.items = (rows / kItemRows + big) * H;
+  s.splits = 2 * s.items <= sms ? sms / s.items : 1;   // few items: share out their tokens
+  return s;
+}
+
+struct Workspace {
+  size_t item_base, partial, tile_partial, bytes;   // offsets; the schedule is at 0
+};
+Workspace workspace_of(int64_t B, const Shape& s, int sms) {
+  Workspace w{};
+  w.item_base = align256((B + 1) * 8);
+  w.partial = w.item_base + align256(B * 4);
+  w.tile_partial = w.partial + align256(static_cast<size_t>(sms) * 2 * kPartialFloats * 4);
+  w.bytes = w.tile_partial;
+  if (s.splits > 1) w.bytes += static_cast<size_t>(s.items) * s.splits * kTilePartialFloats * 4;
+  return w;
+}
+
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t H,
                                     int sms) {
-  (void)T;
-  (void)max_q;
-  (void)Hq;
-  (void)H;
-  return align256((B + 1) * 8) + static_cast<size_t>(sms) * 2 * kPartialFloats * 4;
+  return workspace_of(B, shape_of(B, T, max_q, Hq / H, H, sms), sms).bytes;
 }
 
 int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c, void* stream) {
@@ -710,7 +1341,7 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   };
   if (!rows16(a.q_bf16, a.q_stride_token, a.q_stride_head) ||
       !rows16(a.out_bf16, a.out_stride_token, a.out_stride_head) || a.batch > 0x7FFFFFFF ||
-      a.max_blocks > 0x7FFFFFFF || a.n_heads > 65535 * 64 || a.tokens > 0x7FFFFFFF)
+      a.max_blocks > 0x7FFFFFFF || a.tokens > 0x7FFFFFFF / a.n_heads)
     return BFP8_ERR_UNSUPPORTED;
   rc = check_device_ptrs({a.q_bf16, a.out_bf16, a.lse, a.q_offsets, a.kv_len, a.block_table,
                           c.k_e4m3, c.v_e4m3, c.k_exp, c.v_exp, a.workspace});
@@ -718,8 +1349,9 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   int sms = 0;
   rc = sm_count(&sms);
   if (rc != BFP8_OK) return rc;
-  const size_t need = kv_attention_workspace_bytes(a.batch, a.tokens, a.max_q_len, a.n_heads, H, sms);
-  if (!a.workspace || a.ws_bytes < need || reinterpret_cast<uintptr_t>(a.workspace) % 256)
+  const Shape shape = shape_of(a.batch, a.tokens, a.max_q_len, a.n_heads / H, H, sms);
+  const Workspace ws = workspace_of(a.batch, shape, sms);
+  if (!a.workspace || a.ws_bytes < ws.bytes || reinterpret_cast<uintptr_t>(a.workspace) % 256)
     return BFP8_ERR_INVALID_ARG;
   AttnParams p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q_bf16);
@@ -730,8 +1362,11 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.table = a.block_table;
   p.q_offsets = a.q_offsets;
   p.kv_len = a.kv_len;
-  p.schedule = static_cast<uint64_t*>(a.workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + align256((a.batch + 1) * 8));
+  uint8_t* scratch = static_cast<uint8_t*>(a.workspace);
+  p.schedule = reinterpret_cast<uint64_t*>(scratch);
+  p.item_base = reinterpret_cast<uint32_t*>(scratch + ws.item_base);
+  p.partial = reinterpret_cast<float*>(scratch + ws.partial);
+  p.tile_partial = reinterpret_cast<float*>(scratch + ws.tile_partial);
   p.q_ldt = a.q_stride_token;
   p.q_ldh = a.q_stride_head;
   p.o_ldt = a.out_stride_token;
@@ -749,27 +1384,58 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.max_blocks = static_cast<int32_t>(a.max_blocks);
   p.window = a.window < 0 ? -1 : a.window;
   p.scale_log2 = a.softmax_scale * kLog2e;
-  CUtensorMap tk, tv;
-  const uint32_t box = c.page_size < kUnit ? c.page_size : kUnit;
-  rc = make_tmap_4d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.k_e4m3, kHeadDim, c.page_size, H,
-                    c.n_pages, c.k_stride_token, c.k_stride_head, c.k_stride_page, kHeadDim, box, 1,
-                    1, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc != BFP8_OK) return rc;
-  rc = make_tmap_4d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.v_e4m3, kHeadDim, c.page_size, H,
-                    c.n_pages, c.v_stride_token, c.v_stride_head, c.v_stride_page, kHeadDim, box, 1,
-                    1, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc != BFP8_OK) return rc;
-  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_attention_rows_kernel), kSmemBytes);
-  if (rc != BFP8_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = launch_dependent(kv_attention_rows_kernel, sms, kThreads, kSmemBytes, st, tk, tv, p);
-  if (rc != BFP8_OK) return rc;
+  // a split has two tiles at least, at the table's full width
+  const int64_t tiles = (a.max_blocks * c.page_size + kTileTokens - 1) / kTileTokens;
+  p.splits = static_cast<int32_t>(shape.splits <= tiles / 2 ? shape.splits : tiles / 2);
+  if (p.splits < 1) p.splits = 1;
+  // one request has only one kernel to go to; of several, each is looked at on the device
+  p.few_rows = !shape.tiles ? 0x7FFFFFFF : a.batch > 1 ? kFewRows : 0;
   const int64_t max_rb = (a.max_q_len * p.G + kRows - 1) / kRows;
-  const int64_t blocks = a.batch * H * max_rb;
-  if (blocks > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
-  rc = launch_dependent(kv_attention_join_kernel, static_cast<unsigned>(blocks), 128, 0, st, p,
-                        static_cast<uint32_t>(sms), static_cast<uint32_t>(max_rb));
-  if (rc != BFP8_OK) return rc;
+  const int64_t join_rb = shape.tiles && p.splits == 1 && max_rb > kFewRows / kRows ? kFewRows / kRows : max_rb;
+  const int64_t items = shape.items * p.splits, joins = a.batch * H * join_rb;
+  if (items > 0x7FFFFFFF || joins > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
+  auto maps = [&](uint32_t rows, CUtensorMap* tk, CUtensorMap* tv) {
+    const int r = make_tmap_4d(tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.k_e4m3, kHeadDim, c.page_size, H,
+                               c.n_pages, c.k_stride_token, c.k_stride_head, c.k_stride_page,
+                               kHeadDim, rows, 1, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (r != BFP8_OK) return r;
+    return make_tmap_4d(tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.v_e4m3, kHeadDim, c.page_size, H,
+                        c.n_pages, c.v_stride_token, c.v_stride_head, c.v_stride_page, kHeadDim,
+                        rows, 1, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CUtensorMap tk, tv;
+  const bool rows_kernel = p.few_rows > 0;
+  if (rows_kernel) {
+    rc = maps(c.page_size < kUnit ? c.page_size : kUnit, &tk, &tv);
+    if (rc != BFP8_OK) return rc;
+    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_attention_rows_kernel), kSmemBytes);
+    if (rc != BFP8_OK) return rc;
+    rc = launch_dependent(kv_attention_rows_kernel, sms, kThreads, kSmemBytes, st, tk, tv, p);
+    if (rc != BFP8_OK) return rc;
+  }
+  if (shape.tiles) {
+    // setmaxnreg's split is made for the registers that the kernel was built with
+    static const int regs = [] {
+      cudaFuncAttributes attr{};
+      return cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(kv_attention_tiles_kernel)) ==
+                     cudaSuccess
+                 ? attr.numRegs : -1;
+    }();
+    if (regs != kTileLaunchRegs) return BFP8_ERR_UNSUPPORTED;
+    rc = maps(c.page_size, &tk, &tv);
+    if (rc != BFP8_OK) return rc;
+    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_attention_tiles_kernel), kTileSmem);
+    if (rc != BFP8_OK) return rc;
+    rc = launch_dependent(kv_attention_tiles_kernel, static_cast<unsigned>(items), kTileThreads,
+                          kTileSmem, st, tk, tv, p);
+    if (rc != BFP8_OK) return rc;
+  }
+  if (rows_kernel || p.splits > 1) {
+    rc = launch_dependent(kv_attention_join_kernel, static_cast<unsigned>(joins), 128, 0, st, p,
+                          static_cast<uint32_t>(sms), static_cast<uint32_t>(join_rb));
+    if (rc != BFP8_OK) return rc;
+  }
   return check_launch();
 }
 
