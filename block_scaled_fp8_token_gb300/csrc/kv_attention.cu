@@ -49,6 +49,7 @@ struct AttnParams {
   int64_t q_ldt, q_ldh, o_ldt, o_ldh, l_ldt, ld_table, exp_page, exp_head;
   int64_t T, n_pages;
   int32_t B, H, G, page_shift, max_blocks, window;
+  int32_t seg_rows;          // query rows of a segment of the rows kernel: 8 or 16
   int32_t few_rows;          // requests of at most this many rows of a KV head go to the rows kernel
   int32_t splits;            // parts that the tiles kernel cuts an item's tokens into
   float* tile_partial;       // [items * splits] of kTilePartialFloats
@@ -56,22 +57,27 @@ struct AttnParams {
 };
 
 // ============================================================ few query rows
-// A unit of work is 32 tokens of one segment; a segment is 16 query rows (the
-// heads of a group, times the tokens of a draft) of one request and KV head.
-// All units are numbered request by request and cut into equal contiguous
+// A unit of work is 32 tokens of one segment; a segment is 8 or 16 query rows
+// (the heads of a group, times the tokens of a draft) of one request and KV
+// head. All units are numbered request by request and cut into equal contiguous
 // ranges, one per block, so ragged lengths balance; a block's warps take its
 // units in turn, each with its own ring of shared-memory stages and no barrier
 // between them inside a segment.
+//
+// The products are transposed, tokens (and then columns of V) as the 16 rows of
+// an m16n8k16 product and query rows as its 8 columns: HBM bounds this kernel
+// only if the widening of the codes, two to an instruction, is all that is done
+// 128 bytes at a time, and a group of 8 heads fills such a product.
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 32;                 // tokens
-constexpr int kRows = 16;                 // query rows of a segment
+constexpr int kMaxRows = 16;              // query rows of a segment, at most
 constexpr int kStages = 2;
 constexpr int kStageBytes = 2 * kUnit * kHeadDim;            // keys, then values
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kMergeBytes = kWarps * kRows * kHeadDim * 4;
+constexpr int kMergeBytes = kWarps * 8 * kHeadDim * 4;
 constexpr int kSmemBytes = kRingBytes + kMergeBytes + 1024;  // + alignment
-constexpr int kPartialFloats = kRows * kHeadDim + 2 * kRows; // O, then M, then Z
+constexpr int kPartialFloats = kMaxRows * (kHeadDim + 2);    // O, then M, then Z
 // P is kept at 2^4 times the weight and the maximum moves only when a score
 // passes it by 2^10, so F16 holds P up to 2^14 and, to full precision, down to
 // 2^-18 of the maximum.
@@ -80,7 +86,7 @@ constexpr float kLazy = 10.0f;
 
 struct ReqUnits {
   int32_t q0, n, kv, lo;   // first row, new tokens, length, first unit
-  uint32_t nt, nseg;       // units of a segment, segments
+  uint32_t nt, nseg, nrb;  // units of a segment, segments, segments of a head
 };
 BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   ReqUnits r;
@@ -96,7 +102,8 @@ BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   const int64_t hi = (held + kUnit - 1) / kUnit;
   r.nt = r.n > 0 && hi > r.lo ? static_cast<uint32_t>(hi - r.lo) : 0u;
   const int64_t rows = static_cast<int64_t>(r.n) * p.G;
-  r.nseg = static_cast<uint32_t>((rows + kRows - 1) / kRows) * p.H;
+  r.nrb = static_cast<uint32_t>((rows + p.seg_rows - 1) / p.seg_rows);
+  r.nseg = r.nrb * p.H;
   if (rows > p.few_rows) r.nt = 0;   // the tiles kernel's
   return r;
 }
@@ -105,26 +112,28 @@ BFP8_DEV uint64_t units_of(const AttnParams& p, int b) {
   return static_cast<uint64_t>(r.nt) * r.nseg;
 }
 
-// A warp's place in the sequence of units.
-struct Cursor {
-  uint64_t base;    // first unit of request b
-  int b;
+// A segment, and the part of it inside a block's range: units u0 .. of it, at
+// `at` units into the range.
+struct SegPart {
   ReqUnits r;
-  uint32_t seg, u;  // segment of the request, unit of the segment
+  int b;
+  uint32_t seg, h, u0, at, len;
 };
-// Moves to unit g >= base. False past the last request.
-BFP8_DEV bool locate(const AttnParams& p, Cursor& c, uint64_t g) {
-  while (true) {
-    const uint64_t cnt = static_cast<uint64_t>(c.r.nt) * c.r.nseg;
-    if (g < c.base + cnt) break;
-    c.base += cnt;
-    if (++c.b >= p.B) return false;
-    c.r = req_units(p, c.b);
+BFP8_DEV void next_segment(const AttnParams& p, SegPart& s, uint32_t range) {
+  s.at += s.len;
+  s.u0 = 0;
+  if (++s.seg >= s.r.nseg) {
+    s.seg = 0;
+    do {   // some request behind this one has units: the range is not used up
+      if (++s.b >= p.B) {
+        s.len = 0;
+        return;
+      }
+      s.r = req_units(p, s.b);
+    } while (s.r.nt == 0 || s.r.nseg == 0);
   }
-  const uint32_t rel = static_cast<uint32_t>(g - c.base);
-  c.seg = rel / c.r.nt;
-  c.u = rel - c.seg * c.r.nt;
-  return true;
+  s.h = s.seg / s.r.nrb;
+  s.len = min(s.r.nt, range - s.at);
 }
 
 // Blocks that share U units: every warp of each gets one at least.
@@ -138,12 +147,18 @@ BFP8_DEV uint32_t owner_of(uint64_t g, uint64_t U, uint32_t C) {
   return static_cast<uint32_t>(((g + 1) * C - 1) / U);
 }
 
-BFP8_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+BFP8_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                      const uint32_t (&b)[2]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+BFP8_DEV uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 BFP8_DEV uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -154,18 +169,16 @@ BFP8_DEV uint32_t f16_pair(uint32_t word, int half) {
   return e4m3x2_to_f16x2(static_cast<uint16_t>(half ? word >> 16 : word & 0xFFFFu));
 }
 
-// Row r of a segment: which query and head it is.
+// Row `row` of a segment: which query and head it is.
 struct RowAt {
   int64_t token;
   int head;
   int pos;
   bool real;
 };
-BFP8_DEV RowAt row_at(const AttnParams& p, const ReqUnits& r, uint32_t seg, int row) {
+BFP8_DEV RowAt row_at(const AttnParams& p, const ReqUnits& r, uint32_t h, uint32_t rb, int row) {
   RowAt a;
-  const uint32_t nrb = r.nseg / p.H;
-  const uint32_t h = seg / nrb, rb = seg - h * nrb;
-  const uint32_t i = rb * kRows + row;
+  const uint32_t i = rb * p.seg_rows + row;
   const uint32_t tok = i / p.G;
   a.real = tok < static_cast<uint32_t>(r.n);
   a.token = r.q0 + static_cast<int64_t>(a.real ? tok : 0);
@@ -174,35 +187,40 @@ BFP8_DEV RowAt row_at(const AttnParams& p, const ReqUnits& r, uint32_t seg, int 
   return a;
 }
 
-// What a warp keeps of a unit between issuing its copies and using them.
-// The scale bytes are loaded when the copies are issued and first looked at when
+// What a warp keeps of a unit between issuing its copies and using them. The
+// scale bytes are loaded when the copies are issued and first looked at when
 // those have landed, so their latency hides behind the copies'.
 struct Pending {
   uint32_t k0, k1, v0, v1;   // scale bytes of the unit's two halves
   uint32_t valid;            // one bit per token that exists
 };
 
-BFP8_DEV void store_row16(__nv_bfloat16* dst, const float (&v)[16], float f) {
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1] * f), "f"(v[2 * j] * f));
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
 // out = O / Z and lse, from sums at maximum M; a row that saw nothing gives 0 and -inf.
 BFP8_DEV float row_factor(float Z) { return Z == 0.0f ? 0.0f : __frcp_rn(Z); }
 BFP8_DEV float row_lse(float M, float Z) {
   return Z == 0.0f ? kNegInf : kLn2 * (M - kPBase + log2f(Z));
 }
+BFP8_DEV uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+BFP8_DEV void store_row16(__nv_bfloat16* dst, const float (&v)[16], float f) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j] * f, v[2 * j + 1] * f);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
 
+// NB: query rows of a segment, in eights.
+template <int NB>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tk,
                              const __grid_constant__ CUtensorMap tv, const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[kWarps * kStages];
-  __shared__ float sm_m[kWarps][kRows], sm_z[kWarps][kRows];
+  __shared__ float sm_m[kWarps][8 * NB], sm_z[kWarps][8 * NB];
   __shared__ uint64_t scan[kWarps];
   __shared__ uint64_t start_base;
   __shared__ int start_b;
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t C = used_blocks(U, gridDim.x);
   const bool idle = blockIdx.x >= C || U == 0;
   const uint64_t g0 = idle ? 0 : range_begin(U, blockIdx.x, C);
-  const uint64_t g1 = idle ? 0 : range_begin(U, blockIdx.x + 1, C);
+  const uint32_t range = idle ? 0 : static_cast<uint32_t>(range_begin(U, blockIdx.x + 1, C) - g0);
   {
     uint64_t run = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -256,359 +274,383 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0 && tid == 0) p.schedule[p.B] = U;
   }
   __syncthreads();
-  if (idle) return;
+  if (range == 0) return;
 
   const uint32_t bar0 = smem_u32(&bars[warp * kStages]);
   const uint32_t stage0 = ring + warp * kStages * kStageBytes;
   const int page = 1 << p.page_shift;
   const int box = min(page, kUnit);
-  const int c = lane & 3, nrow = lane >> 2;
-  const int ktok = nrow ^ ((nrow & 1) << 2);   // see "Fragments" below
+  const uint32_t two = page < kUnit ? 1u : 0u;   // a unit's second half has a page of its own
+  const int c = lane & 3, g = lane >> 2;
+  const int gtok = g ^ ((g & 1) << 2);           // see "Fragments" below
 
-  // ---- issuing: this warp's next unit
-  Cursor pc;
-  pc.b = start_b;
-  pc.base = start_base;
-  pc.r = req_units(p, pc.b);
-  uint64_t pg = g0 + ((warp - g0) & (kWarps - 1));   // unit g belongs to warp g mod kWarps
-  int32_t id0 = -1, id1 = -1;                        // its page numbers (two when pages hold 16)
-  bool more = false;
+  SegPart cs;   // the segment being computed; the one being loaded starts the same
+  cs.b = start_b;
+  cs.r = req_units(p, cs.b);
+  {
+    const uint32_t rel = static_cast<uint32_t>(g0 - start_base);
+    cs.seg = rel / cs.r.nt;
+    cs.u0 = rel - cs.seg * cs.r.nt;
+    cs.h = cs.seg / cs.r.nrb;
+    cs.at = 0;
+    cs.len = min(cs.r.nt - cs.u0, range);
+  }
+  SegPart ps = cs;
+
+  // ---- issuing: this warp's next unit, px units into the range
+  uint32_t px = warp;
+  int32_t id0 = -1, id1 = -1;                    // its page numbers (two when pages hold 16)
+  int32_t pt0 = 0;                               // its first token
   auto fetch_ids = [&] {
-    more = pg < g1 && locate(p, pc, pg);
-    if (!more) return;
-    const int64_t t0 = static_cast<int64_t>(pc.r.lo + pc.u) * kUnit;
-    const int32_t* row = p.table + pc.b * p.ld_table;
-    const int64_t blk = t0 >> p.page_shift;
-    id0 = __ldg(row + blk);   // blk < max_blocks: units stop at the table's width
-    id1 = page < kUnit && blk + 1 < p.max_blocks && t0 + page < pc.r.kv ? __ldg(row + blk + 1) : -1;
+    if (px >= range) return;
+    while (px >= ps.at + ps.len) next_segment(p, ps, range);
+    pt0 = (ps.r.lo + static_cast<int32_t>(ps.u0 + px - ps.at)) * kUnit;
+    const int32_t* row = p.table + ps.b * p.ld_table + (pt0 >> p.page_shift);
+    id0 = __ldg(row);   // inside the table: units stop at its width
+    if (two) {
+      const bool in = (pt0 >> p.page_shift) + 1 < p.max_blocks && pt0 + page < ps.r.kv;
+      id1 = in ? __ldg(row + 1) : -1;
+    }
   };
   Pending pend0{}, pend1{};             // of stages 0 and 1
   uint32_t armed = 0, phase_bits = 0;   // stages with copies in flight; their parities
   auto issue = [&](Pending& pd, const int s) __attribute__((always_inline)) {
-    const uint32_t seg = pc.seg, nrb = pc.r.nseg / p.H;
-    const int h = seg / nrb;
-    const int64_t t0 = static_cast<int64_t>(pc.r.lo + pc.u) * kUnit;
-    const int off = static_cast<int>(t0 & (page - 1));
     const bool ok0 = id0 >= 0 && id0 < p.n_pages, ok1 = id1 >= 0 && id1 < p.n_pages;
-    const int64_t left = min(static_cast<int64_t>(pc.r.kv),
-                             static_cast<int64_t>(p.max_blocks) << p.page_shift) - t0;
+    const int64_t left = min(static_cast<int64_t>(ps.r.kv),
+                             static_cast<int64_t>(p.max_blocks) << p.page_shift) - pt0;
     uint32_t valid = left >= 32 ? 0xffffffffu : (1u << left) - 1u;   // left >= 1
-    const uint32_t half0 = page < kUnit ? 0xffffu : 0xffffffffu;
-    valid &= (ok0 ? half0 : 0u) | (page < kUnit && ok1 ? 0xffff0000u : 0u);
+    valid &= two ? (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u) : (ok0 ? 0xffffffffu : 0u);
     pd.valid = valid;
-    const int64_t e0 = id0 * p.exp_page + h * p.exp_head, e1 = id1 * p.exp_page + h * p.exp_head;
+    const int64_t e0 = id0 * p.exp_page + ps.h * p.exp_head;
     pd.k0 = pd.k1 = pd.v0 = pd.v1 = 127u;
     if (ok0) pd.k0 = __ldg(p.k_exp + e0), pd.v0 = __ldg(p.v_exp + e0);
-    if (page < kUnit && ok1) pd.k1 = __ldg(p.k_exp + e1), pd.v1 = __ldg(p.v_exp + e1);
+    if (two && ok1) {
+      const int64_t e1 = id1 * p.exp_page + ps.h * p.exp_head;
+      pd.k1 = __ldg(p.k_exp + e1), pd.v1 = __ldg(p.v_exp + e1);
+    }
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * s, dst = stage0 + s * kStageBytes;
       const uint32_t bytes = box * kHeadDim;
-      mbar_arrive_expect_tx(bar, 2 * bytes * ((ok0 ? 1 : 0) + (ok1 ? 1 : 0)));
+      mbar_arrive_expect_tx(bar, 2 * bytes * ((ok0 ? 1 : 0) + (two && ok1 ? 1 : 0)));
       if (ok0) {
-        tma_load_4d(dst, &tk, 0, off, h, id0, bar);
-        tma_load_4d(dst + kUnit * kHeadDim, &tv, 0, off, h, id0, bar);
+        tma_load_4d(dst, &tk, 0, pt0 & (page - 1), ps.h, id0, bar);
+        tma_load_4d(dst + kUnit * kHeadDim, &tv, 0, pt0 & (page - 1), ps.h, id0, bar);
       }
-      if (ok1) {
-        tma_load_4d(dst + bytes, &tk, 0, 0, h, id1, bar);
-        tma_load_4d(dst + kUnit * kHeadDim + bytes, &tv, 0, 0, h, id1, bar);
+      if (two && ok1) {
+        tma_load_4d(dst + bytes, &tk, 0, 0, ps.h, id1, bar);
+        tma_load_4d(dst + kUnit * kHeadDim + bytes, &tv, 0, 0, ps.h, id1, bar);
       }
     }
     armed |= 1u << s;
-    pg += kWarps;
+    px += kWarps;
     fetch_ids();
   };
   fetch_ids();
-  if (more) issue(pend0, 0);
-  if (more) issue(pend1, 1);
+  if (px < range) issue(pend0, 0);
+  if (px < range) issue(pend1, 1);
 
-  // ---- segments of this block's range
-  Cursor cc;
-  cc.b = start_b;
-  cc.base = start_base;
-  cc.r = req_units(p, cc.b);
-  int stage = 0;
-  bool ok = true;
-  for (uint64_t g = g0; g < g1;) {
-    if (!locate(p, cc, g)) break;
-    const uint64_t seg_begin = g - cc.u, seg_end = seg_begin + cc.r.nt;
-    const uint64_t pe = seg_end < g1 ? seg_end : g1;
-    const uint32_t seg = cc.seg;
-    const int rows_left = [&] {
-      const uint32_t nrb = cc.r.nseg / p.H, rb = seg - seg / nrb * nrb;
-      const int64_t left = static_cast<int64_t>(cc.r.n) * p.G - static_cast<int64_t>(rb) * kRows;
-      return static_cast<int>(left < kRows ? left : kRows);
-    }();
-
-    // Query rows nrow and nrow + 8 as F16 at a power of two that puts the row's
-    // largest entry in [2^8, 2^9): a BF16 has 8 significant bits and F16 11, so
-    // entries down to 2^-22 of the largest are exact.
-    const RowAt ra = row_at(p, cc.r, seg, nrow), rb = row_at(p, cc.r, seg, nrow + 8);
-    uint32_t qa[8][4];
-    float fac[2];
-    {
-      uint4 raw[2][4];
+  // ---- query rows: lane (g, c) loads 16-byte chunks c and c + 4 of rows 8 nb + g
+  uint4 raw[NB][4];
+  auto load_q = [&](const SegPart& s) {
+    const uint32_t rb = s.seg - s.h * s.r.nrb;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const RowAt& r = i ? rb : ra;
-        const __nv_bfloat16* src = p.q + r.token * p.q_ldt + r.head * p.q_ldh + 16 * c;
+    for (int nb = 0; nb < NB; ++nb) {
+      const RowAt r = row_at(p, s.r, s.h, rb, 8 * nb + g);
+      const __nv_bfloat16* src = p.q + r.token * p.q_ldt + r.head * p.q_ldh + 16 * c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          raw[i][j] = make_uint4(0u, 0u, 0u, 0u);
-          if (r.real) raw[i][j] = __ldg(reinterpret_cast<const uint4*>(src + 64 * (j >> 1) + 8 * (j & 1)));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w[4] = {raw[i][j].x, raw[i][j].y, raw[i][j].z, raw[i][j].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-        }
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int e = m ? min(max(8 - (static_cast<int>(m >> 7) - 127), -110), 110) : 0;
-        const float up = exp2_int(e);
-        fac[i] = exp2_int(-e) * p.scale_log2;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w[4] = {raw[i][j].x, raw[i][j].y, raw[i][j].z, raw[i][j].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t v = pack_f16x2(__uint_as_float(w[x] << 16) * up,
-                                          __uint_as_float(w[x] & 0xFFFF0000u) * up);
-            // 16 columns of chunk c + 4 (j >> 1): step s holds columns 4 (s & 3) .. + 3
-            const int s = 4 * (j >> 1) + 2 * (j & 1) + (x >> 1);
-            qa[s][i + 2 * (x & 1)] = v;
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        raw[nb][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r.real) raw[nb][j] = __ldg(reinterpret_cast<const uint4*>(src + 64 * (j >> 1) + 8 * (j & 1)));
       }
     }
-    const int lim0 = ra.real ? ra.pos + 1 : 0, lim1 = rb.real ? rb.pos + 1 : 0;
-    const int win0 = p.window >= 0 ? max(ra.pos - p.window, 0) : 0;
-    const int win1 = p.window >= 0 ? max(rb.pos - p.window, 0) : 0;
+  };
+  load_q(cs);
 
-    float o[16][4];
+  int stage = 0;
+  bool ok = true;
+  while (cs.at < range) {
+    const uint32_t rb = cs.seg - cs.h * cs.r.nrb;
+    const int rows_left = static_cast<int>(
+        min(static_cast<int64_t>(8 * NB),
+            static_cast<int64_t>(cs.r.n) * p.G - static_cast<int64_t>(rb) * (8 * NB)));
+
+    // Query rows as F16 at a power of two that puts the row's largest entry in
+    // [2^8, 2^9): a BF16 has 8 significant bits and F16 11, so entries down to
+    // 2^-22 of the largest are exact.
+    uint32_t qb[NB][8][2];
+    float fac[NB][2];              // of rows 2c and 2c + 1: what a score is in log2 units
+    int lim[NB][2], win[NB][2];    // they see [win, lim)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-    float M[2] = {kNegInf, kNegInf}, Z[2] = {0.0f, 0.0f};
+    for (int nb = 0; nb < NB; ++nb) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+      }
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = m ? min(max(8 - (static_cast<int>(m >> 7) - 127), -110), 110) : 0;
+      const float up = exp2_int(e), f = exp2_int(-e) * p.scale_log2;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)   // step s holds columns 4 (s & 3) .. + 3 of chunk c + 4 (s / 4)
+          qb[nb][4 * (j >> 1) + 2 * (j & 1) + (x >> 1)][x & 1] =
+              pack_f16x2(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xFFFF0000u) * up);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        fac[nb][j] = __shfl_sync(0xffffffffu, f, (2 * c + j) * 4);
+        const RowAt r = row_at(p, cs.r, cs.h, rb, 8 * nb + 2 * c + j);
+        lim[nb][j] = r.real ? r.pos + 1 : 0x7FFFFFFF;   // rows that do not exist never ask for a mask
+        win[nb][j] = r.real && p.window >= 0 ? max(r.pos - p.window, 0) : 0;
+      }
+    }
+    int lim_min = lim[0][0], win_max = win[0][0];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lim_min = min(lim_min, lim[nb][j]), win_max = max(win_max, win[nb][j]);
+    }
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+    win_max = __reduce_max_sync(0xffffffffu, win_max);
+
+    float o[NB][8][4];
+    float M[NB][2], Z[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.0f;
+      M[nb][0] = M[nb][1] = kNegInf;
+      Z[nb][0] = Z[nb][1] = 0.0f;
+    }
 
     // One unit, from stage ST. False when the wait for it ran out.
-    auto unit = [&](const uint64_t x, Pending& pd, const int ST) __attribute__((always_inline)) {
+    auto unit = [&](const uint32_t u, Pending& pd, const int ST) __attribute__((always_inline)) {
       const uint32_t bar = bar0 + 8 * ST;
       const uint32_t kb = stage0 + ST * kStageBytes, vb = kb + kUnit * kHeadDim;
       if (!__all_sync(0xffffffffu, mbar_wait(bar, (phase_bits >> ST) & 1u, &abort_flag))) return false;
       armed &= ~(1u << ST);
       phase_bits ^= 1u << ST;
-      const uint32_t two = page < kUnit ? 1u : 0u;   // the second half has a page of its own
       const int ek[2] = {static_cast<int>(pd.k0) - 127, static_cast<int>(two ? pd.k1 : pd.k0) - 127};
       const int ev[2] = {static_cast<int>(pd.v0) - 127, static_cast<int>(two ? pd.v1 : pd.v0) - 127};
       const uint32_t valid = pd.valid;
-      const int t0 = static_cast<int>((cc.r.lo + static_cast<uint32_t>(x - seg_begin)) * kUnit);
+      const int t0 = (cs.r.lo + static_cast<int32_t>(u)) * kUnit;
 
-      // Fragments. QK: rows x 8 tokens x 16 columns a step, and which column is
-      // which does not matter as long as q agrees, so a lane reads its token's
-      // 16-byte chunks c and c + 4 whole. PV: a lane reads 16 columns
-      // (lane / 4) of four tokens, and O's columns come out as 32 in a row per
-      // lane. Token n of a block of eight is n ^ 4(n & 1): with the 128-byte
-      // swizzle both reads are then free of bank conflicts.
-      float s[4][4];
+      // Fragments. S^T: 16 tokens x 16 columns of K a step, and which column is
+      // which does not matter as long as q agrees, so a lane reads its tokens'
+      // 16-byte chunks c and c + 4 whole. O^T: a lane reads 16 columns (chunk g)
+      // of four tokens, and holds 16 columns in a row of O for rows 2c, 2c + 1.
+      // Token n of a block of eight is n ^ 4(n & 1): with the 128-byte swizzle
+      // both reads are then free of bank conflicts.
+      float s[NB][2][4];
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
-        const uint32_t row = kb + (nb * 8 + ktok) * kHeadDim;
-        const uint4 ka = lds128(row + ((c ^ ktok) << 4));
-        const uint4 kc = lds128(row + (((c + 4) ^ ktok) << 4));
-        const uint32_t w[8] = {ka.x, ka.y, ka.z, ka.w, kc.x, kc.y, kc.z, kc.w};
+      for (int mb = 0; mb < 2; ++mb) {
+        const uint32_t row = kb + (16 * mb + gtok) * kHeadDim;
+        const uint32_t x0 = (c ^ gtok) << 4, x1 = ((c + 4) ^ gtok) << 4;
+        const uint4 a = lds128(row + x0), b = lds128(row + x1);
+        const uint4 d = lds128(row + 8 * kHeadDim + x0), e = lds128(row + 8 * kHeadDim + x1);
+        const uint32_t w1[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t w2[8] = {d.x, d.y, d.z, d.w, e.x, e.y, e.z, e.w};
 #pragma unroll
-        for (int st = 0; st < 8; ++st) mma_f16(s[nb], qa[st], f16_pair(w[st], 0), f16_pair(w[st], 1));
+        for (int nb = 0; nb < NB; ++nb) s[nb][mb][0] = s[nb][mb][1] = s[nb][mb][2] = s[nb][mb][3] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < 8; ++st) {
+          const uint32_t a0 = f16_pair(w1[st], 0), a1 = f16_pair(w2[st], 0);
+          const uint32_t a2 = f16_pair(w1[st], 1), a3 = f16_pair(w2[st], 1);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16(s[nb][mb], a0, a1, a2, a3, qb[nb][st]);
+        }
       }
-      // scores in units of log2, the value scale's exponent added; column e of
-      // block nb is token nb * 8 + 2c + e, moved as above
-      const float kf[2] = {exp2_int(ek[0]), exp2_int(ek[1])};
+      // s[nb][mb]: tokens 16 mb + gtok (entries 0, 1) and 8 on (2, 3), rows 2c
+      // and 2c + 1. In log2 units, with the value scale's exponent:
+      const bool masked = valid != 0xffffffffu || t0 + kUnit > lim_min || t0 < win_max;
       const float lv[2] = {static_cast<float>(ev[0]), static_cast<float>(ev[1])};
-      float mx[2] = {kNegInf, kNegInf};
-      const bool masked = valid != 0xffffffffu || t0 + kUnit > min(lim0, lim1) ||
-                          t0 < max(win0, win1);
+      const float kf[2] = {exp2_int(ek[0]), exp2_int(ek[1])};
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e >> 1;
-          s[nb][e] = fmaf(s[nb][e], fac[i] * kf[nb >> 1], lv[nb >> 1]);
+        for (int mb = 0; mb < 2; ++mb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[nb][mb][e] = fmaf(s[nb][mb][e], fac[nb][e & 1] * kf[mb], lv[mb]);
         }
       }
       if (masked) {
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = e >> 1;
-            const int tk_ = nb * 8 + ((2 * c + (e & 1)) ^ ((e & 1) << 2));
-            const int at = t0 + tk_;
-            const bool see = ((valid >> tk_) & 1u) && at < (i ? lim1 : lim0) &&
-                             at >= (i ? win1 : win0);
-            if (!see) s[nb][e] = kNegInf;
+          for (int mb = 0; mb < 2; ++mb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = 16 * mb + gtok + 8 * (e >> 1), at = t0 + tok;
+              if (!((valid >> tok) & 1u) || at >= lim[nb][e & 1] || at < win[nb][e & 1])
+                s[nb][mb][e] = kNegInf;
+            }
+          }
+        }
+      }
+      float mx[NB][2];
+      bool grow = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float m = fmaxf(fmaxf(s[nb][0][j], s[nb][0][2 + j]), fmaxf(s[nb][1][j], s[nb][1][2 + j]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+          mx[nb][j] = m;
+          grow |= m > M[nb][j] + kLazy;   // from -inf: any score
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float f[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool up = mx[nb][j] > M[nb][j] + kLazy;
+            f[j] = !up ? 1.0f : M[nb][j] == kNegInf ? 0.0f : ex2_approx(M[nb][j] - mx[nb][j]);
+            if (up) M[nb][j] = mx[nb][j];
+            Z[nb][j] *= f[j];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nb][i][e] *= f[e & 1];
+          }
+        }
+      }
+      const float iv[2] = {exp2_int(-ev[0]), exp2_int(-ev[1])};
+      uint32_t pb[NB][2][2];   // P^T as the B operand of two 16-token steps
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float sub[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sub[j] = M[nb][j] == kNegInf ? 0.0f : M[nb][j] - kPBase;
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nb][mb][e] = ex2_approx(s[nb][mb][e] - sub[e & 1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            pb[nb][mb][j] = transpose8x8(pack_f16x2(s[nb][mb][2 * j], s[nb][mb][2 * j + 1]));
+            Z[nb][j] = fmaf(s[nb][mb][j] + s[nb][mb][2 + j], iv[mb], Z[nb][j]);
           }
         }
       }
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        mx[0] = fmaxf(mx[0], fmaxf(s[nb][0], s[nb][1]));
-        mx[1] = fmaxf(mx[1], fmaxf(s[nb][2], s[nb][3]));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-      }
-      const bool up0 = mx[0] > M[0] + kLazy, up1 = mx[1] > M[1] + kLazy;   // from -inf: any score
-      if (__any_sync(0xffffffffu, up0 || up1)) {
-        const float f0 = up0 ? (M[0] == kNegInf ? 0.0f : ex2_approx(M[0] - mx[0])) : 1.0f;
-        const float f1 = up1 ? (M[1] == kNegInf ? 0.0f : ex2_approx(M[1] - mx[1])) : 1.0f;
-        if (up0) M[0] = mx[0];
-        if (up1) M[1] = mx[1];
-        Z[0] *= f0;
-        Z[1] *= f1;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j][0] *= f0;
-          o[j][1] *= f0;
-          o[j][2] *= f1;
-          o[j][3] *= f1;
-        }
-      }
-      const float sub[2] = {M[0] == kNegInf ? 0.0f : M[0] - kPBase,
-                            M[1] == kNegInf ? 0.0f : M[1] - kPBase};
-      const float iv[2] = {exp2_int(-ev[0]), exp2_int(-ev[1])};
-      uint32_t pa[2][4];   // P as the A operand of two 16-token steps
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nb][e] = ex2_approx(s[nb][e] - sub[e >> 1]);
-        pa[nb >> 1][2 * (nb & 1)] = pack_f16x2(s[nb][0], s[nb][1]);
-        pa[nb >> 1][2 * (nb & 1) + 1] = pack_f16x2(s[nb][2], s[nb][3]);
-        Z[0] = fmaf(s[nb][0] + s[nb][1], iv[nb >> 1], Z[0]);
-        Z[1] = fmaf(s[nb][2] + s[nb][3], iv[nb >> 1], Z[1]);
-      }
-#pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2) {
+      for (int mb = 0; mb < 2; ++mb) {
         uint4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // tokens of fragment rows 2c, 2c + 1, 2c + 8, 2c + 9
-          const int tk_ = 16 * h2 + 8 * (i >> 1) + ((2 * c + (i & 1)) ^ ((i & 1) << 2));
-          v[i] = lds128(vb + tk_ * kHeadDim + ((nrow ^ (tk_ & 7)) << 4));
+          // the tokens of fragment columns 2c, 2c + 1, 2c + 8, 2c + 9
+          const int tok = 16 * mb + 8 * (i >> 1) + ((2 * c + (i & 1)) ^ ((i & 1) << 2));
+          v[i] = lds128(vb + tok * kHeadDim + ((g ^ (tok & 7)) << 4));
           // rows never written may hold NaN codes: 0 * NaN would reach every column
-          if (masked && !((valid >> tk_) & 1u)) v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (masked && !((valid >> tok) & 1u)) v[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        const uint32_t a0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, a1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-        const uint32_t a2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, a3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+        const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+        const uint32_t v2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t lo01 = __byte_perm(a0[w], a1[w], 0x5140), lo23 = __byte_perm(a0[w], a1[w], 0x7362);
-          const uint32_t hi01 = __byte_perm(a2[w], a3[w], 0x5140), hi23 = __byte_perm(a2[w], a3[w], 0x7362);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma_f16(o[4 * w + e], pa[h2], f16_pair(e < 2 ? lo01 : lo23, e & 1),
-                    f16_pair(e < 2 ? hi01 : hi23, e & 1));
+          for (int e = 0; e < 2; ++e) {   // columns 4w + 2e and one on, of two tokens a word
+            const uint32_t sel = e ? 0x7362 : 0x5140;
+            const uint32_t ab = __byte_perm(v0[w], v1[w], sel), cd = __byte_perm(v2[w], v3[w], sel);
+            const uint32_t a0 = f16_pair(ab, 0), a1 = f16_pair(ab, 1);
+            const uint32_t a2 = f16_pair(cd, 0), a3 = f16_pair(cd, 1);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * w + e], a0, a1, a2, a3, pb[nb][mb]);
+          }
         }
       }
       __syncwarp();   // every lane has read the stage
-      if (more) issue(pd, ST);
+      if (px < range) issue(pd, ST);
       return true;
     };
-    for (uint64_t x = g + ((warp - g) & (kWarps - 1)); ok && x < pe; x += kWarps) {
-      ok = stage ? unit(x, pend1, 1) : unit(x, pend0, 0);
+    for (uint32_t x = cs.at + ((warp - cs.at) & (kWarps - 1)); ok && x < cs.at + cs.len; x += kWarps) {
+      const uint32_t u = cs.u0 + x - cs.at;
+      ok = stage ? unit(u, pend1, 1) : unit(u, pend0, 0);
       stage ^= 1;
     }
     if (!ok) abort_flag = 1;
 
-    // ---- the block's warps together: M, Z and O of rows nrow and nrow + 8
+    // the next segment's query rows are on their way while this one is finished
+    SegPart nx = cs;
+    next_segment(p, nx, range);
+    if (nx.at < range) load_q(nx);
+
+    // ---- the block's warps together, eight rows at a time
+    const bool whole = cs.u0 == 0 && cs.len == cs.r.nt;
+    float* part = p.partial +
+                  static_cast<int64_t>(2 * blockIdx.x + (cs.u0 == 0 ? 1 : 0)) * kPartialFloats;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      Z[i] += __shfl_xor_sync(0xffffffffu, Z[i], 1);
-      Z[i] += __shfl_xor_sync(0xffffffffu, Z[i], 2);
-      if (Z[i] != Z[i] && M[i] == kNegInf) M[i] = 0.0f;   // nothing but NaN scores: the row is NaN
-      if (c == 0) {
-        sm_m[warp][nrow + 8 * i] = M[i];
-        sm_z[warp][nrow + 8 * i] = Z[i];
-      }
-    }
-    // a lane's 32 columns 32c .. 32c + 31 as 16-byte chunks 8c .. 8c + 7,
-    // chunk 8c + k kept at 8c + (k ^ 2c ^ (row & 1)): free of bank conflicts
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = nrow + 8 * i;
-      if (row >= rows_left || M[i] == kNegInf) continue;
-      float* dst = merge + (warp * kRows + row) * kHeadDim;
+      for (int j = 0; j < 2; ++j) {
+        float z = Z[nb][j], m = M[nb][j];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+        for (int x = 4; x < 32; x <<= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
+        if (z != z && m == kNegInf) m = 0.0f;   // nothing but NaN scores: the row is NaN
+        if (g == 0) {
+          sm_m[warp][8 * nb + 2 * c + j] = m;
+          sm_z[warp][8 * nb + 2 * c + j] = z;
+        }
+        // a lane's 16 columns as 16-byte chunks 4g .. 4g + 3, chunk k of row r
+        // kept at k ^ (r / 2): free of bank conflicts
+        const int row = 2 * c + j;
+        if (8 * nb + row < rows_left && m != kNegInf) {
+          float* dst = merge + (warp * 8 + row) * kHeadDim;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 4 * e + j;
-          *reinterpret_cast<float4*>(dst + 4 * (8 * c + (k ^ (2 * c) ^ (row & 1)))) =
-              make_float4(o[4 * j][2 * i + e], o[4 * j + 1][2 * i + e], o[4 * j + 2][2 * i + e],
-                          o[4 * j + 3][2 * i + e]);
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(dst + 4 * ((4 * g + k) ^ c)) =
+                make_float4(o[nb][2 * k][j], o[nb][2 * k][2 + j], o[nb][2 * k + 1][j],
+                            o[nb][2 * k + 1][2 + j]);
         }
       }
-    }
-    __syncthreads();
-    const bool whole = g == seg_begin && pe == seg_end;
-    const uint32_t slot = 2 * blockIdx.x + (g == seg_begin ? 1 : 0);
-    float* part = p.partial + static_cast<int64_t>(slot) * kPartialFloats;
-    {
-      const int row = tid >> 4, ch = tid & 15;   // 8 columns of a row per thread
-      if (row < rows_left) {
+      __syncthreads();
+      for (int it = tid; it < 8 * 32; it += kThreads) {   // a row's 16-byte chunk each
+        const int row = it >> 5, ch = it & 31, srow = 8 * nb + row;
+        if (srow >= rows_left) continue;
         float m = kNegInf;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w][row]);
-        float z = 0.0f, v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w][srow]);
+        float z = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = sm_m[w][row];
+          const float mw = sm_m[w][srow];
           if (mw == kNegInf) continue;
           const float f = ex2_approx(mw - m);
-          z = fmaf(sm_z[w][row], f, z);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int chunk = 2 * ch + e, cg = chunk >> 3;
-            const float4 x = *reinterpret_cast<const float4*>(
-                merge + (w * kRows + row) * kHeadDim +
-                4 * (8 * cg + ((chunk & 7) ^ (2 * cg) ^ (row & 1))));
-            v[4 * e] = fmaf(x.x, f, v[4 * e]);
-            v[4 * e + 1] = fmaf(x.y, f, v[4 * e + 1]);
-            v[4 * e + 2] = fmaf(x.z, f, v[4 * e + 2]);
-            v[4 * e + 3] = fmaf(x.w, f, v[4 * e + 3]);
-          }
+          z = fmaf(sm_z[w][srow], f, z);
+          const float4 y = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * kHeadDim +
+                                                            4 * (ch ^ (row >> 1)));
+          v.x = fmaf(y.x, f, v.x);
+          v.y = fmaf(y.y, f, v.y);
+          v.z = fmaf(y.z, f, v.z);
+          v.w = fmaf(y.w, f, v.w);
         }
         if (whole) {
-          const RowAt r = row_at(p, cc.r, seg, row);
+          const RowAt r = row_at(p, cs.r, cs.h, rb, srow);
           const float f = row_factor(z);
-          uint32_t w4[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                : "=r"(w4[j]) : "f"(v[2 * j + 1] * f), "f"(v[2 * j] * f));
-          *reinterpret_cast<uint4*>(p.out + r.token * p.o_ldt + r.head * p.o_ldh + 8 * ch) =
-              make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          *reinterpret_cast<uint2*>(p.out + r.token * p.o_ldt + r.head * p.o_ldh + 4 * ch) =
+              make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
           if (p.lse && ch == 0) p.lse[r.token * p.l_ldt + r.head] = row_lse(m, z);
         } else {
-          float4* dst = reinterpret_cast<float4*>(part + row * kHeadDim + 8 * ch);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          *reinterpret_cast<float4*>(part + srow * kHeadDim + 4 * ch) = v;
           if (ch == 0) {
-            part[kRows * kHeadDim + row] = m;
-            part[kRows * kHeadDim + kRows + row] = z;
+            part[8 * NB * kHeadDim + srow] = m;
+            part[8 * NB * (kHeadDim + 1) + srow] = z;
           }
         }
       }
+      __syncthreads();   // before the next rows replace these
     }
-    __syncthreads();   // before the next segment's rows replace these
-    g = pe;
+    cs = nx;
   }
   if (!ok && lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
   // no copy may still be landing in shared memory when the block exits
@@ -1202,45 +1244,44 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   const uint32_t rest = blockIdx.x - b * per_b;
   const uint32_t h = rest / max_rb, rb = rest - h * max_rb;
   const ReqUnits r = req_units(p, b);
-  const uint32_t nrb = r.nseg / p.H;
-  if (rb >= nrb) return;
-  const uint32_t seg = h * nrb + rb;
+  if (rb >= r.nrb) return;
+  const uint32_t seg = h * r.nrb + rb;
   const int64_t rows = static_cast<int64_t>(r.n) * p.G;
   // partial sums: `count` of them, `step` floats apart; M and Z behind the rows
   const float* first = nullptr;
   int64_t step = 0;
-  uint32_t count = 0, part_rows = kRows, row0 = 0;
-  if (rows > p.few_rows) {
+  uint32_t count = 0, part_rows = p.seg_rows, row0 = 0;
+  const bool tiled = rows > p.few_rows;
+  if (tiled) {
     if (p.splits == 1) return;
     const uint32_t pairs = static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows);
-    const uint32_t pair = rb / (kItemRows / kRows);
+    const uint32_t at = rb * p.seg_rows, pair = at / kItemRows;
     const uint32_t item = __ldg(p.item_base + b) + (pairs - 1 - pair) * p.H + h;
     first = p.tile_partial + static_cast<int64_t>(item) * p.splits * kTilePartialFloats;
     step = kTilePartialFloats;
     count = p.splits;
     part_rows = kItemRows;
-    row0 = (rb % (kItemRows / kRows)) * kRows;
+    row0 = at - pair * kItemRows;
   } else if (r.nt) {
     const uint64_t U = __ldg(p.schedule + p.B);
     const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.nt, e = a + r.nt;
     const uint32_t C = used_blocks(U, grid);
     const uint32_t c0 = owner_of(a, U, C), c1 = owner_of(e - 1, U, C);
     if (c0 == c1) return;
-    // the first block's slot is its second if the segment begins inside its
-    // range (it always does, or begins exactly with it); the others' the first
+    // the segment begins inside the first block's range (its second slot) and
+    // before the others' (their first slot)
     first = p.partial + static_cast<int64_t>(2 * c0 + 1) * kPartialFloats;
     step = 2 * kPartialFloats;
     count = c1 - c0 + 1;
   }
   const int row = threadIdx.x >> 3, ch = threadIdx.x & 7;   // 16 columns of a row per thread
-  const RowAt at = row_at(p, r, seg, row);
+  if (row >= p.seg_rows) return;
+  const RowAt at = row_at(p, r, h, rb, row);
   if (!at.real) return;
   float m = kNegInf, z = 0.0f, v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  auto part_at = [&](uint32_t c) {   // blocks after the first begin inside the segment: first slot
-    return first + c * step - (part_rows == kRows && c ? kPartialFloats : 0);
-  };
+  auto part_at = [&](uint32_t c) { return first + c * step - (!tiled && c ? kPartialFloats : 0); };
   const int64_t m_at = static_cast<int64_t>(part_rows) * kHeadDim + row0 + row;
   for (uint32_t c = 0; c < count; ++c) m = fmaxf(m, part_at(c)[m_at]);
   for (uint32_t c = 0; c < count; ++c) {
@@ -1390,8 +1431,11 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   if (p.splits < 1) p.splits = 1;
   // one request has only one kernel to go to; of several, each is looked at on the device
   p.few_rows = !shape.tiles ? 0x7FFFFFFF : a.batch > 1 ? kFewRows : 0;
-  const int64_t max_rb = (a.max_q_len * p.G + kRows - 1) / kRows;
-  const int64_t join_rb = shape.tiles && p.splits == 1 && max_rb > kFewRows / kRows ? kFewRows / kRows : max_rb;
+  const int64_t most_rows = a.max_q_len * p.G;
+  p.seg_rows = most_rows <= 8 ? 8 : kMaxRows;
+  const int64_t max_rb = (most_rows + p.seg_rows - 1) / p.seg_rows;
+  const int64_t few_rb = kFewRows / p.seg_rows;
+  const int64_t join_rb = shape.tiles && p.splits == 1 && max_rb > few_rb ? few_rb : max_rb;
   const int64_t items = shape.items * p.splits, joins = a.batch * H * join_rb;
   if (items > 0x7FFFFFFF || joins > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
   auto maps = [&](uint32_t rows, CUtensorMap* tk, CUtensorMap* tv) {
@@ -1409,9 +1453,10 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   if (rows_kernel) {
     rc = maps(c.page_size < kUnit ? c.page_size : kUnit, &tk, &tv);
     if (rc != BFP8_OK) return rc;
-    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_attention_rows_kernel), kSmemBytes);
+    auto kernel = p.seg_rows == 8 ? kv_attention_rows_kernel<1> : kv_attention_rows_kernel<2>;
+    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes);
     if (rc != BFP8_OK) return rc;
-    rc = launch_dependent(kv_attention_rows_kernel, sms, kThreads, kSmemBytes, st, tk, tv, p);
+    rc = launch_dependent(kernel, sms, kThreads, kSmemBytes, st, tk, tv, p);
     if (rc != BFP8_OK) return rc;
   }
   if (shape.tiles) {
