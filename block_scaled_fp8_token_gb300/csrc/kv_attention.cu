@@ -65,19 +65,27 @@ struct AttnParams {
 // between them inside a segment.
 //
 // The products are transposed, tokens (and then columns of V) as the 16 rows of
-// an m16n8k16 product and query rows as its 8 columns: HBM bounds this kernel
-// only if the widening of the codes, two to an instruction, is all that is done
-// 128 bytes at a time, and a group of 8 heads fills such a product.
-constexpr int kWarps = 8;
+// a matrix instruction and query rows as its 8 columns: a group of 8 heads fills
+// one. S^T = K Q^T takes the codes as they are, an FP8 product with the query
+// row split exactly into E5M2 + E4M3 (see query_terms); O^T += V^T P^T widens
+// the codes to F16, two to an instruction, and rounds P to 11 bits.
+//
+// HBM bounds it. What kept it from that was copies in flight and warps to hide
+// latencies: several small blocks an SM instead of one large one, so that one's
+// merge and query loads overlap the others' products.
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 32;                 // tokens
 constexpr int kMaxRows = 16;              // query rows of a segment, at most
-constexpr int kStages = 2;
 constexpr int kStageBytes = 2 * kUnit * kHeadDim;            // keys, then values
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kMergeBytes = kWarps * 8 * kHeadDim * 4;
-constexpr int kSmemBytes = kRingBytes + kMergeBytes + 1024;  // + alignment
+constexpr int kMergeBytes = kWarps * 8 * (kHeadDim / 2) * 4;
+constexpr int kRowsPerSm = 2;             // blocks (three of two stages each: 130 us a pass, against 120)
+constexpr int kStages = 3;
+constexpr int kRowsSmem = kWarps * kStages * kStageBytes + kMergeBytes + 1024;   // + alignment
 constexpr int kPartialFloats = kMaxRows * (kHeadDim + 2);    // O, then M, then Z
+// Ending a segment costs a block about as long as this many units, which the
+// schedule counts behind each segment's own.
+constexpr uint32_t kPadUnits = 8;
 // P is kept at 2^4 times the weight and the maximum moves only when a score
 // passes it by 2^10, so F16 holds P up to 2^14 and, to full precision, down to
 // 2^-18 of the maximum.
@@ -87,6 +95,7 @@ constexpr float kLazy = 10.0f;
 struct ReqUnits {
   int32_t q0, n, kv, lo;   // first row, new tokens, length, first unit
   uint32_t nt, nseg, nrb;  // units of a segment, segments, segments of a head
+  BFP8_DEV uint32_t cost() const { return nt ? nt + kPadUnits : 0; }   // a segment's, in units
 };
 BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   ReqUnits r;
@@ -109,23 +118,25 @@ BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
 }
 BFP8_DEV uint64_t units_of(const AttnParams& p, int b) {
   const ReqUnits r = req_units(p, b);
-  return static_cast<uint64_t>(r.nt) * r.nseg;
+  return static_cast<uint64_t>(r.cost()) * r.nseg;
 }
 
-// A segment, and the part of it inside a block's range: units u0 .. of it, at
-// `at` units into the range.
+// A segment, and the part of it inside a block's range: `len` units from its
+// u0-th on, `at` units into the range; the ones that exist are below nt.
 struct SegPart {
   ReqUnits r;
   int b;
   uint32_t seg, h, u0, at, len;
+  BFP8_DEV uint32_t units() const { return u0 < r.nt ? min(len, r.nt - u0) : 0; }
 };
 BFP8_DEV void next_segment(const AttnParams& p, SegPart& s, uint32_t range) {
   s.at += s.len;
   s.u0 = 0;
   if (++s.seg >= s.r.nseg) {
     s.seg = 0;
-    do {   // some request behind this one has units: the range is not used up
+    do {
       if (++s.b >= p.B) {
+        s.at = range;
         s.len = 0;
         return;
       }
@@ -133,7 +144,7 @@ BFP8_DEV void next_segment(const AttnParams& p, SegPart& s, uint32_t range) {
     } while (s.r.nt == 0 || s.r.nseg == 0);
   }
   s.h = s.seg / s.r.nrb;
-  s.len = min(s.r.nt, range - s.at);
+  s.len = min(s.r.cost(), range - s.at);
 }
 
 // Blocks that share U units: every warp of each gets one at least.
@@ -154,6 +165,45 @@ BFP8_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+// E4M3 times E5M2, and E4M3 times E4M3.
+BFP8_DEV void mma_e4m3_e5m2(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e5m2.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+BFP8_DEV void mma_e4m3_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+BFP8_DEV uint32_t join16(uint16_t lo, uint16_t hi) {
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+// A query row as two FP8 terms, at a power of two that puts its largest entry
+// in [2^11, 2^12). An entry of 2^e .. 2^(e+1) is a multiple of 2^(e-7) (a BF16
+// has 8 significant bits); hi, E5M2, keeps 3 bits of it, so the rest is at most
+// 16 of those steps, which E4M3's 4 bits hold, and 2^8 at most. hi + lo is exact
+// for entries down to 2^-13 of the largest; below, it is within 2^-21 of it.
+BFP8_DEV int query_exponent(uint32_t amax_bits) {
+  return amax_bits ? min(max(11 - (static_cast<int>(amax_bits >> 7) - 127), -110), 110) : 0;
+}
+// Four entries (two BF16 pairs) times `up`: a word of codes of each term.
+BFP8_DEV void query_terms(uint32_t ab, uint32_t cd, float up, uint32_t& hi, uint32_t& lo) {
+  const float f[4] = {__uint_as_float(ab << 16) * up, __uint_as_float(ab & 0xFFFF0000u) * up,
+                      __uint_as_float(cd << 16) * up, __uint_as_float(cd & 0xFFFF0000u) * up};
+  const uint16_t h0 = f32x2_to_e5m2x2(f[0], f[1]), h1 = f32x2_to_e5m2x2(f[2], f[3]);
+  const uint32_t w0 = e5m2x2_to_f16x2(h0), w1 = e5m2x2_to_f16x2(h1);
+  const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
+  const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
+  hi = join16(h0, h1);
+  lo = join16(f32x2_to_e4m3x2(f[0] - g0.x, f[1] - g0.y), f32x2_to_e4m3x2(f[2] - g1.x, f[3] - g1.y));
 }
 BFP8_DEV uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -187,14 +237,6 @@ BFP8_DEV RowAt row_at(const AttnParams& p, const ReqUnits& r, uint32_t h, uint32
   return a;
 }
 
-// What a warp keeps of a unit between issuing its copies and using them. The
-// scale bytes are loaded when the copies are issued and first looked at when
-// those have landed, so their latency hides behind the copies'.
-struct Pending {
-  uint32_t k0, k1, v0, v1;   // scale bytes of the unit's two halves
-  uint32_t valid;            // one bit per token that exists
-};
-
 // out = O / Z and lse, from sums at maximum M; a row that saw nothing gives 0 and -inf.
 BFP8_DEV float row_factor(float Z) { return Z == 0.0f ? 0.0f : __frcp_rn(Z); }
 BFP8_DEV float row_lse(float M, float Z) {
@@ -215,24 +257,27 @@ BFP8_DEV void store_row16(__nv_bfloat16* dst, const float (&v)[16], float f) {
 
 // NB: query rows of a segment, in eights.
 template <int NB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, kRowsPerSm)
     kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tk,
                              const __grid_constant__ CUtensorMap tv, const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[kWarps * kStages];
+  __shared__ uint2 infos[kWarps][kStages];   // a unit's scale bytes (k, k, v, v of its halves) and valid tokens
   __shared__ float sm_m[kWarps][8 * NB], sm_z[kWarps][8 * NB];
+  // each warp's places in the sequence of segments: computing, and loading
+  __shared__ SegPart seg_at[kWarps][2], seg_next[kWarps];
   __shared__ uint64_t scan[kWarps];
   __shared__ uint64_t start_base;
   __shared__ int start_b;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + kRingBytes);
+  float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
+                                          kWarps * kStages * kStageBytes);
   if (tid < kWarps * kStages) mbar_init(smem_u32(&bars[tid]), 1);
   if (tid == 0) abort_flag = 0, start_b = 0, start_base = 0;
   mbar_fence_init();
   pdl_wait();
-  pdl_launch_dependents();
 
   // ---- this block's range of units
   uint64_t U = 0;
@@ -284,70 +329,109 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int c = lane & 3, g = lane >> 2;
   const int gtok = g ^ ((g & 1) << 2);           // see "Fragments" below
 
-  SegPart cs;   // the segment being computed; the one being loaded starts the same
-  cs.b = start_b;
-  cs.r = req_units(p, cs.b);
+  SegPart& cs = seg_at[warp][0];
+  SegPart& ps = seg_at[warp][1];
   {
+    SegPart x;
+    x.b = start_b;
+    x.r = req_units(p, x.b);
     const uint32_t rel = static_cast<uint32_t>(g0 - start_base);
-    cs.seg = rel / cs.r.nt;
-    cs.u0 = rel - cs.seg * cs.r.nt;
-    cs.h = cs.seg / cs.r.nrb;
-    cs.at = 0;
-    cs.len = min(cs.r.nt - cs.u0, range);
+    x.seg = rel / x.r.cost();
+    x.u0 = rel - x.seg * x.r.cost();
+    x.h = x.seg / x.r.nrb;
+    x.at = 0;
+    x.len = min(x.r.cost() - x.u0, range);
+    while (x.at < range && x.units() == 0) next_segment(p, x, range);
+    if (lane == 0) cs = ps = x;
+    __syncwarp();
   }
-  SegPart ps = cs;
 
-  // ---- issuing: this warp's next unit, px units into the range
-  uint32_t px = warp;
-  int32_t id0 = -1, id1 = -1;                    // its page numbers (two when pages hold 16)
+  // ---- issuing: this warp's next unit, the px-th of a segment's part; the
+  // warps take a part's units in turn, from the one that its place gives
+  uint32_t px = 0, p_units = 0;
+  int32_t p_t0 = 0, p_held = 0, p_h = 0;         // of the segment: first token of the part, tokens, head
+  const int32_t* p_row = nullptr;                // its request's row of the table
+  int32_t id0 = -1, id1 = -1;                    // the unit's page numbers (two when pages hold 16)
   int32_t pt0 = 0;                               // its first token
-  auto fetch_ids = [&] {
-    if (px >= range) return;
-    while (px >= ps.at + ps.len) next_segment(p, ps, range);
-    pt0 = (ps.r.lo + static_cast<int32_t>(ps.u0 + px - ps.at)) * kUnit;
-    const int32_t* row = p.table + ps.b * p.ld_table + (pt0 >> p.page_shift);
-    id0 = __ldg(row);   // inside the table: units stop at its width
-    if (two) {
-      const bool in = (pt0 >> p.page_shift) + 1 < p.max_blocks && pt0 + page < ps.r.kv;
-      id1 = in ? __ldg(row + 1) : -1;
-    }
+  bool more = true;
+  auto enter = [&](const SegPart& x) {
+    px = (warp - x.at) & (kWarps - 1);
+    p_units = x.units();
+    p_t0 = (x.r.lo + static_cast<int32_t>(x.u0)) * kUnit;
+    p_held = static_cast<int32_t>(min(static_cast<int64_t>(x.r.kv),
+                                      static_cast<int64_t>(p.max_blocks) << p.page_shift));
+    p_h = x.h;
+    p_row = p.table + x.b * p.ld_table;
   };
-  Pending pend0{}, pend1{};             // of stages 0 and 1
-  uint32_t armed = 0, phase_bits = 0;   // stages with copies in flight; their parities
-  auto issue = [&](Pending& pd, const int s) __attribute__((always_inline)) {
-    const bool ok0 = id0 >= 0 && id0 < p.n_pages, ok1 = id1 >= 0 && id1 < p.n_pages;
-    const int64_t left = min(static_cast<int64_t>(ps.r.kv),
-                             static_cast<int64_t>(p.max_blocks) << p.page_shift) - pt0;
-    uint32_t valid = left >= 32 ? 0xffffffffu : (1u << left) - 1u;   // left >= 1
-    valid &= two ? (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u) : (ok0 ? 0xffffffffu : 0u);
-    pd.valid = valid;
-    const int64_t e0 = id0 * p.exp_page + ps.h * p.exp_head;
-    pd.k0 = pd.k1 = pd.v0 = pd.v1 = 127u;
-    if (ok0) pd.k0 = __ldg(p.k_exp + e0), pd.v0 = __ldg(p.v_exp + e0);
-    if (two && ok1) {
-      const int64_t e1 = id1 * p.exp_page + ps.h * p.exp_head;
-      pd.k1 = __ldg(p.k_exp + e1), pd.v1 = __ldg(p.v_exp + e1);
+  auto fetch_ids = [&] {
+    if (px >= p_units) {
+      SegPart x = ps;
+      while (px >= p_units) {
+        next_segment(p, x, range);
+        if (x.at >= range) {
+          more = false;
+          return;
+        }
+        enter(x);
+      }
+      __syncwarp();
+      if (lane == 0) ps = x;
+      __syncwarp();
     }
+    pt0 = p_t0 + static_cast<int32_t>(px) * kUnit;
+    const int32_t* row = p_row + (pt0 >> p.page_shift);
+    id0 = __ldg(row);   // inside the table: units stop at its width
+    if (two) id1 = pt0 + page < p_held ? __ldg(row + 1) : -1;
+  };
+  uint32_t armed = 0, phase_bits = 0;   // stages with copies in flight; their parities
+  // Scale bytes of the unit issued last. They are stored for its use only when
+  // the next one is issued, so their latency hides behind a unit's products.
+  uint32_t k0 = 127, k1 = 127, v0 = 127, v1 = 127, valid_next = 0;
+  int pending = -1;
+  auto flush = [&] {
+    if (pending >= 0 && lane == 0)
+      infos[warp][pending] = make_uint2(k0 | (k1 << 8) | (v0 << 16) | (v1 << 24), valid_next);
+    pending = -1;
+  };
+  auto issue = [&](const int s) {
+    const bool ok0 = id0 >= 0 && id0 < p.n_pages, ok1 = two && id1 >= 0 && id1 < p.n_pages;
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * s, dst = stage0 + s * kStageBytes;
       const uint32_t bytes = box * kHeadDim;
-      mbar_arrive_expect_tx(bar, 2 * bytes * ((ok0 ? 1 : 0) + (two && ok1 ? 1 : 0)));
+      mbar_arrive_expect_tx(bar, 2 * bytes * ((ok0 ? 1 : 0) + (ok1 ? 1 : 0)));
       if (ok0) {
-        tma_load_4d(dst, &tk, 0, pt0 & (page - 1), ps.h, id0, bar);
-        tma_load_4d(dst + kUnit * kHeadDim, &tv, 0, pt0 & (page - 1), ps.h, id0, bar);
+        tma_load_4d(dst, &tk, 0, pt0 & (page - 1), p_h, id0, bar);
+        tma_load_4d(dst + kUnit * kHeadDim, &tv, 0, pt0 & (page - 1), p_h, id0, bar);
       }
-      if (two && ok1) {
-        tma_load_4d(dst + bytes, &tk, 0, 0, ps.h, id1, bar);
-        tma_load_4d(dst + kUnit * kHeadDim + bytes, &tv, 0, 0, ps.h, id1, bar);
+      if (ok1) {
+        tma_load_4d(dst + bytes, &tk, 0, 0, p_h, id1, bar);
+        tma_load_4d(dst + kUnit * kHeadDim + bytes, &tv, 0, 0, p_h, id1, bar);
       }
     }
+    const int32_t left = p_held - pt0;
+    valid_next = left >= 32 ? 0xffffffffu : (1u << left) - 1u;   // left >= 1
+    valid_next &= two ? (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u) : (ok0 ? 0xffffffffu : 0u);
+    k0 = k1 = v0 = v1 = 127u;
+    if (ok0) {
+      const int64_t e = id0 * p.exp_page + p_h * p.exp_head;
+      k0 = __ldg(p.k_exp + e), v0 = __ldg(p.v_exp + e);
+    }
+    if (ok1) {
+      const int64_t e = id1 * p.exp_page + p_h * p.exp_head;
+      k1 = __ldg(p.k_exp + e), v1 = __ldg(p.v_exp + e);
+    }
     armed |= 1u << s;
+    pending = s;
     px += kWarps;
     fetch_ids();
   };
+  enter(ps);
   fetch_ids();
-  if (px < range) issue(pend0, 0);
-  if (px < range) issue(pend1, 1);
+  for (int s = 0; s < kStages && more; ++s) {
+    flush();
+    issue(s);
+  }
+  if (!more) flush();   // nothing may be issued any more that would do it
 
   // ---- query rows: lane (g, c) loads 16-byte chunks c and c + 4 of rows 8 nb + g
   uint4 raw[NB][4];
@@ -364,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   };
-  load_q(cs);
+  if (cs.at < range) load_q(cs);
 
   int stage = 0;
   bool ok = true;
@@ -374,10 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         min(static_cast<int64_t>(8 * NB),
             static_cast<int64_t>(cs.r.n) * p.G - static_cast<int64_t>(rb) * (8 * NB)));
 
-    // Query rows as F16 at a power of two that puts the row's largest entry in
-    // [2^8, 2^9): a BF16 has 8 significant bits and F16 11, so entries down to
-    // 2^-22 of the largest are exact.
-    uint32_t qb[NB][8][2];
+    uint32_t qh[NB][8], ql[NB][8];   // the two terms' codes: four columns a word
     float fac[NB][2];              // of rows 2c and 2c + 1: what a score is in log2 units
     int lim[NB][2], win[NB][2];    // they see [win, lim)
 #pragma unroll
@@ -391,15 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int e = m ? min(max(8 - (static_cast<int>(m >> 7) - 127), -110), 110) : 0;
+      const int e = query_exponent(m);
       const float up = exp2_int(e), f = exp2_int(-e) * p.scale_log2;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x)   // step s holds columns 4 (s & 3) .. + 3 of chunk c + 4 (s / 4)
-          qb[nb][4 * (j >> 1) + 2 * (j & 1) + (x >> 1)][x & 1] =
-              pack_f16x2(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xFFFF0000u) * up);
+      for (int j = 0; j < 4; ++j) {   // eight columns: words 2j, 2j + 1
+        query_terms(raw[nb][j].x, raw[nb][j].y, up, qh[nb][2 * j], ql[nb][2 * j]);
+        query_terms(raw[nb][j].z, raw[nb][j].w, up, qh[nb][2 * j + 1], ql[nb][2 * j + 1]);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -428,19 +506,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       Z[nb][0] = Z[nb][1] = 0.0f;
     }
 
-    // One unit, from stage ST. False when the wait for it ran out.
-    auto unit = [&](const uint32_t u, Pending& pd, const int ST) __attribute__((always_inline)) {
-      const uint32_t bar = bar0 + 8 * ST;
-      const uint32_t kb = stage0 + ST * kStageBytes, vb = kb + kUnit * kHeadDim;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar, (phase_bits >> ST) & 1u, &abort_flag))) return false;
-      armed &= ~(1u << ST);
-      phase_bits ^= 1u << ST;
-      const int ek[2] = {static_cast<int>(pd.k0) - 127, static_cast<int>(two ? pd.k1 : pd.k0) - 127};
-      const int ev[2] = {static_cast<int>(pd.v0) - 127, static_cast<int>(two ? pd.v1 : pd.v0) - 127};
-      const uint32_t valid = pd.valid;
-      const int t0 = (cs.r.lo + static_cast<int32_t>(u)) * kUnit;
+    const uint32_t units = cs.units();
+    const int t_part = (cs.r.lo + static_cast<int32_t>(cs.u0)) * kUnit;
+    for (uint32_t x = (warp - cs.at) & (kWarps - 1); ok && x < units; x += kWarps) {
+      const uint32_t bar = bar0 + 8 * stage;
+      const uint32_t kb = stage0 + stage * kStageBytes, vb = kb + kUnit * kHeadDim;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, (phase_bits >> stage) & 1u, &abort_flag));
+      if (!ok) break;
+      __syncwarp();
+      armed &= ~(1u << stage);
+      phase_bits ^= 1u << stage;
+      const uint2 info = infos[warp][stage];
+      const int kx = static_cast<int>(info.x & 0xffu), vx = static_cast<int>((info.x >> 16) & 0xffu);
+      const int ek[2] = {kx - 127, (two ? static_cast<int>((info.x >> 8) & 0xffu) : kx) - 127};
+      const int ev[2] = {vx - 127, (two ? static_cast<int>(info.x >> 24) : vx) - 127};
+      const uint32_t valid = info.y;
+      const int t0 = t_part + static_cast<int>(x) * kUnit;
 
-      // Fragments. S^T: 16 tokens x 16 columns of K a step, and which column is
+      // Fragments. S^T: 16 tokens x 32 columns of K a step, and which column is
       // which does not matter as long as q agrees, so a lane reads its tokens'
       // 16-byte chunks c and c + 4 whole. O^T: a lane reads 16 columns (chunk g)
       // of four tokens, and holds 16 columns in a row of O for rows 2c, 2c + 1.
@@ -456,13 +539,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t w1[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         const uint32_t w2[8] = {d.x, d.y, d.z, d.w, e.x, e.y, e.z, e.w};
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb][mb][0] = s[nb][mb][1] = s[nb][mb][2] = s[nb][mb][3] = 0.0f;
+        for (int nb = 0; nb < NB; ++nb) {
+          s[nb][mb][0] = s[nb][mb][1] = s[nb][mb][2] = s[nb][mb][3] = 0.0f;
 #pragma unroll
-        for (int st = 0; st < 8; ++st) {
-          const uint32_t a0 = f16_pair(w1[st], 0), a1 = f16_pair(w2[st], 0);
-          const uint32_t a2 = f16_pair(w1[st], 1), a3 = f16_pair(w2[st], 1);
+          for (int st = 0; st < 4; ++st)
+            mma_e4m3_e5m2(s[nb][mb], w1[2 * st], w2[2 * st], w1[2 * st + 1], w2[2 * st + 1],
+                          qh[nb][2 * st], qh[nb][2 * st + 1]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(s[nb][mb], a0, a1, a2, a3, qb[nb][st]);
+          for (int st = 0; st < 4; ++st)
+            mma_e4m3_e4m3(s[nb][mb], w1[2 * st], w2[2 * st], w1[2 * st + 1], w2[2 * st + 1],
+                          ql[nb][2 * st], ql[nb][2 * st + 1]);
         }
       }
       // s[nb][mb]: tokens 16 mb + gtok (entries 0, 1) and 8 on (2, 3), rows 2c
@@ -568,90 +654,99 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      flush();
       __syncwarp();   // every lane has read the stage
-      if (px < range) issue(pd, ST);
-      return true;
-    };
-    for (uint32_t x = cs.at + ((warp - cs.at) & (kWarps - 1)); ok && x < cs.at + cs.len; x += kWarps) {
-      const uint32_t u = cs.u0 + x - cs.at;
-      ok = stage ? unit(u, pend1, 1) : unit(u, pend0, 0);
-      stage ^= 1;
+      if (more) issue(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     if (!ok) abort_flag = 1;
 
     // the next segment's query rows are on their way while this one is finished
     SegPart nx = cs;
-    next_segment(p, nx, range);
+    do next_segment(p, nx, range);
+    while (nx.at < range && nx.units() == 0);
     if (nx.at < range) load_q(nx);
+    __syncwarp();
+    if (lane == 0) seg_next[warp] = nx;
 
-    // ---- the block's warps together, eight rows at a time
-    const bool whole = cs.u0 == 0 && cs.len == cs.r.nt;
+    // ---- the block's warps together, eight rows and 64 columns at a time
+    const bool whole = cs.u0 == 0 && units == cs.r.nt;
     float* part = p.partial +
                   static_cast<int64_t>(2 * blockIdx.x + (cs.u0 == 0 ? 1 : 0)) * kPartialFloats;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float z = Z[nb][j], m = M[nb][j];
+        float z = Z[nb][j];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-        if (z != z && m == kNegInf) m = 0.0f;   // nothing but NaN scores: the row is NaN
+        if (z != z && M[nb][j] == kNegInf) M[nb][j] = 0.0f;   // nothing but NaN scores: the row is NaN
         if (g == 0) {
-          sm_m[warp][8 * nb + 2 * c + j] = m;
+          sm_m[warp][8 * nb + 2 * c + j] = M[nb][j];
           sm_z[warp][8 * nb + 2 * c + j] = z;
         }
-        // a lane's 16 columns as 16-byte chunks 4g .. 4g + 3, chunk k of row r
-        // kept at k ^ (r / 2): free of bank conflicts
-        const int row = 2 * c + j;
-        if (8 * nb + row < rows_left && m != kNegInf) {
-          float* dst = merge + (warp * 8 + row) * kHeadDim;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<float4*>(dst + 4 * ((4 * g + k) ^ c)) =
-                make_float4(o[nb][2 * k][j], o[nb][2 * k][2 + j], o[nb][2 * k + 1][j],
-                            o[nb][2 * k + 1][2 + j]);
-        }
       }
-      __syncthreads();
-      for (int it = tid; it < 8 * 32; it += kThreads) {   // a row's 16-byte chunk each
-        const int row = it >> 5, ch = it & 31, srow = 8 * nb + row;
-        if (srow >= rows_left) continue;
-        float m = kNegInf;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w][srow]);
-        float z = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int half = 0; half < 2; ++half) {
+        // a lane's 16 columns as 16-byte chunks 4 (g & 3) .. of its half, chunk k
+        // of row r kept at k ^ (r / 2): free of bank conflicts
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = sm_m[w][srow];
-          if (mw == kNegInf) continue;
-          const float f = ex2_approx(mw - m);
-          z = fmaf(sm_z[w][srow], f, z);
-          const float4 y = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * kHeadDim +
-                                                            4 * (ch ^ (row >> 1)));
-          v.x = fmaf(y.x, f, v.x);
-          v.y = fmaf(y.y, f, v.y);
-          v.z = fmaf(y.z, f, v.z);
-          v.w = fmaf(y.w, f, v.w);
-        }
-        if (whole) {
-          const RowAt r = row_at(p, cs.r, cs.h, rb, srow);
-          const float f = row_factor(z);
-          *reinterpret_cast<uint2*>(p.out + r.token * p.o_ldt + r.head * p.o_ldh + 4 * ch) =
-              make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
-          if (p.lse && ch == 0) p.lse[r.token * p.l_ldt + r.head] = row_lse(m, z);
-        } else {
-          *reinterpret_cast<float4*>(part + srow * kHeadDim + 4 * ch) = v;
-          if (ch == 0) {
-            part[8 * NB * kHeadDim + srow] = m;
-            part[8 * NB * (kHeadDim + 1) + srow] = z;
+        for (int j = 0; j < 2; ++j) {
+          const int row = 2 * c + j;
+          if ((g >> 2) == half && 8 * nb + row < rows_left && M[nb][j] != kNegInf) {
+            float* dst = merge + (warp * 8 + row) * (kHeadDim / 2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<float4*>(dst + 4 * ((4 * (g & 3) + k) ^ c)) =
+                  make_float4(o[nb][2 * k][j], o[nb][2 * k][2 + j], o[nb][2 * k + 1][j],
+                              o[nb][2 * k + 1][2 + j]);
           }
         }
+        __syncthreads();
+        const int row = tid >> 4, k = tid & 15, srow = 8 * nb + row;   // a 16-byte chunk per thread
+        if (srow < rows_left) {
+          const int col = 64 * half + 4 * k;
+          float m = kNegInf;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w][srow]);
+          float z = 0.0f;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float mw = sm_m[w][srow];
+            if (mw == kNegInf) continue;
+            const float f = ex2_approx(mw - m);
+            z = fmaf(sm_z[w][srow], f, z);
+            const float4 y = *reinterpret_cast<const float4*>(
+                merge + (w * 8 + row) * (kHeadDim / 2) + 4 * (k ^ (row >> 1)));
+            v.x = fmaf(y.x, f, v.x);
+            v.y = fmaf(y.y, f, v.y);
+            v.z = fmaf(y.z, f, v.z);
+            v.w = fmaf(y.w, f, v.w);
+          }
+          if (whole) {
+            const RowAt r = row_at(p, cs.r, cs.h, rb, srow);
+            const float f = row_factor(z);
+            *reinterpret_cast<uint2*>(p.out + r.token * p.o_ldt + r.head * p.o_ldh + col) =
+                make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+            if (p.lse && col == 0) p.lse[r.token * p.l_ldt + r.head] = row_lse(m, z);
+          } else {
+            *reinterpret_cast<float4*>(part + srow * kHeadDim + col) = v;
+            if (col == 0) {
+              part[8 * NB * kHeadDim + srow] = m;
+              part[8 * NB * (kHeadDim + 1) + srow] = z;
+            }
+          }
+        }
+        __syncthreads();   // before the next rows replace these
       }
-      __syncthreads();   // before the next rows replace these
     }
-    cs = nx;
+    if (lane == 0) cs = seg_next[warp];
+    __syncwarp();
   }
+  // Not earlier: blocks of the kernels behind that wait on an SM hold registers
+  // and shared memory that this launch's or the next's need (130 -> 180 us a pass).
+  pdl_launch_dependents();
   if (!ok && lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
   // no copy may still be landing in shared memory when the block exits
   for (int s = 0; s < kStages; ++s)
@@ -734,10 +829,6 @@ BFP8_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-BFP8_DEV uint32_t join16(uint16_t lo, uint16_t hi) {
-  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
-
 struct TileShared {
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
   uint64_t w_full[2], w_empty[2];      // the widened values' buffers
@@ -792,7 +883,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  pdl_launch_dependents();
 
   // ---- which item: block index = item * splits + part, items request by request
   {
@@ -1026,11 +1116,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int pos = x.kv - x.n + static_cast<int>(tok);
     bool ok = true;
 
-    // The row's queries as two terms at a power of two that puts the largest
-    // entry in [2^11, 2^12). An entry of 2^e .. 2^(e+1) is a multiple of 2^(e-7);
-    // hi keeps 3 bits of it, so the rest is at most 16 of those steps, which
-    // E4M3's 4 bits hold, and 2^8 at most. Exact for entries down to 2^-13 of the
-    // largest; below, within 2^-21 of it.
     float fac = 0.0f;
     if (nt > 0) {
       uint4 raw[16];
@@ -1045,7 +1130,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max(m, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
       }
-      const int e = m ? min(max(11 - (static_cast<int>(m >> 7) - 127), -110), 110) : 0;
+      const int e = query_exponent(m);
       // a negative scale turns the queries round, so that the factor is positive
       const float up = p.scale_log2 < 0.0f ? -exp2_int(e) : exp2_int(e);
       fac = exp2_int(-e) * fabsf(p.scale_log2);
@@ -1055,16 +1140,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const uint4 q4 = raw[2 * c + (d >> 1)];
-          const uint32_t a = d & 1 ? q4.z : q4.x, b = d & 1 ? q4.w : q4.y;
-          const float f[4] = {__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up,
-                              __uint_as_float(b << 16) * up, __uint_as_float(b & 0xFFFF0000u) * up};
-          const uint16_t h0 = f32x2_to_e5m2x2(f[0], f[1]), h1 = f32x2_to_e5m2x2(f[2], f[3]);
-          const uint32_t b0 = e5m2x2_to_f16x2(h0), b1 = e5m2x2_to_f16x2(h1);
-          const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
-          const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
-          hi[d] = join16(h0, h1);
-          lo[d] = join16(f32x2_to_e4m3x2(f[0] - g0.x, f[1] - g0.y),
-                         f32x2_to_e4m3x2(f[2] - g1.x, f[3] - g1.y));
+          query_terms(d & 1 ? q4.z : q4.x, d & 1 ? q4.w : q4.y, up, hi[d], lo[d]);
         }
         const uint32_t at = sQ + 2 * w * kQBytes + r * kHeadDim + ((c ^ (r & 7)) << 4);
         sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
@@ -1237,7 +1313,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // per segment; a segment that one block finished is done.
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams p, uint32_t grid,
                                                                 uint32_t max_rb) {
-  pdl_launch_dependents();
   pdl_wait();
   const uint32_t per_b = max_rb * p.H;
   const int b = blockIdx.x / per_b;
@@ -1264,7 +1339,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
     row0 = at - pair * kItemRows;
   } else if (r.nt) {
     const uint64_t U = __ldg(p.schedule + p.B);
-    const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.nt, e = a + r.nt;
+    const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.cost(), e = a + r.nt;
     const uint32_t C = used_blocks(U, grid);
     const uint32_t c0 = owner_of(a, U, C), c1 = owner_of(e - 1, U, C);
     if (c0 == c1) return;
@@ -1350,7 +1425,7 @@ Workspace workspace_of(int64_t B, const Shape& s, int sms) {
   Workspace w{};
   w.item_base = align256((B + 1) * 8);
   w.partial = w.item_base + align256(B * 4);
-  w.tile_partial = w.partial + align256(static_cast<size_t>(sms) * 2 * kPartialFloats * 4);
+  w.tile_partial = w.partial + align256(static_cast<size_t>(sms) * kRowsPerSm * 2 * kPartialFloats * 4);
   w.bytes = w.tile_partial;
   if (s.splits > 1) w.bytes += static_cast<size_t>(s.items) * s.splits * kTilePartialFloats * 4;
   return w;
@@ -1450,13 +1525,14 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tk, tv;
   const bool rows_kernel = p.few_rows > 0;
+  const unsigned rows_grid = static_cast<unsigned>(sms) * kRowsPerSm;
   if (rows_kernel) {
     rc = maps(c.page_size < kUnit ? c.page_size : kUnit, &tk, &tv);
     if (rc != BFP8_OK) return rc;
     auto kernel = p.seg_rows == 8 ? kv_attention_rows_kernel<1> : kv_attention_rows_kernel<2>;
-    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes);
+    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kRowsSmem);
     if (rc != BFP8_OK) return rc;
-    rc = launch_dependent(kernel, sms, kThreads, kSmemBytes, st, tk, tv, p);
+    rc = launch_dependent(kernel, rows_grid, kThreads, kRowsSmem, st, tk, tv, p);
     if (rc != BFP8_OK) return rc;
   }
   if (shape.tiles) {
@@ -1478,7 +1554,7 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   }
   if (rows_kernel || p.splits > 1) {
     rc = launch_dependent(kv_attention_join_kernel, static_cast<unsigned>(joins), 128, 0, st, p,
-                          static_cast<uint32_t>(sms), static_cast<uint32_t>(join_rb));
+                          rows_grid, static_cast<uint32_t>(join_rb));
     if (rc != BFP8_OK) return rc;
   }
   return check_launch();
