@@ -766,21 +766,23 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 //   warps 2, 3   widen the values' codes to F16, MN-major, in two buffers
 //   warps 4..7   softmax of tile 0, one thread a row; warps 8..11 of tile 1
 // While one tile's softmax runs, the tensor cores work on the other's. S is
-// FP32 in tensor memory; P replaces it there and is the PV product's A
-// operand, so weights never touch shared memory. O stays in tensor memory and
-// is scaled down only when a row's maximum has outgrown the kept one by 2^10.
+// FP32 in tensor memory; P replaces it there, 64 tokens at a time, and is the PV
+// product's A operand, so weights never touch shared memory. O stays in tensor
+// memory and is scaled down only when a row's maximum has outgrown the kept one
+// by 2^10.
 constexpr int kTileRows = 128, kTileTokens = 128;
 constexpr int kItemRows = 2 * kTileRows;
+constexpr int kHalf = kTileTokens / 2;
 constexpr int kTileThreads = 384;
-constexpr int kTileStages = 3;
+constexpr int kTileStages = 3;                           // of keys
+constexpr int kValueStages = 2;                          // freed as soon as they are widened
 constexpr int kInfos = kTileStages + 1;                  // see TileShared
 constexpr int kQBytes = kTileRows * kHeadDim;            // one term of one query tile
 constexpr int kKvBytes = kTileTokens * kHeadDim;
 constexpr int kV16Bytes = 2 * kKvBytes;
-constexpr int kTileSmem = 4 * kQBytes + kTileStages * 2 * kKvBytes + 2 * kV16Bytes + 1024;
+constexpr int kTileSmem =
+    4 * kQBytes + (kTileStages + kValueStages) * kKvBytes + 2 * kV16Bytes + 1024;
 constexpr int kTilePartialFloats = kItemRows * kHeadDim + 2 * kItemRows;
-constexpr int kTileLaunchRegs = 168, kTileCtrlRegs = 72, kTileSoftRegs = 216;
-static_assert(kTileCtrlRegs + 2 * kTileSoftRegs == 3 * kTileLaunchRegs, "register split");
 constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w, O at 256 + 128 w
 
 struct TileItem {
@@ -823,17 +825,48 @@ BFP8_DEV uint32_t tile_items_of(const AttnParams& p, int b) {
   return static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows) * p.H;
 }
 
+// Row `row` of an item (none of a block that has no item).
+BFP8_DEV RowAt tile_row(const AttnParams& p, const TileItem& x, bool some, int row) {
+  RowAt a;
+  const uint32_t i = x.row0 + row;
+  const uint32_t tok = some ? i / p.G : 0;
+  a.real = some && tok < static_cast<uint32_t>(x.n);
+  a.token = x.q0 + static_cast<int64_t>(a.real ? tok : 0);
+  a.head = x.h * p.G + (some ? i - tok * p.G : 0);
+  a.pos = x.kv - x.n + static_cast<int>(tok);
+  return a;
+}
+
 // Three-way maximum, one instruction.
 BFP8_DEV float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// 2^x, without the ordering that act_math.cuh's asks for.
+BFP8_DEV float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// n FP32 columns of this lane's row of tensor memory times f. Rare, so kept
+// small rather than fast.
+BFP8_DEV void scale_columns(uint32_t taddr, int n, float f) {
+#pragma unroll 1
+  for (int i = 0; i < n; i += 16) {
+    uint32_t r[16];
+    tmem_ld16(taddr + i, r);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * f);
+    tmem_st16(taddr + i, r);
+  }
+}
+
 struct TileShared {
-  uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
+  uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kValueStages], v_empty[kValueStages];
   uint64_t w_full[2], w_empty[2];      // the widened values' buffers
   uint64_t info_full[kInfos];
-  uint64_t q_full, s_full[2], p_full[2], o_done[2], drained;
+  uint64_t q_full, s_full[2], p_full[2][2], o_done[2], drained;   // p_full: of a tile's halves
   // What softmax needs of a tile. One slot more than there are stages: tile m's
   // keys are loaded once S of tile m - 3 is complete for both query tiles, which
   // follows their P of tile m - 4.
@@ -841,8 +874,7 @@ struct TileShared {
   uint16_t valid[kInfos][8];           // per 16 tokens: a bit for each that exists
   uint32_t tmem;
   uint32_t scan[kTileThreads / 32];
-  uint32_t found_it;
-  int found_b;
+  TileItem item;                       // this block's; b < 0: none
   int abort_flag;
 };
 
@@ -856,11 +888,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t sQ = base;                         // [tile][hi, lo]
   const uint32_t sK = base + 4 * kQBytes;
   const uint32_t sV = sK + kTileStages * kKvBytes;
-  const uint32_t sW = sV + kTileStages * kKvBytes;  // [buffer][64 columns][token]
+  const uint32_t sW = sV + kValueStages * kKvBytes;  // [buffer][64 columns][token]
   if (tid == 0) {
     for (int s = 0; s < kTileStages; ++s) {
       mbar_init(smem_u32(&sh.k_full[s]), 1);
       mbar_init(smem_u32(&sh.k_empty[s]), 1);
+    }
+    for (int s = 0; s < kValueStages; ++s) {
       mbar_init(smem_u32(&sh.v_full[s]), 1);
       mbar_init(smem_u32(&sh.v_empty[s]), 2);
     }
@@ -871,11 +905,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(smem_u32(&sh.w_full[w]), 2);
       mbar_init(smem_u32(&sh.w_empty[w]), 1);
       mbar_init(smem_u32(&sh.s_full[w]), 1);
-      mbar_init(smem_u32(&sh.p_full[w]), 4);
+      for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&sh.p_full[w][b]), 4);
       mbar_init(smem_u32(&sh.o_done[w]), 1);
     }
     sh.abort_flag = 0;
-    sh.found_b = -1;
+    sh.item = TileItem{};
+    sh.item.b = -1;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -906,7 +941,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         total += sh.scan[w];
       }
       const uint32_t at = run + off + inc - mine;
-      if (mine && item >= at && item < at + mine) sh.found_b = b0 + tid, sh.found_it = item - at;
+      if (mine && item >= at && item < at + mine)
+        sh.item = tile_item(p, b0 + tid, item - at, blockIdx.x % p.splits);
       if (blockIdx.x == 0 && b0 + tid < p.B) p.item_base[b0 + tid] = at;
       run += total;
     }
@@ -915,21 +951,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int part = blockIdx.x % p.splits;
   const volatile int* abort_flag = &sh.abort_flag;
-  const bool some = sh.found_b >= 0;
-  TileItem x{};
-  if (some) x = tile_item(p, sh.found_b, sh.found_it, part);
+  const TileItem& x = sh.item;
+  const bool some = x.b >= 0;
   const int nt = x.hi - x.lo;
 
   if (warp < 4) {
-    warpgroup_reg_dealloc<kTileCtrlRegs>();
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer
       const int page = 1 << p.page_shift;
       const uint32_t box_bytes = page * kHeadDim;
       bool ok = true;
-      uint32_t armed = 0, phases = 0;   // stages loaded, and the parity of each one's last load
+      int loaded = 0;   // tiles
       const int32_t* row = p.table + x.b * p.ld_table;
       auto page_id = [&](int j) {   // lane l < 8: the page of tokens 16 l .. of tile j
         const int t = (x.lo + j) * kTileTokens + 16 * lane;
@@ -939,10 +972,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int j = 0; j < nt; ++j) {
         const int s = j % kTileStages;
         const uint32_t ph = (j / kTileStages) & 1;
-        const uint32_t kf = smem_u32(&sh.k_full[s]), vf = smem_u32(&sh.v_full[s]);
+        const int vs = j % kValueStages;
+        const uint32_t vph = (j / kValueStages) & 1;
+        const uint32_t kf = smem_u32(&sh.k_full[s]), vf = smem_u32(&sh.v_full[vs]);
         if (!__all_sync(0xffffffffu,
                         mbar_wait_sleep(smem_u32(&sh.k_empty[s]), ph ^ 1u, abort_flag) &&
-                            mbar_wait_sleep(smem_u32(&sh.v_empty[s]), ph ^ 1u, abort_flag))) {
+                            mbar_wait_sleep(smem_u32(&sh.v_empty[vs]), vph ^ 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -956,9 +991,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
         if (leads) {
-          const uint32_t at = s * kKvBytes + 16 * lane * kHeadDim;
-          tma_load_4d(sK + at, &tk, 0, 0, x.h, id, kf);
-          tma_load_4d(sV + at, &tv, 0, 0, x.h, id, vf);
+          const uint32_t at = 16 * lane * kHeadDim;
+          tma_load_4d(sK + s * kKvBytes + at, &tk, 0, 0, x.h, id, kf);
+          tma_load_4d(sV + vs * kKvBytes + at, &tv, 0, 0, x.h, id, vf);
         }
         int ek = 127, ev = 127;
         if (there) {
@@ -979,16 +1014,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_arrive(vf);
           mbar_arrive(smem_u32(&sh.info_full[j % kInfos]));
         }
-        armed |= 1u << s;
-        phases = (phases & ~(1u << s)) | (ph << s);
+        ++loaded;
       }
       if (!ok) sh.abort_flag = 1;
       // every stage's last load has landed before the block may end
-      for (int s = 0; s < kTileStages; ++s)
-        if ((armed >> s) & 1u) {
-          drain(smem_u32(&sh.k_full[s]), (phases >> s) & 1u);
-          drain(smem_u32(&sh.v_full[s]), (phases >> s) & 1u);
-        }
+      for (int j = max(loaded - kTileStages, 0); j < loaded; ++j)
+        drain(smem_u32(&sh.k_full[j % kTileStages]), (j / kTileStages) & 1);
+      for (int j = max(loaded - kValueStages, 0); j < loaded; ++j)
+        drain(smem_u32(&sh.v_full[j % kValueStages]), (j / kValueStages) & 1);
       if (!ok && lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -1015,15 +1048,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
       };
-      auto pv = [&](int j, int w) {
+      auto pv = [&](int j, int w, int b) {   // half b of the tile's tokens
         if (elect_one()) {
-          const uint64_t db = smem_desc_sw128_mn(sW + (j & 1) * kV16Bytes, kKvBytes);
+          const uint64_t db = smem_desc_sw128_mn(sW + (j & 1) * kV16Bytes + b * kHalf * 128, kKvBytes);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)   // 16 tokens a step: 16 rows of 128 bytes
-            umma_f16_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 8 * k, db + 128 * k, kPv,
-                        j > 0 || k);
+          for (int k = 0; k < 4; ++k)   // 16 tokens a step: 16 rows of 128 bytes
+            umma_f16_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + kHalf * b + 8 * k,
+                        db + 128 * k, kPv, j > 0 || b || k);
           umma_commit(smem_u32(&sh.o_done[w]));
-          if (w == 1) umma_commit(smem_u32(&sh.w_empty[j & 1]));
+          if (w == 1 && b == 1) umma_commit(smem_u32(&sh.w_empty[j & 1]));
         }
         __syncwarp();
       };
@@ -1037,10 +1070,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int j = 0; ok && j < nt; ++j) {
         wait(sh.w_full[j & 1], (j >> 1) & 1);
         for (int w = 0; w < 2; ++w) {
-          wait(sh.p_full[w], j & 1);
+          for (int b = 0; b < 2; ++b) {
+            wait(sh.p_full[w][b], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            pv(j, w, b);
+          }
           if (!ok) break;
-          tc_fence_after();
-          pv(j, w);
           if (j + 1 == nt) continue;
           if (w == 0) wait(sh.k_full[(j + 1) % kTileStages], ((j + 1) / kTileStages) & 1);
           if (!ok) break;
@@ -1064,31 +1100,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int c = lane & 7, r0 = 4 * (warp - 2) + (lane >> 3);
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
-        const int s = j % kTileStages;
+        const int s = j % kValueStages;
         if (!__all_sync(0xffffffffu,
                         mbar_wait_sleep(smem_u32(&sh.w_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag) &&
-                            mbar_wait_sleep(smem_u32(&sh.v_full[s]), (j / kTileStages) & 1, abort_flag))) {
+                            mbar_wait_sleep(smem_u32(&sh.v_full[s]), (j / kValueStages) & 1, abort_flag))) {
           ok = false;
           break;
         }
-        const uint32_t src = sV + s * kKvBytes;
-        const uint32_t dst = sW + (j & 1) * kV16Bytes + (c >> 2) * kKvBytes;
+        const uint32_t src = sV + s * kKvBytes + r0 * kHeadDim;
+        const uint32_t dst = sW + (j & 1) * kV16Bytes + (c >> 2) * kKvBytes + r0 * 128;
         const uint16_t* valid = sh.valid[j % kInfos];
+        const uint4 vw = *reinterpret_cast<const uint4*>(valid);
+        const bool full = (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
+        // the two halves' lanes store their two chunks in opposite order, which
+        // keeps the stores free of bank conflicts; rows 8 apart swizzle alike
+        const int first = c >> 2, x = r0 & 7;
+        const uint32_t at = src + ((c ^ x) << 4);
+        const uint32_t to0 = dst + (((2 * (c & 3) + first) ^ x) << 4);
+        const uint32_t to1 = dst + (((2 * (c & 3) + 1 - first) ^ x) << 4);
 #pragma unroll 4
         for (int i = 0; i < kTileTokens; i += 8) {
-          const int r = i + r0;
-          const bool there = (valid[r >> 4] >> (r & 15)) & 1u;
-          const uint4 v = lds128(src + r * kHeadDim + ((c ^ (r & 7)) << 4));
-          uint4 o[2];
-          o[0] = make_uint4(f16_pair(v.x, 0), f16_pair(v.x, 1), f16_pair(v.y, 0), f16_pair(v.y, 1));
-          o[1] = make_uint4(f16_pair(v.z, 0), f16_pair(v.z, 1), f16_pair(v.w, 0), f16_pair(v.w, 1));
-          if (!there) o[0] = o[1] = make_uint4(0u, 0u, 0u, 0u);
-          // the two halves' lanes store their two chunks in opposite order: no bank conflicts
-          const int first = c >> 2;
-          const uint32_t row = dst + r * 128;
-          const int k0 = 2 * (c & 3) + first, k1 = k0 ^ 1;
-          sts128(row + ((k0 ^ (r & 7)) << 4), first ? o[1] : o[0]);
-          sts128(row + ((k1 ^ (r & 7)) << 4), first ? o[0] : o[1]);
+          uint4 v = lds128(at + i * kHeadDim);
+          if (!full && !((valid[(i + r0) >> 4] >> ((i + r0) & 15)) & 1u)) v = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 lo = make_uint4(f16_pair(v.x, 0), f16_pair(v.x, 1), f16_pair(v.y, 0), f16_pair(v.y, 1));
+          const uint4 hi = make_uint4(f16_pair(v.z, 0), f16_pair(v.z, 1), f16_pair(v.w, 0), f16_pair(v.w, 1));
+          sts128(to0 + i * 128, first ? hi : lo);
+          sts128(to1 + i * 128, first ? lo : hi);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1104,198 +1141,200 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else {
     // ------------------------------------------------- softmax, one thread a row
-    warpgroup_reg_alloc<kTileSoftRegs>();
     const int w = (warp >> 2) - 1;                 // query tile
     const int r = tid & 127;                       // row of the tile = TMEM lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 (warp mod 4)
-    const uint32_t i = x.row0 + w * kTileRows + r;
-    const uint32_t tok = some ? i / p.G : 0;
-    const bool real = some && tok < static_cast<uint32_t>(x.n);
-    const int64_t token = x.q0 + static_cast<int64_t>(real ? tok : 0);
-    const int head = x.h * p.G + (some ? i - tok * p.G : 0);
-    const int pos = x.kv - x.n + static_cast<int>(tok);
     bool ok = true;
-
     float fac = 0.0f;
+    RowAt at = tile_row(p, x, some, w * kTileRows + r);
     if (nt > 0) {
-      uint4 raw[16];
-      const __nv_bfloat16* src = p.q + token * p.q_ldt + head * p.q_ldh;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        raw[c] = real ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t m = 0;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+      // The queries as two FP8 terms: a half-warp takes a row, 16 bytes a lane
+      // (one thread a row would touch 32 rows with every load), and the lane that
+      // owns the row keeps its factor. A negative softmax scale turns the queries
+      // round, so that the factor is positive.
+      const int64_t mine = at.real ? at.token * p.q_ldt + at.head * p.q_ldh : -1;
+      const int half = lane >> 4, c = lane & 15;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 2) {
+        const int64_t off = __shfl_sync(0xffffffffu, mine, i + half);
+        uint4 q4 = make_uint4(0u, 0u, 0u, 0u);
+        if (off >= 0) q4 = __ldg(reinterpret_cast<const uint4*>(p.q + off) + c);
+        const uint32_t v[4] = {q4.x, q4.y, q4.z, q4.w};
+        uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max(m, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
-      }
-      const int e = query_exponent(m);
-      // a negative scale turns the queries round, so that the factor is positive
-      const float up = p.scale_log2 < 0.0f ? -exp2_int(e) : exp2_int(e);
-      fac = exp2_int(-e) * fabsf(p.scale_log2);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint4 q4 = raw[2 * c + (d >> 1)];
-          query_terms(d & 1 ? q4.z : q4.x, d & 1 ? q4.w : q4.y, up, hi[d], lo[d]);
-        }
-        const uint32_t at = sQ + 2 * w * kQBytes + r * kHeadDim + ((c ^ (r & 7)) << 4);
-        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(at + kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = query_exponent(m);
+        const float up = p.scale_log2 < 0.0f ? -exp2_int(e) : exp2_int(e);
+        const int e0 = __shfl_sync(0xffffffffu, e, 0), e1 = __shfl_sync(0xffffffffu, e, 16);
+        if ((lane & ~1) == i) fac = exp2_int(-(lane & 1 ? e1 : e0)) * fabsf(p.scale_log2);
+        uint2 hi, lo;
+        query_terms(q4.x, q4.y, up, hi.x, lo.x);
+        query_terms(q4.z, q4.w, up, hi.y, lo.y);
+        const int row = 32 * (warp & 3) + i + half;
+        const uint32_t to = sQ + 2 * w * kQBytes + row * kHeadDim + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
+        sts64(to, hi);
+        sts64(to + kQBytes, lo);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
     }
 
-    // rows that do not exist never ask for a mask; what they compute is not stored
-    const int lim = real ? pos + 1 : 0x7FFFFFFF;
-    const int win = real && p.window >= 0 ? max(pos - p.window, 0) : 0;
-    const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
-    const int win_warp = __reduce_max_sync(0xffffffffu, win);
+    // the positions that the row sees; rows that do not exist never ask for a
+    // mask, and what they compute is not stored
+    const int first = at.real && p.window >= 0 ? max(at.pos - p.window, 0) : 0;
+    const int last = at.real ? at.pos : 0x7FFFFFFE;
+    const int last_warp = __reduce_min_sync(0xffffffffu, last);
+    const int first_warp = __reduce_max_sync(0xffffffffu, first);
 
-    float M = kNegInf, Z = 0.0f;
-    for (int j = 0; j < nt; ++j) {
-      const int t0 = (x.lo + j) * kTileTokens;
-      ok = mbar_wait(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
-           mbar_wait(smem_u32(&sh.s_full[w]), j & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+    // the maximum of a row that has seen nothing: any score outgrows it, and its
+    // weights, of scores of -inf, are 0
+    constexpr float kNoMax = -3e38f;
+    const uint32_t o_col = lane_base + kColO + 128 * w;
+    float M = kNoMax, Z = 0.0f;
+    // The loop is kept short: unrolled over 128 tokens, softmax ran at half the
+    // speed, out of instructions.
+#pragma unroll 1
+    for (int u = 0; u < 2 * nt; ++u) {
+      const int j = u >> 1, b = u & 1;
+      const int t0 = (x.lo + j) * kTileTokens + kHalf * b;
+      const uint32_t s_col = lane_base + kColS + 128 * w + kHalf * b;
+      if (b == 0) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
+                            mbar_wait(smem_u32(&sh.s_full[w]), j & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
       }
-      tc_fence_after();
-      float z[128];
-      {
-        float half[64];
-        tmem_ld64(lane_base + kColS + 128 * w, half);
+      uint32_t y[64];
+      tmem_ld64_bits(s_col, y);
+      float4 info[4];   // 2^ek, ev, 2^-ev per 16 tokens
 #pragma unroll
-        for (int c = 0; c < 64; ++c) z[c] = half[c];
-        tmem_ld64(lane_base + kColS + 128 * w + 64, half);
+      for (int g = 0; g < 4; ++g) info[g] = sh.scale[j % kInfos][4 * b + g];
+      const uint2 vw = *reinterpret_cast<const uint2*>(&sh.valid[j % kInfos][4 * b]);
+      if ((vw.x & vw.y) != 0xffffffffu || t0 + kHalf - 1 > last_warp || t0 < first_warp) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) z[64 + c] = half[c];
-      }
-      const uint4 vw = *reinterpret_cast<const uint4*>(&sh.valid[j % kInfos][0]);
-      if ((vw.x & vw.y & vw.z & vw.w) != 0xffffffffu || t0 + kTileTokens > lim_warp || t0 < win_warp) {
-        const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int top = min(max(lim - t0 - 32 * k, 0), 32), low = min(max(win - t0 - 32 * k, 0), 32);
-          const uint32_t below = top == 32 ? 0xffffffffu : (1u << top) - 1u;
-          const uint32_t under = low == 32 ? 0xffffffffu : (1u << low) - 1u;
-          const uint32_t see = words[k] & below & ~under;
+        for (int k = 0; k < 2; ++k) {
+          const int t = t0 + 32 * k;
+          const int hi = min(max(last + 1 - t, 0), 32), lo = min(max(first - t, 0), 32);
+          const uint32_t below = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+          const uint32_t under = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
+          const uint32_t see = (k ? vw.y : vw.x) & below & ~under;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (!((see >> c) & 1u)) z[32 * k + c] = kNegInf;
+            if (!((see >> c) & 1u)) y[32 * k + c] = 0xFF800000u;   // -inf
         }
       }
-      // x = z * fac * 2^ek + ev per group of 16 tokens; the row's maximum of x
-      float top = kNegInf;
+      // the maximum of x = y * fac * 2^ek + ev
+      float ck[4], top = kNegInf;
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float4 sc = sh.scale[j % kInfos][g];
-        float m = max3(z[16 * g], z[16 * g + 1], z[16 * g + 2]);
-#pragma unroll
-        for (int c = 3; c < 15; c += 2) m = max3(m, z[16 * g + c], z[16 * g + c + 1]);
-        m = fmaxf(m, z[16 * g + 15]);
-        top = fmaxf(top, fmaf(m, fmaxf(fac * sc.x, 1e-37f), sc.y));
+      for (int g = 0; g < 4; ++g) {
+        ck[g] = fmaxf(fac * info[g].x, 1e-37f);
+        auto v = [&](int c) { return __uint_as_float(y[16 * g + c]); };
+        const float m0 = max3(max3(v(0), v(1), v(2)), v(3), v(4));
+        const float m1 = max3(max3(v(5), v(6), v(7)), v(8), v(9));
+        const float m2 = max3(max3(v(10), v(11), v(12)), v(13), max3(v(14), v(15), m0));
+        top = fmaxf(top, fmaf(fmaxf(m1, m2), ck[g], info[g].y));
       }
       const bool grow = top > M + kLazy;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = !grow ? 1.0f : M == kNegInf ? 0.0f : ex2_approx(M - top);
+      if (__any_sync(0xffffffffu, grow)) {   // rare but for the first tokens
+        const float f = grow ? exp2_fast(M - top) : 1.0f;
         if (grow) M = top;
-        if (j > 0) {
-          ok = mbar_wait(smem_u32(&sh.o_done[w]), (j - 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
+        Z *= f;
+        if (u > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w]), (u - 1) & 1, abort_flag));
+          if (!ok) break;
           tc_fence_after();
-          Z *= f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            uint32_t u[32];
-            tmem_ld32(lane_base + kColO + 128 * w + 32 * c, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * f);
-            tmem_st32(lane_base + kColO + 128 * w + 32 * c, u);
-          }
+          scale_columns(o_col, kHeadDim, f);
         }
       }
-      const float sub = M == kNegInf ? 0.0f : M - kPBase;
-      float2 zsum = make_float2(0.0f, 0.0f);
+      const float sub = M - kPBase;
+      uint32_t pw[32];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t pw[32];
+      for (int g = 0; g < 4; ++g) {
+        const float cb = info[g].y - sub;
+        const float2 ck2 = make_float2(ck[g], ck[g]), cb2 = make_float2(cb, cb);
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int g = 4 * q; g < 4 * q + 4; ++g) {
-          const float4 sc = sh.scale[j % kInfos][g];
-          const float ck = fmaxf(fac * sc.x, 1e-37f), cb = sc.y - sub;
-          const float2 ck2 = make_float2(ck, ck), cb2 = make_float2(cb, cb);
-          float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float2 y = __ffma2_rn(make_float2(z[16 * g + 2 * c], z[16 * g + 2 * c + 1]), ck2, cb2);
-            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            sum = __fadd2_rn(sum, e);
-            pw[8 * (g - 4 * q) + c] = pack_f16x2(e.x, e.y);
-          }
-          zsum = __ffma2_rn(sum, make_float2(sc.z, sc.z), zsum);
+        for (int c = 0; c < 8; ++c) {
+          const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(y[16 * g + 2 * c]),
+                                                   __uint_as_float(y[16 * g + 2 * c + 1])), ck2, cb2);
+          const float2 e = make_float2(exp2_fast(x2.x), exp2_fast(x2.y));
+          sum = __fadd2_rn(sum, e);
+          pw[8 * g + c] = pack_f16x2(e.x, e.y);
         }
-        tmem_st32(lane_base + kColS + 128 * w + 32 * q, pw);
+        Z = fmaf(sum.x + sum.y, info[g].z, Z);
       }
-      Z += zsum.x + zsum.y;
+      tmem_st32(s_col, pw);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w][b]));
     }
     if (ok && nt > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w]), (nt - 1) & 1, abort_flag));
+      // the last scores followed every product but the last two, which are waited for in turn
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w]), 0, abort_flag) &&
+                                       mbar_wait(smem_u32(&sh.o_done[w]), 1, abort_flag));
       tc_fence_after();
     }
     if (!ok) {
       sh.abort_flag = 1;
       if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
     }
-    if (Z != Z && M == kNegInf) M = 0.0f;   // nothing but NaN scores: the row is NaN
     if (some && ok) {
       const bool split = p.splits > 1;
       float* part_at = p.tile_partial + static_cast<int64_t>(blockIdx.x) * kTilePartialFloats;
       const int row = w * kTileRows + r;
+      at = tile_row(p, x, some, row);
       if (split) {
         part_at[kItemRows * kHeadDim + row] = nt > 0 ? M : kNegInf;
         part_at[kItemRows * kHeadDim + kItemRows + row] = Z;
-      } else if (real && p.lse) {
-        p.lse[token * p.l_ldt + head] = Z == 0.0f ? kNegInf : kLn2 * (M - kPBase + log2f(Z));
+      } else if (at.real && p.lse) {
+        p.lse[at.token * p.l_ldt + at.head] = row_lse(M, Z);
       }
       const float f = row_factor(Z);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
+      // BF16 rows go through this warp's 8 KB of the queries' memory (every product
+      // has read it), so that a half-warp stores a whole row; 16-byte chunk k of
+      // row r is kept at k ^ (r % 16)
+      const uint32_t stage = sQ + (warp - 4) * 32 * 2 * kHeadDim;
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim; c += 16) {
+        uint32_t o[16];
         if (nt > 0) {
-          tmem_ld32(lane_base + kColO + 128 * w + 32 * c, o);
+          tmem_ld16(o_col + c, o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+          for (int k = 0; k < 16; ++k) o[k] = 0u;
         }
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]);
         if (split) {
-          float4* dst = reinterpret_cast<float4*>(part_at + row * kHeadDim + 32 * c);
+          float4* dst = reinterpret_cast<float4*>(part_at + row * kHeadDim + c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else if (real) {
-          __nv_bfloat16* dst = p.out + token * p.o_ldt + head * p.o_ldh + 32 * c;
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
+          uint32_t p2[8];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = o[16 * k + e];
-            store_row16(dst + 16 * k, v, f);
-          }
+          for (int k = 0; k < 8; ++k) p2[k] = pack_bf16x2(v[2 * k] * f, v[2 * k + 1] * f);
+          const int k = c >> 3;
+          sts128(stage + lane * 256 + ((k ^ (lane & 15)) << 4), make_uint4(p2[0], p2[1], p2[2], p2[3]));
+          sts128(stage + lane * 256 + (((k + 1) ^ (lane & 15)) << 4), make_uint4(p2[4], p2[5], p2[6], p2[7]));
+        }
+      }
+      if (!split) {
+        __syncwarp();
+        const int64_t mine = at.real ? at.token * p.o_ldt + at.head * p.o_ldh : -1;
+        const int half = lane >> 4, k = lane & 15;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += 2) {
+          const int from = i + half;
+          const int64_t off = __shfl_sync(0xffffffffu, mine, from);
+          const uint4 v = lds128(stage + from * 256 + ((k ^ (from & 15)) << 4));
+          if (off >= 0) *(reinterpret_cast<uint4*>(p.out + off) + k) = v;
         }
       }
     }
@@ -1536,14 +1575,6 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
     if (rc != BFP8_OK) return rc;
   }
   if (shape.tiles) {
-    // setmaxnreg's split is made for the registers that the kernel was built with
-    static const int regs = [] {
-      cudaFuncAttributes attr{};
-      return cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(kv_attention_tiles_kernel)) ==
-                     cudaSuccess
-                 ? attr.numRegs : -1;
-    }();
-    if (regs != kTileLaunchRegs) return BFP8_ERR_UNSUPPORTED;
     rc = maps(c.page_size, &tk, &tv);
     if (rc != BFP8_OK) return rc;
     rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_attention_tiles_kernel), kTileSmem);
