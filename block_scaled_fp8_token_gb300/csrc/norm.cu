@@ -16,7 +16,8 @@
 // once, plus its codes.
 #include "bfp8_internal.h"
 #include "ptx.cuh"
-#include "act_math.cuh"
+
+#include <type_traits>
 
 namespace bfp8 {
 namespace {
@@ -35,7 +36,7 @@ struct NormParams {
   float* s;
   int64_t T, ldy, ldr, ldg, ldro, ldn, ldq, ssm, sskb;
   int32_t H, w_f32;
-  float res_scale, eps, w_offset;
+  float res_scale, eps, w_offset, inv_H;
 };
 
 // p[c .. c+8) of a BF16 row as four bf16x2 words, zero past H.
@@ -101,104 +102,173 @@ BFP8_DEV void store8(__nv_bfloat16* p, int c, int H, const float (&v)[8]) {
 }
 
 // Sum over the block, in an order fixed by the launch shape: within the warp by
-// shuffles, then every warp adds the warps' sums. `red` alternates between two
-// buffers, so the barrier of one reduction also separates the reads of the
-// one before it from the writes of the one after.
+// shuffles, then every warp adds the warps' sums. `red` is zero past the warps
+// and alternates between two buffers, so the barrier of one reduction also
+// separates the reads of the one before it from the writes of the one after.
 BFP8_DEV float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int nw = blockDim.x >> 5;
   if (nw == 1) return v;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < nw ? red[lane] : 0.0f;
+  v = 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int k = 0; k < 8; ++k) {
+    if (4 * k >= nw) break;
+    const float4 r = reinterpret_cast<const float4*>(red)[k];
+    v += (r.x + r.y) + (r.z + r.w);
+  }
   return v;
 }
 
-BFP8_DEV float inv_rms(float sum_sq, int H, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fdiv_rn(sum_sq, static_cast<float>(H)) + eps));
+BFP8_DEV float inv_rms(float sum_sq, float inv_H, float eps) {
+  return rsqrtf(fmaf(sum_sq, inv_H, eps));
 }
 
-// One block per row (grid-stride). Thread t holds the 8-column vectors t,
-// t + blockDim, ...: 16 consecutive lanes of a warp hold one 128-column group,
-// so a group's maximum is four shuffles. VEC: every row, pitch and H is a
-// multiple of 8 elements and 16-byte aligned.
-template <bool VEC, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) residual_norm_kernel(const NormParams p) {
-  __shared__ float red[2][32];
+// A block takes rows blockIdx, blockIdx + gridDim, ... Thread t holds the
+// 8-column vectors t, t + blockDim, ...: 16 consecutive lanes of a warp hold one
+// 128-column group, so a group's maximum is four shuffles. VEC: every row, pitch
+// and H is a multiple of 8 elements and 16-byte aligned.
+//
+// VPT = 1 is for few rows: the most threads a row can use, everything loaded at
+// once. VPT = 4 is for many: a thread has the same columns in every row, so the
+// weights are read and widened once, into shared memory (the post-norm's
+// multiplied by a gate that all rows share), a row's loads are issued before the
+// second reduction of the row ahead of it, and a row's reductions cost fewer
+// warps. At 8192 rows of 5120, VPT = 2, 3, 4: 88, 65, 62 us; weights kept in
+// registers: 98 us (one block an SM); rows copied to shared memory two ahead
+// with the weights shared by four rows: 64 us. At 949 rows of 2072: 10.7 us with
+// VPT = 1 and 12.6 with 4.
+template <bool VEC, bool ROW_GATE, int VPT>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512)
+    residual_norm_kernel(const NormParams p) {
+  constexpr bool kMany = VPT > 1;
+  extern __shared__ float4 keep[];   // kMany: [VPT][4][blockDim]: 8 post factors, 8 weights of h
+  __shared__ __align__(16) float red[2][32];
   pdl_launch_dependents();
   pdl_wait();
   const int nt = blockDim.x, tid = threadIdx.x, H = p.H;
+  for (int i = tid; i < 64; i += nt) red[i >> 5][i & 31] = 0.0f;
+  __syncthreads();
+  const bool norm = p.q || p.norm_out;
   int buf = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    uint4 yr[VPT], rr[VPT], gr[VPT];
+  int64_t row = blockIdx.x;
+  uint4 yr[VPT], rr[VPT], gr[ROW_GATE ? VPT : 1];
+  auto load = [&](int64_t at) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = 8 * (tid + i * nt);
-      if (p.y) yr[i] = load8<VEC>(p.y + row * p.ldy, c, H);
-      rr[i] = load8<VEC>(p.res + row * p.ldr, c, H);
-      if (p.y && p.gate) gr[i] = load8<VEC>(p.gate + row * p.ldg, c, H);
+      if (p.y) yr[i] = load8<VEC>(p.y + at * p.ldy, c, H);
+      rr[i] = load8<VEC>(p.res + at * p.ldr, c, H);
+    }
+  };
+  load(row);
+  // factor of y apart from its row's: weight times shared gate (exact in FP32
+  // for BF16 weights: 8 significant bits each)
+  auto post = [&](int i, float (&f)[8]) {
+    const int c = 8 * (tid + i * nt);
+    if (p.w_post) {
+      load_weight8<VEC>(p.w_post, p.w_f32, p.w_offset, c, H, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 1.0f;
+    }
+    if (!ROW_GATE && p.gate) {
+      float g[8];
+      widen8(load8<VEC>(p.gate, c, H), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= g[e];
+    }
+  };
+  auto put8 = [&](int i, int k, const float (&v)[8]) {
+    keep[(4 * i + k) * nt + tid] = make_float4(v[0], v[1], v[2], v[3]);
+    keep[(4 * i + k + 1) * nt + tid] = make_float4(v[4], v[5], v[6], v[7]);
+  };
+  auto get8 = [&](int i, int k, float (&v)[8]) {
+    const float4 a = keep[(4 * i + k) * nt + tid], b = keep[(4 * i + k + 1) * nt + tid];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  };
+  if (kMany) {   // each thread reads back only what it wrote: no barrier
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float f[8];
+      if (p.y) {
+        post(i, f);
+        put8(i, 0, f);
+      }
+      if (norm) {
+        load_weight8<VEC>(p.w_pre, p.w_f32, p.w_offset, 8 * (tid + i * nt), H, f);
+        put8(i, 2, f);
+      }
+    }
+  }
+  for (; row < p.T; row += gridDim.x) {
+    if (ROW_GATE) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        gr[ROW_GATE ? i : 0] = load8<VEC>(p.gate + row * p.ldg, 8 * (tid + i * nt), H);
     }
     float ry = 1.0f;
-    if (p.y && p.w_post) {
-      float ss = 0.0f;
+    if (p.w_post) {
+      float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         float y[8];
         widen8(yr[i], y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+        for (int e = 0; e < 8; e += 2) {
+          const float2 y2 = make_float2(y[e], y[e + 1]);
+          ss = __ffma2_rn(y2, y2, ss);
+        }
       }
-      ry = inv_rms(block_sum(ss, red[buf]), H, p.eps);
+      ry = inv_rms(block_sum(ss.x + ss.y, red[buf]), p.inv_H, p.eps);
       buf ^= 1;
     }
     float h[VPT][8];
-    float sh = 0.0f;
+    float2 sh = make_float2(0.0f, 0.0f);
+    const float2 a2 = make_float2(p.res_scale, p.res_scale), ry2 = make_float2(ry, ry);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = 8 * (tid + i * nt);
       widen8(rr[i], h[i]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] *= p.res_scale;
+      float y[8], f[8], g[8];
       if (p.y) {
-        // y times weight times gate is exact in FP32 when all are BF16 (8
-        // significant bits each), so the row's factor and the sum round once
-        float y[8], f[8];
         widen8(yr[i], y);
-        if (p.w_post) {
-          load_weight8<VEC>(p.w_post, p.w_f32, p.w_offset, c, H, f);
-        } else {
+        if (kMany) get8(i, 0, f);
+        else post(i, f);
+        if (ROW_GATE) widen8(gr[ROW_GATE ? i : 0], g);
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = 1.0f;
+      for (int e = 0; e < 8; e += 2) {
+        float2 h2 = __fmul2_rn(make_float2(h[i][e], h[i][e + 1]), a2);
+        if (p.y) {
+          float2 f2 = make_float2(f[e], f[e + 1]);
+          if (ROW_GATE) f2 = __fmul2_rn(f2, make_float2(g[e], g[e + 1]));
+          h2 = __ffma2_rn(__fmul2_rn(make_float2(y[e], y[e + 1]), f2), ry2, h2);
         }
-        if (p.gate) {
-          float g[8];
-          widen8(gr[i], g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= g[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = fmaf(y[e] * f[e], ry, h[i][e]);
+        h[i][e] = h2.x, h[i][e + 1] = h2.y;
+        sh = __ffma2_rn(h2, h2, sh);   // columns past H hold 0
       }
       if (p.res_out) store8<VEC>(p.res_out + row * p.ldro, c, H, h[i]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sh = fmaf(h[i][e], h[i][e], sh);   // columns past H hold 0
     }
-    if (!p.q && !p.norm_out) continue;
-    const float rh = inv_rms(block_sum(sh, red[buf]), H, p.eps);
+    if (row + gridDim.x < p.T) load(row + gridDim.x);
+    if (!norm) continue;
+    const float rh = inv_rms(block_sum(sh.x + sh.y, red[buf]), p.inv_H, p.eps);
     buf ^= 1;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = 8 * (tid + i * nt);
       float w[8];
-      load_weight8<VEC>(p.w_pre, p.w_f32, p.w_offset, c, H, w);
+      if (kMany) get8(i, 2, w);
+      else load_weight8<VEC>(p.w_pre, p.w_f32, p.w_offset, c, H, w);
       float am = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[i][e] *= w[e];   // n = h * rh
-        am = fmaxf(am, fabsf(h[i][e]));
+      for (int e = 0; e < 8; e += 2) {
+        const float2 h2 = __fmul2_rn(make_float2(h[i][e], h[i][e + 1]), make_float2(w[e], w[e + 1]));
+        h[i][e] = h2.x, h[i][e + 1] = h2.y;   // n = h * rh
+        am = fmaxf(am, fmaxf(fabsf(h2.x), fabsf(h2.y)));
       }
       if (p.norm_out) {
         float n[8];
@@ -209,18 +279,25 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) residual_norm_kernel(co
       if (!p.q) continue;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-      // n / s with the row's factor cancelled: h / (max|h| / 448), unless the floor holds
+      // The codes are h * (448 / max|h|), which leaves the row's factor out. The
+      // reciprocal and the product are a few 2^-24 off the quotient n / s: less
+      // than what n itself carries.
       const float an = am * rh;
-      const float sc = __fdiv_rn(fmaxf(an, 1e-10f), 448.0f);
-      const float dv = an >= 1e-10f ? __fdiv_rn(am, 448.0f) : __fdiv_rn(sc, rh);
+      float sc = an * (1.0f / 448.0f), inv;
+      sc = fmaf(fmaf(-448.0f, sc, an), 1.0f / 448.0f, sc);   // the rounded quotient
+      if (an >= 1e-10f && am >= 1e-30f && am <= 1e30f && an <= 1e30f) {
+        inv = __fdividef(448.0f, am);
+      } else {
+        sc = __fdiv_rn(fmaxf(an, 1e-10f), 448.0f);
+        inv = an >= 1e-10f ? __fdiv_rn(448.0f, am) : __fdiv_rn(rh, sc);
+      }
       if ((tid & 15) == 0 && c < H) p.s[row * p.ssm + static_cast<int64_t>(c >> 7) * p.sskb] = sc;
-      const float rc = __frcp_rn(dv);
-      const float2 y2 = make_float2(rc, rc), ns2 = make_float2(-dv, -dv);
+      const float2 inv2 = make_float2(inv, inv);
       uint32_t cw[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float2 a = div_by_scale2(make_float2(h[i][4 * j], h[i][4 * j + 1]), ns2, y2);
-        const float2 b = div_by_scale2(make_float2(h[i][4 * j + 2], h[i][4 * j + 3]), ns2, y2);
+        const float2 a = __fmul2_rn(make_float2(h[i][4 * j], h[i][4 * j + 1]), inv2);
+        const float2 b = __fmul2_rn(make_float2(h[i][4 * j + 2], h[i][4 * j + 3]), inv2);
         cw[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(a.x, a.y)) |
                 (static_cast<uint32_t>(f32x2_to_e4m3x2(b.x, b.y)) << 16);
       }
@@ -236,21 +313,38 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) residual_norm_kernel(co
   }
 }
 
-template <bool VEC, int VPT>
+template <bool VEC, bool ROW_GATE, int VPT>
 int launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   const int vecs = (p.H + 7) / 8;
   const int threads = ((vecs + VPT - 1) / VPT + 31) / 32 * 32;
-  const int64_t cap = static_cast<int64_t>(sms) * (2048 / threads > 32 ? 32 : 2048 / threads);
+  const int smem = VPT > 1 ? VPT * 4 * threads * 16 : 0;
+  if (smem > 48 * 1024) {
+    const int rc = set_max_dynamic_smem(
+        reinterpret_cast<const void*>(residual_norm_kernel<VEC, ROW_GATE, VPT>), VPT * 4 * 512 * 16);
+    if (rc != BFP8_OK) return rc;
+  }
+  // as many blocks as stay resident: each keeps its weights for all its rows
+  static const int regs = [] {
+    cudaFuncAttributes at{};
+    const cudaError_t e = cudaFuncGetAttributes(&at, residual_norm_kernel<VEC, ROW_GATE, VPT>);
+    return e == cudaSuccess ? at.numRegs : 128;
+  }();
+  const int by_regs = 65536 / (threads * ((regs + 7) / 8 * 8));
+  const int by_smem = 224 * 1024 / (smem + 2048);
+  int fit = by_regs < by_smem ? by_regs : by_smem;
+  fit = fit < 1 ? 1 : fit > 2048 / threads ? 2048 / threads : fit > 32 ? 32 : fit;
+  const int64_t cap = static_cast<int64_t>(sms) * fit;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(p.T < cap ? p.T : cap));
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, residual_norm_kernel<VEC, VPT>, p) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, residual_norm_kernel<VEC, ROW_GATE, VPT>, p) != cudaSuccess)
     return BFP8_ERR_CUDA;
   return check_launch();
 }
@@ -309,6 +403,7 @@ int launch_residual_norm(const bfp8_norm_args& a, int64_t T, int64_t H, void* st
   p.res_scale = a.residual_scale;
   p.eps = a.eps;
   p.w_offset = a.weight_offset;
+  p.inv_H = 1.0f / static_cast<float>(H);
   auto row16 = [](const void* ptr, int64_t ld) { return !ptr || (aligned(ptr, 16) && ld % 8 == 0); };
   const bool vec = H % 8 == 0 && row16(a.y, a.ldy) && row16(a.residual, a.ld_residual) &&
                    row16(a.gate, a.ld_gate) && row16(a.residual_out, a.ld_residual_out) &&
@@ -317,12 +412,18 @@ int launch_residual_norm(const bfp8_norm_args& a, int64_t T, int64_t H, void* st
                    (!a.q_e4m3 || (aligned(a.q_e4m3, 8) && a.ldq % 8 == 0));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int vecs = (p.H + 7) / 8;
-  // few rows: the most threads a row can use; many rows: fewer threads with
-  // more loads in flight each, so that several rows share an SM
-  const int vpt = vecs > 1024 ? 4 : (T > sms && vecs >= 256) ? 2 : 1;
-  if (vpt == 1) return vec ? launch_norm<true, 1>(p, sms, st) : launch_norm<false, 1>(p, sms, st);
-  if (vpt == 2) return vec ? launch_norm<true, 2>(p, sms, st) : launch_norm<false, 2>(p, sms, st);
-  return vec ? launch_norm<true, 4>(p, sms, st) : launch_norm<false, 4>(p, sms, st);
+  // VPT = 4 where a row has no 1024 threads to itself or the rows are more than two
+  // waves of one vector a thread
+  const int vpt = vecs > 1024 || T * vecs > sms * int64_t{4096} ? 4 : 1;
+  auto go = [&](auto v, auto g) {
+    constexpr bool V = decltype(v)::value, G = decltype(g)::value;
+    return vpt == 1 ? launch_norm<V, G, 1>(p, sms, st) : launch_norm<V, G, 4>(p, sms, st);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  const bool row_gate = p.gate && p.ldg != 0;
+  if (vec) return row_gate ? go(yes, yes) : go(yes, no);
+  return row_gate ? go(no, yes) : go(no, no);
 }
 
 }  // namespace bfp8
