@@ -8,6 +8,8 @@
 #include "kv_common.cuh"
 #include "ptx.cuh"
 
+#include <algorithm>
+
 namespace bfp8 {
 namespace {
 
@@ -204,18 +206,15 @@ struct AppendParams {
   int32_t heads, window;
 };
 
-constexpr int kAppendThreads = 128;
-constexpr int kRowsInRegs = 16;   // rows of a run held between its two passes
+constexpr int kRowsInRegs = 16;   // rows of a run that a warp holds between its two passes
 
-// Largest |x| of eight BF16 values, as bits; a NaN counts as nothing.
-BFP8_DEV uint32_t amax8(const uint4& r) {
+// Largest |x| so far per half, as BF16 bits; a NaN counts as nothing (max takes
+// the other operand, and m is never one).
+BFP8_DEV uint32_t amax8(const uint4& r, uint32_t m) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
-    m = max(m, max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi));
-  }
+  for (int j = 0; j < 4; ++j)
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[j] & 0x7FFF7FFFu));
   return m;
 }
 
@@ -223,9 +222,11 @@ BFP8_DEV uint2 quant8(const uint4& r, float inv) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   uint32_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = f32x2_to_e4m3x2(__uint_as_float(w[j] << 16) * inv,
-                           __uint_as_float(w[j] & 0xFFFF0000u) * inv);
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    const float2 x = __fmul2_rn(v, make_float2(inv, inv));
+    c[j] = f32x2_to_e4m3x2(x.x, x.y);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
@@ -243,50 +244,77 @@ BFP8_DEV uint2 rescale8(const uint2& v, float f) {
   return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
 }
 
-// A warp owns one (window of tokens, head, K or V) and quantizes every run that
-// begins in its window: a run is the consecutive rows that fill consecutive
-// slots of one page, so one warp sees all new tokens of a page and head, and
-// the page's scale needs no atomics. A half-warp holds a row (8 elements a
-// lane), a load covers two rows. Bound by HBM on prompts and by latency on a
-// decode step, where every run is one row.
-template <int PAGE>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+// A team of WARPS warps owns one (window of tokens, head, K or V) and quantizes
+// every run that begins in its window: a run is the consecutive rows that fill
+// consecutive slots of one page, so one team sees all new tokens of a page and
+// head, and the page's scale needs no atomics. A half-warp holds a row (8
+// elements a lane), a load covers two rows.
+//
+// WARPS = 1 (four teams a block) is for calls whose every (token, head) can have
+// a warp, such as a decode step's, whose runs are one row each: bound by latency.
+// Otherwise a team has a warp for every 16 rows of a page, so that a page's rows
+// are read once and stay in registers until its scale is known: bound by HBM on
+// prompts. Runs short enough for one warp are dealt out to the team's in turn.
+// 16,000 prompt tokens of 8 heads (99 MB moved): 20 us, 4.8 TB/s, where one warp
+// for every run took 27; a decode step of 128 tokens: 4.4 us.
+template <int PAGE, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS)
+    kv_append_kernel(const AppendParams p) {
+  constexpr int kTeams = WARPS == 1 ? 4 : 1;
+  __shared__ uint32_t team_max[2][WARPS];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
   const int sub = lane >> 4, chunk = lane & 15;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kTeams + (WARPS == 1 ? threadIdx.x >> 5 : 0);
   const int64_t win = id / (2 * p.heads);
   const int rest = static_cast<int>(id - win * (2 * p.heads));
   const int head = rest >> 1, kv = rest & 1;
   const int64_t t_end = min((win + 1) * p.window, p.T);
   const __nv_bfloat16* x = p.x[kv] + head * p.ldh[kv] + 8 * chunk;
   const int64_t ldt = p.ldt[kv];
+  int turn = 0, buf = 0;
   for (int64_t t = win * p.window; t < t_end;) {
-    const int64_t slot = __ldg(p.slots + t);
+    // the run's slots, as far as a page goes, and the one before it, in one round of loads
+    int64_t next[(PAGE + 31) / 32];
+#pragma unroll
+    for (int c = 0; c < PAGE; c += 32)
+      next[c / 32] = t + c + lane < p.T ? __ldg(p.slots + t + c + lane) : -1;
+    const int64_t before = t > 0 ? __ldg(p.slots + t - 1) : -1;
+    const int64_t slot = __shfl_sync(0xffffffffu, next[0], 0);
     if (slot < 0 || slot >= p.n_slots) {
       ++t;
       continue;
     }
     const int64_t page = slot / PAGE;
     const int off = static_cast<int>(slot - page * PAGE);
-    // rows of this run: the lanes compare the next slots with the ones expected
-    int n = 0;
+    int n = 0;   // rows of this run: the lanes compare the slots with the ones expected
 #pragma unroll
     for (int c = 0; c < PAGE; c += 32) {
       const int i = c + lane;
-      const bool in = i < PAGE - off && t + i < p.T && __ldg(p.slots + t + i) == slot + i;
+      const bool in = i < PAGE - off && next[c / 32] == slot + i;
       const uint32_t gap = ~__ballot_sync(0xffffffffu, in);
       const int k = gap ? __ffs(gap) - 1 : 32;
       if (n == c) n += k;
     }
-    const bool inside = off > 0 && t > 0 && __ldg(p.slots + t - 1) == slot - 1;
+    const bool inside = off > 0 && before == slot - 1;
     const int64_t t0 = t;
     t += n;
     if (inside) continue;   // the run began in an earlier window
+    // `first` and `step`: this warp's rows are first, first + 2, ... in groups of 16
+    const bool together = WARPS > 1 && n > kRowsInRegs;
+    if (WARPS > 1 && !together) {
+      const bool mine = turn == warp;
+      turn = turn + 1 < WARPS ? turn + 1 : 0;
+      if (!mine) continue;
+    }
+    const int first = together ? kRowsInRegs * warp : 0;
+    uint8_t* exp_at = p.exps[kv] + page * p.ep + head * p.eh;
+    uint8_t* base = p.codes[kv] + page * p.sp[kv] + head * p.sh[kv] + 8 * chunk;
+    const int held = off > 0 ? static_cast<int>(*exp_at) - 127 : -128;
     uint4 r[kRowsInRegs / 2];
     uint32_t am = 0;
-    for (int i0 = 0; i0 < n; i0 += kRowsInRegs) {
+    for (int i0 = first; i0 < (WARPS > 1 ? first + 1 : n); i0 += kRowsInRegs) {
 #pragma unroll
       for (int i = 0; i < kRowsInRegs / 2; ++i) {
         const int row = i0 + 2 * i + sub;
@@ -294,30 +322,30 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         if (row < n) r[i] = __ldg(reinterpret_cast<const uint4*>(x + (t0 + row) * ldt));
       }
 #pragma unroll
-      for (int i = 0; i < kRowsInRegs / 2; ++i) am = max(am, amax8(r[i]));
+      for (int i = 0; i < kRowsInRegs / 2; ++i) am = amax8(r[i], am);
     }
-    am = __reduce_max_sync(0xffffffffu, am);
-    int e = scale_exponent(__uint_as_float(am << 16));
-    uint8_t* exp_at = p.exps[kv] + page * p.ep + head * p.eh;
-    uint8_t* base = p.codes[kv] + page * p.sp[kv] + head * p.sh[kv] + 8 * chunk;
-    if (off > 0) {
-      const int held = static_cast<int>(*exp_at) - 127;
-      if (e > held) {
-        // a louder token than the page has seen: its older codes move to the new scale
-        const float f = exp2_int(held - e);
-        for (int row = sub; row < off; row += 2) {
-          uint2* at = reinterpret_cast<uint2*>(base + row * p.st[kv]);
-          *at = rescale8(*at, f);
-        }
-      } else {
-        e = held;
+    am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+    if (together) {
+      if (lane == 0) team_max[buf][warp] = am;
+      __syncthreads();   // also: every warp has read the page's scale before it changes
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) am = max(am, team_max[buf][w]);
+      buf ^= 1;
+    }
+    const int fit = scale_exponent(__uint_as_float(am << 16)), e = max(fit, held);
+    if (off > 0 && fit > held) {
+      // a louder token than the page has seen: its older codes move to the new scale
+      const float f = exp2_int(held - e);
+      for (int row = sub + (together ? 2 * warp : 0); row < off; row += together ? 2 * WARPS : 2) {
+        uint2* at = reinterpret_cast<uint2*>(base + row * p.st[kv]);
+        *at = rescale8(*at, f);
       }
     }
     __syncwarp();
-    if (lane == 0) *exp_at = static_cast<uint8_t>(e + 127);
+    if (lane == 0 && first == 0) *exp_at = static_cast<uint8_t>(e + 127);
     const float inv = exp2_int(-e);
-    for (int i0 = 0; i0 < n; i0 += kRowsInRegs) {
-      if (n > kRowsInRegs) {   // more rows than the registers hold: read again (from L1 or L2)
+    for (int i0 = first; i0 < (WARPS > 1 ? first + 1 : n); i0 += kRowsInRegs) {
+      if (WARPS == 1 && n > kRowsInRegs) {   // more rows than one warp holds: read again (L1 or L2)
 #pragma unroll
         for (int i = 0; i < kRowsInRegs / 2; ++i) {
           const int row = i0 + 2 * i + sub;
@@ -416,25 +444,25 @@ int launch_kv_append(const void* k, int64_t k_ldt, int64_t k_ldh, const void* v,
   p.T = T;
   p.n_slots = c.n_pages * c.page_size;
   p.heads = c.n_kv_heads;
-  // one token a warp while that does not fill the GPU's warps (a decode step's
-  // tokens are runs of one row each), then longer windows, up to a page
   const int64_t pairs = 2 * static_cast<int64_t>(p.heads);
   const int64_t warps = static_cast<int64_t>(sms) * 32;
-  int64_t w = T * pairs / warps;
-  w = w < 1 ? 1 : w > c.page_size ? c.page_size : w;
-  p.window = static_cast<int32_t>(w);
-  const int64_t per = kAppendThreads / 32;
-  const int64_t blocks = ((T + w - 1) / w * pairs + per - 1) / per;
-  if (blocks > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
-  auto go = [&](auto kernel) {
-    return launch_dependent(kernel, dim3(static_cast<unsigned>(blocks)), kAppendThreads, 0,
+  auto go = [&](auto kernel, int team, int block_warps) {
+    // a team's window: one token while the GPU's warps suffice, then as many as fill
+    // them once, up to a page
+    const int64_t w = std::clamp<int64_t>(T * pairs * team / warps, 1, c.page_size);
+    const int64_t teams = (T + w - 1) / w * pairs, per = block_warps / team;
+    const int64_t blocks = (teams + per - 1) / per;
+    if (blocks > 0x7FFFFFFF) return static_cast<int>(BFP8_ERR_UNSUPPORTED);
+    p.window = static_cast<int32_t>(w);
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(blocks)), 32 * block_warps, 0,
                             static_cast<cudaStream_t>(stream), p);
   };
+  const bool few = T * pairs <= warps;
   switch (c.page_size) {
-    case 16: return go(kv_append_kernel<16>);
-    case 32: return go(kv_append_kernel<32>);
-    case 64: return go(kv_append_kernel<64>);
-    default: return go(kv_append_kernel<128>);
+    case 16: return go(kv_append_kernel<16, 1>, 1, 4);
+    case 32: return few ? go(kv_append_kernel<32, 1>, 1, 4) : go(kv_append_kernel<32, 2>, 2, 2);
+    case 64: return few ? go(kv_append_kernel<64, 1>, 1, 4) : go(kv_append_kernel<64, 4>, 4, 4);
+    default: return few ? go(kv_append_kernel<128, 1>, 1, 4) : go(kv_append_kernel<128, 8>, 8, 8);
   }
 }
 

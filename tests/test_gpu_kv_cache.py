@@ -159,6 +159,18 @@ def test_append_many_tokens(bfp8, cuda_device):
     _check_append(bfp8, cuda_device, k, v, slots, _cache(cuda_device, 300, 4, 64, rng))
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_append_many_short_runs(bfp8, cuda_device, page):
+    """More (token, head) pairs than warps: runs of one row, of a few and of a page, dealt out and shared."""
+    rng = np.random.default_rng(page)
+    lengths = [(int(rng.integers(0, page)), 1) for _ in range(500)]
+    lengths += [(int(rng.integers(0, page)), int(rng.integers(2, 2 * page))) for _ in range(20)]
+    lengths = [lengths[i] for i in rng.permutation(len(lengths))]
+    slots, used = _slots(rng, page, lengths, 700)
+    k, v = _kv(cuda_device, len(slots), 6, rng)
+    _check_append(bfp8, cuda_device, k, v, slots, _cache(cuda_device, 700, 6, page, rng))
+
+
 def test_append_skips_rows_and_repeats(bfp8, cuda_device):
     rng = np.random.default_rng(3)
     dev, cache = cuda_device, _cache(cuda_device, 6, 2, 16, rng)
