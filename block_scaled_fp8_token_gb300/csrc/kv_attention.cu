@@ -45,14 +45,14 @@ struct AttnParams {
   const int32_t* kv_len;
   float* partial;            // split rows' partial sums
   uint64_t* schedule;        // [B + 1]: the rows kernel's units before each request, and in all
-  uint32_t* item_base;       // [B]: the tiles kernel's items before each request
   int64_t q_ldt, q_ldh, o_ldt, o_ldh, l_ldt, ld_table, exp_page, exp_head;
   int64_t T, n_pages;
   int32_t B, H, G, page_shift, max_blocks, window;
   int32_t seg_rows;          // query rows of a segment of the rows kernel: 8 or 16
   int32_t few_rows;          // requests of at most this many rows of a KV head go to the rows kernel
-  int32_t splits;            // parts that the tiles kernel cuts an item's tokens into
-  float* tile_partial;       // [items * splits] of kTilePartialFloats
+  int32_t whole_items;       // the tiles kernel's blocks take whole items
+  struct TileDesc* tile_desc;   // [blocks]
+  float* tile_partial;       // [blocks][2] of kTilePartialFloats
   float scale_log2;          // softmax scale * log2(e)
 };
 
@@ -782,57 +782,63 @@ constexpr int kKvBytes = kTileTokens * kHeadDim;
 constexpr int kV16Bytes = 2 * kKvBytes;
 constexpr int kTileSmem =
     4 * kQBytes + (kTileStages + kValueStages) * kKvBytes + 2 * kV16Bytes + 1024;
+// Queries' rows of an unfinished item: O as [column / 4][row][4], then M, then Z.
 constexpr int kTilePartialFloats = kItemRows * kHeadDim + 2 * kItemRows;
 constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w, O at 256 + 128 w
+// Beginning and ending an item costs about as long as this many tiles, which
+// the schedule counts behind each item's own; a block gets kTileShare at least.
+constexpr uint32_t kTilePad = 2, kTileShare = 4;
 
-struct TileItem {
-  int32_t b, h, q0, n, kv, held;
-  int32_t row0;          // first row of the item in its request
-  int32_t lo, hi;        // tiles of tokens, this part's
+struct TileReq {
+  int32_t q0, n, kv, held;   // first row, new tokens, length, tokens inside the table
+  uint32_t pairs;            // items of a KV head; 0: not this kernel's
 };
-
-// Item `it` of request b (heaviest first: the last rows of a prompt see the most).
-BFP8_DEV TileItem tile_item(const AttnParams& p, int b, uint32_t it, int part) {
-  TileItem x;
-  x.b = b;
-  x.q0 = max(__ldg(p.q_offsets + b), 0);
-  x.n = static_cast<int32_t>(min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T) - x.q0);
-  x.kv = max(__ldg(p.kv_len + b), 0);
-  x.held = static_cast<int32_t>(min(static_cast<int64_t>(x.kv),
+BFP8_DEV TileReq tile_req(const AttnParams& p, int b) {
+  TileReq r;
+  r.q0 = max(__ldg(p.q_offsets + b), 0);
+  const int64_t q1 = min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T);
+  r.n = static_cast<int32_t>(max(q1 - r.q0, static_cast<int64_t>(0)));
+  r.kv = max(__ldg(p.kv_len + b), 0);
+  r.held = static_cast<int32_t>(min(static_cast<int64_t>(r.kv),
                                     static_cast<int64_t>(p.max_blocks) << p.page_shift));
-  const uint32_t rows = static_cast<uint32_t>(x.n) * p.G;
-  const uint32_t pairs = (rows + kItemRows - 1) / kItemRows;
-  const uint32_t back = it / p.H;
-  x.h = it - back * p.H;
-  x.row0 = (pairs - 1 - back) * kItemRows;
-  const uint32_t last = min(rows, static_cast<uint32_t>(x.row0 + kItemRows)) - 1;
-  const int pos0 = x.kv - x.n + static_cast<int>(static_cast<uint32_t>(x.row0) / p.G);
-  const int pos1 = x.kv - x.n + static_cast<int>(last / p.G);
-  const int end = min(pos1 + 1, x.held);
+  const int64_t rows = static_cast<int64_t>(r.n) * p.G;
+  r.pairs = rows > p.few_rows ? static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows) : 0u;
+  return r;
+}
+// The tiles of tokens that the rows of pair `q` see: [x, y).
+BFP8_DEV int2 pair_tiles(const AttnParams& p, const TileReq& r, uint32_t q) {
+  const uint32_t row0 = q * kItemRows, rows = static_cast<uint32_t>(r.n) * p.G;
+  const uint32_t last = min(rows, row0 + kItemRows) - 1;
+  const int pos0 = r.kv - r.n + static_cast<int>(row0 / p.G);
+  const int pos1 = r.kv - r.n + static_cast<int>(last / p.G);
+  const int end = min(pos1 + 1, r.held);
   const int begin = p.window >= 0 ? max(pos0 - p.window, 0) : 0;
   const int lo = begin / kTileTokens;
-  const int hi = end > begin ? (end + kTileTokens - 1) / kTileTokens : lo;
-  const int64_t tiles = hi - lo;
-  x.lo = lo + static_cast<int>(tiles * part / p.splits);
-  x.hi = lo + static_cast<int>(tiles * (part + 1) / p.splits);
-  return x;
-}
-BFP8_DEV uint32_t tile_items_of(const AttnParams& p, int b) {
-  const int64_t q0 = max(__ldg(p.q_offsets + b), 0);
-  const int64_t n = min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T) - q0;
-  const int64_t rows = n * p.G;
-  if (n <= 0 || rows <= p.few_rows) return 0;
-  return static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows) * p.H;
+  return make_int2(lo, end > begin ? (end + kTileTokens - 1) / kTileTokens : lo);
 }
 
-// Row `row` of an item (none of a block that has no item).
-BFP8_DEV RowAt tile_row(const AttnParams& p, const TileItem& x, bool some, int row) {
+// A block's next piece of work: an item, or a part of its tokens.
+struct TileItem {
+  int32_t b, h, q0, n, kv, held;   // b < 0: there is no more
+  int32_t row0;                    // first row of the item in its request
+  int32_t lo, hi;                  // tiles of tokens
+  int32_t begins, ends;            // holds the item's first tile, its last
+};
+
+// What the join has to know of a block: its last item, when the block began it and
+// others finish it, and whether its first part finishes another's.
+struct TileDesc {
+  int32_t open, b, h, row0, closes, pad[3];
+};
+
+// Row `row` of an item.
+BFP8_DEV RowAt tile_row(const AttnParams& p, const TileItem& x, int row) {
   RowAt a;
   const uint32_t i = x.row0 + row;
-  const uint32_t tok = some ? i / p.G : 0;
-  a.real = some && tok < static_cast<uint32_t>(x.n);
+  const uint32_t tok = i / p.G;
+  a.real = tok < static_cast<uint32_t>(x.n);
   a.token = x.q0 + static_cast<int64_t>(a.real ? tok : 0);
-  a.head = x.h * p.G + (some ? i - tok * p.G : 0);
+  a.head = x.h * p.G + (i - tok * p.G);
   a.pos = x.kv - x.n + static_cast<int>(tok);
   return a;
 }
@@ -866,15 +872,18 @@ struct TileShared {
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kValueStages], v_empty[kValueStages];
   uint64_t w_full[2], w_empty[2];      // the widened values' buffers
   uint64_t info_full[kInfos];
-  uint64_t q_full, s_full[2], p_full[2][2], o_done[2], drained;   // p_full: of a tile's halves
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_done[2][2], drained;   // p_full, o_done: of a tile's halves
+  uint64_t item_full[2], item_empty[2];
   // What softmax needs of a tile. One slot more than there are stages: tile m's
   // keys are loaded once S of tile m - 3 is complete for both query tiles, which
   // follows their P of tile m - 4.
   float4 scale[kInfos][8];             // per 16 tokens: 2^ek, ev, 2^-ev
   uint16_t valid[kInfos][8];           // per 16 tokens: a bit for each that exists
   uint32_t tmem;
-  uint32_t scan[kTileThreads / 32];
-  TileItem item;                       // this block's; b < 0: none
+  uint64_t scan[kTileThreads / 32];
+  TileItem item[2];                    // the one in work and the next
+  uint64_t start_rel;                  // where the block's range begins: units into its request's
+  int start_b;
   int abort_flag;
 };
 
@@ -899,18 +908,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(smem_u32(&sh.v_empty[s]), 2);
     }
     for (int s = 0; s < kInfos; ++s) mbar_init(smem_u32(&sh.info_full[s]), 1);
-    mbar_init(smem_u32(&sh.q_full), 8);
     mbar_init(smem_u32(&sh.drained), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&sh.w_full[w]), 2);
       mbar_init(smem_u32(&sh.w_empty[w]), 1);
+      mbar_init(smem_u32(&sh.q_full[w]), 4);
       mbar_init(smem_u32(&sh.s_full[w]), 1);
-      for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&sh.p_full[w][b]), 4);
-      mbar_init(smem_u32(&sh.o_done[w]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&sh.p_full[w][b]), 4);
+        mbar_init(smem_u32(&sh.o_done[w][b]), 1);
+      }
+      mbar_init(smem_u32(&sh.item_full[w]), 1);
+      mbar_init(smem_u32(&sh.item_empty[w]), kTileThreads / 32 - 1);
     }
     sh.abort_flag = 0;
-    sh.item = TileItem{};
-    sh.item.b = -1;
+    sh.start_b = 0;
+    sh.start_rel = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -919,31 +932,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   pdl_wait();
 
-  // ---- which item: block index = item * splits + part, items request by request
-  {
-    const uint32_t item = blockIdx.x / p.splits;
-    uint32_t run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kTileThreads) {
-      const uint32_t mine = b0 + tid < p.B ? tile_items_of(p, b0 + tid) : 0;
-      uint32_t inc = mine;
+  // ---- this block's range of units: an item has its tiles and kTilePad
+  uint64_t range = 0;
+  if (!p.whole_items) {
+    uint64_t mine = 0, before = 0;   // this thread's request in the last pass of the scan
+    auto scan_pass = [&](int b0) {   // exclusive prefix of one request per thread; returns the total
+      TileReq r{};
+      if (b0 + tid < p.B) r = tile_req(p, b0 + tid);
+      mine = 0;
+      for (uint32_t todo = __ballot_sync(0xffffffffu, r.pairs > 0); todo; todo &= todo - 1) {
+        const int l = __ffs(todo) - 1;   // the warp counts this lane's request together
+        TileReq o;
+        o.n = __shfl_sync(0xffffffffu, r.n, l);
+        o.kv = __shfl_sync(0xffffffffu, r.kv, l);
+        o.held = __shfl_sync(0xffffffffu, r.held, l);
+        o.pairs = __shfl_sync(0xffffffffu, r.pairs, l);
+        uint64_t sum = 0;
+        for (uint32_t q = lane; q < o.pairs; q += 32) {
+          const int2 t = pair_tiles(p, o, q);
+          sum += t.y - t.x + kTilePad;
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        if (lane == l) mine = sum * p.H;
+      }
+      uint64_t inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        const uint64_t v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
       __syncthreads();
       if (lane == 31) sh.scan[warp] = inc;
       __syncthreads();
-      uint32_t total = 0, off = 0;
+      uint64_t total = 0, off = 0;
 #pragma unroll
       for (int w = 0; w < kTileThreads / 32; ++w) {
         if (w == warp) off = total;
         total += sh.scan[w];
       }
-      const uint32_t at = run + off + inc - mine;
-      if (mine && item >= at && item < at + mine)
-        sh.item = tile_item(p, b0 + tid, item - at, blockIdx.x % p.splits);
-      if (blockIdx.x == 0 && b0 + tid < p.B) p.item_base[b0 + tid] = at;
+      before = off + inc - mine;
+      return total;
+    };
+    uint64_t U = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kTileThreads) U += scan_pass(b0);
+    const uint64_t want = (U + kTileShare - 1) / kTileShare;
+    const uint32_t C = static_cast<uint32_t>(min(want, static_cast<uint64_t>(gridDim.x)));
+    const uint64_t g0 = blockIdx.x < C ? range_begin(U, blockIdx.x, C) : 0;
+    range = blockIdx.x < C ? range_begin(U, blockIdx.x + 1, C) - g0 : 0;
+    uint64_t run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kTileThreads) {
+      const uint64_t total = p.B > kTileThreads ? scan_pass(b0) : U;   // one pass: still in registers
+      const uint64_t at = run + before;
+      if (mine && g0 >= at && g0 < at + mine) sh.start_b = b0 + tid, sh.start_rel = g0 - at;
       run += total;
     }
   }
@@ -952,9 +993,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const volatile int* abort_flag = &sh.abort_flag;
-  const TileItem& x = sh.item;
-  const bool some = x.b >= 0;
-  const int nt = x.hi - x.lo;
+  // Tiles are counted on across the block's items (`tiles`), and so are the rings'
+  // stages and the barriers' phases; so are the items (`items`).
+  uint32_t tiles = 0, items = 0;
 
   if (warp < 4) {
     if (warp == 0) {
@@ -962,62 +1003,158 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int page = 1 << p.page_shift;
       const uint32_t box_bytes = page * kHeadDim;
       bool ok = true;
-      int loaded = 0;   // tiles
-      const int32_t* row = p.table + x.b * p.ld_table;
-      auto page_id = [&](int j) {   // lane l < 8: the page of tokens 16 l .. of tile j
-        const int t = (x.lo + j) * kTileTokens + 16 * lane;
-        return j < nt && lane < 8 && t < x.held ? __ldg(row + (t >> p.page_shift)) : -1;
-      };
-      int32_t id = page_id(0);
-      for (int j = 0; j < nt; ++j) {
-        const int s = j % kTileStages;
-        const uint32_t ph = (j / kTileStages) & 1;
-        const int vs = j % kValueStages;
-        const uint32_t vph = (j / kValueStages) & 1;
-        const uint32_t kf = smem_u32(&sh.k_full[s]), vf = smem_u32(&sh.v_full[vs]);
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait_sleep(smem_u32(&sh.k_empty[s]), ph ^ 1u, abort_flag) &&
-                            mbar_wait_sleep(smem_u32(&sh.v_empty[vs]), vph ^ 1u, abort_flag))) {
-          ok = false;
-          break;
+      // where the walk over the items stands: request, pair from its last one, head,
+      // units into the item; whole items come in rounds over the blocks instead, in
+      // alternating directions, as the heaviest are first
+      int b = sh.start_b;
+      TileReq r = tile_req(p, b);
+      uint32_t back = 0, h = 0, u0 = 0, round = 0;
+      uint64_t left = range;
+      if (left) {
+        uint64_t rel = sh.start_rel;
+        for (; back < r.pairs; back += 32) {   // the pair that holds it: 32 at a time
+          const int2 t = back + lane < r.pairs ? pair_tiles(p, r, r.pairs - 1 - back - lane) : make_int2(0, 0);
+          const uint64_t cost = back + lane < r.pairs ? static_cast<uint64_t>(t.y - t.x + kTilePad) * p.H : 0;
+          uint64_t inc = cost;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, inc > rel);
+          if (past) {
+            const int l = __ffs(past) - 1;
+            rel -= __shfl_sync(0xffffffffu, inc - cost, l);
+            const uint32_t one = static_cast<uint32_t>(__shfl_sync(0xffffffffu, cost, l) / p.H);
+            back += l;
+            h = static_cast<uint32_t>(rel / one);
+            u0 = static_cast<uint32_t>(rel - static_cast<uint64_t>(h) * one);
+            break;
+          }
+          rel -= __shfl_sync(0xffffffffu, inc, 31);
         }
-        const int t = (x.lo + j) * kTileTokens + 16 * lane;
-        const bool there = lane < 8 && id >= 0 && id < p.n_pages;
-        const bool leads = there && (t & (page - 1)) == 0;
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, leads));
-        if (lane == 0) {
-          mbar_expect_tx(kf, boxes * box_bytes);
-          mbar_expect_tx(vf, boxes * box_bytes);
-        }
-        __syncwarp();
-        if (leads) {
-          const uint32_t at = 16 * lane * kHeadDim;
-          tma_load_4d(sK + s * kKvBytes + at, &tk, 0, 0, x.h, id, kf);
-          tma_load_4d(sV + vs * kKvBytes + at, &tv, 0, 0, x.h, id, vf);
-        }
-        int ek = 127, ev = 127;
-        if (there) {
-          const int64_t at = id * p.exp_page + x.h * p.exp_head;
-          ek = __ldg(p.k_exp + at);
-          ev = __ldg(p.v_exp + at);
-        }
-        id = page_id(j + 1);
-        if (lane < 8) {
-          const int left = there ? min(x.held - t, 16) : 0;
-          sh.scale[j % kInfos][lane] = make_float4(exp2_int(ek - 127), static_cast<float>(ev - 127),
-                                                   exp2_int(127 - ev), 0.0f);
-          sh.valid[j % kInfos][lane] = static_cast<uint16_t>((1u << left) - 1u);
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(kf);
-          mbar_arrive(vf);
-          mbar_arrive(smem_u32(&sh.info_full[j % kInfos]));
-        }
-        ++loaded;
       }
+      auto next_item = [&] {
+        TileItem x{};
+        x.b = -1;
+        if (p.whole_items) {
+          const uint32_t at = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+          ++round;
+          if (at >= r.pairs * p.H) return x;
+          back = at / p.H;
+          h = at - back * p.H;
+        }
+        while (p.whole_items || left) {
+          if (!p.whole_items && back >= r.pairs) {   // the next request with items: 32 at a time
+            back = 0;
+            uint32_t has = 0;
+            for (++b; b < p.B; b += 32) {
+              has = __ballot_sync(0xffffffffu, b + lane < p.B && tile_req(p, b + lane).pairs > 0);
+              if (has) break;
+            }
+            if (!has) return x;
+            b += __ffs(has) - 1;
+            r = tile_req(p, b);
+          }
+          const uint32_t pair = r.pairs - 1 - back;
+          const int2 t = pair_tiles(p, r, pair);
+          const uint32_t nt = t.y - t.x, begin = u0;
+          uint32_t end = nt + kTilePad;
+          if (!p.whole_items) {
+            end = static_cast<uint32_t>(min(static_cast<uint64_t>(end), u0 + left));
+            left -= end - u0;
+          }
+          x.h = h;
+          if (!p.whole_items) {
+            u0 = 0;
+            if (++h >= static_cast<uint32_t>(p.H)) h = 0, ++back;
+          }
+          if (begin >= nt && !(nt == 0 && begin == 0)) continue;   // nothing but the padding
+          x.b = b;
+          x.q0 = r.q0, x.n = r.n, x.kv = r.kv, x.held = r.held;
+          x.row0 = pair * kItemRows;
+          x.lo = t.x + begin;
+          x.hi = t.x + min(end, nt);
+          x.begins = begin == 0;
+          x.ends = end >= nt;
+          return x;
+        }
+        return x;
+      };
+      TileDesc desc{};
+      while (true) {
+        TileItem x = next_item();
+        const int slot = items & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_empty[slot]), ((items >> 1) & 1) ^ 1u, abort_flag));
+        if (!ok) break;
+        if (lane == 0) {
+          sh.item[slot] = x;
+          mbar_arrive(smem_u32(&sh.item_full[slot]));
+        }
+        __syncwarp();
+        ++items;
+        if (x.b < 0) break;
+        if (!x.begins && x.ends) desc.closes = 1;
+        if (x.begins && !x.ends) desc.open = 1, desc.b = x.b, desc.h = x.h, desc.row0 = x.row0;
+        const int nt = x.hi - x.lo;
+        const int32_t* row = p.table + x.b * p.ld_table;
+        auto page_id = [&](int j) {   // lane l < 8: the page of tokens 16 l .. of tile j
+          const int t = (x.lo + j) * kTileTokens + 16 * lane;
+          return j < nt && lane < 8 && t < x.held ? __ldg(row + (t >> p.page_shift)) : -1;
+        };
+        int32_t id = page_id(0);
+        for (int j = 0; j < nt; ++j, ++tiles) {
+          const int s = tiles % kTileStages;
+          const uint32_t ph = (tiles / kTileStages) & 1;
+          const int vs = tiles % kValueStages;
+          const uint32_t vph = (tiles / kValueStages) & 1;
+          const uint32_t kf = smem_u32(&sh.k_full[s]), vf = smem_u32(&sh.v_full[vs]);
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait_sleep(smem_u32(&sh.k_empty[s]), ph ^ 1u, abort_flag) &&
+                              mbar_wait_sleep(smem_u32(&sh.v_empty[vs]), vph ^ 1u, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const int t = (x.lo + j) * kTileTokens + 16 * lane;
+          const bool there = lane < 8 && id >= 0 && id < p.n_pages;
+          const bool leads = there && (t & (page - 1)) == 0;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, leads));
+          if (lane == 0) {
+            mbar_expect_tx(kf, boxes * box_bytes);
+            mbar_expect_tx(vf, boxes * box_bytes);
+          }
+          __syncwarp();
+          if (leads) {
+            const uint32_t at = 16 * lane * kHeadDim;
+            tma_load_4d(sK + s * kKvBytes + at, &tk, 0, 0, x.h, id, kf);
+            tma_load_4d(sV + vs * kKvBytes + at, &tv, 0, 0, x.h, id, vf);
+          }
+          int ek = 127, ev = 127;
+          if (there) {
+            const int64_t at = id * p.exp_page + x.h * p.exp_head;
+            ek = __ldg(p.k_exp + at);
+            ev = __ldg(p.v_exp + at);
+          }
+          id = page_id(j + 1);
+          if (lane < 8) {
+            const int left_here = there ? min(x.held - t, 16) : 0;
+            sh.scale[tiles % kInfos][lane] = make_float4(exp2_int(ek - 127), static_cast<float>(ev - 127),
+                                                         exp2_int(127 - ev), 0.0f);
+            sh.valid[tiles % kInfos][lane] = static_cast<uint16_t>((1u << left_here) - 1u);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(kf);
+            mbar_arrive(vf);
+            mbar_arrive(smem_u32(&sh.info_full[tiles % kInfos]));
+          }
+        }
+        if (!ok) break;
+      }
+      if (!p.whole_items && lane == 0) p.tile_desc[blockIdx.x] = desc;
       if (!ok) sh.abort_flag = 1;
       // every stage's last load has landed before the block may end
+      const int loaded = static_cast<int>(tiles);
       for (int j = max(loaded - kTileStages, 0); j < loaded; ++j)
         drain(smem_u32(&sh.k_full[j % kTileStages]), (j / kTileStages) & 1);
       for (int j = max(loaded - kValueStages, 0); j < loaded; ++j)
@@ -1032,7 +1169,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto wait = [&](uint64_t& bar, uint32_t parity) {
         if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&bar), parity, abort_flag))) ok = false;
       };
-      auto qk = [&](int j, int w) {
+      auto qk = [&](uint32_t j, int w) {
         const int s = j % kTileStages;
         if (elect_one()) {
           const uint64_t db = smem_desc_sw128(sK + s * kKvBytes);
@@ -1048,40 +1185,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
       };
-      auto pv = [&](int j, int w, int b) {   // half b of the tile's tokens
+      auto pv = [&](uint32_t j, int w, int b, bool add) {   // half b of the tile's tokens
         if (elect_one()) {
           const uint64_t db = smem_desc_sw128_mn(sW + (j & 1) * kV16Bytes + b * kHalf * 128, kKvBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 16 tokens a step: 16 rows of 128 bytes
             umma_f16_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + kHalf * b + 8 * k,
-                        db + 128 * k, kPv, j > 0 || b || k);
-          umma_commit(smem_u32(&sh.o_done[w]));
+                        db + 128 * k, kPv, add || k);
+          umma_commit(smem_u32(&sh.o_done[w][b]));
           if (w == 1 && b == 1) umma_commit(smem_u32(&sh.w_empty[j & 1]));
         }
         __syncwarp();
       };
-      if (nt > 0) {
-        wait(sh.q_full, 0);
-        wait(sh.k_full[0], 0);
-        tc_fence_after();
-        if (ok) qk(0, 0);
-        if (ok) qk(0, 1);
-      }
-      for (int j = 0; ok && j < nt; ++j) {
-        wait(sh.w_full[j & 1], (j >> 1) & 1);
-        for (int w = 0; w < 2; ++w) {
-          for (int b = 0; b < 2; ++b) {
-            wait(sh.p_full[w][b], j & 1);
-            if (!ok) break;
+      for (uint32_t queries = 0; ok; ++items) {
+        const int slot = items & 1;
+        wait(sh.item_full[slot], (items >> 1) & 1);
+        if (!ok || sh.item[slot].b < 0) break;
+        const uint32_t nt = sh.item[slot].hi - sh.item[slot].lo;
+        if (nt > 0) {
+          wait(sh.k_full[tiles % kTileStages], (tiles / kTileStages) & 1);
+          for (int w = 0; w < 2; ++w) {
+            wait(sh.q_full[w], queries & 1);
             tc_fence_after();
-            pv(j, w, b);
+            if (ok) qk(tiles, w);
           }
-          if (!ok) break;
-          if (j + 1 == nt) continue;
-          if (w == 0) wait(sh.k_full[(j + 1) % kTileStages], ((j + 1) / kTileStages) & 1);
-          if (!ok) break;
-          qk(j + 1, w);
+          ++queries;
         }
+        for (uint32_t j = 0; ok && j < nt; ++j, ++tiles) {
+          wait(sh.w_full[tiles & 1], (tiles >> 1) & 1);
+          for (int w = 0; w < 2; ++w) {
+            for (int b = 0; b < 2; ++b) {
+              wait(sh.p_full[w][b], tiles & 1);
+              if (!ok) break;
+              tc_fence_after();
+              pv(tiles, w, b, j > 0 || b);
+            }
+            if (!ok) break;
+            if (j + 1 == nt) continue;
+            if (w == 0) wait(sh.k_full[(tiles + 1) % kTileStages], ((tiles + 1) / kTileStages) & 1);
+            if (!ok) break;
+            qk(tiles + 1, w);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot]));
       }
       if (!ok) {
         sh.abort_flag = 1;
@@ -1099,7 +1246,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // does not silence those.
       const int c = lane & 7, r0 = 4 * (warp - 2) + (lane >> 3);
       bool ok = true;
-      for (int j = 0; j < nt; ++j) {
+      uint32_t nt = 0;   // tiles left of the item
+      for (;; ++tiles, --nt) {
+        while (nt == 0) {
+          __syncwarp();
+          if (items > 0 && lane == 0) mbar_arrive(smem_u32(&sh.item_empty[(items - 1) & 1]));
+          const int slot = items & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
+          if (!ok || sh.item[slot].b < 0) break;
+          nt = sh.item[slot].hi - sh.item[slot].lo;
+          ++items;
+        }
+        if (nt == 0) break;
+        const uint32_t j = tiles;
         const int s = j % kValueStages;
         if (!__all_sync(0xffffffffu,
                         mbar_wait_sleep(smem_u32(&sh.w_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag) &&
@@ -1144,9 +1303,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int w = (warp >> 2) - 1;                 // query tile
     const int r = tid & 127;                       // row of the tile = TMEM lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 (warp mod 4)
-    bool ok = true;
+    const uint32_t o_col = lane_base + kColO + 128 * w;
+    bool ok = true, open = false;
+    float M = 0.0f, Z = 0.0f;
+    // where the open item's row goes: elements into out and lse, or a partial sum's slot
+    int64_t out_at = -1, lse_at = -1;
+    int part = -1;
+    bool any = false;    // the item had tiles
+    // Each round makes the queries of the next item, so that its first products can
+    // run, writes out the item before it, and then works through the next one.
+    while (true) {
+    const int slot = items & 1;
+    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
+    if (!ok) break;
+    const TileItem& x = sh.item[slot];
+    const bool more = x.b >= 0;
+    const int nt = more ? x.hi - x.lo : 0;
     float fac = 0.0f;
-    RowAt at = tile_row(p, x, some, w * kTileRows + r);
+    RowAt at{};
+    if (more) at = tile_row(p, x, w * kTileRows + r);
     if (nt > 0) {
       // The queries as two FP8 terms: a half-warp takes a row, 16 bytes a lane
       // (one thread a row would touch 32 rows with every load), and the lane that
@@ -1179,8 +1354,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[w]));
     }
+    if (open) {
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w][1]), (tiles - 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      float* dst = p.tile_partial + (2 * static_cast<int64_t>(blockIdx.x) + part) * kTilePartialFloats;
+      const int row = w * kTileRows + r;
+      if (part >= 0) {
+        dst[kItemRows * kHeadDim + row] = M;
+        dst[kItemRows * kHeadDim + kItemRows + row] = Z;
+      } else if (lse_at >= 0) {
+        p.lse[lse_at] = row_lse(M, Z);
+      }
+      const float f = row_factor(Z);
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim; c += 32) {
+        float o[32];
+        if (any) {
+          tmem_ld32(o_col + c, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+        }
+        if (part >= 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<float4*>(dst)[(c / 4 + k) * kItemRows + row] =
+                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (out_at >= 0) {
+          uint32_t p2[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p2[k] = pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            reinterpret_cast<uint4*>(p.out + out_at + c)[k] =
+                make_uint4(p2[4 * k], p2[4 * k + 1], p2[4 * k + 2], p2[4 * k + 3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot ^ 1]));
+    }
+    if (!more) break;
+    open = true;
+    any = nt > 0;
+    part = x.begins && x.ends ? -1 : x.begins ? 1 : 0;
+    out_at = at.real ? at.token * p.o_ldt + at.head * p.o_ldh : -1;
+    lse_at = at.real && p.lse ? at.token * p.l_ldt + at.head : -1;
 
     // the positions that the row sees; rows that do not exist never ask for a
     // mask, and what they compute is not stored
@@ -1192,14 +1415,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // the maximum of a row that has seen nothing: any score outgrows it, and its
     // weights, of scores of -inf, are 0
     constexpr float kNoMax = -3e38f;
-    const uint32_t o_col = lane_base + kColO + 128 * w;
-    float M = kNoMax, Z = 0.0f;
+    M = kNoMax;
+    Z = 0.0f;
     // The loop is kept short: unrolled over 128 tokens, softmax ran at half the
     // speed, out of instructions.
 #pragma unroll 1
     for (int u = 0; u < 2 * nt; ++u) {
-      const int j = u >> 1, b = u & 1;
-      const int t0 = (x.lo + j) * kTileTokens + kHalf * b;
+      const int b = u & 1, t0 = (x.lo + (u >> 1)) * kTileTokens + kHalf * b;
+      const uint32_t j = tiles + (u >> 1);
       const uint32_t s_col = lane_base + kColS + 128 * w + kHalf * b;
       if (b == 0) {
         ok = __all_sync(0xffffffffu,
@@ -1244,7 +1467,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (grow) M = top;
         Z *= f;
         if (u > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w]), (u - 1) & 1, abort_flag));
+          // the product before this one: the half ahead, or the last of the tile ahead
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w][b ^ 1]), (j - 1 + b) & 1, abort_flag));
           if (!ok) break;
           tc_fence_after();
           scale_columns(o_col, kHeadDim, f);
@@ -1273,70 +1497,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w][b]));
     }
-    if (ok && nt > 0) {
-      // the last scores followed every product but the last two, which are waited for in turn
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w]), 0, abort_flag) &&
-                                       mbar_wait(smem_u32(&sh.o_done[w]), 1, abort_flag));
-      tc_fence_after();
+    if (!ok) break;
+    tiles += nt;
+    ++items;
     }
     if (!ok) {
       sh.abort_flag = 1;
       if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
-    }
-    if (some && ok) {
-      const bool split = p.splits > 1;
-      float* part_at = p.tile_partial + static_cast<int64_t>(blockIdx.x) * kTilePartialFloats;
-      const int row = w * kTileRows + r;
-      at = tile_row(p, x, some, row);
-      if (split) {
-        part_at[kItemRows * kHeadDim + row] = nt > 0 ? M : kNegInf;
-        part_at[kItemRows * kHeadDim + kItemRows + row] = Z;
-      } else if (at.real && p.lse) {
-        p.lse[at.token * p.l_ldt + at.head] = row_lse(M, Z);
-      }
-      const float f = row_factor(Z);
-      // BF16 rows go through this warp's 8 KB of the queries' memory (every product
-      // has read it), so that a half-warp stores a whole row; 16-byte chunk k of
-      // row r is kept at k ^ (r % 16)
-      const uint32_t stage = sQ + (warp - 4) * 32 * 2 * kHeadDim;
-#pragma unroll 1
-      for (int c = 0; c < kHeadDim; c += 16) {
-        uint32_t o[16];
-        if (nt > 0) {
-          tmem_ld16(o_col + c, o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0u;
-        }
-        float v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]);
-        if (split) {
-          float4* dst = reinterpret_cast<float4*>(part_at + row * kHeadDim + c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else {
-          uint32_t p2[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) p2[k] = pack_bf16x2(v[2 * k] * f, v[2 * k + 1] * f);
-          const int k = c >> 3;
-          sts128(stage + lane * 256 + ((k ^ (lane & 15)) << 4), make_uint4(p2[0], p2[1], p2[2], p2[3]));
-          sts128(stage + lane * 256 + (((k + 1) ^ (lane & 15)) << 4), make_uint4(p2[4], p2[5], p2[6], p2[7]));
-        }
-      }
-      if (!split) {
-        __syncwarp();
-        const int64_t mine = at.real ? at.token * p.o_ldt + at.head * p.o_ldh : -1;
-        const int half = lane >> 4, k = lane & 15;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += 2) {
-          const int from = i + half;
-          const int64_t off = __shfl_sync(0xffffffffu, mine, from);
-          const uint4 v = lds128(stage + from * 256 + ((k ^ (from & 15)) << 4));
-          if (off >= 0) *(reinterpret_cast<uint4*>(p.out + off) + k) = v;
-        }
-      }
     }
   }
   tc_fence_before();
@@ -1347,66 +1514,91 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-// Joins the partial sums of segments that several blocks shared, in block
-// order, and writes the rows of segments that had no unit at all. One block
-// per segment; a segment that one block finished is done.
+// Joins the partial sums of segments and items that several blocks shared, in
+// block order, and writes the rows of segments that had no unit at all. The
+// first `seg_blocks` blocks take a segment each (one that one block finished
+// is done), then come 16 blocks for each block of the tiles kernel: the item
+// that it began and others finished, 128 rows and 16 columns each.
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams p, uint32_t grid,
-                                                                uint32_t max_rb) {
+                                                                uint32_t max_rb, uint32_t seg_blocks) {
   pdl_wait();
+  float m = kNegInf, z = 0.0f, v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  if (blockIdx.x >= seg_blocks) {
+    const uint32_t i = blockIdx.x - seg_blocks, c0 = i >> 4;
+    const int row = 128 * (i & 1) + threadIdx.x, c = 16 * ((i & 15) >> 1);
+    const TileDesc d = p.tile_desc[c0];
+    if (!d.open) return;
+    const uint32_t blocks = (gridDim.x - seg_blocks) / 16;
+    uint32_t c1 = c0 + 1;   // the block that finished it
+    while (c1 + 1 < blocks && !p.tile_desc[c1].closes) ++c1;
+    if (c1 >= blocks) return;
+    TileItem x{};
+    x.h = d.h;
+    x.row0 = d.row0;
+    const TileReq r = tile_req(p, d.b);
+    x.q0 = r.q0, x.n = r.n, x.kv = r.kv;
+    const RowAt at = tile_row(p, x, row);
+    if (!at.real) return;
+    auto part_at = [&](uint32_t k) {
+      return p.tile_partial + static_cast<int64_t>(2 * k + (k == c0)) * kTilePartialFloats;
+    };
+    for (uint32_t k = c0; k <= c1; ++k) m = fmaxf(m, part_at(k)[kItemRows * kHeadDim + row]);
+    for (uint32_t k = c0; k <= c1; ++k) {
+      const float* part = part_at(k);
+      const float f = ex2_approx(part[kItemRows * kHeadDim + row] - m);
+      z = fmaf(part[kItemRows * kHeadDim + kItemRows + row], f, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 o = reinterpret_cast<const float4*>(part)[(c / 4 + e) * kItemRows + row];
+        v[4 * e] = fmaf(o.x, f, v[4 * e]);
+        v[4 * e + 1] = fmaf(o.y, f, v[4 * e + 1]);
+        v[4 * e + 2] = fmaf(o.z, f, v[4 * e + 2]);
+        v[4 * e + 3] = fmaf(o.w, f, v[4 * e + 3]);
+      }
+    }
+    store_row16(p.out + at.token * p.o_ldt + at.head * p.o_ldh + c, v, row_factor(z));
+    if (p.lse && c == 0) p.lse[at.token * p.l_ldt + at.head] = row_lse(m, z);
+    return;
+  }
   const uint32_t per_b = max_rb * p.H;
   const int b = blockIdx.x / per_b;
   const uint32_t rest = blockIdx.x - b * per_b;
   const uint32_t h = rest / max_rb, rb = rest - h * max_rb;
   const ReqUnits r = req_units(p, b);
-  if (rb >= r.nrb) return;
+  if (rb >= r.nrb || static_cast<int64_t>(r.n) * p.G > p.few_rows) return;
   const uint32_t seg = h * r.nrb + rb;
-  const int64_t rows = static_cast<int64_t>(r.n) * p.G;
-  // partial sums: `count` of them, `step` floats apart; M and Z behind the rows
+  // partial sums: `count` of them, M and Z behind the rows. The segment begins
+  // inside the first block's range (its second slot) and before the others'
+  // (their first slot).
   const float* first = nullptr;
-  int64_t step = 0;
-  uint32_t count = 0, part_rows = p.seg_rows, row0 = 0;
-  const bool tiled = rows > p.few_rows;
-  if (tiled) {
-    if (p.splits == 1) return;
-    const uint32_t pairs = static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows);
-    const uint32_t at = rb * p.seg_rows, pair = at / kItemRows;
-    const uint32_t item = __ldg(p.item_base + b) + (pairs - 1 - pair) * p.H + h;
-    first = p.tile_partial + static_cast<int64_t>(item) * p.splits * kTilePartialFloats;
-    step = kTilePartialFloats;
-    count = p.splits;
-    part_rows = kItemRows;
-    row0 = at - pair * kItemRows;
-  } else if (r.nt) {
+  uint32_t count = 0;
+  if (r.nt) {
     const uint64_t U = __ldg(p.schedule + p.B);
     const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.cost(), e = a + r.nt;
     const uint32_t C = used_blocks(U, grid);
     const uint32_t c0 = owner_of(a, U, C), c1 = owner_of(e - 1, U, C);
     if (c0 == c1) return;
-    // the segment begins inside the first block's range (its second slot) and
-    // before the others' (their first slot)
     first = p.partial + static_cast<int64_t>(2 * c0 + 1) * kPartialFloats;
-    step = 2 * kPartialFloats;
     count = c1 - c0 + 1;
   }
   const int row = threadIdx.x >> 3, ch = threadIdx.x & 7;   // 16 columns of a row per thread
   if (row >= p.seg_rows) return;
   const RowAt at = row_at(p, r, h, rb, row);
   if (!at.real) return;
-  float m = kNegInf, z = 0.0f, v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  auto part_at = [&](uint32_t c) { return first + c * step - (!tiled && c ? kPartialFloats : 0); };
-  const int64_t m_at = static_cast<int64_t>(part_rows) * kHeadDim + row0 + row;
+  auto part_at = [&](uint32_t c) { return first + (2 * c - (c ? 1 : 0)) * static_cast<int64_t>(kPartialFloats); };
+  const int64_t m_at = static_cast<int64_t>(p.seg_rows) * kHeadDim + row;
   for (uint32_t c = 0; c < count; ++c) m = fmaxf(m, part_at(c)[m_at]);
   for (uint32_t c = 0; c < count; ++c) {
     const float* part = part_at(c);
     const float mc = part[m_at];
     if (mc == kNegInf) continue;
     const float f = ex2_approx(mc - m);
-    z = fmaf(part[m_at + part_rows], f, z);
+    z = fmaf(part[m_at + p.seg_rows], f, z);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(part + (row0 + row) * kHeadDim + 16 * ch + 4 * i);
+      const float4 x = *reinterpret_cast<const float4*>(part + row * kHeadDim + 16 * ch + 4 * i);
       v[4 * i] = fmaf(x.x, f, v[4 * i]);
       v[4 * i + 1] = fmaf(x.y, f, v[4 * i + 1]);
       v[4 * i + 2] = fmaf(x.z, f, v[4 * i + 2]);
@@ -1442,31 +1634,27 @@ constexpr int32_t kFewRows = 64;
 
 // What the host knows of a call's shape, from upper bounds alone.
 struct Shape {
-  bool tiles;          // some request may have more than kFewRows rows
-  int64_t items;       // at most so many items of the tiles kernel
-  int64_t splits;      // parts of each, before the tokens are looked at
+  bool tiles;   // some request may have more than kFewRows rows
+  bool whole;   // the tiles kernel's blocks take whole items
 };
 Shape shape_of(int64_t B, int64_t T, int64_t max_q, int64_t G, int64_t H, int sms) {
   Shape s{};
   s.tiles = max_q * G > kFewRows;
-  if (!s.tiles) return s;
-  const int64_t rows = (max_q < T ? max_q * (B < T ? B : T) < T ? max_q * B : T : T) * G;
-  const int64_t big = B < rows / (kFewRows + 1) + 1 ? B : rows / (kFewRows + 1) + 1;
-  s.items = (rows / kItemRows + big) * H;
-  s.splits = 2 * s.items <= sms ? sms / s.items : 1;   // few items: share out their tokens
+  const int64_t rows = (max_q < T ? max_q : T) * G;
+  s.whole = s.tiles && B == 1 && (rows + kItemRows - 1) / kItemRows * H >= 4 * sms;
   return s;
 }
 
 struct Workspace {
-  size_t item_base, partial, tile_partial, bytes;   // offsets; the schedule is at 0
+  size_t partial, tile_desc, tile_partial, bytes;   // offsets; the schedule is at 0
 };
 Workspace workspace_of(int64_t B, const Shape& s, int sms) {
   Workspace w{};
-  w.item_base = align256((B + 1) * 8);
-  w.partial = w.item_base + align256(B * 4);
-  w.tile_partial = w.partial + align256(static_cast<size_t>(sms) * kRowsPerSm * 2 * kPartialFloats * 4);
+  w.partial = align256((B + 1) * 8);
+  w.tile_desc = w.partial + align256(static_cast<size_t>(sms) * kRowsPerSm * 2 * kPartialFloats * 4);
+  w.tile_partial = w.tile_desc + align256(sms * sizeof(TileDesc));
   w.bytes = w.tile_partial;
-  if (s.splits > 1) w.bytes += static_cast<size_t>(s.items) * s.splits * kTilePartialFloats * 4;
+  if (s.tiles && !s.whole) w.bytes += static_cast<size_t>(sms) * 2 * kTilePartialFloats * 4;
   return w;
 }
 
@@ -1519,8 +1707,8 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.kv_len = a.kv_len;
   uint8_t* scratch = static_cast<uint8_t*>(a.workspace);
   p.schedule = reinterpret_cast<uint64_t*>(scratch);
-  p.item_base = reinterpret_cast<uint32_t*>(scratch + ws.item_base);
   p.partial = reinterpret_cast<float*>(scratch + ws.partial);
+  p.tile_desc = reinterpret_cast<TileDesc*>(scratch + ws.tile_desc);
   p.tile_partial = reinterpret_cast<float*>(scratch + ws.tile_partial);
   p.q_ldt = a.q_stride_token;
   p.q_ldh = a.q_stride_head;
@@ -1539,19 +1727,17 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.max_blocks = static_cast<int32_t>(a.max_blocks);
   p.window = a.window < 0 ? -1 : a.window;
   p.scale_log2 = a.softmax_scale * kLog2e;
-  // a split has two tiles at least, at the table's full width
-  const int64_t tiles = (a.max_blocks * c.page_size + kTileTokens - 1) / kTileTokens;
-  p.splits = static_cast<int32_t>(shape.splits <= tiles / 2 ? shape.splits : tiles / 2);
-  if (p.splits < 1) p.splits = 1;
+  p.whole_items = shape.whole;
   // one request has only one kernel to go to; of several, each is looked at on the device
   p.few_rows = !shape.tiles ? 0x7FFFFFFF : a.batch > 1 ? kFewRows : 0;
   const int64_t most_rows = a.max_q_len * p.G;
   p.seg_rows = most_rows <= 8 ? 8 : kMaxRows;
   const int64_t max_rb = (most_rows + p.seg_rows - 1) / p.seg_rows;
   const int64_t few_rb = kFewRows / p.seg_rows;
-  const int64_t join_rb = shape.tiles && p.splits == 1 && max_rb > few_rb ? few_rb : max_rb;
-  const int64_t items = shape.items * p.splits, joins = a.batch * H * join_rb;
-  if (items > 0x7FFFFFFF || joins > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
+  const bool rows_kernel = p.few_rows > 0, join_items = shape.tiles && !shape.whole;
+  const int64_t join_rb = shape.tiles && max_rb > few_rb ? few_rb : max_rb;
+  const int64_t segs = rows_kernel ? a.batch * H * join_rb : 0, joins = segs + (join_items ? 16 * sms : 0);
+  if (joins > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
   auto maps = [&](uint32_t rows, CUtensorMap* tk, CUtensorMap* tv) {
     const int r = make_tmap_4d(tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.k_e4m3, kHeadDim, c.page_size, H,
                                c.n_pages, c.k_stride_token, c.k_stride_head, c.k_stride_page,
@@ -1563,7 +1749,6 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   };
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tk, tv;
-  const bool rows_kernel = p.few_rows > 0;
   const unsigned rows_grid = static_cast<unsigned>(sms) * kRowsPerSm;
   if (rows_kernel) {
     rc = maps(c.page_size < kUnit ? c.page_size : kUnit, &tk, &tv);
@@ -1579,13 +1764,13 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
     if (rc != BFP8_OK) return rc;
     rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kv_attention_tiles_kernel), kTileSmem);
     if (rc != BFP8_OK) return rc;
-    rc = launch_dependent(kv_attention_tiles_kernel, static_cast<unsigned>(items), kTileThreads,
+    rc = launch_dependent(kv_attention_tiles_kernel, static_cast<unsigned>(sms), kTileThreads,
                           kTileSmem, st, tk, tv, p);
     if (rc != BFP8_OK) return rc;
   }
-  if (rows_kernel || p.splits > 1) {
+  if (joins) {
     rc = launch_dependent(kv_attention_join_kernel, static_cast<unsigned>(joins), 128, 0, st, p,
-                          rows_grid, static_cast<uint32_t>(join_rb));
+                          rows_grid, static_cast<uint32_t>(join_rb), static_cast<uint32_t>(segs));
     if (rc != BFP8_OK) return rc;
   }
   return check_launch();
