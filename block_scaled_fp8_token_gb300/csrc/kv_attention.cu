@@ -183,6 +183,11 @@ BFP8_DEV void mma_e4m3_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+BFP8_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 BFP8_DEV uint32_t join16(uint16_t lo, uint16_t hi) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
@@ -194,25 +199,26 @@ BFP8_DEV uint32_t join16(uint16_t lo, uint16_t hi) {
 BFP8_DEV int query_exponent(uint32_t amax_bits) {
   return amax_bits ? min(max(11 - (static_cast<int>(amax_bits >> 7) - 127), -110), 110) : 0;
 }
-// Four entries (two BF16 pairs) times `up`: a word of codes of each term.
+// Four entries (two BF16 pairs) times `up`: a word of codes of each term. F16
+// holds every scaled entry down to 2^-26 of the largest exactly, and hi and the
+// difference too.
 BFP8_DEV void query_terms(uint32_t ab, uint32_t cd, float up, uint32_t& hi, uint32_t& lo) {
-  const float f[4] = {__uint_as_float(ab << 16) * up, __uint_as_float(ab & 0xFFFF0000u) * up,
-                      __uint_as_float(cd << 16) * up, __uint_as_float(cd & 0xFFFF0000u) * up};
-  const uint16_t h0 = f32x2_to_e5m2x2(f[0], f[1]), h1 = f32x2_to_e5m2x2(f[2], f[3]);
-  const uint32_t w0 = e5m2x2_to_f16x2(h0), w1 = e5m2x2_to_f16x2(h1);
-  const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
-  const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
-  hi = join16(h0, h1);
-  lo = join16(f32x2_to_e4m3x2(f[0] - g0.x, f[1] - g0.y), f32x2_to_e4m3x2(f[2] - g1.x, f[3] - g1.y));
+  const uint32_t in[2] = {ab, cd};
+  uint16_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = __fmul2_rn(make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xFFFF0000u)),
+                                make_float2(up, up));
+    const uint32_t x = pack_f16x2(f.x, f.y);
+    h[i] = f16x2_to_e5m2x2(x);
+    l[i] = f16x2_to_e4m3x2(sub_f16x2(x, e5m2x2_to_f16x2(h[i])));
+  }
+  hi = join16(h[0], h[1]);
+  lo = join16(l[0], l[1]);
 }
 BFP8_DEV uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-BFP8_DEV uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 BFP8_DEV uint32_t f16_pair(uint32_t word, int half) {
@@ -780,14 +786,15 @@ constexpr int kInfos = kTileStages + 1;                  // see TileShared
 constexpr int kQBytes = kTileRows * kHeadDim;            // one term of one query tile
 constexpr int kKvBytes = kTileTokens * kHeadDim;
 constexpr int kV16Bytes = 2 * kKvBytes;
+constexpr int kOutStage = 32 * 64;                        // a softmax warp's, for 32 columns of BF16
 constexpr int kTileSmem =
-    4 * kQBytes + (kTileStages + kValueStages) * kKvBytes + 2 * kV16Bytes + 1024;
+    4 * kQBytes + (kTileStages + kValueStages) * kKvBytes + 2 * kV16Bytes + 8 * kOutStage + 1024;
 // Queries' rows of an unfinished item: O as [column / 4][row][4], then M, then Z.
 constexpr int kTilePartialFloats = kItemRows * kHeadDim + 2 * kItemRows;
 constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w, O at 256 + 128 w
 // Beginning and ending an item costs about as long as this many tiles, which
 // the schedule counts behind each item's own; a block gets kTileShare at least.
-constexpr uint32_t kTilePad = 2, kTileShare = 4;
+constexpr uint32_t kTilePad = 4, kTileShare = 8;
 
 struct TileReq {
   int32_t q0, n, kv, held;   // first row, new tokens, length, tokens inside the table
@@ -1304,6 +1311,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int r = tid & 127;                       // row of the tile = TMEM lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 (warp mod 4)
     const uint32_t o_col = lane_base + kColO + 128 * w;
+    const uint32_t stage = sW + 2 * kV16Bytes + (warp - 4) * kOutStage;
     bool ok = true, open = false;
     float M = 0.0f, Z = 0.0f;
     // where the open item's row goes: elements into out and lse, or a partial sum's slot
@@ -1385,14 +1393,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int k = 0; k < 8; ++k)
             reinterpret_cast<float4*>(dst)[(c / 4 + k) * kItemRows + row] =
                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else if (out_at >= 0) {
+        } else {
+          // through 2 KB of the warp's own, so that four lanes store a row's 64 bytes;
+          // chunk k of row r is kept at k ^ (r / 2 % 4)
           uint32_t p2[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) p2[k] = pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            reinterpret_cast<uint4*>(p.out + out_at + c)[k] =
-                make_uint4(p2[4 * k], p2[4 * k + 1], p2[4 * k + 2], p2[4 * k + 3]);
+            sts128(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4),
+                   make_uint4(p2[4 * k], p2[4 * k + 1], p2[4 * k + 2], p2[4 * k + 3]));
+          __syncwarp();
+          const int k = lane & 3;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            const int from = i + (lane >> 2);
+            const int64_t off = __shfl_sync(0xffffffffu, out_at, from);
+            const uint4 v = lds128(stage + from * 64 + ((k ^ ((from >> 1) & 3)) << 4));
+            if (off >= 0) *(reinterpret_cast<uint4*>(p.out + off + c) + k) = v;
+          }
         }
       }
       __syncwarp();

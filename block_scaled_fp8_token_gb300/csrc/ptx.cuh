@@ -387,9 +387,19 @@ BFP8_DEV uint16_t f32x2_to_e4m3x2(float a, float b) {
 }
 
 // The same as E5M2, and two E5M2 codes -> two F16 (exact).
-BFP8_DEV uint16_t f32x2_to_e5m2x2(float a, float b) {
+BFP8_DEV uint16_t f16x2_to_e5m2x2(uint32_t v) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+BFP8_DEV uint16_t f16x2_to_e4m3x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+BFP8_DEV uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 BFP8_DEV uint32_t e5m2x2_to_f16x2(uint16_t pair) {
