@@ -441,6 +441,11 @@ BFP8_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read
 BFP8_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Named barrier over a subset of warps (id 0 is __syncthreads).
+// 16 bytes from global to shared memory past the registers; zeros unless `in`.
+BFP8_DEV void cp_async16_zfill(uint32_t to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+BFP8_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 BFP8_DEV void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
