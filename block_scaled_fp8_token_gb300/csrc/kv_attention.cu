@@ -802,7 +802,7 @@ constexpr int kTilePartialFloats = kItemRows * kHeadDim + 2 * kItemRows;
 constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w, O at 256 + 128 w
 // Beginning and ending an item costs about as long as this many tiles, which
 // the schedule counts behind each item's own; a block gets kTileShare at least.
-constexpr uint32_t kTilePad = 4, kTileShare = 8;
+constexpr uint32_t kTilePad = 3, kTileShare = 6;
 
 struct TileReq {
   int32_t q0, n, kv, held;   // first row, new tokens, length, tokens inside the table
@@ -843,7 +843,7 @@ struct TileItem {
 // What the join has to know of a block: its last item, when the block began it and
 // others finish it, and whether its first part finishes another's.
 struct TileDesc {
-  int32_t open, b, h, row0, closes, pad[3];
+  int32_t open, closes, h, row0, q0, n, kv, pad;
 };
 
 // Row `row` of an item.
@@ -1110,7 +1110,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ++items;
         if (x.b < 0) break;
         if (!x.begins && x.ends) desc.closes = 1;
-        if (x.begins && !x.ends) desc.open = 1, desc.b = x.b, desc.h = x.h, desc.row0 = x.row0;
+        if (x.begins && !x.ends) {
+          desc.open = 1;
+          desc.h = x.h, desc.row0 = x.row0, desc.q0 = x.q0, desc.n = x.n, desc.kv = x.kv;
+        }
         const int nt = x.hi - x.lo;
         const int32_t* row = p.table + x.b * p.ld_table;
         auto page_id = [&](int j) {   // lane l < 8: the page of tokens 16 l .. of tile j
@@ -1343,7 +1346,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // (the first 64 columns of a row to its row of hi, the others to that of lo)
       // and replaced row by row, a half-warp each: all of them are in flight at once,
       // and the loop stays small, for instructions that are not in the cache cost
-      // more than the arithmetic (unrolled 16 times: 13,000 clocks, and this 4,000).
+      // more than the arithmetic (unrolled 16 times: 13,000 clocks; this: 6,000, and
+      // 4,000 of them the terms).
       // The lane that owns a row keeps its factor. A negative softmax scale turns the
       // queries round, so that the factor is positive.
       const int64_t mine = at.real ? at.token * p.q_ldt + at.head * p.q_ldh : -1;
@@ -1567,41 +1571,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams p, uint32_t grid,
                                                                 uint32_t max_rb, uint32_t seg_blocks) {
   pdl_wait();
-  float m = kNegInf, z = 0.0f, v[16];
+  // Sums so far at maximum m. Every part's numbers are loaded before the maximum is
+  // known, so that parts' loads overlap.
+  float m = -3e38f, z = 0.0f, v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  auto add = [&](float mc, float zc, const float4 (&x)[4]) {
+    const float top = fmaxf(m, mc), a = ex2_approx(m - top), f = ex2_approx(mc - top);
+    m = top;
+    z = fmaf(zc, f, z * a);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[4 * e] = fmaf(x[e].x, f, v[4 * e] * a);
+      v[4 * e + 1] = fmaf(x[e].y, f, v[4 * e + 1] * a);
+      v[4 * e + 2] = fmaf(x[e].z, f, v[4 * e + 2] * a);
+      v[4 * e + 3] = fmaf(x[e].w, f, v[4 * e + 3] * a);
+    }
+  };
   if (blockIdx.x >= seg_blocks) {
     const uint32_t i = blockIdx.x - seg_blocks, c0 = i >> 4;
     const int row = 128 * (i & 1) + threadIdx.x, c = 16 * ((i & 15) >> 1);
     const TileDesc d = p.tile_desc[c0];
     if (!d.open) return;
     const uint32_t blocks = (gridDim.x - seg_blocks) / 16;
-    uint32_t c1 = c0 + 1;   // the block that finished it
-    while (c1 + 1 < blocks && !p.tile_desc[c1].closes) ++c1;
-    if (c1 >= blocks) return;
     TileItem x{};
-    x.h = d.h;
-    x.row0 = d.row0;
-    const TileReq r = tile_req(p, d.b);
-    x.q0 = r.q0, x.n = r.n, x.kv = r.kv;
+    x.h = d.h, x.row0 = d.row0, x.q0 = d.q0, x.n = d.n, x.kv = d.kv;
     const RowAt at = tile_row(p, x, row);
     if (!at.real) return;
-    auto part_at = [&](uint32_t k) {
-      return p.tile_partial + static_cast<int64_t>(2 * k + (k == c0)) * kTilePartialFloats;
-    };
-    for (uint32_t k = c0; k <= c1; ++k) m = fmaxf(m, part_at(k)[kItemRows * kHeadDim + row]);
-    for (uint32_t k = c0; k <= c1; ++k) {
-      const float* part = part_at(k);
-      const float f = ex2_approx(part[kItemRows * kHeadDim + row] - m);
-      z = fmaf(part[kItemRows * kHeadDim + kItemRows + row], f, z);
+    for (uint32_t k = c0;; ++k) {   // to the block that finished it
+      const float* part = p.tile_partial + static_cast<int64_t>(2 * k + (k == c0)) * kTilePartialFloats;
+      float4 o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 o = reinterpret_cast<const float4*>(part)[(c / 4 + e) * kItemRows + row];
-        v[4 * e] = fmaf(o.x, f, v[4 * e]);
-        v[4 * e + 1] = fmaf(o.y, f, v[4 * e + 1]);
-        v[4 * e + 2] = fmaf(o.z, f, v[4 * e + 2]);
-        v[4 * e + 3] = fmaf(o.w, f, v[4 * e + 3]);
-      }
+      for (int e = 0; e < 4; ++e) o[e] = reinterpret_cast<const float4*>(part)[(c / 4 + e) * kItemRows + row];
+      const bool last = k + 1 >= blocks || (k > c0 && p.tile_desc[k].closes);
+      add(part[kItemRows * kHeadDim + row], part[kItemRows * kHeadDim + kItemRows + row], o);
+      if (last) break;
     }
     store_row16(p.out + at.token * p.o_ldt + at.head * p.o_ldh + c, v, row_factor(z));
     if (p.lse && c == 0) p.lse[at.token * p.l_ldt + at.head] = row_lse(m, z);
@@ -1611,6 +1615,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   const int b = blockIdx.x / per_b;
   const uint32_t rest = blockIdx.x - b * per_b;
   const uint32_t h = rest / max_rb, rb = rest - h * max_rb;
+  const uint64_t U = p.schedule[p.B], unit0 = p.schedule[b];
   const ReqUnits r = req_units(p, b);
   if (rb >= r.nrb || static_cast<int64_t>(r.n) * p.G > p.few_rows) return;
   const uint32_t seg = h * r.nrb + rb;
@@ -1620,8 +1625,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   const float* first = nullptr;
   uint32_t count = 0;
   if (r.nt) {
-    const uint64_t U = __ldg(p.schedule + p.B);
-    const uint64_t a = __ldg(p.schedule + b) + static_cast<uint64_t>(seg) * r.cost(), e = a + r.nt;
+    const uint64_t a = unit0 + static_cast<uint64_t>(seg) * r.cost(), e = a + r.nt;
     const uint32_t C = used_blocks(U, grid);
     const uint32_t c0 = owner_of(a, U, C), c1 = owner_of(e - 1, U, C);
     if (c0 == c1) return;
@@ -1632,23 +1636,14 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   if (row >= p.seg_rows) return;
   const RowAt at = row_at(p, r, h, rb, row);
   if (!at.real) return;
-  auto part_at = [&](uint32_t c) { return first + (2 * c - (c ? 1 : 0)) * static_cast<int64_t>(kPartialFloats); };
   const int64_t m_at = static_cast<int64_t>(p.seg_rows) * kHeadDim + row;
-  for (uint32_t c = 0; c < count; ++c) m = fmaxf(m, part_at(c)[m_at]);
+#pragma unroll 4
   for (uint32_t c = 0; c < count; ++c) {
-    const float* part = part_at(c);
-    const float mc = part[m_at];
-    if (mc == kNegInf) continue;
-    const float f = ex2_approx(mc - m);
-    z = fmaf(part[m_at + p.seg_rows], f, z);
+    const float* part = first + (2 * c - (c ? 1 : 0)) * static_cast<int64_t>(kPartialFloats);
+    float4 x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(part + row * kHeadDim + 16 * ch + 4 * i);
-      v[4 * i] = fmaf(x.x, f, v[4 * i]);
-      v[4 * i + 1] = fmaf(x.y, f, v[4 * i + 1]);
-      v[4 * i + 2] = fmaf(x.z, f, v[4 * i + 2]);
-      v[4 * i + 3] = fmaf(x.w, f, v[4 * i + 3]);
-    }
+    for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float4*>(part + row * kHeadDim + 16 * ch + 4 * e);
+    add(part[m_at], part[m_at + p.seg_rows], x);
   }
   store_row16(p.out + at.token * p.o_ldt + at.head * p.o_ldh + 16 * ch, v, row_factor(z));
   if (p.lse && ch == 0) p.lse[at.token * p.l_ldt + at.head] = row_lse(m, z);
