@@ -1333,7 +1333,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // run, writes out the item before it, and then works through the next one.
     while (true) {
     const int slot = items & 1;
-    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
+    ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
     if (!ok) break;
     const TileItem& x = sh.item[slot];
     const bool more = x.b >= 0;
@@ -1395,7 +1395,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (open) {
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w][1]), (tiles - 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][1]), (tiles - 1) & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
       }
@@ -1475,8 +1475,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t s_col = lane_base + kColS + 128 * w + kHalf * b;
       if (b == 0) {
         ok = __all_sync(0xffffffffu,
-                        mbar_wait(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
-                            mbar_wait(smem_u32(&sh.s_full[w]), j & 1, abort_flag));
+                        mbar_wait_sleep(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
+                            mbar_wait_sleep(smem_u32(&sh.s_full[w]), j & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
       }
@@ -1517,7 +1517,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         Z *= f;
         if (u > 0) {
           // the product before this one: the half ahead, or the last of the tile ahead
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.o_done[w][b ^ 1]), (j - 1 + b) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][b ^ 1]), (j - 1 + b) & 1, abort_flag));
           if (!ok) break;
           tc_fence_after();
           scale_columns(o_col, kHeadDim, f);
