@@ -772,8 +772,8 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 // of 128. S = Q K^T runs on the FP8 tensor cores with the codes of the keys as
 // they lie in memory: a query row goes in as two terms, hi in E5M2 (3 of a
 // BF16's 8 significant bits, and the range) and lo in E4M3 (the rest, exactly),
-// at the cost of one BF16 product and half its operand bytes. O += P V runs on the F16 ones, P rounded to 11 significant
-// bits and the codes of V widened exactly.
+// at the cost of one BF16 product and half its operand bytes. O += P V runs on the
+// F16 ones, P rounded to 11 significant bits and the codes of V widened exactly.
 //   warp 0       loads pages by TMA into a ring of keys and one of values
 //   warp 1       issues the products
 //   warps 2, 3   widen the values' codes to F16, MN-major, in two buffers
@@ -783,6 +783,24 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 // product's A operand, so weights never touch shared memory. O stays in tensor
 // memory and is scaled down only when a row's maximum has outgrown the kept one
 // by 2^10.
+//
+// One block an SM stays for the whole call. The items' tiles are cut into equal
+// contiguous ranges, so that one long chunk does not hold the others up; an item
+// cut by a range's end leaves FP32 partial sums that the join kernel adds. A
+// single prompt with four items an SM or more keeps them whole, in rounds over
+// the blocks of alternating direction, and needs no join. (4096 tokens of 64 heads
+// on 8: 232 us whole, 250 us cut; six chunks behind prefixes of up to 6000 tokens:
+// 49 us cut, 73 us as whole items of blocks that came and went.)
+//
+// What bounds it: 4096 tokens run at 1.19 PFLOP/s, counting the masked half of the
+// diagonal tiles. A pair of tiles takes 3,400 clocks, of which the products need
+// 2,048 (and their operands, with the widening, 2,200 of shared memory): a tile's
+// scores wait for the PV product of the tile before, that for its softmax, and
+// softmax of 64 tokens takes some 900 clocks of latency against 530 of issue. Tried
+// and slower: scores in halves of 64 tokens, so that the next ones are made while
+// softmax is still at work (238; shared memory binds N = 64 products); two threads
+// a row (303); weights taken before the maximum is known (275); two issuing warps
+// (279 when one took 263).
 constexpr int kTileRows = 128, kTileTokens = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kHalf = kTileTokens / 2;
@@ -1100,7 +1118,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       while (true) {
         TileItem x = next_item();
         const int slot = items & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_empty[slot]), ((items >> 1) & 1) ^ 1u, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_empty[slot]),
+                                                     ((items >> 1) & 1) ^ 1u, abort_flag));
         if (!ok) break;
         if (lane == 0) {
           sh.item[slot] = x;
@@ -1270,7 +1289,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           __syncwarp();
           if (items > 0 && lane == 0) mbar_arrive(smem_u32(&sh.item_empty[(items - 1) & 1]));
           const int slot = items & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_full[slot]),
+                                                       (items >> 1) & 1, abort_flag));
           if (!ok || sh.item[slot].b < 0) break;
           nt = sh.item[slot].hi - sh.item[slot].lo;
           ++items;
@@ -1332,223 +1352,223 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // Each round makes the queries of the next item, so that its first products can
     // run, writes out the item before it, and then works through the next one.
     while (true) {
-    const int slot = items & 1;
-    ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
-    if (!ok) break;
-    const TileItem& x = sh.item[slot];
-    const bool more = x.b >= 0;
-    const int nt = more ? x.hi - x.lo : 0;
-    float fac = 0.0f;
-    RowAt at{};
-    if (more) at = tile_row(p, x, w * kTileRows + r);
-    if (nt > 0) {
-      // The queries as two FP8 terms. The BF16 rows are copied to where the terms go
-      // (the first 64 columns of a row to its row of hi, the others to that of lo)
-      // and replaced row by row, a half-warp each: all of them are in flight at once,
-      // and the loop stays small, for instructions that are not in the cache cost
-      // more than the arithmetic (unrolled 16 times: 13,000 clocks; this: 6,000, and
-      // 4,000 of them the terms).
-      // The lane that owns a row keeps its factor. A negative softmax scale turns the
-      // queries round, so that the factor is positive.
-      const int64_t mine = at.real ? at.token * p.q_ldt + at.head * p.q_ldh : -1;
-      const int half = lane >> 4, c = lane & 15;
-      const uint32_t rows_at = sQ + 2 * w * kQBytes + 32 * (warp & 3) * kHeadDim;
+      const int slot = items & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.item_full[slot]), (items >> 1) & 1, abort_flag));
+      if (!ok) break;
+      const TileItem& x = sh.item[slot];
+      const bool more = x.b >= 0;
+      const int nt = more ? x.hi - x.lo : 0;
+      float fac = 0.0f;
+      RowAt at{};
+      if (more) at = tile_row(p, x, w * kTileRows + r);
+      if (nt > 0) {
+        // The queries as two FP8 terms. The BF16 rows are copied to where the terms go
+        // (the first 64 columns of a row to its row of hi, the others to that of lo)
+        // and replaced row by row, a half-warp each: all of them are in flight at once,
+        // and the loop stays small, for instructions that are not in the cache cost
+        // more than the arithmetic (unrolled 16 times: 13,000 clocks; this: 6,000, and
+        // 4,000 of them the terms).
+        // The lane that owns a row keeps its factor. A negative softmax scale turns the
+        // queries round, so that the factor is positive.
+        const int64_t mine = at.real ? at.token * p.q_ldt + at.head * p.q_ldh : -1;
+        const int half = lane >> 4, c = lane & 15;
+        const uint32_t rows_at = sQ + 2 * w * kQBytes + 32 * (warp & 3) * kHeadDim;
 #pragma unroll 4
-      for (int i = half; i < 32; i += 2) {
-        const int64_t off = __shfl_sync(0xffffffffu, mine, i);
-        const __nv_bfloat16* src = p.q + (off >= 0 ? off : 0) + 8 * c;
-        cp_async16_zfill(rows_at + (c >> 3) * kQBytes + i * kHeadDim + (((c & 7) ^ (i & 7)) << 4), src, off >= 0);
-      }
-      cp_async_wait_all();
+        for (int i = half; i < 32; i += 2) {
+          const int64_t off = __shfl_sync(0xffffffffu, mine, i);
+          const __nv_bfloat16* src = p.q + (off >= 0 ? off : 0) + 8 * c;
+          cp_async16_zfill(rows_at + (c >> 3) * kQBytes + i * kHeadDim + (((c & 7) ^ (i & 7)) << 4), src, off >= 0);
+        }
+        cp_async_wait_all();
 #pragma unroll 1
-      for (int i0 = 0; i0 < 32; i0 += 2 * kQueryPairs) {
-        uint4 v[kQueryPairs];
-        int e[kQueryPairs][2];
+        for (int i0 = 0; i0 < 32; i0 += 2 * kQueryPairs) {
+          uint4 v[kQueryPairs];
+          int e[kQueryPairs][2];
 #pragma unroll
-        for (int k = 0; k < kQueryPairs; ++k) {
-          const int i = i0 + 2 * k + half;
-          v[k] = lds128(rows_at + (c >> 3) * kQBytes + i * kHeadDim + (((c & 7) ^ (i & 7)) << 4));
-        }
+          for (int k = 0; k < kQueryPairs; ++k) {
+            const int i = i0 + 2 * k + half;
+            v[k] = lds128(rows_at + (c >> 3) * kQBytes + i * kHeadDim + (((c & 7) ^ (i & 7)) << 4));
+          }
 #pragma unroll
-        for (int k = 0; k < kQueryPairs; ++k) {
-          uint32_t m = max_abs_bf16x2(max_abs_bf16x2(v[k].x, v[k].y), max_abs_bf16x2(v[k].z, v[k].w));
-          m = max(m & 0xFFFFu, m >> 16);
-          e[k][0] = query_exponent(__reduce_max_sync(0xffffffffu, half ? 0u : m));
-          e[k][1] = query_exponent(__reduce_max_sync(0xffffffffu, half ? m : 0u));
-        }
+          for (int k = 0; k < kQueryPairs; ++k) {
+            uint32_t m = max_abs_bf16x2(max_abs_bf16x2(v[k].x, v[k].y), max_abs_bf16x2(v[k].z, v[k].w));
+            m = max(m & 0xFFFFu, m >> 16);
+            e[k][0] = query_exponent(__reduce_max_sync(0xffffffffu, half ? 0u : m));
+            e[k][1] = query_exponent(__reduce_max_sync(0xffffffffu, half ? m : 0u));
+          }
 #pragma unroll
-        for (int k = 0; k < kQueryPairs; ++k) {
-          const int i = i0 + 2 * k + half;
-          if ((lane & ~1) == i0 + 2 * k) fac = exp2_int(-(lane & 1 ? e[k][1] : e[k][0])) * fabsf(p.scale_log2);
-          const float up = copysignf(exp2_int(half ? e[k][1] : e[k][0]), p.scale_log2);
-          uint2 hi, lo;
-          query_terms(v[k].x, v[k].y, up, hi.x, lo.x);
-          query_terms(v[k].z, v[k].w, up, hi.y, lo.y);
-          const uint32_t to = rows_at + i * kHeadDim + (((c >> 1) ^ (i & 7)) << 4) + 8 * (c & 1);
-          sts64(to, hi);   // every lane has its row's 16 bytes: the maximum needed them
-          sts64(to + kQBytes, lo);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[w]));
-    }
-    if (open) {
-      if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][1]), (tiles - 1) & 1, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      float* dst = p.tile_partial + (2 * static_cast<int64_t>(blockIdx.x) + part) * kTilePartialFloats;
-      const int row = w * kTileRows + r;
-      if (part >= 0) {
-        dst[kItemRows * kHeadDim + row] = M;
-        dst[kItemRows * kHeadDim + kItemRows + row] = Z;
-      } else if (lse_at >= 0) {
-        p.lse[lse_at] = row_lse(M, Z);
-      }
-      const float f = row_factor(Z);
-#pragma unroll 1
-      for (int c = 0; c < kHeadDim; c += 32) {
-        float o[32];
-        if (any) {
-          tmem_ld32(o_col + c, o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.0f;
-        }
-        if (part >= 0) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<float4*>(dst)[(c / 4 + k) * kItemRows + row] =
-                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else {
-          // through 2 KB of the warp's own, so that four lanes store a row's 64 bytes;
-          // chunk k of row r is kept at k ^ (r / 2 % 4)
-          uint32_t p2[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) p2[k] = pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            sts128(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4),
-                   make_uint4(p2[4 * k], p2[4 * k + 1], p2[4 * k + 2], p2[4 * k + 3]));
-          __syncwarp();
-          const int k = lane & 3;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const int from = i + (lane >> 2);
-            const int64_t off = __shfl_sync(0xffffffffu, out_at, from);
-            const uint4 v = lds128(stage + from * 64 + ((k ^ ((from >> 1) & 3)) << 4));
-            if (off >= 0) *(reinterpret_cast<uint4*>(p.out + off + c) + k) = v;
+          for (int k = 0; k < kQueryPairs; ++k) {
+            const int i = i0 + 2 * k + half;
+            if ((lane & ~1) == i0 + 2 * k) fac = exp2_int(-(lane & 1 ? e[k][1] : e[k][0])) * fabsf(p.scale_log2);
+            const float up = copysignf(exp2_int(half ? e[k][1] : e[k][0]), p.scale_log2);
+            uint2 hi, lo;
+            query_terms(v[k].x, v[k].y, up, hi.x, lo.x);
+            query_terms(v[k].z, v[k].w, up, hi.y, lo.y);
+            const uint32_t to = rows_at + i * kHeadDim + (((c >> 1) ^ (i & 7)) << 4) + 8 * (c & 1);
+            sts64(to, hi);   // every lane has its row's 16 bytes: the maximum needed them
+            sts64(to + kQBytes, lo);
           }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[w]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot ^ 1]));
-    }
-    if (!more) break;
-    open = true;
-    any = nt > 0;
-    part = x.begins && x.ends ? -1 : x.begins ? 1 : 0;
-    out_at = at.real ? at.token * p.o_ldt + at.head * p.o_ldh : -1;
-    lse_at = at.real && p.lse ? at.token * p.l_ldt + at.head : -1;
-
-    // the positions that the row sees; rows that do not exist never ask for a
-    // mask, and what they compute is not stored
-    const int first = at.real && p.window >= 0 ? max(at.pos - p.window, 0) : 0;
-    const int last = at.real ? at.pos : 0x7FFFFFFE;
-    const int last_warp = __reduce_min_sync(0xffffffffu, last);
-    const int first_warp = __reduce_max_sync(0xffffffffu, first);
-
-    // the maximum of a row that has seen nothing: any score outgrows it, and its
-    // weights, of scores of -inf, are 0
-    constexpr float kNoMax = -3e38f;
-    M = kNoMax;
-    Z = 0.0f;
-    // The loop is kept short: unrolled over 128 tokens, softmax ran at half the
-    // speed, out of instructions.
-#pragma unroll 1
-    for (int u = 0; u < 2 * nt; ++u) {
-      const int b = u & 1, t0 = (x.lo + (u >> 1)) * kTileTokens + kHalf * b;
-      const uint32_t j = tiles + (u >> 1);
-      const uint32_t s_col = lane_base + kColS + 128 * w + kHalf * b;
-      if (b == 0) {
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_sleep(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
-                            mbar_wait_sleep(smem_u32(&sh.s_full[w]), j & 1, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      uint32_t y[64];
-      tmem_ld64_bits(s_col, y);
-      float4 info[4];   // 2^ek, ev, 2^-ev per 16 tokens
-#pragma unroll
-      for (int g = 0; g < 4; ++g) info[g] = sh.scale[j % kInfos][4 * b + g];
-      const uint2 vw = *reinterpret_cast<const uint2*>(&sh.valid[j % kInfos][4 * b]);
-      if ((vw.x & vw.y) != 0xffffffffu || t0 + kHalf - 1 > last_warp || t0 < first_warp) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = t0 + 32 * k;
-          const int hi = min(max(last + 1 - t, 0), 32), lo = min(max(first - t, 0), 32);
-          const uint32_t below = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
-          const uint32_t under = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
-          const uint32_t see = (k ? vw.y : vw.x) & below & ~under;
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (!((see >> c) & 1u)) y[32 * k + c] = 0xFF800000u;   // -inf
-        }
-      }
-      // the maximum of x = y * fac * 2^ek + ev
-      float ck[4], top = kNegInf;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        ck[g] = fmaxf(fac * info[g].x, 1e-37f);
-        auto v = [&](int c) { return __uint_as_float(y[16 * g + c]); };
-        const float m0 = max3(max3(v(0), v(1), v(2)), v(3), v(4));
-        const float m1 = max3(max3(v(5), v(6), v(7)), v(8), v(9));
-        const float m2 = max3(max3(v(10), v(11), v(12)), v(13), max3(v(14), v(15), m0));
-        top = fmaxf(top, fmaf(fmaxf(m1, m2), ck[g], info[g].y));
-      }
-      const bool grow = top > M + kLazy;
-      if (__any_sync(0xffffffffu, grow)) {   // rare but for the first tokens
-        const float f = grow ? exp2_fast(M - top) : 1.0f;
-        if (grow) M = top;
-        Z *= f;
-        if (u > 0) {
-          // the product before this one: the half ahead, or the last of the tile ahead
-          ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][b ^ 1]), (j - 1 + b) & 1, abort_flag));
+      if (open) {
+        if (any) {
+          ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][1]), (tiles - 1) & 1, abort_flag));
           if (!ok) break;
           tc_fence_after();
-          scale_columns(o_col, kHeadDim, f);
         }
-      }
-      const float sub = M - kPBase;
-      uint32_t pw[32];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float cb = info[g].y - sub;
-        const float2 ck2 = make_float2(ck[g], ck[g]), cb2 = make_float2(cb, cb);
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(y[16 * g + 2 * c]),
-                                                   __uint_as_float(y[16 * g + 2 * c + 1])), ck2, cb2);
-          const float2 e = make_float2(exp2_fast(x2.x), exp2_fast(x2.y));
-          sum = __fadd2_rn(sum, e);
-          pw[8 * g + c] = pack_f16x2(e.x, e.y);
+        float* dst = p.tile_partial + (2 * static_cast<int64_t>(blockIdx.x) + part) * kTilePartialFloats;
+        const int row = w * kTileRows + r;
+        if (part >= 0) {
+          dst[kItemRows * kHeadDim + row] = M;
+          dst[kItemRows * kHeadDim + kItemRows + row] = Z;
+        } else if (lse_at >= 0) {
+          p.lse[lse_at] = row_lse(M, Z);
         }
-        Z = fmaf(sum.x + sum.y, info[g].z, Z);
+        const float f = row_factor(Z);
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 32) {
+          float o[32];
+          if (any) {
+            tmem_ld32(o_col + c, o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+          }
+          if (part >= 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              reinterpret_cast<float4*>(dst)[(c / 4 + k) * kItemRows + row] =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else {
+            // through 2 KB of the warp's own, so that four lanes store a row's 64 bytes;
+            // chunk k of row r is kept at k ^ (r / 2 % 4)
+            uint32_t p2[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) p2[k] = pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sts128(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4),
+                     make_uint4(p2[4 * k], p2[4 * k + 1], p2[4 * k + 2], p2[4 * k + 3]));
+            __syncwarp();
+            const int k = lane & 3;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              const int from = i + (lane >> 2);
+              const int64_t off = __shfl_sync(0xffffffffu, out_at, from);
+              const uint4 v = lds128(stage + from * 64 + ((k ^ ((from >> 1) & 3)) << 4));
+              if (off >= 0) *(reinterpret_cast<uint4*>(p.out + off + c) + k) = v;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot ^ 1]));
       }
-      tmem_st32(s_col, pw);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w][b]));
-    }
-    if (!ok) break;
-    tiles += nt;
-    ++items;
+      if (!more) break;
+      open = true;
+      any = nt > 0;
+      part = x.begins && x.ends ? -1 : x.begins ? 1 : 0;
+      out_at = at.real ? at.token * p.o_ldt + at.head * p.o_ldh : -1;
+      lse_at = at.real && p.lse ? at.token * p.l_ldt + at.head : -1;
+
+      // the positions that the row sees; rows that do not exist never ask for a
+      // mask, and what they compute is not stored
+      const int first = at.real && p.window >= 0 ? max(at.pos - p.window, 0) : 0;
+      const int last = at.real ? at.pos : 0x7FFFFFFE;
+      const int last_warp = __reduce_min_sync(0xffffffffu, last);
+      const int first_warp = __reduce_max_sync(0xffffffffu, first);
+
+      // the maximum of a row that has seen nothing: any score outgrows it, and its
+      // weights, of scores of -inf, are 0
+      constexpr float kNoMax = -3e38f;
+      M = kNoMax;
+      Z = 0.0f;
+      // The loop is kept short: unrolled over 128 tokens, softmax ran at half the
+      // speed, out of instructions.
+#pragma unroll 1
+      for (int u = 0; u < 2 * nt; ++u) {
+        const int b = u & 1, t0 = (x.lo + (u >> 1)) * kTileTokens + kHalf * b;
+        const uint32_t j = tiles + (u >> 1);
+        const uint32_t s_col = lane_base + kColS + 128 * w + kHalf * b;
+        if (b == 0) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_sleep(smem_u32(&sh.info_full[j % kInfos]), (j / kInfos) & 1, abort_flag) &&
+                              mbar_wait_sleep(smem_u32(&sh.s_full[w]), j & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        uint32_t y[64];
+        tmem_ld64_bits(s_col, y);
+        float4 info[4];   // 2^ek, ev, 2^-ev per 16 tokens
+#pragma unroll
+        for (int g = 0; g < 4; ++g) info[g] = sh.scale[j % kInfos][4 * b + g];
+        const uint2 vw = *reinterpret_cast<const uint2*>(&sh.valid[j % kInfos][4 * b]);
+        if ((vw.x & vw.y) != 0xffffffffu || t0 + kHalf - 1 > last_warp || t0 < first_warp) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = t0 + 32 * k;
+            const int hi = min(max(last + 1 - t, 0), 32), lo = min(max(first - t, 0), 32);
+            const uint32_t below = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+            const uint32_t under = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
+            const uint32_t see = (k ? vw.y : vw.x) & below & ~under;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((see >> c) & 1u)) y[32 * k + c] = 0xFF800000u;   // -inf
+          }
+        }
+        // the maximum of x = y * fac * 2^ek + ev
+        float ck[4], top = kNegInf;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          ck[g] = fmaxf(fac * info[g].x, 1e-37f);
+          auto v = [&](int c) { return __uint_as_float(y[16 * g + c]); };
+          const float m0 = max3(max3(v(0), v(1), v(2)), v(3), v(4));
+          const float m1 = max3(max3(v(5), v(6), v(7)), v(8), v(9));
+          const float m2 = max3(max3(v(10), v(11), v(12)), v(13), max3(v(14), v(15), m0));
+          top = fmaxf(top, fmaf(fmaxf(m1, m2), ck[g], info[g].y));
+        }
+        const bool grow = top > M + kLazy;
+        if (__any_sync(0xffffffffu, grow)) {   // rare but for the first tokens
+          const float f = grow ? exp2_fast(M - top) : 1.0f;
+          if (grow) M = top;
+          Z *= f;
+          if (u > 0) {
+            // the product before this one: the half ahead, or the last of the tile ahead
+            ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][b ^ 1]), (j - 1 + b) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            scale_columns(o_col, kHeadDim, f);
+          }
+        }
+        const float sub = M - kPBase;
+        uint32_t pw[32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float cb = info[g].y - sub;
+          const float2 ck2 = make_float2(ck[g], ck[g]), cb2 = make_float2(cb, cb);
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(y[16 * g + 2 * c]),
+                                                     __uint_as_float(y[16 * g + 2 * c + 1])), ck2, cb2);
+            const float2 e = make_float2(exp2_fast(x2.x), exp2_fast(x2.y));
+            sum = __fadd2_rn(sum, e);
+            pw[8 * g + c] = pack_f16x2(e.x, e.y);
+          }
+          Z = fmaf(sum.x + sum.y, info[g].z, Z);
+        }
+        tmem_st32(s_col, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w][b]));
+      }
+      if (!ok) break;
+      tiles += nt;
+      ++items;
     }
     if (!ok) {
       sh.abort_flag = 1;

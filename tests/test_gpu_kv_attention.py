@@ -164,6 +164,24 @@ def test_long_cache(bfp8, cuda_device):
     _check(bfp8, s, rows=set(range(0, 70, 9)) | {69})
 
 
+def test_a_prompt_of_many_heads(bfp8, cuda_device):
+    """One prompt with several 256-row items an SM, behind a cached prefix."""
+    rng = np.random.default_rng(31)
+    s = _setup(cuda_device, rng, [(911, 700)], 16, 16, 32)
+    _check(bfp8, s, rows={0, 1, 15, 16, 333, 698, 699})
+
+
+@pytest.mark.parametrize("batch", [390, 900])
+def test_many_requests_with_prompts_among_them(bfp8, cuda_device, batch):
+    """More requests than a block has threads; prompts at the ends and between single tokens."""
+    rng = np.random.default_rng(batch)
+    lengths = [(int(rng.integers(1, 40)), 1) for _ in range(batch)]
+    for b in (0, 130, 131, 383, 384, batch - 1):
+        n = int(rng.integers(33, 90))
+        lengths[b] = (n + int(rng.integers(0, 300)), n)
+    _check(bfp8, _setup(cuda_device, rng, lengths, 1, 2, 16))
+
+
 def test_sharp_and_flat_softmax(bfp8, cuda_device):
     rng = np.random.default_rng(23)
     for gain in (0.0, 30.0):
