@@ -51,6 +51,7 @@ struct AttnParams {
   int32_t seg_rows;          // query rows of a segment of the rows kernel: 8 or 16
   int32_t few_rows;          // requests of at most this many rows of a KV head go to the rows kernel
   int32_t whole_items;       // the tiles kernel's blocks take whole items
+  int32_t tiles_follow;      // it runs right behind the rows kernel
   struct TileDesc* tile_desc;   // [blocks]
   float* tile_partial;       // [blocks][2] of kTilePartialFloats
   float scale_log2;          // softmax scale * log2(e)
@@ -291,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
   if (tid == 0) abort_flag = 0, start_b = 0, start_base = 0;
   mbar_fence_init();
   pdl_wait();
+  // The tiles kernel needs nothing of this one: its blocks start as these end (six
+  // chunks and single tokens: 46 us a pass, against 47).
+  if (p.tiles_follow) pdl_launch_dependents();
 
   // ---- this block's range of units
   uint64_t U = 0;
@@ -790,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 // single prompt with four items an SM or more keeps them whole, in rounds over
 // the blocks of alternating direction, and needs no join. (4096 tokens of 64 heads
 // on 8: 232 us whole, 250 us cut; six chunks behind prefixes of up to 6000 tokens:
-// 49 us cut, 73 us as whole items of blocks that came and went.)
+// 46 us cut, 73 us as whole items of blocks that came and went.)
 //
 // What bounds it: 4096 tokens run at 1.19 PFLOP/s, counting the masked half of the
 // diagonal tiles. A pair of tiles takes 3,400 clocks, of which the products need
@@ -963,7 +967,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
-  pdl_wait();
+  // Behind the rows kernel there is nothing to wait for: its blocks let this one
+  // start only when whatever came before them was complete.
+  if (!p.tiles_follow) pdl_wait();
 
   // ---- this block's range of units: an item has its tiles and kTilePad
   uint64_t range = 0;
@@ -1575,6 +1581,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
     }
   }
+  if (p.tiles_follow) pdl_wait();   // the join waits for this kernel, and so for both
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1788,10 +1795,13 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.window = a.window < 0 ? -1 : a.window;
   p.scale_log2 = a.softmax_scale * kLog2e;
   p.whole_items = shape.whole;
+  p.tiles_follow = shape.tiles && a.batch > 1;
   // one request has only one kernel to go to; of several, each is looked at on the device
   p.few_rows = !shape.tiles ? 0x7FFFFFFF : a.batch > 1 ? kFewRows : 0;
   const int64_t most_rows = a.max_q_len * p.G;
-  p.seg_rows = most_rows <= 8 ? 8 : kMaxRows;
+  // what goes to the rows kernel next to prompts is single tokens for the most part
+  // (six chunks and single tokens, groups of 8: 47 us a pass with 8 rows, 49 with 16)
+  p.seg_rows = most_rows <= 8 || (shape.tiles && p.G <= 8) ? 8 : kMaxRows;
   const int64_t max_rb = (most_rows + p.seg_rows - 1) / p.seg_rows;
   const int64_t few_rb = kFewRows / p.seg_rows;
   const bool rows_kernel = p.few_rows > 0, join_items = shape.tiles && !shape.whole;
