@@ -16,6 +16,7 @@ Modules:
             quantizer, reference dequantization, SiLU(gate)*up glue.
   linear    W8A8 and W8A16 block-scaled projections, member-local scale
             origins, grouped (per-expert) projection, MoE top-k routing.
+  kv        block plan, 8-bit paged KV cache, attention over it, residual norm.
   validate  the weight/scale-grid refusal table.
 
 Parity pins: every function is checked in ``tests/test_oracle_*.py`` against
