@@ -282,6 +282,53 @@ def test_graph_replay_follows_the_lengths(bfp8, cuda_device):
         _check(bfp8, dict(s, lengths=[(n, 1) for n in lengths]), got=(out, lse))
 
 
+def test_graph_replay_of_a_mixed_batch(bfp8, cuda_device):
+    """Prompts and single tokens in one captured call, replayed with other lengths and row counts."""
+    rng = np.random.default_rng(34)
+    s = _setup(cuda_device, rng, [(300, 90), (640, 1), (500, 200)], 2, 4, 32)
+    out, lse = torch.empty_like(s["q"]), torch.empty(s["T"], 8, device=cuda_device)
+    ws = torch.empty(bfp8.bfp8_kv_attention_workspace(3, s["T"], 200, 8, 2), dtype=torch.uint8, device=cuda_device)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bfp8.bfp8_kv_attention(s["q"], s["k"][0], s["v"][0], s["k"][1], s["v"][1], s["table"], s["off"], s["kv"], out,
+                               200, lse=lse, workspace=ws)
+    for lengths in ([(300, 90), (640, 1), (500, 200)], [(299, 1), (20, 20), (499, 3)], [(64, 0), (640, 150), (1, 1)]):
+        s["kv"].copy_(torch.tensor([kv for kv, _ in lengths], dtype=torch.int32))
+        s["off"].copy_(torch.tensor(np.cumsum([0] + [n for _, n in lengths]), dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        assert bfp8.bfp8_device_status() == 0
+        _check(bfp8, dict(s, lengths=lengths), got=(out, lse))
+
+
+def test_appends_and_attention_back_to_back(bfp8, cuda_device):
+    """Each call reads what the append before it wrote, with nothing between them that waits."""
+    rng = np.random.default_rng(35)
+    s = _setup(cuda_device, rng, [(700, 1), (400, 120), (333, 2), (900, 300)], 2, 4, 32)
+    slots = torch.cat([s["table"][b, torch.arange(n, device=cuda_device) // 32].long() * 32
+                       + torch.arange(n, device=cuda_device) % 32 for b, n in enumerate((700, 400, 333, 900))])
+    new = [torch.randn(2, len(slots), 2, D, device=cuda_device).to(torch.bfloat16) for _ in range(6)]
+    cache = (s["k"][0], s["v"][0], s["k"][1], s["v"][1])
+    n = bfp8.bfp8_kv_attention_workspace(4, s["T"], 300, 8, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device=cuda_device)
+
+    def go(i, out, sync):
+        bfp8.bfp8_kv_append(new[i][0], new[i][1], slots, *cache)
+        if sync:
+            torch.cuda.synchronize()
+        bfp8.bfp8_kv_attention(s["q"], *cache, s["table"], s["off"], s["kv"], out, 300, workspace=ws)
+        if sync:
+            torch.cuda.synchronize()
+
+    outs = [[torch.empty_like(s["q"]) for _ in new] for _ in range(3)]
+    for k, sync in enumerate((True, False, False)):
+        for i in range(len(new)):
+            go(i, outs[k][i], sync)
+    torch.cuda.synchronize()
+    for i in range(len(new)):
+        assert torch.equal(outs[0][i], outs[1][i]) and torch.equal(outs[0][i], outs[2][i]), i
+
+
 def test_two_streams_at_once(bfp8, cuda_device):
     rng = np.random.default_rng(31)
     a = _setup(cuda_device, rng, [(3000, 1)] * 3 + [(400, 200)], 2, 4, 64)
