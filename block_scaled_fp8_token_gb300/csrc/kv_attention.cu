@@ -1721,7 +1721,9 @@ Workspace workspace_of(int64_t B, const Shape& s, int sms) {
   w.tile_desc = w.partial + align256(static_cast<size_t>(sms) * kRowsPerSm * 2 * kPartialFloats * 4);
   w.tile_partial = w.tile_desc + align256(sms * sizeof(TileDesc));
   w.bytes = w.tile_partial;
-  if (s.tiles && !s.whole) w.bytes += static_cast<size_t>(sms) * 2 * kTilePartialFloats * 4;
+  // whole items need none of these, but a workspace that holds a long prompt has to
+  // hold its shorter chunks too
+  if (s.tiles) w.bytes += static_cast<size_t>(sms) * 2 * kTilePartialFloats * 4;
   return w;
 }
 

@@ -613,7 +613,8 @@ int bfp8_kv_append(const void* k_bf16, int64_t k_stride_token, int64_t k_stride_
  * a page at or behind kv_len are never used, whatever they hold.  A NaN among
  * the values a request does see may reach every row of that request.
  *   workspace   at least bfp8_kv_attention_workspace() bytes, 256-byte aligned,
- *               contents free; calls sharing it must not overlap.
+ *               contents free (its size grows with every argument, so one for the
+ *               largest call serves the others); calls sharing it must not overlap.
  * Nothing synchronises with the host: the schedule comes from the lengths on
  * the device, so a step can be captured in a CUDA graph and replayed as lengths
  * grow. Results do not depend on what else runs. Errors: INVALID_ARG (null

@@ -370,6 +370,16 @@ def test_cache_past_32_bits(bfp8, cuda_device):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_a_workspace_holds_every_smaller_call(bfp8, cuda_device):
+    """What is enough for a batch, tokens and lengths is enough for fewer of any of them."""
+    sizes = [(b, t, q) for b in (1, 2, 17, 300) for t in (1, 40, 700, 5000) for q in (1, 8, 9, 64, 65, 700, 5000)]
+    need = {x: bfp8.bfp8_kv_attention_workspace(*x, 64, 8) for x in sizes}
+    for a in sizes:
+        for b in sizes:
+            if all(x <= y for x, y in zip(a, b)):
+                assert need[a] <= need[b], (a, b)
+
+
 def test_refusals(bfp8, cuda_device):
     rng = np.random.default_rng(33)
     s = _setup(cuda_device, rng, [(70, 1), (20, 2)], 2, 2, 32)
