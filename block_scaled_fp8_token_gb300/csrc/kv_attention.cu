@@ -796,15 +796,17 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 // on 8: 232 us whole, 250 us cut; six chunks behind prefixes of up to 6000 tokens:
 // 46 us cut, 73 us as whole items of blocks that came and went.)
 //
-// What bounds it: 4096 tokens run at 1.19 PFLOP/s, counting the masked half of the
-// diagonal tiles. A pair of tiles takes 3,400 clocks, of which the products need
-// 2,048 (and their operands, with the widening, 2,200 of shared memory): a tile's
-// scores wait for the PV product of the tile before, that for its softmax, and
-// softmax of 64 tokens takes some 900 clocks of latency against 530 of issue. Tried
-// and slower: scores in halves of 64 tokens, so that the next ones are made while
-// softmax is still at work (238; shared memory binds N = 64 products); two threads
-// a row (303); weights taken before the maximum is known (275); two issuing warps
-// (279 when one took 263).
+// What bounds it: 4096 tokens run at 1.19 PFLOP/s, counting the causal half of the
+// scores. A pair of tiles takes 3,400 clocks, of which the products need 2,048 and
+// their operands, with the widening and the copies, 2,300 of shared memory; a
+// tile's scores wait for the PV product of the tile before, that for its softmax,
+// and softmax of 64 tokens takes 900 to 1,200 clocks of latency. Tried: scores in
+// halves of 64 tokens, made while softmax is still at work (273, and 238 with one
+// thread that waits and issues) or one right behind the other (255), as N = 64
+// products are bound by shared memory; two threads a row (303); weights taken
+// before the maximum is known (275) or with no maximum unless their sum is too
+// large (244); two issuing warps (279 when one took 263). One issuing thread, half
+// the instructions in the widening, P stored in two parts: no change.
 constexpr int kTileRows = 128, kTileTokens = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kHalf = kTileTokens / 2;
