@@ -740,6 +740,9 @@ def _matrix(t, name: str, kind: str, shape, dev: int) -> tuple[int, int]:
     of one row has no row stride: its width stands in.)"""
     if t.shape != shape:
         raise ValueError(f"bfp8: {name} has shape {list(t.shape)}, expected {list(shape)}")
+    st = t.stride()
+    if shape[0] > 1 and st[1] == 1 and t.dtype is _PLAIN[kind] and t.get_device() == dev:
+        return t.data_ptr(), st[0]
     if t.dtype not in _KINDS[kind] or t.get_device() != dev or (shape[1] > 1 and t.stride(1) != 1):
         _dtypes(**{name: (t, kind)})
         _ptr(t)
@@ -751,6 +754,10 @@ def _matrix(t, name: str, kind: str, shape, dev: int) -> tuple[int, int]:
 def _out_matrix(t, name: str, kind: str, rows: int, cols: int, elem_bytes: int,
                 dev: int) -> tuple[int, int]:
     """The same for an output, which may be larger than what is written."""
+    st = t.stride()
+    if (rows > 1 and t.shape == (rows, cols) and st[1] == 1 and t.dtype in _KINDS[kind]
+            and t.get_device() == dev):
+        return t.data_ptr(), st[0]
     if t.dtype not in _KINDS[kind] or t.get_device() != dev or t.shape != (rows, cols):
         _dtypes(**{name: (t, kind)})
         _out(t, name, rows, cols, elem_bytes)
@@ -780,6 +787,16 @@ def _kv_cache(k_cache, v_cache, k_exp, v_exp, dev: int) -> tuple[bytes, int, int
         raise ValueError("bfp8: k_cache and v_cache must be [pages, heads, page size, head dim], "
                          f"got {list(k_cache.shape)} and {list(v_cache.shape)}")
     P, H, page, D = k_cache.shape
+    ks, vs, es = k_cache.stride(), v_cache.stride(), k_exp.stride()
+    # what a cache nearly always is; anything else is looked at piece by piece below
+    e4m3 = _KINDS["e4m3"]
+    if (P > 1 and H > 1 and page > 1 and ks[3] == 1 == vs[3] and k_cache.dtype in e4m3
+            and v_cache.dtype in e4m3 and k_exp.dtype is v_exp.dtype is torch.uint8
+            and k_exp.shape == v_exp.shape == (P, H) and v_exp.stride() == es
+            and k_cache.get_device() == dev == v_cache.get_device()
+            and k_exp.get_device() == dev == v_exp.get_device()):
+        return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
+                              v_exp.data_ptr(), P, page, H, D, *ks[:3], *vs[:3], *es), H, D
     lone = 128 * page * H   # the stride of a dimension of one element, which is never stepped along
     flat = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS)
     const int64_t t0 = t;
     t += n;
     if (inside) continue;   // the run began in an earlier window
-    // `first` and `step`: this warp's rows are first, first + 2, ... in groups of 16
+    // a long run is shared by the team, 16 rows a warp from `first` on
     const bool together = WARPS > 1 && n > kRowsInRegs;
     if (WARPS > 1 && !together) {
       const bool mine = turn == warp;
