@@ -87,11 +87,16 @@ constexpr int kPartialFloats = kMaxRows * (kHeadDim + 2);    // O, then M, then 
 // Ending a segment costs a block about as long as this many units, which the
 // schedule counts behind each segment's own.
 constexpr uint32_t kPadUnits = 8;
-// P is kept at 2^4 times the weight and the maximum moves only when a score
-// passes it by 2^10, so F16 holds P up to 2^14 and, to full precision, down to
-// 2^-18 of the maximum.
+// P is 2^(score - M), and M is taken 4 below the largest score and moves only when
+// a score passes it by more than 14, so F16 holds P up to 2^14 and, to full
+// precision, down to 2^-18 of the largest weight. Both steps are on M as it was
+// rounded, not on the score it came from: at scores of 2^26 and more, where
+// FP32's steps are 8 and up, M is a step away from what was meant, and the
+// weights are within bounds all the same.
 constexpr float kPBase = 4.0f;
-constexpr float kLazy = 10.0f;
+constexpr float kReach = 14.0f;
+// M of a row that has seen nothing: any score passes it.
+constexpr float kNoMax = -3.40282347e38f;
 
 struct ReqUnits {
   int32_t q0, n, kv, lo;   // first row, new tokens, length, first unit
@@ -251,10 +256,10 @@ BFP8_DEV RowAt row_at(const AttnParams& p, const ReqUnits& r, uint32_t h, uint32
   return a;
 }
 
-// out = O / Z and lse, from sums at maximum M; a row that saw nothing gives 0 and -inf.
+// out = O / Z and lse, from sums of 2^(score - M); a row that saw nothing gives 0 and -inf.
 BFP8_DEV float row_factor(float Z) { return Z == 0.0f ? 0.0f : __frcp_rn(Z); }
 BFP8_DEV float row_lse(float M, float Z) {
-  return Z == 0.0f ? kNegInf : kLn2 * (M - kPBase + log2f(Z));
+  return Z == 0.0f ? kNegInf : kLn2 * (M + log2f(Z));
 }
 BFP8_DEV uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
           mx[nb][j] = m;
-          grow |= m > M[nb][j] + kLazy;   // from -inf: any score
+          grow |= m - M[nb][j] > kReach;   // from -inf: any score
         }
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -615,9 +620,10 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
           float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const bool up = mx[nb][j] > M[nb][j] + kLazy;
-            f[j] = !up ? 1.0f : M[nb][j] == kNegInf ? 0.0f : ex2_approx(M[nb][j] - mx[nb][j]);
-            if (up) M[nb][j] = mx[nb][j];
+            const bool up = mx[nb][j] - M[nb][j] > kReach;
+            const float to = mx[nb][j] - kPBase;
+            f[j] = !up ? 1.0f : M[nb][j] == kNegInf ? 0.0f : ex2_approx(M[nb][j] - to);
+            if (up) M[nb][j] = to;
             Z[nb][j] *= f[j];
           }
 #pragma unroll
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
       for (int nb = 0; nb < NB; ++nb) {
         float sub[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sub[j] = M[nb][j] == kNegInf ? 0.0f : M[nb][j] - kPBase;
+        for (int j = 0; j < 2; ++j) sub[j] = M[nb][j] == kNegInf ? 0.0f : M[nb][j];
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
 #pragma unroll
@@ -785,8 +791,12 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 // While one tile's softmax runs, the tensor cores work on the other's. S is
 // FP32 in tensor memory; P replaces it there, 64 tokens at a time, and is the PV
 // product's A operand, so weights never touch shared memory. O stays in tensor
-// memory and is scaled down only when a row's maximum has outgrown the kept one
-// by 2^10.
+// memory and is scaled down only when a row's largest score has outgrown M.
+// A weight's exponent is one fused step, y 2^ek + (ev - M), from a score that was
+// never rounded, while M comes from one that was. That difference, half a step of
+// the largest score, must stay small against kReach: from kBigScore on, where a
+// step is 1/2, a row rounds its scores first (in pairs, for the registers: 238 us a
+// pass of 4096 tokens, with or without this; one at a time it cost 8 more).
 //
 // One block an SM stays for the whole call. The items' tiles are cut into equal
 // contiguous ranges, so that one long chunk does not hold the others up; an item
@@ -827,6 +837,8 @@ constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w, O at 256 +
 // Beginning and ending an item costs about as long as this many tiles, which
 // the schedule counts behind each item's own; a block gets kTileShare at least.
 constexpr uint32_t kTilePad = 3, kTileShare = 6;
+
+constexpr float kBigScore = 4194304.0f;   // 2^22
 
 struct TileReq {
   int32_t q0, n, kv, held;   // first row, new tokens, length, tokens inside the table
@@ -1489,10 +1501,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int last_warp = __reduce_min_sync(0xffffffffu, last);
       const int first_warp = __reduce_max_sync(0xffffffffu, first);
 
-      // the maximum of a row that has seen nothing: any score outgrows it, and its
-      // weights, of scores of -inf, are 0
-      constexpr float kNoMax = -3e38f;
-      M = kNoMax;
+      M = kNoMax;   // weights of scores of -inf are 0
       Z = 0.0f;
       // The loop is kept short: unrolled over 128 tokens, softmax ran at half the
       // speed, out of instructions.
@@ -1538,11 +1547,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const float m2 = max3(max3(v(10), v(11), v(12)), v(13), max3(v(14), v(15), m0));
           top = fmaxf(top, fmaf(fmaxf(m1, m2), ck[g], info[g].y));
         }
-        const bool grow = top > M + kLazy;
-        if (__any_sync(0xffffffffu, grow)) {   // rare but for the first tokens
-          const float f = grow ? exp2_fast(M - top) : 1.0f;
-          if (grow) M = top;
+        const bool grow = top - M > kReach;
+        const bool big = fabsf(top) >= kBigScore && top > kNegInf;
+        if (__any_sync(0xffffffffu, grow || big)) {   // rare but for the first tokens
+          const float to = top - kPBase, f = grow ? exp2_fast(M - to) : 1.0f;
+          if (grow) M = to;
           Z *= f;
+          if (big) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+#pragma unroll
+              for (int c = 16 * g; c < 16 * g + 16; c += 2) {
+                const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])),
+                                             make_float2(ck[g], ck[g]), make_float2(info[g].y, info[g].y));
+                y[c] = __float_as_uint(x2.x), y[c + 1] = __float_as_uint(x2.y);
+              }
+              ck[g] = 1.0f;
+              info[g].y = 0.0f;
+            }
+          }
           if (u > 0) {
             // the product before this one: the half ahead, or the last of the tile ahead
             ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sh.o_done[w][b ^ 1]), (j - 1 + b) & 1, abort_flag));
@@ -1551,11 +1574,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             scale_columns(o_col, kHeadDim, f);
           }
         }
-        const float sub = M - kPBase;
         uint32_t pw[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float cb = info[g].y - sub;
+          const float cb = info[g].y - M;
           const float2 ck2 = make_float2(ck[g], ck[g]), cb2 = make_float2(cb, cb);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -1602,7 +1624,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   pdl_wait();
   // Sums so far at maximum m. Every part's numbers are loaded before the maximum is
   // known, so that parts' loads overlap.
-  float m = -3e38f, z = 0.0f, v[16];
+  float m = kNoMax, z = 0.0f, v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
   auto add = [&](float mc, float zc, const float4 (&x)[4]) {

@@ -1,0 +1,86 @@
+"""bfp8_kv_attention at the ends of its range: scores far past what a softmax resolves,
+queries that are infinite or nearly so, what lies behind a window, and limits that
+meet 32 bits.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as KV
+from test_gpu_kv_attention import D, _check, _run, _setup
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(s):
+    """(token, head, keys that it sees, values that it sees) of every row, in float64."""
+    q, (kd, vd), G = s["q"].double().cpu().numpy(), s["deq"], s["G"]
+    table, off = s["table"].cpu().numpy(), s["off"].cpu().numpy()
+    page = kd.shape[2]
+    for b, (kv, n) in enumerate(s["lengths"]):
+        pages = table[b, :-(-kv // page)]
+        for h in range(kd.shape[1]):
+            k, v = (x[pages, h].reshape(-1, D)[:kv] for x in (kd, vd))
+            for t in range(off[b], off[b + 1]):
+                end = kv - n + (t - off[b]) + 1
+                for g in range(G):
+                    yield t, h * G + g, q[t, h * G + g], k[:end], v[:end]
+
+
+BIG = [[(300, 1), (64, 2)], [(300, 200)], [(260, 1), (400, 200), (70, 70)]]   # few rows; a prompt; both
+
+
+@pytest.mark.parametrize("lengths", BIG)
+@pytest.mark.parametrize("ek", [12, 16, 18, 19, 20, 21, 22, 24, 28, 34, 40])
+def test_large_scores_find_the_largest(bfp8, cuda_device, lengths, ek):
+    """Keys with large scales: scores of 2^(8 + ek), whose float32 steps pass the softmax's range. A
+    row's score is off by FP32's rounding of its products' sum, less than 2^-16 of the sum of their
+    sizes; where the largest score leads by more than twice that and by 30, the output is its value (a
+    weight's and BF16's rounding apart) and lse the score."""
+    rng = np.random.default_rng(ek)
+    s = _setup(cuda_device, rng, lengths, 2, 4, 32)
+    s["k"][1].fill_(127 + ek)
+    s["deq"] = [KV.dequantize(c[0].cpu().numpy(), c[1].cpu().numpy()) for c in (s["k"], s["v"])]
+    out, lse = (x.double().cpu().numpy() for x in _run(bfp8, s))
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    seen = 0
+    for t, h, q, k, v in _rows(s):
+        z = k @ q * D ** -0.5
+        off = 2.0 ** -16 * (np.abs(k) @ np.abs(q)).max() * D ** -0.5
+        best = int(z.argmax())
+        assert abs(lse[t, h] - z[best]) <= off + np.log(len(z)), (t, h)
+        if len(z) > 1 and z[best] - np.partition(z, -2)[-2] < 2 * off + 30:
+            continue
+        seen += 1
+        assert np.all(np.abs(out[t, h] - v[best]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v[best])), (t, h)
+    assert seen > 0
+
+
+@pytest.mark.parametrize("lengths", BIG + [[(4100, 1)] * 40])
+@pytest.mark.parametrize("ek", [10, 13, 14, 15, 16, 17, 18, 19, 20, 21, 22, 26, 40])
+def test_large_scores_a_step_apart(bfp8, cuda_device, lengths, ek):
+    """Scores of 2^(8 + ek) in log2 units that go up and down by a float32 step every 128 tokens. All
+    tokens hold the same value, so whatever the weights, the output is that value; and lse is the
+    score, to its rounding and the number of tokens."""
+    rng = np.random.default_rng(ek)
+    s = _setup(cuda_device, rng, lengths, 1, 4, 32)
+    P, _, page, _ = s["deq"][0].shape
+    value = rng.integers(0x20, 0x60, D).astype(np.uint8)
+    codes = np.zeros((2, P, 1, page, D), np.uint8)
+    codes[0, ..., 0] = 0x78                                  # 256
+    codes[1] = value
+    table = s["table"].cpu().numpy()
+    for b, (kv, _) in enumerate(lengths):
+        for j in range(-(-kv // page)):                      # 0.25, then 0.5: one step, then two
+            codes[0, table[b, j], 0, :, 1] = 0x30 if j * page // 128 % 2 else 0x28
+    for x, c, e in (("k", codes[0], 127 + ek), ("v", codes[1], 127)):
+        s[x][0].copy_(torch.from_numpy(c))
+        s[x][1].fill_(e)
+    s["q"].zero_()
+    s["q"][..., 0], s["q"][..., 1] = 1.0, 2.0 ** -13
+    out, lse = (x.double().cpu().numpy() for x in _run(bfp8, s, scale=float(np.float32(np.log(2)))))
+    want = KV.dequantize(value[None, None, None], np.full((1, 1), 127, np.uint8))[0, 0, 0]
+    assert np.all(np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want))
+    x = np.log(2) * 2.0 ** (8 + ek)
+    assert np.all(np.abs(lse - x) <= 2.0 ** -16 * x + np.log(4100))
