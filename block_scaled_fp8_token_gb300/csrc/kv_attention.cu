@@ -201,9 +201,10 @@ BFP8_DEV uint32_t join16(uint16_t lo, uint16_t hi) {
 // in [2^11, 2^12). An entry of 2^e .. 2^(e+1) is a multiple of 2^(e-7) (a BF16
 // has 8 significant bits); hi, E5M2, keeps 3 bits of it, so the rest is at most
 // 16 of those steps, which E4M3's 4 bits hold, and 2^8 at most. hi + lo is exact
-// for entries down to 2^-13 of the largest; below, it is within 2^-21 of it.
+// for entries down to 2^-13 of the largest; below, it is within 2^-21 of it. (Rows
+// below 2^-99 stay short of 2^11: at such sizes no score is of any weight.)
 BFP8_DEV int query_exponent(uint32_t amax_bits) {
-  return amax_bits ? min(max(11 - (static_cast<int>(amax_bits >> 7) - 127), -110), 110) : 0;
+  return amax_bits ? min(11 - (static_cast<int>(amax_bits >> 7) - 127), 110) : 0;
 }
 // Largest |x| of each half, as BF16 bits with their sign cleared (a NaN stays one
 // only where both operands are).
@@ -214,7 +215,8 @@ BFP8_DEV uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 }
 // Four entries (two BF16 pairs) times `up`: a word of codes of each term. F16
 // holds every scaled entry down to 2^-26 of the largest exactly, and hi and the
-// difference too.
+// difference too. FP8 conversions saturate; an infinite entry's difference takes a
+// NaN, x * 0, so that its row's scores are NaN.
 BFP8_DEV void query_terms(uint32_t ab, uint32_t cd, float up, uint32_t& hi, uint32_t& lo) {
   const uint32_t in[2] = {ab, cd};
   uint16_t h[2], l[2];
@@ -224,7 +226,7 @@ BFP8_DEV void query_terms(uint32_t ab, uint32_t cd, float up, uint32_t& hi, uint
                                 make_float2(up, up));
     const uint32_t x = pack_f16x2(f.x, f.y);
     h[i] = f16x2_to_e5m2x2(x);
-    l[i] = f16x2_to_e4m3x2(sub_f16x2(x, e5m2x2_to_f16x2(h[i])));
+    l[i] = f16x2_to_e4m3x2(fma_f16x2(x, 0u, sub_f16x2(x, e5m2x2_to_f16x2(h[i]))));
   }
   hi = join16(h[0], h[1]);
   lo = join16(l[0], l[1]);

@@ -84,3 +84,33 @@ def test_large_scores_a_step_apart(bfp8, cuda_device, lengths, ek):
     assert np.all(np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want))
     x = np.log(2) * 2.0 ** (8 + ek)
     assert np.all(np.abs(lse - x) <= 2.0 ** -16 * x + np.log(4100))
+
+
+@pytest.mark.parametrize("lengths", BIG)
+def test_infinite_queries_give_nan(bfp8, cuda_device, lengths):
+    """An infinity among a row's queries makes its scores infinite, of either sign or NaN: the row is
+    NaN, and no other is."""
+    rng = np.random.default_rng(41)
+    s = _setup(cuda_device, rng, lengths, 2, 4, 32)
+    bad = [(0, 1, 5, np.inf), (0, 6, 127, -np.inf), (s["T"] - 1, 3, 64, np.inf), (s["T"] // 2, 0, 0, -np.inf)]
+    want = torch.zeros(s["T"], 8, dtype=torch.bool)
+    for t, h, d, x in bad:
+        s["q"][t, h, d] = x
+        want[t, h] = True
+    s["q"][s["T"] - 1, 5] = float("inf")
+    want[s["T"] - 1, 5] = True
+    out, lse = _run(bfp8, s)
+    nan = torch.isnan(out.float()).cpu()
+    assert torch.equal(nan.all(2), want) and torch.equal(nan.any(2), want) and torch.equal(torch.isnan(lse).cpu(), want)
+
+
+@pytest.mark.parametrize("lengths", BIG)
+@pytest.mark.parametrize("top", [2.0 ** 126, 3.0e38, 2.0 ** 127, 2.0 ** -90])
+def test_queries_near_the_ends_of_their_range(bfp8, cuda_device, lengths, top):
+    """The largest finite queries, under a scale that brings their scores back, and very small ones."""
+    rng = np.random.default_rng(42)
+    s = _setup(cuda_device, rng, lengths, 2, 4, 32)
+    q = s["q"].float()
+    s["q"] = (q / q.abs().amax(2, keepdim=True) * top).to(torch.bfloat16)
+    assert bool(torch.isfinite(s["q"]).all())
+    _check(bfp8, s, scale=0.5 / top)
