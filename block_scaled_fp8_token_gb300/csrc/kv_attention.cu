@@ -99,7 +99,8 @@ constexpr float kReach = 14.0f;
 constexpr float kNoMax = -3.40282347e38f;
 
 struct ReqUnits {
-  int32_t q0, n, kv, lo;   // first row, new tokens, length, first unit
+  int32_t q0, n, kv;       // first row, new tokens, length
+  int32_t first, lo;       // first token that any row sees, and its unit
   uint32_t nt, nseg, nrb;  // units of a segment, segments, segments of a head
   BFP8_DEV uint32_t cost() const { return nt ? nt + kPadUnits : 0; }   // a segment's, in units
 };
@@ -111,9 +112,10 @@ BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   r.kv = max(__ldg(p.kv_len + b), 0);
   const int64_t held = min(static_cast<int64_t>(r.kv),
                            static_cast<int64_t>(p.max_blocks) << p.page_shift);
-  int64_t lo = 0;
-  if (p.window >= 0) lo = max(static_cast<int64_t>(r.kv) - r.n - p.window, static_cast<int64_t>(0));
-  r.lo = static_cast<int32_t>(lo / kUnit);
+  r.first = 0;
+  if (p.window >= 0)
+    r.first = static_cast<int32_t>(max(static_cast<int64_t>(r.kv) - r.n - p.window, static_cast<int64_t>(0)));
+  r.lo = r.first / kUnit;
   const int64_t hi = (held + kUnit - 1) / kUnit;
   r.nt = r.n > 0 && hi > r.lo ? static_cast<uint32_t>(hi - r.lo) : 0u;
   const int64_t rows = static_cast<int64_t>(r.n) * p.G;
@@ -418,7 +420,9 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
     pending = -1;
   };
   auto issue = [&](const int s) {
-    const bool ok0 = id0 >= 0 && id0 < p.n_pages, ok1 = two && id1 >= 0 && id1 < p.n_pages;
+    // a page that ends ahead of the first token seen is as good as missing
+    const int32_t ahead = ps.r.first - pt0;   // less than 32: the unit holds that token or follows it
+    const bool ok0 = id0 >= 0 && id0 < p.n_pages && ahead < box, ok1 = two && id1 >= 0 && id1 < p.n_pages;
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * s, dst = stage0 + s * kStageBytes;
       const uint32_t bytes = box * kHeadDim;
@@ -434,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
     }
     const int32_t left = p_held - pt0;
     valid_next = left >= 32 ? 0xffffffffu : (1u << left) - 1u;   // left >= 1
+    if (ahead > 0) valid_next &= 0xffffffffu << ahead;
     valid_next &= two ? (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u) : (ok0 ? 0xffffffffu : 0u);
     k0 = k1 = v0 = v1 = 127u;
     if (ok0) {
@@ -661,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
           // the tokens of fragment columns 2c, 2c + 1, 2c + 8, 2c + 9
           const int tok = 16 * mb + 8 * (i >> 1) + ((2 * c + (i & 1)) ^ ((i & 1) << 2));
           v[i] = lds128(vb + tok * kHeadDim + ((g ^ (tok & 7)) << 4));
-          // rows never written may hold NaN codes: 0 * NaN would reach every column
+          // rows never written, or left to others behind the window, may hold NaN codes:
+          // 0 * NaN would reach every column
           if (masked && !((valid >> tok) & 1u)) v[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
@@ -858,14 +864,18 @@ BFP8_DEV TileReq tile_req(const AttnParams& p, int b) {
   r.pairs = rows > p.few_rows ? static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows) : 0u;
   return r;
 }
+// The first token that a row of pair `q` sees.
+BFP8_DEV int pair_first(const AttnParams& p, const TileReq& r, uint32_t q) {
+  const int pos0 = r.kv - r.n + static_cast<int>(q * kItemRows / p.G);
+  return p.window >= 0 ? max(pos0 - p.window, 0) : 0;
+}
 // The tiles of tokens that the rows of pair `q` see: [x, y).
 BFP8_DEV int2 pair_tiles(const AttnParams& p, const TileReq& r, uint32_t q) {
   const uint32_t row0 = q * kItemRows, rows = static_cast<uint32_t>(r.n) * p.G;
   const uint32_t last = min(rows, row0 + kItemRows) - 1;
-  const int pos0 = r.kv - r.n + static_cast<int>(row0 / p.G);
   const int pos1 = r.kv - r.n + static_cast<int>(last / p.G);
   const int end = min(pos1 + 1, r.held);
-  const int begin = p.window >= 0 ? max(pos0 - p.window, 0) : 0;
+  const int begin = pair_first(p, r, q);
   const int lo = begin / kTileTokens;
   return make_int2(lo, end > begin ? (end + kTileTokens - 1) / kTileTokens : lo);
 }
@@ -875,6 +885,7 @@ struct TileItem {
   int32_t b, h, q0, n, kv, held;   // b < 0: there is no more
   int32_t row0;                    // first row of the item in its request
   int32_t lo, hi;                  // tiles of tokens
+  int32_t first;                   // first token that any of its rows sees
   int32_t begins, ends;            // holds the item's first tile, its last
 };
 
@@ -1130,6 +1141,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           x.row0 = pair * kItemRows;
           x.lo = t.x + begin;
           x.hi = t.x + min(end, nt);
+          x.first = pair_first(p, r, pair);
           x.begins = begin == 0;
           x.ends = end >= nt;
           return x;
@@ -1175,7 +1187,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             break;
           }
           const int t = (x.lo + j) * kTileTokens + 16 * lane;
-          const bool there = lane < 8 && id >= 0 && id < p.n_pages;
+          // a page that ends ahead of the first token seen is as good as missing: it may
+          // be another request's by now
+          const bool there = lane < 8 && id >= 0 && id < p.n_pages && (t | (page - 1)) >= x.first;
           const bool leads = there && (t & (page - 1)) == 0;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, leads));
           if (lane == 0) {
@@ -1197,9 +1211,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           id = page_id(j + 1);
           if (lane < 8) {
             const int left_here = there ? min(x.held - t, 16) : 0;
+            const int unseen = min(max(x.first - t, 0), 16);
             sh.scale[tiles % kInfos][lane] = make_float4(exp2_int(ek - 127), static_cast<float>(ev - 127),
                                                          exp2_int(127 - ev), 0.0f);
-            sh.valid[tiles % kInfos][lane] = static_cast<uint16_t>((1u << left_here) - 1u);
+            sh.valid[tiles % kInfos][lane] = static_cast<uint16_t>(((1u << left_here) - 1u) & (0xffffu << unseen));
           }
           __syncwarp();
           if (lane == 0) {

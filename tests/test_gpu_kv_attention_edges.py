@@ -114,3 +114,25 @@ def test_queries_near_the_ends_of_their_range(bfp8, cuda_device, lengths, top):
     s["q"] = (q / q.abs().amax(2, keepdim=True) * top).to(torch.bfloat16)
     assert bool(torch.isfinite(s["q"]).all())
     _check(bfp8, s, scale=0.5 / top)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("lengths", [[(500, 1), (700, 3), (131, 2), (1000, 1)], [(900, 200)],
+                                     [(600, 200), (500, 1), (333, 64), (90, 90), (777, 130)]])
+def test_what_lies_behind_the_window_is_never_used(bfp8, cuda_device, lengths, page):
+    """Pages behind the window may have gone to other requests: their rows may hold NaN codes, their
+    scale bytes anything, and so may the rows of a page ahead of the first that is seen."""
+    rng = np.random.default_rng(page)
+    window = 100
+    s = _setup(cuda_device, rng, lengths, 2, 4, page)
+    table = s["table"].cpu().numpy()
+    for b, (kv, n) in enumerate(lengths):
+        first = max(kv - n - window, 0)
+        for i in range(first):
+            for x in ("k", "v"):
+                s[x][0][int(table[b, i // page]), :, i % page] = 0x7F
+        for j in range(first // page):
+            for x, e in (("k", 255), ("v", 0 if j % 2 else 255)):
+                s[x][1][int(table[b, j])] = e
+    _check(bfp8, s, window)
+    assert any(kv - n > window + page for kv, n in lengths)
