@@ -98,6 +98,12 @@ constexpr float kReach = 14.0f;
 // M of a row that has seen nothing: any score passes it.
 constexpr float kNoMax = -3.40282347e38f;
 
+// The first position that a row at `pos` sees; from a position below 0, which sees
+// nothing, a large window would go past 32 bits.
+BFP8_DEV int window_begin(const AttnParams& p, int pos) {
+  return p.window >= 0 ? max(max(pos, 0) - p.window, 0) : 0;
+}
+
 struct ReqUnits {
   int32_t q0, n, kv;       // first row, new tokens, length
   int32_t first, lo;       // first token that any row sees, and its unit
@@ -112,9 +118,7 @@ BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   r.kv = max(__ldg(p.kv_len + b), 0);
   const int64_t held = min(static_cast<int64_t>(r.kv),
                            static_cast<int64_t>(p.max_blocks) << p.page_shift);
-  r.first = 0;
-  if (p.window >= 0)
-    r.first = static_cast<int32_t>(max(static_cast<int64_t>(r.kv) - r.n - p.window, static_cast<int64_t>(0)));
+  r.first = window_begin(p, r.kv - r.n);
   r.lo = r.first / kUnit;
   const int64_t hi = (held + kUnit - 1) / kUnit;
   r.nt = r.n > 0 && hi > r.lo ? static_cast<uint32_t>(hi - r.lo) : 0u;
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
         fac[nb][j] = __shfl_sync(0xffffffffu, f, (2 * c + j) * 4);
         const RowAt r = row_at(p, cs.r, cs.h, rb, 8 * nb + 2 * c + j);
         lim[nb][j] = r.real ? r.pos + 1 : 0x7FFFFFFF;   // rows that do not exist never ask for a mask
-        win[nb][j] = r.real && p.window >= 0 ? max(r.pos - p.window, 0) : 0;
+        win[nb][j] = r.real ? window_begin(p, r.pos) : 0;
       }
     }
     int lim_min = lim[0][0], win_max = win[0][0];
@@ -866,8 +870,7 @@ BFP8_DEV TileReq tile_req(const AttnParams& p, int b) {
 }
 // The first token that a row of pair `q` sees.
 BFP8_DEV int pair_first(const AttnParams& p, const TileReq& r, uint32_t q) {
-  const int pos0 = r.kv - r.n + static_cast<int>(q * kItemRows / p.G);
-  return p.window >= 0 ? max(pos0 - p.window, 0) : 0;
+  return window_begin(p, r.kv - r.n + static_cast<int>(q * kItemRows / p.G));
 }
 // The tiles of tokens that the rows of pair `q` see: [x, y).
 BFP8_DEV int2 pair_tiles(const AttnParams& p, const TileReq& r, uint32_t q) {
@@ -1513,7 +1516,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
       // the positions that the row sees; rows that do not exist never ask for a
       // mask, and what they compute is not stored
-      const int first = at.real && p.window >= 0 ? max(at.pos - p.window, 0) : 0;
+      const int first = at.real ? window_begin(p, at.pos) : 0;
       const int last = at.real ? at.pos : 0x7FFFFFFE;
       const int last_warp = __reduce_min_sync(0xffffffffu, last);
       const int first_warp = __reduce_max_sync(0xffffffffu, first);

@@ -136,3 +136,12 @@ def test_what_lies_behind_the_window_is_never_used(bfp8, cuda_device, lengths, p
                 s[x][1][int(table[b, j])] = e
     _check(bfp8, s, window)
     assert any(kv - n > window + page for kv, n in lengths)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 60, 1000, 15])
+def test_windows_of_rows_before_the_first_position(bfp8, cuda_device, window):
+    """More new rows than the cache holds, under windows that a position below 0 must not carry past 32
+    bits: the rows at positions from 0 on see what they see without a window."""
+    rng = np.random.default_rng(43)
+    for lengths in ([(20, 100)], [(20, 100), (9, 12), (300, 1)], [(5, 7), (0, 3)]):
+        _check(bfp8, _setup(cuda_device, rng, lengths, 1, 4, 16), window)
