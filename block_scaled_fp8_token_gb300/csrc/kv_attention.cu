@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
   if (tid == 0) abort_flag = 0, start_b = 0, start_base = 0;
   mbar_fence_init();
   pdl_wait();
-  // The tiles kernel needs nothing of this one: its blocks start as these end (six
-  // chunks and single tokens: 46 us a pass, against 47).
+  // The tiles kernel needs nothing of this one: its blocks set themselves up as these
+  // end, and wait there for whatever both read.
   if (p.tiles_follow) pdl_launch_dependents();
 
   // ---- this block's range of units
@@ -997,9 +997,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
-  // Behind the rows kernel there is nothing to wait for: its blocks let this one
-  // start only when whatever came before them was complete.
-  if (!p.tiles_follow) pdl_wait();
+  // Behind the rows kernel too, which this one needs nothing of: what the calls before
+  // it wrote is only sure to be seen by a grid that waits itself.
+  pdl_wait();
 
   // ---- this block's range of units: an item has its tiles and kTilePad
   uint64_t range = 0;
@@ -1625,7 +1625,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) atomicExch(&g_kv_err, static_cast<int>(BFP8_ERR_TIMEOUT));
     }
   }
-  if (p.tiles_follow) pdl_wait();   // the join waits for this kernel, and so for both
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -145,3 +145,29 @@ def test_windows_of_rows_before_the_first_position(bfp8, cuda_device, window):
     rng = np.random.default_rng(43)
     for lengths in ([(20, 100)], [(20, 100), (9, 12), (300, 1)], [(5, 7), (0, 3)]):
         _check(bfp8, _setup(cuda_device, rng, lengths, 1, 4, 16), window)
+
+
+def test_a_mixed_batch_reads_what_was_written_just_before_it(bfp8, cuda_device):
+    """Queries, lengths, table, codes and scale bytes that kernels right ahead of the call write, each
+    time others, with nothing between them that waits for the device: single tokens and prompts."""
+    rng = np.random.default_rng(45)
+    lengths = [(700, 1), (400, 120), (333, 2), (900, 300), (40, 1)]
+    sets = [_setup(cuda_device, rng, [lengths[i] for i in rng.permutation(len(lengths))], 2, 4, 32) for _ in range(6)]
+    want = [_run(bfp8, s) for s in sets]
+    live = {x: torch.empty_like(sets[0][x]) for x in ("q", "off", "kv", "table")}
+    live |= {x: tuple(torch.zeros_like(t) for t in sets[0][x]) for x in ("k", "v")}
+    n = bfp8.bfp8_kv_attention_workspace(5, sets[0]["T"], 300, 8, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device=cuda_device)
+    outs = []
+    torch.cuda.synchronize()
+    for i in [0, 3, 1, 5, 2, 4, 0, 5]:
+        for x, to in live.items():
+            for dst, src in zip(to, sets[i][x]) if isinstance(to, tuple) else [(to, sets[i][x])]:
+                dst.copy_(src)
+        out, lse = torch.empty_like(live["q"]), torch.empty(live["q"].shape[:2], device=cuda_device)
+        bfp8.bfp8_kv_attention(live["q"], live["k"][0], live["v"][0], live["k"][1], live["v"][1], live["table"], live["off"],
+                               live["kv"], out, 300, lse=lse, workspace=ws)
+        outs.append((i, out, lse))
+    torch.cuda.synchronize()
+    for i, out, lse in outs:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), i
