@@ -47,6 +47,7 @@ struct AttnParams {
   uint64_t* schedule;        // [B + 1]: the rows kernel's units before each request, and in all
   int64_t q_ldt, q_ldh, o_ldt, o_ldh, l_ldt, ld_table, exp_page, exp_head;
   int64_t T, n_pages;
+  int32_t max_q;             // rows of a request past this many are left alone
   int32_t B, H, G, page_shift, max_blocks, window;
   int32_t seg_rows;          // query rows of a segment of the rows kernel: 8 or 16
   int32_t few_rows;          // requests of at most this many rows of a KV head go to the rows kernel
@@ -104,21 +105,34 @@ BFP8_DEV int window_begin(const AttnParams& p, int pos) {
   return p.window >= 0 ? max(max(pos, 0) - p.window, 0) : 0;
 }
 
-struct ReqUnits {
-  int32_t q0, n, kv;       // first row, new tokens, length
+// A request's rows: n of them from q0 on, the first at position pos0 (below 0 where
+// the cache holds fewer tokens than there are new ones).
+struct ReqRows {
+  int32_t q0, n, pos0;
+};
+BFP8_DEV ReqRows req_rows(const AttnParams& p, int b, int kv) {
+  ReqRows r;
+  r.q0 = max(__ldg(p.q_offsets + b), 0);
+  const int64_t q1 = min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T);
+  const int32_t n = static_cast<int32_t>(max(q1 - r.q0, static_cast<int64_t>(0)));
+  r.pos0 = kv - n;
+  r.n = min(n, p.max_q);
+  return r;
+}
+
+struct ReqUnits : ReqRows {
+  int32_t kv;              // its length
   int32_t first, lo;       // first token that any row sees, and its unit
   uint32_t nt, nseg, nrb;  // units of a segment, segments, segments of a head
   BFP8_DEV uint32_t cost() const { return nt ? nt + kPadUnits : 0; }   // a segment's, in units
 };
 BFP8_DEV ReqUnits req_units(const AttnParams& p, int b) {
   ReqUnits r;
-  r.q0 = max(__ldg(p.q_offsets + b), 0);
-  const int64_t q1 = min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T);
-  r.n = static_cast<int32_t>(max(q1 - r.q0, static_cast<int64_t>(0)));
   r.kv = max(__ldg(p.kv_len + b), 0);
+  static_cast<ReqRows&>(r) = req_rows(p, b, r.kv);
   const int64_t held = min(static_cast<int64_t>(r.kv),
                            static_cast<int64_t>(p.max_blocks) << p.page_shift);
-  r.first = window_begin(p, r.kv - r.n);
+  r.first = window_begin(p, r.pos0);
   r.lo = r.first / kUnit;
   const int64_t hi = (held + kUnit - 1) / kUnit;
   r.nt = r.n > 0 && hi > r.lo ? static_cast<uint32_t>(hi - r.lo) : 0u;
@@ -260,7 +274,7 @@ BFP8_DEV RowAt row_at(const AttnParams& p, const ReqUnits& r, uint32_t h, uint32
   a.real = tok < static_cast<uint32_t>(r.n);
   a.token = r.q0 + static_cast<int64_t>(a.real ? tok : 0);
   a.head = h * p.G + (i - tok * p.G);
-  a.pos = r.kv - r.n + static_cast<int>(tok);
+  a.pos = r.pos0 + static_cast<int>(tok);
   return a;
 }
 
@@ -852,17 +866,15 @@ constexpr uint32_t kTilePad = 3, kTileShare = 6;
 
 constexpr float kBigScore = 4194304.0f;   // 2^22
 
-struct TileReq {
-  int32_t q0, n, kv, held;   // first row, new tokens, length, tokens inside the table
+struct TileReq : ReqRows {
+  int32_t held;              // tokens inside the table
   uint32_t pairs;            // items of a KV head; 0: not this kernel's
 };
 BFP8_DEV TileReq tile_req(const AttnParams& p, int b) {
   TileReq r;
-  r.q0 = max(__ldg(p.q_offsets + b), 0);
-  const int64_t q1 = min(static_cast<int64_t>(__ldg(p.q_offsets + b + 1)), p.T);
-  r.n = static_cast<int32_t>(max(q1 - r.q0, static_cast<int64_t>(0)));
-  r.kv = max(__ldg(p.kv_len + b), 0);
-  r.held = static_cast<int32_t>(min(static_cast<int64_t>(r.kv),
+  const int32_t kv = max(__ldg(p.kv_len + b), 0);
+  static_cast<ReqRows&>(r) = req_rows(p, b, kv);
+  r.held = static_cast<int32_t>(min(static_cast<int64_t>(kv),
                                     static_cast<int64_t>(p.max_blocks) << p.page_shift));
   const int64_t rows = static_cast<int64_t>(r.n) * p.G;
   r.pairs = rows > p.few_rows ? static_cast<uint32_t>((rows + kItemRows - 1) / kItemRows) : 0u;
@@ -870,13 +882,13 @@ BFP8_DEV TileReq tile_req(const AttnParams& p, int b) {
 }
 // The first token that a row of pair `q` sees.
 BFP8_DEV int pair_first(const AttnParams& p, const TileReq& r, uint32_t q) {
-  return window_begin(p, r.kv - r.n + static_cast<int>(q * kItemRows / p.G));
+  return window_begin(p, r.pos0 + static_cast<int>(q * kItemRows / p.G));
 }
 // The tiles of tokens that the rows of pair `q` see: [x, y).
 BFP8_DEV int2 pair_tiles(const AttnParams& p, const TileReq& r, uint32_t q) {
   const uint32_t row0 = q * kItemRows, rows = static_cast<uint32_t>(r.n) * p.G;
   const uint32_t last = min(rows, row0 + kItemRows) - 1;
-  const int pos1 = r.kv - r.n + static_cast<int>(last / p.G);
+  const int pos1 = r.pos0 + static_cast<int>(last / p.G);
   const int end = min(pos1 + 1, r.held);
   const int begin = pair_first(p, r, q);
   const int lo = begin / kTileTokens;
@@ -885,7 +897,7 @@ BFP8_DEV int2 pair_tiles(const AttnParams& p, const TileReq& r, uint32_t q) {
 
 // A block's next piece of work: an item, or a part of its tokens.
 struct TileItem {
-  int32_t b, h, q0, n, kv, held;   // b < 0: there is no more
+  int32_t b, h, q0, n, pos0, held;   // b < 0: there is no more
   int32_t row0;                    // first row of the item in its request
   int32_t lo, hi;                  // tiles of tokens
   int32_t first;                   // first token that any of its rows sees
@@ -895,7 +907,7 @@ struct TileItem {
 // What the join has to know of a block: its last item, when the block began it and
 // others finish it, and whether its first part finishes another's.
 struct TileDesc {
-  int32_t open, closes, h, row0, q0, n, kv, pad;
+  int32_t open, closes, h, row0, q0, n, pos0, pad;
 };
 
 // Row `row` of an item.
@@ -906,7 +918,7 @@ BFP8_DEV RowAt tile_row(const AttnParams& p, const TileItem& x, int row) {
   a.real = tok < static_cast<uint32_t>(x.n);
   a.token = x.q0 + static_cast<int64_t>(a.real ? tok : 0);
   a.head = x.h * p.G + (i - tok * p.G);
-  a.pos = x.kv - x.n + static_cast<int>(tok);
+  a.pos = x.pos0 + static_cast<int>(tok);
   return a;
 }
 
@@ -1013,7 +1025,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int l = __ffs(todo) - 1;   // the warp counts this lane's request together
         TileReq o;
         o.n = __shfl_sync(0xffffffffu, r.n, l);
-        o.kv = __shfl_sync(0xffffffffu, r.kv, l);
+        o.pos0 = __shfl_sync(0xffffffffu, r.pos0, l);
         o.held = __shfl_sync(0xffffffffu, r.held, l);
         o.pairs = __shfl_sync(0xffffffffu, r.pairs, l);
         uint64_t sum = 0;
@@ -1140,7 +1152,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           if (begin >= nt && !(nt == 0 && begin == 0)) continue;   // nothing but the padding
           x.b = b;
-          x.q0 = r.q0, x.n = r.n, x.kv = r.kv, x.held = r.held;
+          x.q0 = r.q0, x.n = r.n, x.pos0 = r.pos0, x.held = r.held;
           x.row0 = pair * kItemRows;
           x.lo = t.x + begin;
           x.hi = t.x + min(end, nt);
@@ -1168,7 +1180,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!x.begins && x.ends) desc.closes = 1;
         if (x.begins && !x.ends) {
           desc.open = 1;
-          desc.h = x.h, desc.row0 = x.row0, desc.q0 = x.q0, desc.n = x.n, desc.kv = x.kv;
+          desc.h = x.h, desc.row0 = x.row0, desc.q0 = x.q0, desc.n = x.n, desc.pos0 = x.pos0;
         }
         const int nt = x.hi - x.lo;
         const int32_t* row = p.table + x.b * p.ld_table;
@@ -1665,7 +1677,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
     if (!d.open) return;
     const uint32_t blocks = (gridDim.x - seg_blocks) / 16;
     TileItem x{};
-    x.h = d.h, x.row0 = d.row0, x.q0 = d.q0, x.n = d.n, x.kv = d.kv;
+    x.h = d.h, x.row0 = d.row0, x.q0 = d.q0, x.n = d.n, x.pos0 = d.pos0;
     const RowAt at = tile_row(p, x, row);
     if (!at.real) return;
     for (uint32_t k = c0;; ++k) {   // to the block that finished it
@@ -1831,6 +1843,7 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.exp_page = c.exp_stride_page;
   p.exp_head = c.exp_stride_head;
   p.T = a.tokens;
+  p.max_q = static_cast<int32_t>(a.max_q_len < a.tokens ? a.max_q_len : a.tokens);
   p.n_pages = c.n_pages;
   p.B = static_cast<int32_t>(a.batch);
   p.H = c.n_kv_heads;

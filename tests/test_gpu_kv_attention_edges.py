@@ -171,3 +171,17 @@ def test_a_mixed_batch_reads_what_was_written_just_before_it(bfp8, cuda_device):
     torch.cuda.synchronize()
     for i, out, lse in outs:
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), i
+
+
+@pytest.mark.parametrize("lengths,most", [([(5000, 5), (90, 3), (7, 7)], 2), ([(300, 200)], 100), ([(900, 40)], 3),
+                                          ([(300, 200), (5000, 30), (70, 1), (64, 64)], 20)])
+def test_rows_past_the_most_are_not_written(bfp8, cuda_device, lengths, most):
+    """A request with more new rows than max_q_len: its first max_q_len rows, at their places in the
+    request, and nothing of the others."""
+    rng = np.random.default_rng(most)
+    s = dict(_setup(cuda_device, rng, lengths, 2, 4, 32), maxq=most)
+    out, lse = _run(bfp8, s)
+    off = s["off"].tolist()
+    past = [t for b in range(len(lengths)) for t in range(off[b] + most, off[b + 1])]
+    assert past and bool(torch.isnan(out[past].float()).all()) and bool(torch.isnan(lse[past]).all())
+    _check(bfp8, s, rows=set(range(s["T"])) - set(past), got=(out, lse))
