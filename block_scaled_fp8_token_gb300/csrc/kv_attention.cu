@@ -15,6 +15,8 @@
 #include "ptx.cuh"
 #include "act_math.cuh"
 
+#include <algorithm>
+
 namespace bfp8 {
 namespace {
 
@@ -1754,16 +1756,16 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // tokens (from L2) still beat a tile that is a quarter full.
 constexpr int32_t kFewRows = 64;
 
-// What the host knows of a call's shape, from upper bounds alone.
+// What the host knows of a call's shape, from upper bounds alone: max_q is the most
+// rows of a request, and no more than T.
 struct Shape {
   bool tiles;   // some request may have more than kFewRows rows
   bool whole;   // the tiles kernel's blocks take whole items
 };
-Shape shape_of(int64_t B, int64_t T, int64_t max_q, int64_t G, int64_t H, int sms) {
+Shape shape_of(int64_t B, int64_t max_q, int64_t G, int64_t H, int sms) {
   Shape s{};
   s.tiles = max_q * G > kFewRows;
-  const int64_t rows = (max_q < T ? max_q : T) * G;
-  s.whole = s.tiles && B == 1 && (rows + kItemRows - 1) / kItemRows * H >= 4 * sms;
+  s.whole = s.tiles && B == 1 && (max_q * G + kItemRows - 1) / kItemRows * H >= 4 * sms;
   return s;
 }
 
@@ -1786,7 +1788,7 @@ Workspace workspace_of(int64_t B, const Shape& s, int sms) {
 
 size_t kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t H,
                                     int sms) {
-  return workspace_of(B, shape_of(B, T, max_q, Hq / H, H, sms), sms).bytes;
+  return workspace_of(B, shape_of(B, std::min(max_q, T), Hq / H, H, sms), sms).bytes;
 }
 
 int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c, void* stream) {
@@ -1816,7 +1818,8 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   int sms = 0;
   rc = sm_count(&sms);
   if (rc != BFP8_OK) return rc;
-  const Shape shape = shape_of(a.batch, a.tokens, a.max_q_len, a.n_heads / H, H, sms);
+  const int64_t max_q = std::min(a.max_q_len, a.tokens);
+  const Shape shape = shape_of(a.batch, max_q, a.n_heads / H, H, sms);
   const Workspace ws = workspace_of(a.batch, shape, sms);
   if (!a.workspace || a.ws_bytes < ws.bytes || reinterpret_cast<uintptr_t>(a.workspace) % 256)
     return BFP8_ERR_INVALID_ARG;
@@ -1843,7 +1846,7 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.exp_page = c.exp_stride_page;
   p.exp_head = c.exp_stride_head;
   p.T = a.tokens;
-  p.max_q = static_cast<int32_t>(a.max_q_len < a.tokens ? a.max_q_len : a.tokens);
+  p.max_q = static_cast<int32_t>(max_q);
   p.n_pages = c.n_pages;
   p.B = static_cast<int32_t>(a.batch);
   p.H = c.n_kv_heads;
@@ -1856,7 +1859,7 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.tiles_follow = shape.tiles && a.batch > 1;
   // one request has only one kernel to go to; of several, each is looked at on the device
   p.few_rows = !shape.tiles ? 0x7FFFFFFF : a.batch > 1 ? kFewRows : 0;
-  const int64_t most_rows = a.max_q_len * p.G;
+  const int64_t most_rows = max_q * p.G;
   // what goes to the rows kernel next to prompts is single tokens for the most part
   // (six chunks and single tokens, groups of 8: 47 us a pass with 8 rows, 49 with 16)
   p.seg_rows = most_rows <= 8 || (shape.tiles && p.G <= 8) ? 8 : kMaxRows;

@@ -185,3 +185,14 @@ def test_rows_past_the_most_are_not_written(bfp8, cuda_device, lengths, most):
     past = [t for b in range(len(lengths)) for t in range(off[b] + most, off[b + 1])]
     assert past and bool(torch.isnan(out[past].float()).all()) and bool(torch.isnan(lse[past]).all())
     _check(bfp8, s, rows=set(range(s["T"])) - set(past), got=(out, lse))
+
+
+@pytest.mark.parametrize("most", [1000, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+def test_a_most_beyond_the_tokens(bfp8, cuda_device, most):
+    """max_q_len is an upper bound: any above the call's tokens is as good as their number."""
+    rng = np.random.default_rng(46)
+    for lengths in ([(70, 1), (300, 3)], [(400, 150)], [(400, 150), (60, 1)]):
+        s = _setup(cuda_device, rng, lengths, 2, 4, 32)
+        need = [bfp8.bfp8_kv_attention_workspace(len(lengths), s["T"], q, 8, 2) for q in (s["T"], most)]
+        assert need[0] == need[1]
+        _check(bfp8, dict(s, maxq=most))
