@@ -548,7 +548,7 @@ size_t bfp8_kv_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q_
   if (batch <= 0 || tokens <= 0 || max_q_len <= 0 || n_heads <= 0 || n_kv_heads <= 0 ||
       n_heads % n_kv_heads || sm_count(&sms) != BFP8_OK)
     return 0;
-  return kv_attention_workspace_bytes(batch, tokens, max_q_len, n_heads, n_kv_heads, sms);
+  return kv_attention_workspace_bytes(batch, tokens, max_q_len, n_heads, sms);
 }
 
 int bfp8_kv_attention(const bfp8_kv_attention_args* args, const bfp8_kv_cache* cache,

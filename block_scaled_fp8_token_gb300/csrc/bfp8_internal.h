@@ -134,8 +134,7 @@ int launch_kv_plan(const int32_t* ctx, const int32_t* q_len, int64_t B, const in
 int launch_kv_append(const void* k, int64_t k_ldt, int64_t k_ldh, const void* v, int64_t v_ldt,
                      int64_t v_ldh, const int64_t* slots, int64_t T, const bfp8_kv_cache& cache,
                      void* stream);
-size_t kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t H,
-                                    int sms);
+size_t kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int sms);
 int launch_kv_attention(const bfp8_kv_attention_args& args, const bfp8_kv_cache& cache,
                         void* stream);
 int launch_residual_norm(const bfp8_norm_args& args, int64_t T, int64_t H, void* stream);

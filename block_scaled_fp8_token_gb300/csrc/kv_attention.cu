@@ -1786,9 +1786,11 @@ Workspace workspace_of(int64_t B, const Shape& s, int sms) {
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t H,
-                                    int sms) {
-  return workspace_of(B, shape_of(B, std::min(max_q, T), Hq / H, H, sms), sms).bytes;
+// What a call needs falls as its KV heads rise, for their groups shrink. The size that
+// users ask for is one KV head's, so that it grows with every argument and one
+// workspace serves layers of other head counts too.
+size_t kv_attention_workspace_bytes(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int sms) {
+  return workspace_of(B, shape_of(B, std::min(max_q, T), Hq, 1, sms), sms).bytes;
 }
 
 int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c, void* stream) {

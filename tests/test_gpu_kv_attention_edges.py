@@ -196,3 +196,19 @@ def test_a_most_beyond_the_tokens(bfp8, cuda_device, most):
         need = [bfp8.bfp8_kv_attention_workspace(len(lengths), s["T"], q, 8, 2) for q in (s["T"], most)]
         assert need[0] == need[1]
         _check(bfp8, dict(s, maxq=most))
+
+
+def test_a_workspace_holds_every_smaller_call_of_other_heads(bfp8, cuda_device):
+    """Heads vary too: layers with other numbers of query and KV heads share one workspace."""
+    heads = [(4, 1), (4, 4), (16, 2), (64, 4), (64, 8), (64, 64), (128, 1), (128, 8)]
+    sizes = [(b, t, q, *h) for b in (1, 3) for t in (1, 700) for q in (1, 8, 16, 65, 700) for h in heads]
+    need = {x: bfp8.bfp8_kv_attention_workspace(*x) for x in sizes}
+    for a in sizes:
+        for b in sizes:
+            if all(x <= y for x, y in zip(a, b)):
+                assert need[a] <= need[b], (a, b)
+    # and the call takes it: 8 rows of 8 heads on 2 KV heads, in the workspace of 8 on 8
+    rng = np.random.default_rng(44)
+    s = _setup(cuda_device, rng, [(70, 20), (100, 1)], 2, 4, 32)
+    ws = torch.empty(bfp8.bfp8_kv_attention_workspace(2, s["T"], 20, 8, 8), dtype=torch.uint8, device=cuda_device)
+    _check(bfp8, s, got=_run(bfp8, s, ws=ws))
