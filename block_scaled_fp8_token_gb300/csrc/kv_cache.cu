@@ -120,6 +120,18 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
   uint32_t* pre_page = pre + p.B;
   const bool first = blockIdx.x == 0;
   uint32_t tok = 0, page = 0, missing = 0;
+  if (first) {
+    // tokens that continue a page which is not there; no block writes its entry, and
+    // several requests' loads are in flight at once
+#pragma unroll 4
+    for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
+      const Request r = load_request(p, b);
+      const uint32_t used = r.ctx & ((1u << p.shift) - 1u), held = r.ctx >> p.shift;
+      const bool continues = r.q && used && held < r.before;
+      const int32_t pg = continues ? p.table[b * p.ld_table + held] : 0;
+      if (pg < 0) missing = sat_add(missing, min(r.q, (1u << p.shift) - used));
+    }
+  }
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     Request r{};

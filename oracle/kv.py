@@ -30,11 +30,10 @@ def block_plan(ctx, new, free, table, page, capacity):
             table[b, j] = free[wanted] if wanted < len(free) else -1
             short += wanted >= len(free)
             wanted += 1
-        held = -(-c // page)
         for i in range(n):
             j, t = (c + i) // page, offsets[-1] + i
             pg = table[b, j] if j < width else -1
-            homeless += j >= width or (pg < 0 and j >= held)
+            homeless += pg < 0
             if t < capacity:
                 positions[t] = c + i
                 if pg >= 0:

@@ -90,6 +90,27 @@ def test_plan_of_no_requests(bfp8, cuda_device):
     assert off.tolist() == [0] and counts.tolist() == [0, 0, 0] and slots.tolist() == [-1] * 5 and pos.tolist() == [-1] * 5
 
 
+def test_plan_counts_tokens_of_missing_held_pages(bfp8, cuda_device):
+    """Tokens that continue a page whose table entry is -1 have no page, and are counted: after a step
+    that ran out of pages, the next one says how many tokens it loses."""
+    for page, ctx, new, free, table, lost in [
+            (16, [5], [3], [1], [[-1, -1]], 3),                       # all of them
+            (16, [5], [20], [1], [[-1, -1]], 11),                     # the rest of that page; the next is new
+            (16, [5, 16, 0, 31], [1, 2, 4, 9], [7, 8, 9], [[-1, -1, -1]] * 4, 2),   # requests 0 and 3, one each
+            (32, [40, 64, 33], [5, 0, 1], [3], [[2, -1, -1], [4, -1, -1], [6, 5, -1]], 5),
+            (16, [5], [3], [], [[4]], 0)]:
+        got = _plan(bfp8, cuda_device, ctx, new, free, table, page, sum(new) + 3)
+        assert got[-1][2] == lost, (page, ctx, got[-1])
+        assert int((got[3][:sum(new)] < 0).sum()) == lost
+        _check_plan(bfp8, cuda_device, ctx, new, free, table, page, sum(new) + 3)
+    rng = np.random.default_rng(12)
+    ctx, new, free, table = _random_plan(rng, 700, 16, 30, 100)
+    table[rng.random(table.shape) < 0.3] = -1
+    _check_plan(bfp8, cuda_device, ctx, new, free[:200], table, 16, int(new.sum()))
+    got = _plan(bfp8, cuda_device, ctx, new, free[:200], table, 16, int(new.sum()))
+    assert int((got[3] < 0).sum()) == got[-1][2]
+
+
 # ---- append ------------------------------------------------------------------
 
 

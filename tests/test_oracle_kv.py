@@ -31,6 +31,13 @@ def test_plan_short_of_pages_and_of_width():
     assert pos.tolist() == [0, 1, 2] + list(range(9))
 
 
+def test_plan_counts_every_token_without_a_page():
+    # page 4: request 0 continues a page that is not there (2 tokens) and gets a new one (1 token);
+    # request 1 continues one that is; request 2 needs no page, with 4 tokens on a missing page ahead of its own
+    t, off, kv, slots, pos, counts = KV.block_plan([2, 1, 4], [3, 2, 1], [9, 8], [[-1, -1], [6, -1], [-1, -1]], 4, 6)
+    assert slots.tolist() == [-1, -1, 36, 25, 26, 32] and counts == [2, 0, 2]
+
+
 @pytest.mark.parametrize("amax", [0.0, 1e-30, 448.0, 448.0000001, 449.0, 1.0, 0.875, 0.8750001, 3.5, 3.4e38])
 def test_scale_exponent_is_the_least(amax):
     e = KV.scale_exponent(amax)
