@@ -212,3 +212,51 @@ def test_a_workspace_holds_every_smaller_call_of_other_heads(bfp8, cuda_device):
     s = _setup(cuda_device, rng, [(70, 20), (100, 1)], 2, 4, 32)
     ws = torch.empty(bfp8.bfp8_kv_attention_workspace(2, s["T"], 20, 8, 8), dtype=torch.uint8, device=cuda_device)
     _check(bfp8, s, got=_run(bfp8, s, ws=ws))
+
+
+# ---- one prompt with several items of 256 rows an SM, which blocks take whole ------
+
+
+def _whole(dev, seed, kv, n, page, G=5, H=64):
+    """64 KV heads of five: 640 items for 460 rows and more, on 152 SMs."""
+    return _setup(dev, np.random.default_rng(seed), [(kv, n)], H, G, page)
+
+
+def _boundary_rows(n, G=5):
+    """Tokens on both sides of every 128th row, the first and the last."""
+    return {t for r in range(0, n * G + 1, 128) for t in ((r - 1) // G, r // G, r // G + 1) if 0 <= t < n} | {0, n - 1}
+
+
+@pytest.mark.parametrize("page,window", [(16, -1), (64, 100), (128, 300), (32, 0)])
+def test_whole_items_of_a_prompt(bfp8, cuda_device, page, window):
+    s = _whole(cuda_device, page, 900, 470, page)
+    _check(bfp8, s, window, rows=_boundary_rows(470))
+
+
+def test_whole_items_without_tokens_or_pages(bfp8, cuda_device):
+    """Items whose rows all sit before the first position, and a prompt with pages missing."""
+    _check(bfp8, _whole(cuda_device, 51, 200, 470, 32), rows=_boundary_rows(470))
+    s = _whole(cuda_device, 52, 700, 470, 32)
+    s["table"][0, [0, 3, 4, 5, 6, 15]] = torch.tensor([-1, -1, -7, 10 ** 6, 2 ** 31 - 1, s["deq"][0].shape[0]],
+                                                       dtype=torch.int32, device=cuda_device)
+    _check(bfp8, s, rows=_boundary_rows(470))
+
+
+def test_whole_items_replayed_with_fewer_rows(bfp8, cuda_device):
+    """A call captured for 470 rows, replayed for one, a few and a few hundred."""
+    s = _whole(cuda_device, 53, 900, 470, 64)
+    out, lse = torch.empty_like(s["q"]), torch.empty(470, 320, device=cuda_device)
+    ws = torch.empty(bfp8.bfp8_kv_attention_workspace(1, 470, 470, 320, 64), dtype=torch.uint8, device=cuda_device)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bfp8.bfp8_kv_attention(s["q"], s["k"][0], s["v"][0], s["k"][1], s["v"][1], s["table"], s["off"], s["kv"], out, 470,
+                               lse=lse, workspace=ws)
+    for kv, n in ((900, 470), (899, 1), (12, 9), (640, 300), (77, 0), (0, 4), (470, 470)):
+        s["kv"].fill_(kv)
+        s["off"].copy_(torch.tensor([0, n], dtype=torch.int32))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert bfp8.bfp8_device_status() == 0
+        _check(bfp8, dict(s, lengths=[(kv, n)]), rows=_boundary_rows(n) if n else set(), got=(out, lse))
+        assert bool(torch.isnan(out[n:].float()).all())
