@@ -930,12 +930,6 @@ BFP8_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 2^x, without the ordering that act_math.cuh's asks for.
-BFP8_DEV float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // n FP32 columns of this lane's row of tensor memory times f. Rare, so kept
 // small rather than fast.
 BFP8_DEV void scale_columns(uint32_t taddr, int n, float f) {
@@ -1584,7 +1578,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool grow = top - M > kReach;
         const bool big = fabsf(top) >= kBigScore && top > kNegInf;
         if (__any_sync(0xffffffffu, grow || big)) {   // rare but for the first tokens
-          const float to = top - kPBase, f = grow ? exp2_fast(M - to) : 1.0f;
+          const float to = top - kPBase, f = grow ? ex2_approx(M - to) : 1.0f;
           if (grow) M = to;
           Z *= f;
           if (big) {
@@ -1618,7 +1612,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int c = 0; c < 8; ++c) {
             const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(y[16 * g + 2 * c]),
                                                      __uint_as_float(y[16 * g + 2 * c + 1])), ck2, cb2);
-            const float2 e = make_float2(exp2_fast(x2.x), exp2_fast(x2.y));
+            const float2 e = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
             sum = __fadd2_rn(sum, e);
             pw[8 * g + c] = pack_f16x2(e.x, e.y);
           }
