@@ -1746,9 +1746,17 @@ int launch_dependent(Kernel kernel, unsigned blocks, unsigned threads, size_t sm
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Requests whose rows of a KV head (new tokens times the group) are at most
-// this many go to the rows kernel: at 64 rows, four passes over the request's
-// tokens (from L2) still beat a tile that is a quarter full.
-constexpr int32_t kFewRows = 64;
+// this many go to the rows kernel, which goes over their tokens once for every 16
+// (from L2 but for the first). A call from cold caches, 64 heads on 8, all requests
+// there against all in the tiles kernel, in us:
+//   8 tokens (64 rows) of 4, 16, 64 requests behind 8000: 87, 302, 1133 against 52, 124, 406
+//   5 tokens (40 rows) of 32 behind 300, 2000, 16000: 51, 139, 841 against 51, 90, 395
+//   the same of 1 and of 2 behind 2000: 25 and 27 against 29 and 34
+//   4 tokens (32 rows) of 32 behind 300, 2000, 16000: 41, 103, 570 against 51, 88, 395
+//   the same of 1, 2 and 8 behind 2000: 25, 26 and 40 against 29, 34 and 41
+// Above 32 rows the tiles kernel is up to 2.8 times as fast, and slower by less than 10
+// us on one or two requests; below, it gains 1.4 times at most, on long caches only.
+constexpr int32_t kFewRows = 32;
 
 // What the host knows of a call's shape, from upper bounds alone: max_q is the most
 // rows of a request, and no more than T.
