@@ -653,7 +653,7 @@ int bfp8_kv_attention(const bfp8_kv_attention_args* args, const bfp8_kv_cache* c
  *   residual_out = bf16_rn(h)
  *   n = h * rsqrt(mean(h^2) + eps) * (w_pre + weight_offset)
  *   norm_out = bf16_rn(n); per 128 columns s = max(max|n|, 1e-10f) / 448,
- *   q = RNE_satfinite_e4m3(n / s)                     (the quotient to FP32 rounding)
+ *   q = RNE_satfinite_e4m3(n / s)                     (the quotient within 2^-21)
  * in float32 throughout: the second norm takes h, and the quantizer n, before
  * either is rounded to BF16.
  */
