@@ -260,3 +260,22 @@ def test_whole_items_replayed_with_fewer_rows(bfp8, cuda_device):
         assert bfp8.bfp8_device_status() == 0
         _check(bfp8, dict(s, lengths=[(kv, n)]), rows=_boundary_rows(n) if n else set(), got=(out, lse))
         assert bool(torch.isnan(out[n:].float()).all())
+
+
+@pytest.mark.parametrize("lengths", BIG)
+def test_codes_of_a_token_side_by_side(bfp8, cuda_device, lengths):
+    """A cache whose tokens lie outside of its heads, for prompts too."""
+    s = _setup(cuda_device, np.random.default_rng(47), lengths, 3, 4, 64, order="tokens")
+    _check(bfp8, s)
+
+
+def test_a_table_of_no_width_and_rows_of_no_request(bfp8, cuda_device):
+    """With no table there is nothing to see; rows behind the last request's are left alone."""
+    for lengths in ([(40, 1), (9, 2)], [(100, 90)], [(100, 90), (5, 1)]):
+        s = _setup(cuda_device, np.random.default_rng(48), lengths, 2, 4, 32)
+        out, lse = _run(bfp8, dict(s, table=s["table"][:, :0]))
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+        more = dict(s, q=torch.cat([s["q"], s["q"][:3]]), T=s["T"] + 3)
+        out, lse = _run(bfp8, more)
+        assert bool(torch.isnan(out[s["T"]:].float()).all()) and bool(torch.isnan(lse[s["T"]:]).all())
+        _check(bfp8, s, got=(out[:s["T"]], lse[:s["T"]]))

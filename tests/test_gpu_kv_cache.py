@@ -81,6 +81,15 @@ def test_plan_edges(bfp8, cuda_device):
     _check_plan(bfp8, dev, [0, 100], [300, 5], [big, big - 1, big - 2, 3], [[-1] * 4, [big - 5, -1, -1, -1]], 128, 310)
 
 
+def test_plan_of_the_most_requests(bfp8, cuda_device):
+    """16,384 requests, whose prefixes take 128 KB of a block's shared memory; one more is refused."""
+    rng = np.random.default_rng(13)
+    ctx, new, free, table = _random_plan(rng, 16384, 16, 3, 40)
+    _check_plan(bfp8, cuda_device, ctx, new, free, table, 16, int(new.sum()) + 5)
+    with pytest.raises(bfp8.Bfp8Error, match="UNSUPPORTED"):
+        _plan(bfp8, cuda_device, [0] * 16385, [0] * 16385, [1], [[-1]] * 16385, 16, 4)
+
+
 def test_plan_of_no_requests(bfp8, cuda_device):
     dev = cuda_device
     e = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)   # noqa: E731
