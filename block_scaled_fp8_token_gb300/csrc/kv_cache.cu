@@ -118,9 +118,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
   pdl_wait();
   uint32_t* pre_tok = pre;
   uint32_t* pre_page = pre + p.B;
-  const bool first = blockIdx.x == 0;
+  // the first block writes the requests' offsets and lengths, the last one counts the
+  // tokens that have no page
+  const bool first = blockIdx.x == 0, counts = blockIdx.x + 1 == gridDim.x;
   uint32_t tok = 0, page = 0, missing = 0;
-  if (first) {
+  if (counts) {
     // tokens that continue a page which is not there; no block writes its entry, and
     // several requests' loads are in flight at once
 #pragma unroll 4
@@ -144,6 +146,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
       if (first) {
         p.q_offsets[b] = static_cast<int32_t>(pre_tok[b]);
         p.kv_len[b] = static_cast<int32_t>(r.ctx + r.q);
+      }
+      if (counts) {
         // tokens from the first block on that has no page: past the table's
         // width, or past the end of the free list
         const uint64_t have = p.n_free > pre_page[b] ? p.n_free - pre_page[b] : 0;
@@ -157,7 +161,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
     page = sat_add(page, tp);
   }
   __syncthreads();
-  if (first) {
+  if (first && threadIdx.x == 0) {
+    p.q_offsets[p.B] = static_cast<int32_t>(tok);
+    const uint32_t have = static_cast<uint32_t>(min(p.n_free, static_cast<int64_t>(kMaxCount)));
+    p.counts[0] = static_cast<int32_t>(min(page, have));
+    p.counts[1] = static_cast<int32_t>(page - min(page, have));
+  }
+  if (counts) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       missing = sat_add(missing, __shfl_xor_sync(0xffffffffu, missing, o));
@@ -166,10 +176,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
     if (threadIdx.x == 0) {
       uint32_t m = 0;
       for (int w = 0; w < kPlanThreads / 32; ++w) m = sat_add(m, lost[w]);
-      p.q_offsets[p.B] = static_cast<int32_t>(tok);
-      const uint32_t have = static_cast<uint32_t>(min(p.n_free, static_cast<int64_t>(kMaxCount)));
-      p.counts[0] = static_cast<int32_t>(min(page, have));
-      p.counts[1] = static_cast<int32_t>(page - min(page, have));
       p.counts[2] = static_cast<int32_t>(m);
     }
   }
