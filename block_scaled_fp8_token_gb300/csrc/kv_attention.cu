@@ -830,9 +830,13 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm)
 // contiguous ranges, so that one long chunk does not hold the others up; an item
 // cut by a range's end leaves FP32 partial sums that the join kernel adds. A
 // single prompt with four items an SM or more keeps them whole, in rounds over
-// the blocks of alternating direction, and needs no join. (4096 tokens of 64 heads
-// on 8: 232 us whole, 250 us cut; six chunks behind prefixes of up to 6000 tokens:
-// 46 us cut, 73 us as whole items of blocks that came and went.)
+// the blocks of alternating direction, and needs no join. (Whole and cut, 64 heads on
+// 8, from cold caches: prompts of 1200, 2600, 4000, 8192 tokens 40, 117, 229, 818 us and
+// 52, 130, 249, 857; 1200, 2600, 4000 behind 6000 others 197, 507, 773 and 212, 467,
+// 755; 640 and 2440 behind 30,000, with a last round that few blocks share, 794, 2046
+// and 449, 1700. Fewer items would gain up to a quarter without a prefix, which
+// the host cannot know, and lose up to 77 % behind a long one; from four an SM on
+// either loss is a fifth at most.)
 //
 // What bounds it: 4096 tokens run at 1.19 PFLOP/s, counting the causal half of the
 // scores. A pair of tiles takes 3,400 clocks, of which the products need 2,048 and
@@ -1865,7 +1869,9 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
   p.few_rows = !shape.tiles ? 0x7FFFFFFF : a.batch > 1 ? kFewRows : 0;
   const int64_t most_rows = max_q * p.G;
   // what goes to the rows kernel next to prompts is single tokens for the most part
-  // (six chunks and single tokens, groups of 8: 47 us a pass with 8 rows, 49 with 16)
+  // (6, 24 and 64 requests of up to 900 new tokens behind up to 6000, groups of 8: 54, 151
+  // and 545 us with 8 rows, 60, 163 and 556 with 16; groups of 4: 45, 103, 321 and 50,
+  // 116, 333; of 5: 47, 120, 383 and 53, 131, 394)
   p.seg_rows = most_rows <= 8 || (shape.tiles && p.G <= 8) ? 8 : kMaxRows;
   const int64_t max_rb = (most_rows + p.seg_rows - 1) / p.seg_rows;
   const int64_t few_rb = kFewRows / p.seg_rows;

@@ -56,7 +56,9 @@ class PagePool:
         self.lengths = [0] * batch
 
     def plan(self, new):
-        """Slots and positions of `new[b]` more tokens of each request."""
+        """Slots and positions of `new[b]` more tokens of each request. (The free list is passed
+        from its first unused page on; a captured step would read the same address each time, and
+        the list would have to be moved up to it between replays.)"""
         dev, T = self.free.device, sum(new)
 
         def i32(x):

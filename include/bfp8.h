@@ -548,7 +548,9 @@ typedef struct {
  *               negative length counts as 0)
  *   free_pages  device int32 [n_free]: page numbers; request by request, each
  *               new page takes the next one. The call does not change the list:
- *               the caller drops counts[0] pages from its front.
+ *               the caller drops counts[0] pages from its front. (A captured
+ *               step reads from the address it was captured with, so between
+ *               replays the caller moves the rest of the list there, on the device.)
  *   block_table device int32 [B, max_blocks], row stride ld_table. Entries below
  *               ceil(ctx_len / page_size) are read; the new pages' entries
  *               behind them are written, and no others.
@@ -559,7 +561,8 @@ typedef struct {
  *               a negative page number in the table)
  *   positions   int32 [T] out: a token's place in its request, -1 past the last
  *   counts      int32 [3] out: pages taken, pages that were wanted and not
- *               there (their table entries are -1), and tokens with no page
+ *               there (their table entries are -1), and tokens with no page,
+ *               those that continue a page whose entry is negative among them
  * T is the caller's capacity (a captured step keeps it fixed); rows past the
  * step's tokens are written -1. Repeating a call gives the same result. One
  * launch, no host synchronisation. Errors: INVALID_ARG (null pointers, negative
@@ -579,14 +582,15 @@ int bfp8_kv_plan(const int32_t* ctx_len, const int32_t* q_len, int64_t B,
  *   slots       device int64 [T], as bfp8_kv_plan writes them; a slot outside
  *               [0, n_pages * page_size) skips its row. Rows of one page must
  *               follow one another in consecutive slots.
- * Per page and head, over the page's new rows (finite values):
+ * Per page and head, over the page's new rows:
  *   e = the least integer with max|x| <= 448 * 2^e, clamped to [-40, 40]
  * A page whose first new row is not at offset 0 already holds the rows before
  * it: it keeps the larger of e and its present exponent, and when e is the
  * larger, the codes of those rows are multiplied by the power of two between
  * (rounded to nearest even; exact above E4M3's subnormals). Then
  *   code = RNE_satfinite_e4m3(x * 2^-e).
- * NaN gives the NaN code and does not enter the maximum; infinities saturate.
+ * NaN gives the NaN code and does not enter the maximum. An infinity does: it
+ * makes e 40, at which it saturates and ordinary values become 0.
  * Rows of a page behind the new ones hold nothing afterwards that is defined.
  * T == 0 is a no-op. Errors: INVALID_ARG, UNSUPPORTED (page size, head width,
  * alignment).
@@ -601,17 +605,24 @@ int bfp8_kv_append(const void* k_bf16, int64_t k_stride_token, int64_t k_stride_
  * g = h / (n_heads / n_kv_heads), over the positions i that the query sees. Row
  * i of a request's new rows sits at position kv_len - (its rows) + i and sees
  * the positions up to its own, at most `window` before it when window >= 0.
- * Scores, softmax statistics and sums are float32; out is rounded to BF16 once.
+ * Scores, softmax statistics and sums are float32, the exponentials within 2^-22;
+ * query entries below 2^-13 of their row's largest are carried to 2^-21 of it, and
+ * weights are rounded to 11 bits (F16, 2^-29 of the largest at most) where they
+ * meet the values, not where they are summed; out is rounded to BF16 once.
  *   q_bf16, out_bf16  [tokens, n_heads, 128] BF16, 16-byte aligned, token and
  *               head strides in elements, multiples of 8. They must not overlap.
  *   lse         float32 [tokens, n_heads] or NULL: ln(sum_i exp(score_i))
  *   block_table, q_offsets, kv_len  as bfp8_kv_plan leaves them, on the device.
  *               The new tokens' keys and values are in the cache already.
- *   max_q_len   at least the most new rows of a request; rows past it are not written
+ *   max_q_len   at least the most new rows of a request (any number above `tokens`
+ *               is as good as that); a request's rows past it are not written, nor
+ *               are those behind the last request's
  * A row that sees nothing (its request is empty, or its position is below 0)
  * gives 0 and -inf. A table entry outside [0, n_pages) hides its tokens. Rows of
- * a page at or behind kv_len are never used, whatever they hold.  A NaN among
- * the values a request does see may reach every row of that request.
+ * a page at or behind kv_len, or ahead of the first that a request's window
+ * reaches, are never used, whatever they hold. A NaN among the values a request
+ * does see may reach every row of that request; a NaN or an infinity among a
+ * row's queries, and scores past float32's range, make that row NaN.
  *   workspace   at least bfp8_kv_attention_workspace() bytes, 256-byte aligned,
  *               contents free (its size grows with every argument, so one for the
  *               largest call serves the others); calls sharing it must not overlap.
