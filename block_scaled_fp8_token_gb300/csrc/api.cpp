@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "attention_layer.h"
 #include "bfp8_internal.h"
 
 namespace bfp8 {

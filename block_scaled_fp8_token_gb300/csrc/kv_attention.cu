@@ -10,9 +10,8 @@
 //   out = sum(w code_v) / sum(w 2^-ev),    lse = ln2 (M + log2 sum(w 2^-ev)).
 // One running maximum bounds every product that is summed, whatever the pages'
 // scales; scores, maxima, sums and outputs are FP32.
-#include "bfp8_internal.h"
+#include "attention_layer.cuh"
 #include "kv_common.cuh"
-#include "ptx.cuh"
 #include "act_math.cuh"
 
 #include <algorithm>
@@ -1731,22 +1730,6 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams
   if (p.lse && ch == 0) p.lse[at.token * p.l_ldt + at.head] = row_lse(m, z);
 }
 
-template <typename Kernel, typename... Args>
-int launch_dependent(Kernel kernel, unsigned blocks, unsigned threads, size_t smem, cudaStream_t st,
-                     Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? BFP8_OK : BFP8_ERR_CUDA;
-}
-
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Requests whose rows of a KV head (new tokens times the group) are at most
@@ -1914,7 +1897,7 @@ int launch_kv_attention(const bfp8_kv_attention_args& a, const bfp8_kv_cache& c,
                           rows_grid, static_cast<uint32_t>(join_rb), static_cast<uint32_t>(segs));
     if (rc != BFP8_OK) return rc;
   }
-  return check_launch();
+  return BFP8_OK;
 }
 
 int kv_read_clear_error() {

@@ -4,9 +4,8 @@
 //     the requests' lengths alone;
 //   * the append: new keys and values quantized into their pages with one
 //     power-of-two scale per page and head.
-#include "bfp8_internal.h"
+#include "attention_layer.cuh"
 #include "kv_common.cuh"
-#include "ptx.cuh"
 
 #include <algorithm>
 
@@ -14,23 +13,6 @@ namespace bfp8 {
 namespace {
 
 using namespace dev;
-
-template <typename Kernel, typename... Args>
-int launch_dependent(Kernel kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
-                     Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return BFP8_ERR_CUDA;
-  return check_launch();
-}
 
 // ------------------------------------------------------------------ block plan
 constexpr int kPlanThreads = 512;

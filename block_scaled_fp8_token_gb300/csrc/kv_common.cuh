@@ -9,7 +9,7 @@
 // folds it into exponents.
 #pragma once
 
-#include "bfp8_internal.h"
+#include "attention_layer.h"
 
 namespace bfp8 {
 

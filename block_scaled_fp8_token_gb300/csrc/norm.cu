@@ -14,8 +14,7 @@
 // BF16, so the codes carry one rounding (to E4M3) where the unfused steps
 // carry three. Bound by HBM: a row is read twice (y, residual) and written
 // once, plus its codes.
-#include "bfp8_internal.h"
-#include "ptx.cuh"
+#include "attention_layer.cuh"
 
 #include <type_traits>
 
@@ -337,19 +336,8 @@ int launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   int fit = by_regs < by_smem ? by_regs : by_smem;
   fit = fit < 1 ? 1 : fit > 2048 / threads ? 2048 / threads : fit > 32 ? 32 : fit;
   const int64_t cap = static_cast<int64_t>(sms) * fit;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T < cap ? p.T : cap));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, residual_norm_kernel<VEC, ROW_GATE, VPT>, p) != cudaSuccess)
-    return BFP8_ERR_CUDA;
-  return check_launch();
+  return launch_dependent(residual_norm_kernel<VEC, ROW_GATE, VPT>,
+                          dim3(static_cast<unsigned>(p.T < cap ? p.T : cap)), threads, smem, st, p);
 }
 
 bool aligned(const void* p, uintptr_t bytes) {

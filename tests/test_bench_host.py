@@ -122,3 +122,13 @@ def test_nvml_stop_without_a_timed_window():
     s.thread = threading.Thread(target=lambda: None)
     s.thread.start()
     assert s.stop() == {}
+
+
+def test_captured_kernels_share_no_source_with_the_attention_layer():
+    """The traffic figures stand while their kernels' sources do: what only the attention layer uses
+    lives in headers of its own, so that a change there leaves them."""
+    for name, entry in bench.NCU_TRAFFIC.items():
+        for f in entry["kernel_files"]:
+            text = (bench.ROOT / "block_scaled_fp8_token_gb300" / "csrc" / f).read_text()
+            for word in ("kv_", "residual_norm", "attention_layer", "tma_load_4d", "f16_ts"):
+                assert word not in text, (name, f, word)
