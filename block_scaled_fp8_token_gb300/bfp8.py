@@ -112,6 +112,72 @@ class bfp8_norm_args(ctypes.Structure):
     ]
 
 
+class bfp8_causal_conv_args(ctypes.Structure):
+    _fields_ = [
+        ("x_bf16", ctypes.c_void_p), ("x_stride_token", ctypes.c_int64),
+        ("out_bf16", ctypes.c_void_p), ("out_stride_token", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("w_dtype", ctypes.c_int32),
+        ("width", ctypes.c_int32), ("silu", ctypes.c_int32), ("state_bf16", ctypes.c_void_p),
+        ("state_stride_slot", ctypes.c_int64), ("state_stride_row", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64), ("slots_in", ctypes.c_void_p), ("slots_out", ctypes.c_void_p),
+        ("q_offsets", ctypes.c_void_p), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+    ]
+
+
+class bfp8_delta_rule_args(ctypes.Structure):
+    _fields_ = [
+        ("q_bf16", ctypes.c_void_p), ("q_stride_token", ctypes.c_int64),
+        ("q_stride_head", ctypes.c_int64), ("k_bf16", ctypes.c_void_p),
+        ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("v_bf16", ctypes.c_void_p), ("v_stride_token", ctypes.c_int64),
+        ("v_stride_head", ctypes.c_int64), ("a_bf16", ctypes.c_void_p),
+        ("a_stride_token", ctypes.c_int64), ("b_bf16", ctypes.c_void_p),
+        ("b_stride_token", ctypes.c_int64), ("a_log", ctypes.c_void_p),
+        ("dt_bias", ctypes.c_void_p), ("state", ctypes.c_void_p),
+        ("state_stride_slot", ctypes.c_int64), ("state_stride_head", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64), ("slots_in", ctypes.c_void_p), ("slots_out", ctypes.c_void_p),
+        ("q_offsets", ctypes.c_void_p), ("out_bf16", ctypes.c_void_p),
+        ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+        ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_q_len", ctypes.c_int64),
+        ("qk_heads", ctypes.c_int64), ("v_heads", ctypes.c_int64), ("head_dim", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("workspace", ctypes.c_void_p),
+        ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
+class bfp8_gated_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("x_bf16", ctypes.c_void_p), ("x_stride_token", ctypes.c_int64),
+        ("x_stride_head", ctypes.c_int64), ("gate_bf16", ctypes.c_void_p),
+        ("gate_stride_token", ctypes.c_int64), ("gate_stride_head", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("w_dtype", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("out_bf16", ctypes.c_void_p),
+        ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+        ("q_e4m3", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("scales", ctypes.c_void_p),
+        ("s_stride_m", ctypes.c_int64), ("s_stride_kb", ctypes.c_int64),
+        ("tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int32),
+    ]
+
+
+class bfp8_rotary_args(ctypes.Structure):
+    _fields_ = [
+        ("q_bf16", ctypes.c_void_p), ("q_stride_token", ctypes.c_int64),
+        ("q_stride_head", ctypes.c_int64), ("q_out_bf16", ctypes.c_void_p),
+        ("q_out_stride_token", ctypes.c_int64), ("q_out_stride_head", ctypes.c_int64),
+        ("k_bf16", ctypes.c_void_p), ("k_stride_token", ctypes.c_int64),
+        ("k_stride_head", ctypes.c_int64), ("k_out_bf16", ctypes.c_void_p),
+        ("k_out_stride_token", ctypes.c_int64), ("k_out_stride_head", ctypes.c_int64),
+        ("positions", ctypes.c_void_p), ("ld_positions", ctypes.c_int64),
+        ("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p), ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float), ("factor", ctypes.c_float), ("tokens", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64), ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+        ("interleaved", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+    ]
+
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {
     "bfp8_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -158,6 +224,11 @@ _SIGS = {
     "bfp8_kv_attention": (ctypes.c_int, [_vp, _vp, _vp]),
     "bfp8_kv_attention_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "bfp8_residual_norm": (ctypes.c_int, [_vp, _i64, _i64, _vp]),
+    "bfp8_causal_conv": (ctypes.c_int, [_vp, _vp]),
+    "bfp8_delta_rule": (ctypes.c_int, [_vp, _vp]),
+    "bfp8_delta_rule_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "bfp8_gated_norm": (ctypes.c_int, [_vp, _vp]),
+    "bfp8_rotary": (ctypes.c_int, [_vp, _vp]),
     "bfp8_device_status": (ctypes.c_int, [_vp]),
     "bfp8_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _vp]),
 }
@@ -927,6 +998,174 @@ def bfp8_residual_norm(y, residual, residual_out=None, *, q=None, scales=None, n
         *(none if norm_out is None else _out_matrix(norm_out, "norm_out", "bf16", T, H, 2, dev)),
         *(none if q is None else _out_matrix(q, "q", "e4m3", T, H, 1, dev)), *scales_at)
     _check(_lib.bfp8_residual_norm(args, T, H, _raw_stream(stream, dev)), "bfp8_residual_norm")
+
+
+# Packed as the library's structs lie in memory (a trailing 0q pads to their size).
+_CAUSAL_CONV = struct.Struct("PqPq2P3iP3q3P3q")        # bfp8_causal_conv_args
+_DELTA_RULE = struct.Struct("P2qP2qP2qPqPq3P3q3PP2q5qiffPN")   # bfp8_delta_rule_args
+_GATED_NORM = struct.Struct("P2qP2qPiiffP2qPqP4qi0q")  # bfp8_gated_norm_args
+_ROTARY = struct.Struct("P2qP2qP2qP2qPq3Pifff3q9i0q")  # bfp8_rotary_args
+BFP8_ACT_SILU, BFP8_ACT_SIGMOID = 0, 1
+
+
+def _slots(state, slots_in, slots_out, B: int, dev: int) -> tuple[int, int, int]:
+    """The pool's slots, and the addresses of the two slot arrays."""
+    if state is None and not (slots_in is None and slots_out is None):
+        raise ValueError("bfp8: slots_in and slots_out need a state")
+    return (0 if state is None else state.shape[0],
+            0 if slots_in is None else _vec(slots_in, "slots_in", "i32", B, dev),
+            0 if slots_out is None else _vec(slots_out, "slots_out", "i32", B, dev))
+
+
+def _weight(w, name: str, shape, dev: int) -> int:
+    """The address of a dense weight on the current device (None: 0)."""
+    if w is None:
+        return 0
+    if w.shape != shape or w.get_device() != dev or not w.is_contiguous():
+        _layout(w, name, shape)
+    return _ptr(w) if w.get_device() != dev else w.data_ptr()
+
+
+def _one_dtype(names: str, *weights) -> int:
+    """The dtype code that the weights share."""
+    kinds = {w.dtype for w in weights if w is not None}
+    if len(kinds) > 1:
+        raise ValueError(f"bfp8: {names} must have the same dtype")
+    return _WEIGHT_CODES.get(kinds.pop(), BFP8_DT_NONE) if kinds else BFP8_DT_BF16
+
+
+def bfp8_causal_conv(x, weight, out, q_offsets, state=None, slots_in=None, slots_out=None, *,
+                     bias=None, silu: bool = True, stream=None) -> None:
+    """The short depthwise convolution of x [T, C] with weight [C, width] over each
+    request's tokens; state [slots, width - 1, C] holds the inputs ahead of them."""
+    dev = _device()
+    T, C = x.shape
+    B, W = q_offsets.shape[0] - 1, weight.shape[1]
+    if state is None:
+        at = (0, 0, 0)
+    else:
+        if state.dim() != 3 or state.shape[1:] != (W - 1, C):
+            raise ValueError(f"bfp8: state has shape {list(state.shape)}, expected "
+                             f"{['slots', W - 1, C]}")
+        if state.dtype is not torch.bfloat16 or state.get_device() != dev:
+            _dtypes(state=(state, "bf16"))
+            _ptr(state)
+        ss, sr, sc = state.stride()
+        if C > 1 and sc != 1:
+            raise ValueError("bfp8: state must have contiguous rows, got strides "
+                             f"{list(state.stride())}")
+        sr = sr if W > 2 else C
+        at = (state.data_ptr(), ss if state.shape[0] > 1 else sr * (W - 1), sr)
+    args = _CAUSAL_CONV.pack(
+        *_matrix(x, "x", "bf16", (T, C), dev), *_out_matrix(out, "out", "bf16", T, C, 2, dev),
+        _weight(weight, "weight", (C, W), dev), _weight(bias, "bias", (C,), dev),
+        _one_dtype("weight and bias", weight, bias), W, silu, *at,
+        *_slots(state, slots_in, slots_out, B, dev),
+        _vec(q_offsets, "q_offsets", "i32", B + 1, dev), B, T, C)
+    _check(_lib.bfp8_causal_conv(args, _raw_stream(stream, dev)), "bfp8_causal_conv")
+
+
+def bfp8_delta_rule_workspace(batch: int, tokens: int, max_q_len: int, qk_heads: int,
+                              v_heads: int) -> int:
+    return int(_lib.bfp8_delta_rule_workspace(batch, tokens, max_q_len, qk_heads, v_heads))
+
+
+def bfp8_delta_rule(q, k, v, a, b, a_log, dt_bias, state, slots_in, slots_out, q_offsets, out,
+                    max_q_len: int, *, scale=None, eps: float = 1e-6, workspace=None,
+                    stream=None) -> None:
+    """The gated delta rule of q, k [T, qk heads, 128] and v [T, v heads, 128] with the
+    gates' inputs a, b [T, v heads]; state [slots, v heads, 128, 128] is float32, a row a
+    value and a column a key. scale defaults to 1 / sqrt(128)."""
+    dev = _device()
+    T, hk, D = q.shape
+    hv, B = v.shape[1], q_offsets.shape[0] - 1
+    if state is None:
+        at = (0, 0, 0)
+    else:
+        if state.dim() != 4 or state.shape[1:] != (hv, D, D):
+            raise ValueError(f"bfp8: state has shape {list(state.shape)}, expected "
+                             f"{['slots', hv, D, D]}")
+        if state.dtype is not torch.float32 or state.get_device() != dev:
+            _dtypes(state=(state, "f32"))
+            _ptr(state)
+        ss, sh, sv, sk = state.stride()
+        if D > 1 and (sv, sk) != (D, 1):
+            raise ValueError("bfp8: state must have dense matrices, got strides "
+                             f"{list(state.stride())}")
+        sh = sh if hv > 1 else D * D
+        at = (state.data_ptr(), ss if state.shape[0] > 1 else sh * hv, sh)
+    args = _DELTA_RULE.pack(
+        *_head_rows(q, "q", T, hk, D, dev), *_head_rows(k, "k", T, hk, D, dev),
+        *_head_rows(v, "v", T, hv, D, dev), *_matrix(a, "a", "bf16", (T, hv), dev),
+        *_matrix(b, "b", "bf16", (T, hv), dev), _vec(a_log, "a_log", "f32", hv, dev),
+        _vec(dt_bias, "dt_bias", "f32", hv, dev), *at,
+        *_slots(state, slots_in, slots_out, B, dev),
+        _vec(q_offsets, "q_offsets", "i32", B + 1, dev), *_head_rows(out, "out", T, hv, D, dev),
+        B, T, max_q_len, hk, hv, D, D ** -0.5 if scale is None else scale, eps,
+        *((0, 0) if workspace is None else _ws(workspace)))
+    _check(_lib.bfp8_delta_rule(args, _raw_stream(stream, dev)), "bfp8_delta_rule")
+
+
+def bfp8_gated_norm(x, gate, weight, out=None, *, q=None, scales=None, eps: float = 1e-6,
+                    weight_offset: float = 0.0, sigmoid: bool = False, s_stride_m=None,
+                    s_stride_kb=None, stream=None) -> None:
+    """The heads x [T, heads, 64, 128 or 256] normed (weight None: not), times SiLU (or the
+    sigmoid) of gate, to BF16 (out) and / or 1x128 codes (q [T, heads * width], scales)."""
+    dev = _device()
+    T, H, D = x.shape
+    scales_at = (0, 0, 0)
+    if q is not None:
+        if scales is None:
+            raise ValueError("bfp8: q needs scales")
+        groups, plain = -(-H * D // 128), s_stride_m is None and s_stride_kb is None
+        ssm = scales.stride(0) if s_stride_m is None else s_stride_m
+        sskb = scales.stride(1) if s_stride_kb is None else s_stride_kb
+        if not plain or scales.dtype is not torch.float32 or scales.get_device() != dev or \
+                scales.shape != (T, groups):
+            _dtypes(scales=(scales, "f32"))
+            _scales_out(scales, "scales", T, groups, ssm, sskb, not plain)
+            _ptr(scales)
+        scales_at = (scales.data_ptr(), ssm if T > 1 else groups, sskb if groups > 1 else 1)
+    args = _GATED_NORM.pack(
+        *_head_rows(x, "x", T, H, D, dev), *_head_rows(gate, "gate", T, H, D, dev),
+        _weight(weight, "weight", (D,), dev), _one_dtype("weight", weight),
+        BFP8_ACT_SIGMOID if sigmoid else BFP8_ACT_SILU, eps, weight_offset,
+        *((0, 0, 0) if out is None else _head_rows(out, "out", T, H, D, dev)),
+        *((0, 0) if q is None else _out_matrix(q, "q", "e4m3", T, H * D, 1, dev)), *scales_at,
+        T, H, D)
+    _check(_lib.bfp8_gated_norm(args, _raw_stream(stream, dev)), "bfp8_gated_norm")
+
+
+def bfp8_rotary(q, k, positions, inv_freq, q_out=None, k_out=None, *, sections=None,
+                interleaved: bool = False, adjacent: bool = False, q_weight=None, k_weight=None,
+                eps: float = 1e-6, weight_offset: float = 0.0, factor: float = 1.0,
+                stream=None) -> None:
+    """Rotary positions on q and k [T, heads, 64, 128 or 256] (k may be None), in place
+    unless q_out and k_out are given, behind the heads' norms where q_weight and k_weight
+    are. positions is [T], or [axes, T] with sections pairs of columns to each axis."""
+    dev = _device()
+    T, _, D = q.shape
+    half = inv_freq.shape[0]
+    axes, pos = (1, (_vec(positions, "positions", "i32", T, dev), T)) if positions.dim() == 1 else \
+        (positions.shape[0], _matrix(positions, "positions", "i32", (positions.shape[0], T), dev))
+    parts = [half] if sections is None else list(sections)
+    if len(parts) != axes or axes > 4:
+        raise ValueError(f"bfp8: {len(parts)} sections for {axes} axes of positions (1 to 4)")
+    at = []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            at += [0] * 6
+            continue
+        H = x.shape[1]
+        at += [*_head_rows(x, name, T, H, D, dev),
+               *_head_rows(x if out is None else out, name + "_out", T, H, D, dev)]
+    args = _ROTARY.pack(
+        *at, *pos, _vec(inv_freq, "inv_freq", "f32", half, dev),
+        _weight(q_weight, "q_weight", (D,), dev), _weight(k_weight, "k_weight", (D,), dev),
+        _one_dtype("q_weight and k_weight", q_weight, k_weight), eps, weight_offset, factor, T,
+        q.shape[1], 0 if k is None else k.shape[1], D, 2 * half, axes,
+        *parts, *(0,) * (4 - axes), interleaved, adjacent)
+    _check(_lib.bfp8_rotary(args, _raw_stream(stream, dev)), "bfp8_rotary")
 
 
 def bfp8_device_status(stream=None) -> int:

@@ -23,7 +23,8 @@ BUILD = PKG / "_build"
 LIB = PKG / "libbfp8.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cpp", "quant.cu", "gemm_sm103.cu", "gemv_decode.cu", "kv_cache.cu",
-           "kv_attention.cu", "norm.cu"]
+           "kv_attention.cu", "norm.cu", "causal_conv.cu", "delta_rule.cu", "gated_norm.cu",
+           "rotary.cu"]
 
 
 def _nvcc() -> str:

@@ -8,6 +8,7 @@
 
 #include "attention_layer.h"
 #include "bfp8_internal.h"
+#include "hybrid_layer.h"
 
 namespace bfp8 {
 
@@ -561,6 +562,34 @@ int bfp8_kv_attention(const bfp8_kv_attention_args* args, const bfp8_kv_cache* c
 int bfp8_residual_norm(const bfp8_norm_args* args, int64_t T, int64_t H, void* stream) {
   if (!args) return BFP8_ERR_INVALID_ARG;
   return launch_residual_norm(*args, T, H, stream);
+}
+
+int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream) {
+  if (!args) return BFP8_ERR_INVALID_ARG;
+  return launch_causal_conv(*args, stream);
+}
+
+size_t bfp8_delta_rule_workspace(int64_t batch, int64_t tokens, int64_t max_q_len,
+                                 int64_t qk_heads, int64_t v_heads) {
+  if (batch <= 0 || tokens <= 0 || max_q_len <= 0 || qk_heads <= 0 || v_heads <= 0 ||
+      v_heads % qk_heads)
+    return 0;
+  return delta_rule_workspace_bytes(batch, tokens, max_q_len, qk_heads, v_heads);
+}
+
+int bfp8_delta_rule(const bfp8_delta_rule_args* args, void* stream) {
+  if (!args) return BFP8_ERR_INVALID_ARG;
+  return launch_delta_rule(*args, stream);
+}
+
+int bfp8_gated_norm(const bfp8_gated_norm_args* args, void* stream) {
+  if (!args) return BFP8_ERR_INVALID_ARG;
+  return launch_gated_norm(*args, stream);
+}
+
+int bfp8_rotary(const bfp8_rotary_args* args, void* stream) {
+  if (!args) return BFP8_ERR_INVALID_ARG;
+  return launch_rotary(*args, stream);
 }
 
 int bfp8_selftest_wait_timeout(uint64_t limit_ns, void* stream) {

@@ -1,0 +1,82 @@
+// hybrid_layer.cuh -- what the kernels of a hybrid decoder's operators share: BF16 vectors,
+// the functions of their gates, and which request of a ragged step a tile of tokens belongs to.
+#pragma once
+
+#include "attention_layer.cuh"
+#include "hybrid_layer.h"
+
+namespace bfp8 {
+namespace dev {
+
+// Eight BF16 of a 16-byte vector, and back with one rounding each.
+BFP8_DEV void widen8(const uint4& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+BFP8_DEV uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+BFP8_DEV uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// 1 / (1 + e^-x), relative error below (4 + 1.2 max(0, -x)) 2^-23: the approximate exponential's
+// is 2 + 1.16 |x| units, and counts in full where e^-x outweighs the 1. That is under 2^-16
+// down to x = -88, below which e^-x overflows and the result is 0: for results that BF16 or
+// E4M3 rounds (2^-8, 2^-4).
+BFP8_DEV float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+BFP8_DEV float silu(float x) { return x * sigmoid(x); }
+
+// The requests of a step lie one behind another: request b has the tokens
+// [offsets[b], offsets[b + 1]), within [0, T] whatever the array holds.
+struct Requests {
+  const int32_t* offsets;
+  const int32_t* slots_in;
+  const int32_t* slots_out;
+  int64_t tokens, n_slots;
+  int32_t batch;
+};
+BFP8_DEV int64_t clamp_token(const Requests& q, int32_t t) {
+  return t < 0 ? 0 : t > q.tokens ? q.tokens : t;
+}
+BFP8_DEV int64_t first_token(const Requests& q, int b) { return clamp_token(q, __ldg(q.offsets + b)); }
+// The slot that request b reads (out: writes), -1 for none.
+BFP8_DEV int64_t slot_of(const Requests& q, const int32_t* slots, int b) {
+  if (!slots) return -1;
+  const int32_t s = __ldg(slots + b);
+  return s < 0 || s >= q.n_slots ? -1 : s;
+}
+
+// Tiles of 2^shift tokens that begin with each request's first: request b's are numbered
+// from key(b) = (offsets[b] >> shift) + b on. As ceil(n / 2^shift) <= (offsets[b + 1] >>
+// shift) - (offsets[b] >> shift) + 1, no two requests share a number, all lie below
+// (T >> shift) + batch, and the numbers need no sum over the requests ahead.
+BFP8_DEV int64_t tile_key(const Requests& q, int b, int shift) {
+  return (first_token(q, b) >> shift) + b;
+}
+// The request whose tile y would be: the last with key(b) <= y, or -1. The whole warp
+// searches, 32 probes at a time.
+BFP8_DEV int find_request(const Requests& q, int64_t y, int shift) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = q.batch;
+  while (true) {
+    const int step = (n + 31) >> 5;
+    const int at = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < n && tile_key(q, lo + at, shift) <= y);
+    if (m == 0) return -1;
+    const int c = 31 - __clz(m);
+    lo += c * step;
+    if (step == 1) return lo;
+    n = min(step, n - c * step);
+  }
+}
+
+}  // namespace dev
+}  // namespace bfp8

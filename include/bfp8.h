@@ -696,6 +696,184 @@ typedef struct {
  * SCALE_DTYPE (w_dtype), UNSUPPORTED (H > 16384). */
 int bfp8_residual_norm(const bfp8_norm_args* args, int64_t T, int64_t H, void* stream);
 
+/* ---- a hybrid decoder's layers: linear attention, and rotary positions ------ */
+/*
+ * Requests as above: their new tokens lie one behind another, q_offsets [batch + 1]
+ * apart. What a request keeps between steps is in a slot of a pool: it is read from
+ * slots_in[b] and left in slots_out[b] (device int32 [batch]; usually the same array,
+ * or two where a step's states are kept until its drafted tokens are accepted). A
+ * slot outside [0, n_slots), or no array, begins from zeros, or keeps nothing. A
+ * request without new tokens touches neither slot. Within one call a slot is
+ * written by one request at most, and read by no other request than the one that
+ * writes it; any number may read a slot that none writes.
+ */
+
+/*
+ * bfp8_causal_conv -- the short depthwise convolution ahead of a linear-attention layer:
+ *   out[t, c] = act(bias[c] + sum_j weight[c, j] * x[t - (width - 1) + j, c])
+ * with float32 sums and one rounding to BF16. The width - 1 inputs ahead of a
+ * request's first token are its state, oldest first; its last ones become it.
+ * T == 0, batch == 0 or channels == 0 is a no-op. Errors: INVALID_ARG (null
+ * pointers, negative sizes, strides below the channels, slots without a state, out
+ * that is x), SCALE_DTYPE (w_dtype), UNSUPPORTED (width, channels not a multiple of
+ * 8, rows or weights that are not 16-byte aligned, more than 65535 requests).
+ */
+typedef struct {
+  const void* x_bf16;            /* [tokens, channels] BF16                      */
+  int64_t x_stride_token;
+  void* out_bf16;                /* [tokens, channels]; must not overlap x       */
+  int64_t out_stride_token;
+  const void* weight;            /* [channels, width], dense                     */
+  const void* bias;              /* [channels]; may be NULL                      */
+  int32_t w_dtype;               /* BFP8_DT_BF16 or BFP8_DT_F32, of both         */
+  int32_t width;                 /* 2, 3 or 4                                    */
+  int32_t silu;                  /* 0: no activation                             */
+  void* state_bf16;              /* [n_slots, width - 1, channels]; may be NULL  */
+  int64_t state_stride_slot, state_stride_row;   /* elements                     */
+  int64_t n_slots;
+  const int32_t* slots_in;
+  const int32_t* slots_out;
+  const int32_t* q_offsets;
+  int64_t batch, tokens, channels;
+} bfp8_causal_conv_args;
+
+int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream);
+
+/*
+ * bfp8_delta_rule -- the gated delta rule: per value head h and token, with the
+ * key head h / (v_heads / qk_heads) and the state S [128 values, 128 keys],
+ *   alpha = exp(-exp(a_log[h]) * softplus(a + dt_bias[h])),  beta = sigmoid(b)
+ *   k' = k * rsqrt(|k|^2 + eps),  q' = scale * q * rsqrt(|q|^2 + eps)
+ *   u = beta * (v - alpha * S k'),  S <- alpha * S + u k'^T,  out = S q'
+ * State, sums and gates are float32; out is rounded to BF16 once. One ragged call
+ * serves single tokens, drafted ones, and prompts.
+ *   q, k, v, out  [tokens, heads, 128] BF16, 16-byte aligned, token and head strides
+ *               in elements, multiples of 8, for example columns of the convolution's
+ *               output. out must not overlap the inputs.
+ *   a, b        [tokens, v_heads] BF16, token strides in elements
+ *   max_q_len   at least the most new tokens of a request; those past it are left out
+ *   workspace   at least bfp8_delta_rule_workspace() bytes, 256-byte aligned, contents
+ *               free (may be NULL where that is 0); calls sharing it must not overlap
+ * A NaN or an infinity among a token's inputs reaches its request's outputs from there
+ * on, and its state. Nothing synchronises with the host, results do not depend on what
+ * else runs, and a step can be captured in a CUDA graph. tokens == 0, batch == 0 or
+ * max_q_len == 0 is a no-op. Errors: INVALID_ARG (null pointers, negative sizes, v_heads
+ * not a multiple of qk_heads, strides below a row, slots without a state, workspace
+ * missing or too small), UNSUPPORTED (head width, alignment).
+ */
+typedef struct {
+  const void* q_bf16;
+  int64_t q_stride_token, q_stride_head;
+  const void* k_bf16;
+  int64_t k_stride_token, k_stride_head;
+  const void* v_bf16;
+  int64_t v_stride_token, v_stride_head;
+  const void* a_bf16;
+  int64_t a_stride_token;
+  const void* b_bf16;
+  int64_t b_stride_token;
+  const float* a_log;            /* [v_heads]                                    */
+  const float* dt_bias;          /* [v_heads]                                    */
+  float* state;                  /* [n_slots, v_heads, 128 values, 128 keys], each head's
+                                    matrix dense; may be NULL                    */
+  int64_t state_stride_slot, state_stride_head;  /* elements, multiples of 4     */
+  int64_t n_slots;
+  const int32_t* slots_in;
+  const int32_t* slots_out;
+  const int32_t* q_offsets;
+  void* out_bf16;
+  int64_t out_stride_token, out_stride_head;
+  int64_t batch, tokens, max_q_len, qk_heads, v_heads;
+  int32_t head_dim;              /* 128                                          */
+  float scale, eps;
+  void* workspace;
+  size_t ws_bytes;
+} bfp8_delta_rule_args;
+
+size_t bfp8_delta_rule_workspace(int64_t batch, int64_t tokens, int64_t max_q_len,
+                                 int64_t qk_heads, int64_t v_heads);
+int bfp8_delta_rule(const bfp8_delta_rule_args* args, void* stream);
+
+/*
+ * bfp8_gated_norm -- the heads' outputs normed, gated and quantized for the output
+ * projection, per token and head:
+ *   y = (weight ? x * rsqrt(mean(x^2) + eps) * (weight + weight_offset) : x) * act(gate)
+ *   out = bf16_rn(y); per 128 columns of a token's heads, one behind another,
+ *   s = max(max|y|, 1e-10f) / 448, q = RNE_satfinite_e4m3(y / s)   (the quotient within 2^-21)
+ * in float32: the quantizer takes y before it is rounded to BF16.
+ * tokens == 0 or heads == 0 is a no-op. Errors: INVALID_ARG (null x or gate, no
+ * output, strides below a row, q without scales, gate_act, eps < 0), SCALE_DTYPE
+ * (w_dtype), UNSUPPORTED (head width, rows that are not 16-byte aligned, codes' rows
+ * that are not 8-byte aligned).
+ */
+enum bfp8_gate_act { BFP8_ACT_SILU = 0, BFP8_ACT_SIGMOID = 1 };
+
+typedef struct {
+  const void* x_bf16;            /* [tokens, heads, head_dim]; strides in elements */
+  int64_t x_stride_token, x_stride_head;
+  const void* gate_bf16;
+  int64_t gate_stride_token, gate_stride_head;
+  const void* weight;            /* [head_dim]; NULL: no norm                    */
+  int32_t w_dtype;               /* BFP8_DT_BF16 or BFP8_DT_F32                  */
+  int32_t gate_act;              /* enum bfp8_gate_act                           */
+  float eps, weight_offset;
+  void* out_bf16;                /* may be x or gate itself; NULL: not written   */
+  int64_t out_stride_token, out_stride_head;
+  void* q_e4m3;                  /* [tokens, heads * head_dim] E4M3, row stride ldq bytes; NULL: not written */
+  int64_t ldq;
+  float* scales;                 /* (m, g) at scales[m*s_stride_m + g*s_stride_kb] */
+  int64_t s_stride_m, s_stride_kb;
+  int64_t tokens, heads;
+  int32_t head_dim;              /* 64, 128 or 256                               */
+} bfp8_gated_norm_args;
+
+int bfp8_gated_norm(const bfp8_gated_norm_args* args, void* stream);
+
+/*
+ * bfp8_rotary -- rotary positions of one to four axes (an image's row and column, a
+ * video's time) on queries and keys, with the heads' norm ahead of them:
+ *   x = weight ? x * rsqrt(mean(x^2) + eps) * (weight + weight_offset) : x   per head
+ *   angle_i = positions[axis(i), t] * inv_freq[i],  i < rotary_dim / 2
+ *   (x_a, x_b) = factor * (x_a cos - x_b sin, x_b cos + x_a sin)
+ * for the pair (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) where `adjacent`.
+ * Columns from rotary_dim on are normed only. The angle keeps its digits at positions
+ * of any size: it is within 2^-24 of half a turn; the result is rounded once to BF16.
+ * axis(i): sections[n] pairs turn with axis n, one section behind another; or, where
+ * `interleaved`, i % axes while i / axes < sections[that axis], else axis 0. The
+ * sections add up to rotary_dim / 2.
+ * A token with a negative position on any axis is left alone: nothing of it is written.
+ * inv_freq entries of 2^32 and more, and those that are not finite, give NaN.
+ * tokens == 0 or no heads is a no-op. Errors: INVALID_ARG (null pointers, negative
+ * sizes, sections that do not add up, strides below a row, eps < 0, factor not finite),
+ * SCALE_DTYPE (w_dtype), UNSUPPORTED (head width, rotary_dim not a multiple of 16, rows
+ * that are not 16-byte aligned).
+ */
+typedef struct {
+  const void* q_bf16;            /* [tokens, q_heads, head_dim]; strides in elements */
+  int64_t q_stride_token, q_stride_head;
+  void* q_out_bf16;              /* may be q itself                              */
+  int64_t q_out_stride_token, q_out_stride_head;
+  const void* k_bf16;            /* [tokens, k_heads, head_dim]                  */
+  int64_t k_stride_token, k_stride_head;
+  void* k_out_bf16;
+  int64_t k_out_stride_token, k_out_stride_head;
+  const int32_t* positions;      /* [axes, tokens], row stride ld_positions      */
+  int64_t ld_positions;
+  const float* inv_freq;         /* [rotary_dim / 2]                             */
+  const void* q_weight;          /* [head_dim]; NULL: no norm                    */
+  const void* k_weight;
+  int32_t w_dtype;               /* BFP8_DT_BF16 or BFP8_DT_F32, of both         */
+  float eps, weight_offset, factor;
+  int64_t tokens, q_heads, k_heads;
+  int32_t head_dim;              /* 64, 128 or 256                               */
+  int32_t rotary_dim;
+  int32_t axes;                  /* 1 to 4                                       */
+  int32_t sections[4];
+  int32_t interleaved, adjacent;
+} bfp8_rotary_args;
+
+int bfp8_rotary(const bfp8_rotary_args* args, void* stream);
+
 /* ---- diagnostics ---------------------------------------------------------- */
 /*
  * bfp8_device_status -- synchronise `stream`, then read and clear the library's
