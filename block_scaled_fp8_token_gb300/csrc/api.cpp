@@ -602,9 +602,12 @@ int bfp8_device_status(void* stream) {
   const int a = gemm_read_clear_error();
   const int b = gemv_read_clear_error();
   const int c = kv_read_clear_error();
-  if (a == BFP8_ERR_CUDA || b == BFP8_ERR_CUDA || c == BFP8_ERR_CUDA) return BFP8_ERR_CUDA;
-  if (a != BFP8_OK) return a;
-  return b != BFP8_OK ? b : c;
+  const int d = delta_read_clear_error();
+  for (int status : {a, b, c, d})
+    if (status == BFP8_ERR_CUDA) return status;
+  for (int status : {a, b, c, d})
+    if (status != BFP8_OK) return status;
+  return BFP8_OK;
 }
 
 }  // extern "C"
