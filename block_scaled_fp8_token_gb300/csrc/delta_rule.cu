@@ -143,48 +143,87 @@ __global__ void __launch_bounds__(32 * kStepWarps) delta_step_kernel(const Delta
 // ------------------------------------------------------------------ chunks of 64 tokens
 //
 // Within a chunk of C tokens that begins with the state S0, write Gamma_i = alpha_0 .. alpha_i,
-// and k, q for the raw rows with ck, cq their factors (cq has the scale). Then
+// and k, q for the rows with ck, cq their factors. Then
 //   A_ij = beta_i ck_i ck_j (Gamma_i / Gamma_j) (k_i . k_j)      j < i
 //   u = (1 + A)^-1 r,   r_i = beta_i (v_i - Gamma_i ck_i S0 k_i)
-//   out_i = Gamma_i cq_i S0 q_i + sum_j P_ij u_j,   P_ij = cq_i ck_j (Gamma_i / Gamma_j) (q_i . k_j)   j <= i
+//   out_i = scale (Gamma_i cq_i S0 q_i + sum_j P_ij u_j),   P_ij = cq_i ck_j (Gamma_i / Gamma_j) (q_i . k_j)   j <= i
 //   S = Gamma_C S0 + sum_j (Gamma_C / Gamma_j) ck_j u_j k_j^T
 // The first kernel forms T = (1 + A)^-1 and P T of every chunk at once, which need no state;
 // the second walks down each request's chunks, three products one behind another a chunk:
-//   [S0 K^T | S0 Q^T]  ->  r [T^T | (P T)^T] = [u | sum P u]  ->  u K
+//   S0 [K^T | Q^T]  ->  r [T^T | (P T)^T] = [u | sum P u]  ->  u K
 // Ratios of Gamma are running products of the alphas, so no difference of sums of logarithms
 // loses digits and a decay to 0 gives 0.
 //
-// FP32 operands meet the tensor cores in BF16 parts whose sum they are: a value is cut into
-// three of 8 bits each, exactly, and products of parts below 2^-24 are left out; K and Q are
-// BF16 as they come and enter raw, so that their products are exact.
+// On the tensor cores an FP32 value is two F16 parts, the rounded value and its rounded rest:
+// 22 bits, and no less than 2^-25 of what the operand's row or matrix is scaled to. Products of
+// two rests are left out (2^-24). What each operand is scaled by is a power of two:
+//   K, Q   each row to a largest entry in [1, 2): BF16's 8 bits are then exact in F16 down to
+//          2^-17 of the largest, and enter as one part; the factors ck, cq take the power back
+//   T, P T by 2^12. No entry exceeds 1: column j is what the rule answers to a single value at
+//          token j, whose state is a key of length 1 at most and never grows
+//   S, r, u: all three are linear in a row of S and of the values, so one power of two a row
+//          serves them; the walk watches it (below)
 constexpr int kChunk = 64, kShift = 6;
-constexpr int kHalfTile = kChunk * 128;                // 64 rows of 128 bytes: half the columns of a K, Q or V tile
-constexpr int kTile = 2 * kHalfTile;
-constexpr int kPart = kChunk * kChunk * 2;             // one BF16 part of T or P T
-constexpr int kScalars = 5 * kPart;                    // behind T's three parts and P T's two
-// beta, beta Gamma ck, Gamma cq, (Gamma_C / Gamma) ck of each token, then Gamma_C
+constexpr int kHalfTile = kChunk * 128;                // 64 rows of 128 bytes
+constexpr int kTile = 2 * kHalfTile;                   // 128 such rows: K over Q of 64 columns, or T over P T
+constexpr int kKq = 2 * kTile;                         // both halves of the columns
+constexpr int kScalars = 2 * kTile;                    // of a blob: T over P T, the parts, then
+// beta, beta Gamma ck, Gamma cq, (Gamma_C / Gamma) ck 2^-12 of each token, and Gamma_C
 constexpr int kBeta = 0, kKey = 64, kQuery = 128, kUpdate = 192, kGammaC = 256;
 constexpr int kBlob = kScalars + 1152;
+constexpr float kTScale = 4096.0f;
 
 __device__ int g_delta_err;
 
+// Of each chunk's slot the workspace has the K and Q rows of each key head, then a blob for
+// each value head.
 struct ChunkParams {
   DeltaParams d;
   uint8_t* ws;
+  int32_t qk_heads, subgroups, per_block;              // value heads a block of the first kernel takes
 };
-
-BFP8_DEV uint32_t cut_pair(float a, float b) {         // the upper halves of two floats, as a BF16 pair
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+BFP8_DEV int64_t slot_bytes(const ChunkParams& p) {
+  return static_cast<int64_t>(p.qk_heads) * kKq + static_cast<int64_t>(p.d.v_heads) * kBlob;
 }
-// A pair's three parts; what is left after the first two has 8 bits.
-BFP8_DEV void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  hi = cut_pair(x.x, x.y);
-  x = __fadd2_rn(x, make_float2(__uint_as_float((__float_as_uint(x.x) & 0xFFFF0000u) ^ 0x80000000u),
-                                __uint_as_float((__float_as_uint(x.y) & 0xFFFF0000u) ^ 0x80000000u)));
-  mid = cut_pair(x.x, x.y);
-  x = __fadd2_rn(x, make_float2(__uint_as_float((__float_as_uint(x.x) & 0xFFFF0000u) ^ 0x80000000u),
-                                __uint_as_float((__float_as_uint(x.y) & 0xFFFF0000u) ^ 0x80000000u)));
-  lo = cut_pair(x.x, x.y);
+BFP8_DEV uint8_t* kq_at(const ChunkParams& p, int64_t slot, int hk) {
+  return p.ws + slot * slot_bytes(p) + static_cast<int64_t>(hk) * kKq;
+}
+BFP8_DEV uint8_t* blob_at(const ChunkParams& p, int64_t slot, int h) {
+  return p.ws + slot * slot_bytes(p) + static_cast<int64_t>(p.qk_heads) * kKq + static_cast<int64_t>(h) * kBlob;
+}
+
+BFP8_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// A pair's two F16 parts.
+BFP8_DEV void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16x2(x.x, x.y);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = pack_f16x2(x.x - h.x, x.y - h.y);
+}
+// The larger size, of each half of a pair.
+BFP8_DEV uint32_t max_abs_f16x2(uint32_t m, uint32_t v) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&m), __habs2(*reinterpret_cast<const __half2*>(&v)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+BFP8_DEV float max_f16x2(uint32_t m) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+  return fmaxf(f.x, f.y);
+}
+BFP8_DEV uint32_t max_abs_bf16x2(uint32_t m, uint32_t v) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                   __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+BFP8_DEV float max_bf16x2(uint32_t m) {
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+// The power of two that brings m to [2^to, 2^(to + 1)), within 2^-125 .. 2^125.
+BFP8_DEV float power_for(float m, int to) {
+  const int e = 127 + to - static_cast<int>((__float_as_uint(m) >> 23) & 0xFF);
+  return __uint_as_float(static_cast<uint32_t>(127 + min(max(e, -125), 125)) << 23);
 }
 
 BFP8_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -196,8 +235,8 @@ BFP8_DEV void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                : "memory");
 }
-// A tile of 64 tokens of one head, each half of the columns in rows of 128 bytes with the
-// 128-byte swizzle, the halves `apart` bytes apart. Rows past the tensor's are zeros.
+// 64 tokens of one head, each half of the columns in rows of 128 bytes with the 128-byte
+// swizzle, the halves `apart` bytes apart. Rows past the tensor's are zeros.
 BFP8_DEV void load_tile(uint32_t dst, uint32_t apart, const CUtensorMap* map, int head, int row, uint32_t bar) {
   tma_load_3d(dst, map, 0, head, row, bar);
   tma_load_3d(dst + apart, map, 64, head, row, bar);
@@ -209,56 +248,106 @@ BFP8_DEV int64_t chunked_len(const DeltaParams& p, int b, int64_t& first) {
   n = n < p.max_len ? n : p.max_len;
   return n > p.step_len ? n : 0;
 }
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int m, int n) { return idesc_f16(m, n) | (1u << 16); }
+BFP8_DEV void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  umma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);   // the operands' type is in idesc
+}
 
-constexpr int kPrepThreads = 128;
-constexpr int kAtPitch = 68;
+constexpr int kPrepThreads = 256;
+constexpr int kPitch = 68;                             // floats of a row of A, T or Z
+constexpr int kGroup = 4;                              // value heads a block takes, at most
 struct PrepShared {
-  alignas(16) float at[kChunk * kAtPitch];             // A transposed: row j holds A_ij, i > j
-  float alpha[kChunk], ck[kChunk];
-  uint64_t full, done;
+  alignas(16) float A[kChunk * kPitch];                // A, zeros from its diagonal on; then block by block T
+  float Z[32 * kPitch];
+  float alpha[kGroup][kChunk], beta[kGroup][kChunk], gamma[kGroup][kChunk], rest[kGroup][kChunk];
+  float upper[kGroup][kChunk];                         // alpha_32 .. alpha_i
+  float factor[2 * kChunk], squares[2][2 * kChunk], largest[2][2 * kChunk];
+  uint64_t full, gram, product;
   uint32_t tmem;
   int abort_flag;
 };
-constexpr int kPrepSmem = 1024 + kBlob + 1024 + static_cast<int>(sizeof(PrepShared));
+constexpr int kPrepSharedAt = (kBlob + 1023) / 1024 * 1024;   // the blob takes the K and Q rows' place
+constexpr int kPrepSmem = 1024 + kPrepSharedAt + static_cast<int>(sizeof(PrepShared));
 
-// x (1 + A) = w for one row in `w`, columns LIM - 1 down to 0: w_j -= sum_{l > j} w_l A_lj.
-template <int LIM>
-BFP8_DEV void solve_row(float (&w)[kChunk], const float* at) {
+// Running products over the warp, of 32 values from the first to each lane's.
+BFP8_DEV float scan_product(float v, int lane) {
 #pragma unroll
-  for (int j = LIM - 2; j >= 0; --j) {
-    float2 s = make_float2(0.0f, 0.0f), s2 = s;
-#pragma unroll
-    for (int l = (j + 1) & ~3; l < LIM; l += 4) {
-      const float4 c = *reinterpret_cast<const float4*>(at + j * kAtPitch + l);
-      if (l > j) {
-        s = __ffma2_rn(make_float2(w[l], w[l + 1]), make_float2(c.x, c.y), s);
-        s2 = __ffma2_rn(make_float2(w[l + 2], w[l + 3]), make_float2(c.z, c.w), s2);
-      } else {
-        if (l + 1 > j) s.y = fmaf(w[l + 1], c.y, s.y);
-        if (l + 2 > j) s2.x = fmaf(w[l + 2], c.z, s2.x);
-        s2.y = fmaf(w[l + 3], c.w, s2.y);
-      }
-    }
-    w[j] -= (s.x + s2.x) + (s.y + s2.y);
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v *= u;
   }
+  return v;
+}
+// ... and of the values behind each lane's.
+BFP8_DEV float scan_product_behind(float v, int lane) {
+  float r = __shfl_down_sync(0xffffffffu, v, 1);
+  if (lane == 31) r = 1.0f;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_down_sync(0xffffffffu, r, o);
+    if (lane + o < 32) r *= u;
+  }
+  return r;
 }
 
-// T and P T of one chunk of one value head. Threads 0 - 63 have the chunk's key rows, 64 - 127
-// its query rows: one product of both with the keys leaves row i of K K^T and of Q K^T in the
-// threads' registers. Thread i forms row i of A, thread 64 + i row i of P; and as T (1 + A) = 1
-// and (P T)(1 + A) = P, all 128 rows are then solved alike, each by a thread of its own, against
-// A in shared memory.
-__global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const __grid_constant__ CUtensorMap tq,
+// out (rows x 32 of a 4-column piece a thread) = sign * X (rows x N) Y (N x 32), all in shared
+// memory with pitch kPitch.
+template <int N>
+BFP8_DEV float4 product4(const float* x, const float* y) {
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int l = 0; l < N; l += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(x + l);
+    const float c[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 b = *reinterpret_cast<const float4*>(y + (l + e) * kPitch);
+      s.x = fmaf(c[e], b.x, s.x), s.y = fmaf(c[e], b.y, s.y), s.z = fmaf(c[e], b.z, s.z), s.w = fmaf(c[e], b.w, s.w);
+    }
+  }
+  return s;
+}
+// Two rows of it.
+template <int N>
+BFP8_DEV void product2x4(const float* x, const float* y, float4 (&s)[2]) {
+  s[0] = s[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int l = 0; l < N; l += 4) {
+    const float4 a[2] = {*reinterpret_cast<const float4*>(x + l), *reinterpret_cast<const float4*>(x + kPitch + l)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 b = *reinterpret_cast<const float4*>(y + (l + e) * kPitch);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float c = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
+        s[i].x = fmaf(c, b.x, s[i].x), s[i].y = fmaf(c, b.y, s[i].y);
+        s[i].z = fmaf(c, b.z, s[i].z), s[i].w = fmaf(c, b.w, s[i].w);
+      }
+    }
+  }
+}
+BFP8_DEV float4 negate(float4 v) { return make_float4(-v.x, -v.y, -v.z, -v.w); }
+
+// T and P T of one chunk, for up to four value heads of one key head. One product of the K rows
+// and the Q rows with the K rows leaves row i of K K^T and of Q K^T in a lane of tensor memory;
+// two threads share a lane's columns. (1 + A)^-1 is formed by blocks of 16: the diagonal ones
+// column by column, then each lower one as -T_b A_ba T_a, of 16 rows and of 32. P T is a
+// product on the tensor cores again.
+__global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __grid_constant__ CUtensorMap tq,
                                                                      const __grid_constant__ CUtensorMap tk,
                                                                      const ChunkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  PrepShared& sh = *reinterpret_cast<PrepShared*>(base + (kBlob + 1023) / 1024 * 1024);
-  const uint32_t tile = smem_u32(base);                // K and Q rows, then what goes to memory
-  const int tid = threadIdx.x, warp = tid >> 5;
+  PrepShared& sh = *reinterpret_cast<PrepShared*>(base + kPrepSharedAt);
+  const uint32_t kq = smem_u32(base), blob = kq;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const int h = blockIdx.x % p.d.v_heads;
-  const int64_t slot = blockIdx.x / p.d.v_heads;
+  const int hk = blockIdx.x % p.qk_heads, sub = blockIdx.x / p.qk_heads % p.subgroups;
+  const int64_t slot = blockIdx.x / (p.qk_heads * p.subgroups);
+  const int h0 = hk * p.d.group + sub * p.per_block, heads = min(p.per_block, p.d.group - sub * p.per_block);
   const int b = find_request(p.d.req, slot, kShift);
   if (b < 0) return;
   int64_t first;
@@ -267,175 +356,349 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const __gri
   if (done >= len) return;
   const int n = static_cast<int>(len - done < kChunk ? len - done : kChunk);
   const int64_t t0 = first + done;
-  const int i = tid & 63;
-  const bool query = tid >= 64;
+  const int row = (warp & 3) * 32 + lane, i = row & 63, half = warp >> 2;
+  const bool query = row >= kChunk;
 
   if (tid == 0) {
     mbar_init(smem_u32(&sh.full), 1);
-    mbar_init(smem_u32(&sh.done), 1);
+    mbar_init(smem_u32(&sh.gram), 1);
+    mbar_init(smem_u32(&sh.product), 1);
     sh.abort_flag = 0;
     mbar_fence_init();
-    mbar_arrive_expect_tx(smem_u32(&sh.full), 2 * kTile);
-    const int hk = h / p.d.group;
-    load_tile(tile, kTile, &tk, hk, static_cast<int>(t0), smem_u32(&sh.full));
-    load_tile(tile + kHalfTile, kTile, &tq, hk, static_cast<int>(t0), smem_u32(&sh.full));
+    mbar_arrive_expect_tx(smem_u32(&sh.full), kKq);
+    load_tile(kq, kTile, &tk, hk, static_cast<int>(t0), smem_u32(&sh.full));
+    load_tile(kq + kHalfTile, kTile, &tq, hk, static_cast<int>(t0), smem_u32(&sh.full));
   }
-  if (warp == 0) {
-    __syncwarp();
-    tmem_alloc(smem_u32(&sh.tmem), 64);
+  if (warp == 7) {
+    tmem_alloc(smem_u32(&sh.tmem), 128);
     tmem_relinquish();
   }
-  float beta = 0.0f;
-  if (!query) {
-    float alpha = 1.0f;
-    if (i < n) {
-      const float a = __bfloat162float(p.d.a[(t0 + i) * p.d.at + h]);
-      alpha = expf(log_decay(a, __ldg(p.d.dt_bias + h), expf(__ldg(p.d.a_log + h))));
-      beta = beta_of(__bfloat162float(p.d.b[(t0 + i) * p.d.bt + h]));
-    }
-    sh.alpha[i] = alpha;
+  // the gates' inputs, of a value head a warp: asked for here, used while the rows' product runs
+  const int gate = warp - 1;
+  uint16_t ga[2] = {}, gb[2] = {};
+  float rate = 0.0f, dt_bias = 0.0f;
+  if (gate >= 0 && gate < heads) {
+    rate = __ldg(p.d.a_log + h0 + gate), dt_bias = __ldg(p.d.dt_bias + h0 + gate);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 32 * e < n) {
+        ga[e] = *reinterpret_cast<const uint16_t*>(p.d.a + (t0 + lane + 32 * e) * p.d.at + h0 + gate);
+        gb[e] = *reinterpret_cast<const uint16_t*>(p.d.b + (t0 + lane + 32 * e) * p.d.bt + h0 + gate);
+      }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();   // with its tensor memory in hand: a kernel behind may take the rest
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = sh.tmem, lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.full), 0, &sh.abort_flag));
-  float c = 0.0f;                                      // the row's factor
-  if (ok) {
-    if (warp == 0 && elect_one()) {
-      const uint64_t da = smem_desc_sw128(tile);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint64_t d = da + (s >> 2) * (kTile >> 4) + 2 * (s & 3);
-        umma_bf16(tmem, d, d, idesc_bf16(128, 64), s > 0);
-      }
-      umma_commit(smem_u32(&sh.done));
-    }
-    __syncwarp();
-    float ss = 0.0f;
-    const uint32_t row = tile + (query ? kHalfTile : 0) + i * 128;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      float f[8];
-      widen8(lds128(row + (v >> 3) * kTile + (((v & 7) ^ (i & 7)) << 4)), f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-    }
-    if (i < n) c = rsqrtf(ss + p.d.eps) * (query ? p.d.scale : 1.0f);
-    if (!query) sh.ck[i] = c;
-  }
-  __syncthreads();
-  ok = ok && mbar_wait(smem_u32(&sh.done), 0, &sh.abort_flag);
   ok = __syncthreads_and(ok);
-  float w[kChunk];
+
   if (ok) {
-    tc_fence_after();
-    tmem_ld64(tmem + (static_cast<uint32_t>(warp * 32) << 16), w);
-    const float cb = query ? c : c * beta;
-    float ratio = 1.0f, rest = 1.0f;                   // Gamma_i / Gamma_j, and Gamma_C / Gamma_i
-#pragma unroll
-    for (int j = kChunk - 1; j >= 0; --j) {
-      const float next = j + 1 < kChunk ? sh.alpha[j + 1] : 1.0f;
-      if (j < i) ratio *= next;
-      else rest *= next;
-      const float f = cb * sh.ck[j] * ratio;
-      if (query) {
-        w[j] = j <= i && i < n ? f * w[j] : 0.0f;
-      } else {
-        if (j < i) sh.at[j * kAtPitch + i] = i < n ? f * w[j] : 0.0f;
-        w[j] = j == i ? 1.0f : 0.0f;
-      }
-    }
-    const float gamma = ratio * sh.alpha[0];
-    float* scalars = reinterpret_cast<float*>(base + kScalars);
-    if (query) {
-      scalars[kQuery + i] = gamma * c;
-    } else {
-      scalars[kBeta + i] = beta;
-      scalars[kKey + i] = beta * gamma * c;
-      scalars[kUpdate + i] = rest * c;
-      if (i == kChunk - 1) scalars[kGammaC] = gamma;
-    }
-  }
-  __syncthreads();                                     // A is there; the key and query rows have been read
-  if (ok) {
-    if (warp & 1) solve_row<64>(w, sh.at);             // rows 32 - 63 of T or P T
-    else solve_row<32>(w, sh.at);                      // rows 0 - 31 end ahead of column 32
-    const uint32_t row = tile + (query ? 3 * kPart : 0) + i * 128;
+    // a thread's half of its row: its sum of squares and its largest entry, then F16
+    const uint32_t at = kq + half * kTile + row * 128;
+    uint4 raw[8];
+    float2 ss = make_float2(0.0f, 0.0f);
+    uint32_t m = 0;
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      uint32_t hi[4], mid[4], lo[4];
+      raw[v] = lds128(at + ((v ^ (i & 7)) << 4));
+      if (i >= n) raw[v] = make_uint4(0u, 0u, 0u, 0u);   // the next request's, or what lies behind
+      float f[8];
+      widen8(raw[v], f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split3(make_float2(w[8 * v + 2 * e], w[8 * v + 2 * e + 1]), hi[e], mid[e], lo[e]);
-      const uint32_t at = row + ((v ^ (i & 7)) << 4);
-      sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      sts128(at + kPart, make_uint4(mid[0], mid[1], mid[2], mid[3]));
-      if (!query) sts128(at + 2 * kPart, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      for (int e = 0; e < 8; e += 2) ss = __ffma2_rn(make_float2(f[e], f[e + 1]), make_float2(f[e], f[e + 1]), ss);
+      m = max_abs_bf16x2(max_abs_bf16x2(m, raw[v].x), raw[v].y);
+      m = max_abs_bf16x2(max_abs_bf16x2(m, raw[v].z), raw[v].w);
+    }
+    sh.squares[half][row] = ss.x + ss.y;
+    sh.largest[half][row] = max_bf16x2(m);
+    __syncthreads();
+    const float top = fmaxf(sh.largest[0][row], sh.largest[1][row]);
+    const float to_one = top > 0.0f ? power_for(top, 0) : 1.0f;
+    // rsqrt and the power taken back, in an order that does not overflow with it
+    const float c = i < n ? rsqrtf(sh.squares[0][row] + sh.squares[1][row] + p.d.eps) / to_one : 0.0f;
+    if (half == 0) sh.factor[row] = c;
+    const float2 s2 = make_float2(to_one, to_one);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      float f[8];
+      widen8(raw[v], f);
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = __fmul2_rn(make_float2(f[2 * e], f[2 * e + 1]), s2);
+        w[e] = pack_f16x2(x.x, x.y);
+      }
+      sts128(at + ((v ^ (i & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
     }
     fence_proxy_async_smem();
-  } else {
+  }
+  __syncthreads();
+  if (ok && warp == 0 && elect_one()) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint64_t d = smem_desc_sw128(kq) + (s >> 2) * (kTile >> 4) + 2 * (s & 3);
+      umma_f16(tmem, d, d, idesc_f16(128, 64), s > 0);
+    }
+    umma_commit(smem_u32(&sh.gram));
+    if (sub == 0) {
+      bulk_store(kq_at(p, slot, hk), kq, kKq);
+      bulk_commit();
+    }
+  }
+  __syncwarp();
+  if (gate >= 0 && gate < heads) {
+    rate = expf(rate);
+    float alpha[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = lane + 32 * e;
+      alpha[e] = t < n ? expf(log_decay(bf16_bits_to_f32(ga[e]), dt_bias, rate)) : 1.0f;
+      sh.alpha[gate][t] = alpha[e];
+      sh.beta[gate][t] = t < n ? beta_of(bf16_bits_to_f32(gb[e])) : 0.0f;
+    }
+    const float g0 = scan_product(alpha[0], lane), g1 = scan_product(alpha[1], lane);
+    const float all0 = __shfl_sync(0xffffffffu, g0, 31), all1 = __shfl_sync(0xffffffffu, g1, 31);
+    sh.gamma[gate][lane] = g0;
+    sh.gamma[gate][lane + 32] = all0 * g1;
+    sh.rest[gate][lane] = scan_product_behind(alpha[0], lane) * all1;
+    sh.rest[gate][lane + 32] = scan_product_behind(alpha[1], lane);
+    sh.upper[gate][lane] = 1.0f;
+    sh.upper[gate][lane + 32] = g1;
+  }
+  ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.gram), 0, &sh.abort_flag));
+  if (warp == 0) bulk_wait_read_all();                 // the K and Q rows have left shared memory
+  ok = __syncthreads_and(ok);
+
+  for (int g = 0; ok && g < heads; ++g) {
+    const int h = h0 + g;
+    if (g > 0) {                                       // the blob ahead has left shared memory
+      if (warp == 0) bulk_wait_read_all();
+      __syncthreads();
+    }
+    tc_fence_after();
+    {
+      // rows of A, and of P cut into its parts where P T will be; columns 32 half + 31 down to 32 half
+      float w[32];
+      tmem_ld32(tmem + lanes + 32 * half, w);
+      const float c = sh.factor[row], f0 = query ? c * 64.0f : c * sh.beta[g][i];
+      float ratio = half == 0 ? sh.upper[g][i] : 1.0f;   // Gamma_i / Gamma_j
+#pragma unroll
+      for (int jj = 31; jj >= 0; --jj) {
+        const int j = 32 * half + jj;
+        if (jj < 31 && j < i) ratio *= sh.alpha[g][j + 1];
+        const float f = f0 * sh.factor[j] * ratio;
+        w[jj] = (query ? j <= i : j < i) && i < n ? f * w[jj] : 0.0f;
+      }
+      if (query) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split2(make_float2(w[8 * v + 2 * e], w[8 * v + 2 * e + 1]), hi[e], lo[e]);
+          const uint32_t at = blob + kHalfTile + i * 128 + (((4 * half + v) ^ (i & 7)) << 4);
+          sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(at + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+      } else {
+        float4* a = reinterpret_cast<float4*>(sh.A + i * kPitch + 32 * half);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) a[v] = make_float4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+      }
+    }
+    __syncthreads();
+    if (warp < 2) {
+      // column j of a diagonal block: T_ij = 1_ij - sum_{l < i} A_il T_lj
+      const int at = 16 * (tid >> 4), j = tid & 15;
+      const float* a = sh.A + at * kPitch + at;
+      float t[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float s = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int l = 0; l < r; l += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(a + r * kPitch + l);
+          s = fmaf(x.x, t[l], s);
+          if (l + 1 < r) s2 = fmaf(x.y, t[l + 1], s2);
+          if (l + 2 < r) s = fmaf(x.z, t[l + 2], s);
+          if (l + 3 < r) s2 = fmaf(x.w, t[l + 3], s2);
+        }
+        t[r] = (r == j ? 1.0f : 0.0f) - (s + s2);
+      }
+      __syncwarp();                                    // A's blocks have been read
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sh.A[(at + r) * kPitch + at + j] = t[r];
+    }
+    __syncthreads();
+    {
+      // the two lower blocks of 16 rows, next to the diagonal: 2 x 16 x 4 pieces of 4 columns
+      const int pair = (tid >> 6) & 1, r = (tid >> 2) & 15, c4 = (tid & 3) * 4, a0 = 32 * pair, b0 = a0 + 16;
+      if (tid < 128)
+        *reinterpret_cast<float4*>(sh.Z + (16 * pair + r) * kPitch + c4) =
+            product4<16>(sh.A + (b0 + r) * kPitch + a0, sh.A + a0 * kPitch + a0 + c4);
+      __syncthreads();
+      if (tid < 128)
+        *reinterpret_cast<float4*>(sh.A + (b0 + r) * kPitch + a0 + c4) =
+            negate(product4<16>(sh.A + (b0 + r) * kPitch + b0, sh.Z + 16 * pair * kPitch + c4));
+    }
+    __syncthreads();
+    {
+      // the lower block of 32 rows: two rows of four columns a thread, of half of the threads
+      const int r = 2 * (tid >> 3), c4 = (tid & 7) * 4;
+      float4 s[2];
+      if (tid < 128) {
+        product2x4<32>(sh.A + (32 + r) * kPitch, sh.A + c4, s);
+        *reinterpret_cast<float4*>(sh.Z + r * kPitch + c4) = s[0];
+        *reinterpret_cast<float4*>(sh.Z + (r + 1) * kPitch + c4) = s[1];
+      }
+      __syncthreads();
+      if (tid < 128) {
+        product2x4<32>(sh.A + (32 + r) * kPitch + 32, sh.Z + c4, s);
+        *reinterpret_cast<float4*>(sh.A + (32 + r) * kPitch + c4) = negate(s[0]);
+        *reinterpret_cast<float4*>(sh.A + (33 + r) * kPitch + c4) = negate(s[1]);
+      }
+    }
+    __syncthreads();
+    {
+      const int r = tid >> 2, c0 = 16 * (tid & 3);     // T's parts: 16 columns a thread
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 x = *reinterpret_cast<const float4*>(sh.A + r * kPitch + c0 + 8 * v + 4 * e);
+          split2(make_float2(x.x * kTScale, x.y * kTScale), hi[2 * e], lo[2 * e]);
+          split2(make_float2(x.z * kTScale, x.w * kTScale), hi[2 * e + 1], lo[2 * e + 1]);
+        }
+        const uint32_t at = blob + r * 128 + ((((c0 >> 3) + v) ^ (r & 7)) << 4);
+        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(at + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      float* scalars = reinterpret_cast<float*>(base + kScalars);
+      if (tid < kChunk) {
+        const float beta = sh.beta[g][tid], gamma = sh.gamma[g][tid], ck = sh.factor[tid];
+        scalars[kBeta + tid] = beta;
+        scalars[kKey + tid] = beta * gamma * ck;
+        scalars[kQuery + tid] = gamma * sh.factor[kChunk + tid];
+        scalars[kUpdate + tid] = sh.rest[g][tid] * ck * (1.0f / kTScale);
+        if (tid == kChunk - 1) scalars[kGammaC] = gamma;
+      }
+      fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if (warp == 0 && elect_one()) {
+      // rows 64 - 127 of the left operand are whatever lies behind P's: lanes that nothing reads
+      const uint64_t dp = smem_desc_sw128(blob + kHalfTile), dt = smem_desc_sw128_mn(blob, kHalfTile);
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int t = 0; t < 2 - a; ++t)
+#pragma unroll
+          for (int s = 0; s < 4; ++s)                  // 16 rows of T a step
+            umma_f16(tmem + 64, dp + a * (kTile >> 4) + 2 * s, dt + t * (kTile >> 4) + 128 * s, idesc_f16_mn(128, 64),
+                     a || t || s);
+      umma_commit(smem_u32(&sh.product));
+    }
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.product), g & 1, &sh.abort_flag));
+    if (ok && !query) {
+      tc_fence_after();
+      float w[32];
+      tmem_ld32(tmem + lanes + 64 + 32 * half, w);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          split2(make_float2(w[8 * v + 2 * e] * (1.0f / 64.0f), w[8 * v + 2 * e + 1] * (1.0f / 64.0f)), hi[e], lo[e]);
+        const uint32_t at = blob + kHalfTile + i * 128 + (((4 * half + v) ^ (i & 7)) << 4);
+        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(at + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);
+    if (ok && warp == 0 && elect_one()) {
+      bulk_store(blob_at(p, slot, h), blob, kBlob);
+      bulk_commit();
+    }
+    __syncwarp();
+  }
+  if (!ok) {
     sh.abort_flag = 1;
     if (tid == 0) atomicExch(&g_delta_err, static_cast<int>(BFP8_ERR_TIMEOUT));
   }
+  if (warp == 0) bulk_wait_all();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 7) {
     tc_fence_after();
-    tmem_dealloc(tmem, 64);
-  }
-  if (ok && tid == 0) {
-    bulk_store(p.ws + (slot * p.d.v_heads + h) * static_cast<int64_t>(kBlob), tile, kBlob);
-    bulk_commit();
-    bulk_wait_all();
+    tmem_dealloc(tmem, 128);
   }
 }
 
 // ---- the walk down a request's chunks. Lane r of tensor memory is row r of S (a value), its
 // columns keys or tokens: what one product leaves in a lane is, scaled and cut, the next one's
-// operand from tensor memory, so nothing passes between threads. Two warpgroups share the
-// columns: keys 0 - 63 and 64 - 127 of S (kept in registers), tokens 0 - 31 and 32 - 63.
-constexpr int kWalkThreads = 320;                      // 8 warps of rows, one of products, one of loads
-constexpr int kRowWarps = 8;
-constexpr int kStageBytes = 3 * kTile + (kBlob + 1023) / 1024 * 1024;
-constexpr int kStages = 2;
-// Columns of tensor memory. A chunk of 16 keys or tokens of one part takes 8. Parts 0 and 1
-// of S lie where u K comes (read before they are written anew), those of r where S K^T came,
-// those of u' where u came; each warpgroup overwrites only columns that it alone has read.
-constexpr uint32_t kColNew = 0, kColS2 = 128, kColX = 192, kColY = 256, kColU = 320, kColO = 384, kColR2 = 448,
-                   kColU2 = 480;
+// operand from tensor memory, so nothing passes between threads but the row's power of two. Two
+// warpgroups share the columns: keys 0 - 63 and 64 - 127 of S (kept in registers), tokens 0 - 31
+// and 32 - 63.
+//
+// A row's power of two brings the larger of its state's and its values' entries near 2^2. With
+// all of them below 2^6, no u and no S of the chunk reaches 2^13 (|u| <= |v| + |S|, and |S| grows
+// by |v| a token at most), and with the largest above 2^-3, the rests' 2^-25 is 2^-22 of it. It
+// is looked at once a chunk: Gamma_C times the state's largest at the chunk's begin, the largest
+// update, and the next chunk's values stand for what the next chunk meets.
+//
+// What the chain of three products does not need runs beside it: S0 Q^T and the out rows of
+// T behind the products that the chain waits for, and the out rows' arithmetic in a third
+// warpgroup. Each product begins on the first half of its operand while the second is cut.
+constexpr int kRowWarps = 8, kOutWarps = 4;
+constexpr int kWalkThreads = 32 * (kRowWarps + kOutWarps + 4);   // and a warp of products and one of loads
+constexpr int kBlobAt = kKq;
+constexpr int kStageBytes = kBlobAt + (kBlob + 1023) / 1024 * 1024;
+constexpr int kStages = 2, kValueStages = 3;           // values are looked at a chunk ahead
+constexpr int kValuesAt = kStages * kStageBytes, kOutAt = kValuesAt + kValueStages * kTile;
+constexpr int kOutPitch = 320;                         // of 64 rows of 128 BF16: two rows' banks apart
+constexpr int kWalkSharedAt = kOutAt + kChunk * kOutPitch;
+// Columns of tensor memory. 16 keys or tokens of one part take 8. The parts of S lie where u K
+// comes (read before they are written anew), those of r where S K^T came, those of u where u
+// came; each warpgroup overwrites only columns that it alone has read.
+constexpr uint32_t kColNew = 0, kColX = 128, kColY = 192, kColU = 256, kColO = 320;
 BFP8_DEV uint32_t col_s(int part, int step) {          // step: 16 keys
-  return part < 2 ? kColNew + 64 * (step >> 2) + 32 * part + 8 * (step & 3) : kColS2 + 32 * (step >> 2) + 8 * (step & 3);
+  return kColNew + 64 * (step >> 2) + 32 * part + 8 * (step & 3);
 }
 BFP8_DEV uint32_t col_r(int part, int step) {          // step: 16 tokens
-  return part < 2 ? kColX + 32 * (step >> 1) + 16 * part + 8 * (step & 1) : kColR2 + 16 * (step >> 1) + 8 * (step & 1);
+  return kColX + 32 * (step >> 1) + 16 * part + 8 * (step & 1);
 }
-BFP8_DEV uint32_t col_u(int part, int step) {
-  return part < 2 ? kColU + 32 * (step >> 1) + 16 * part + 8 * (step & 1) : kColU2 + 16 * (step >> 1) + 8 * (step & 1);
+BFP8_DEV uint32_t col_u(int part, int step) { return col_r(part, step) + (kColU - kColX); }
+
+// 8 columns of this thread's lane written; complete after tmem_wait_st().
+BFP8_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
 }
 
 struct WalkShared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t s_full, x_done, r_full, u_done, p_full, o_done, new_done, drained;
+  float most[2][2][kD];                                // what each half of a row offers for its power of two
+  float power[2][kD];                                  // a chunk's, for its rows of out
+  uint64_t full[kStages], empty[kStages], v_full[kValueStages], v_empty[kValueStages];
+  uint64_t s_full[2], x_done, r_full[2], u_done, p_full[2], o_done, y_free, new_done, told, out_full, drained;
   uint32_t tmem;
   int abort_flag;
 };
-constexpr int kWalkSmem = 1024 + kStages * kStageBytes + static_cast<int>(sizeof(WalkShared));
+constexpr int kWalkSmem = 1024 + kWalkSharedAt + static_cast<int>(sizeof(WalkShared));
 
-// D = A B: A from tensor memory, B a tile of N rows in shared memory, BF16.
-BFP8_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  umma_f16_ts(d_tmem, a_tmem, b_desc, idesc, accumulate);   // the operands' type is in idesc
-}
-
-__global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __grid_constant__ CUtensorMap tq,
-                                                                     const __grid_constant__ CUtensorMap tk,
-                                                                     const __grid_constant__ CUtensorMap tv,
+__global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __grid_constant__ CUtensorMap tv,
                                                                      const ChunkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  WalkShared& sh = *reinterpret_cast<WalkShared*>(base + kStages * kStageBytes);
+  WalkShared& sh = *reinterpret_cast<WalkShared*>(base + kWalkSharedAt);
   const uint32_t stages = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kMmaWarp = kRowWarps + kOutWarps;
   pdl_wait();
   const int h = blockIdx.x % p.d.v_heads, b = blockIdx.x / p.d.v_heads;
   int64_t first;
@@ -447,11 +710,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh.full[s]), 1);
-      mbar_init(smem_u32(&sh.empty[s]), kRowWarps + 1);
+      mbar_init(smem_u32(&sh.empty[s]), kRowWarps + kOutWarps + 1);
     }
-    mbar_init(smem_u32(&sh.s_full), kRowWarps);
-    mbar_init(smem_u32(&sh.r_full), kRowWarps);
-    mbar_init(smem_u32(&sh.p_full), kRowWarps);
+    for (int s = 0; s < kValueStages; ++s) {
+      mbar_init(smem_u32(&sh.v_full[s]), 1);
+      mbar_init(smem_u32(&sh.v_empty[s]), kRowWarps);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(smem_u32(&sh.s_full[q]), kRowWarps);
+      mbar_init(smem_u32(&sh.r_full[q]), kRowWarps);
+      mbar_init(smem_u32(&sh.p_full[q]), kRowWarps);
+    }
+    mbar_init(smem_u32(&sh.told), kRowWarps);
+    mbar_init(smem_u32(&sh.y_free), kOutWarps);
+    mbar_init(smem_u32(&sh.out_full), kOutWarps);
     mbar_init(smem_u32(&sh.x_done), 1);
     mbar_init(smem_u32(&sh.u_done), 1);
     mbar_init(smem_u32(&sh.o_done), 1);
@@ -460,7 +732,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     sh.abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == kRowWarps) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
@@ -475,226 +747,355 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag));
     return ok;
   };
+  auto tell_bar = [&](uint64_t& bar) {                 // one arrival a warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
+  };
 
-  if (warp == kRowWarps + 1) {
-    // ------------------------------------------------ loads, a chunk ahead
-    const int64_t key = tile_key(p.d.req, b, kShift);
-    int c = 0;
-    for (; c < chunks; ++c) {
-      const int s = c % kStages;
-      if (!wait(sh.empty[s], ((c / kStages) & 1) ^ 1)) break;
-      if (elect_one()) {
-        const uint32_t dst = stages + s * kStageBytes, bar = smem_u32(&sh.full[s]);
-        const int t0 = static_cast<int>(first) + c * kChunk, hk = h / p.d.group;
-        mbar_arrive_expect_tx(bar, 3 * kTile + kBlob);
-        load_tile(dst, kHalfTile, &tk, hk, t0, bar);
-        bulk_load(dst + 3 * kTile, p.ws + ((key + c) * p.d.v_heads + h) * static_cast<int64_t>(kBlob), kBlob, bar);
-        load_tile(dst + 2 * kTile, kHalfTile, &tv, h, t0, bar);
-        load_tile(dst + kTile, kHalfTile, &tq, hk, t0, bar);
+  if (warp >= kMmaWarp) {
+    warpgroup_reg_dealloc<64>();
+    if (warp == kMmaWarp) {
+      // ---------------------------------------------- products
+      constexpr uint32_t kN64 = idesc_f16(128, 64), kKeys = idesc_f16_mn(128, 128);
+      for (int c = 0; c < chunks; ++c) {
+        const int s = c % kStages;
+        const uint32_t at = stages + s * kStageBytes;
+        const uint64_t dk = smem_desc_sw128(at), dt = smem_desc_sw128(at + kBlobAt), dn = smem_desc_sw128_mn(at, kTile);
+        if (!wait(sh.full[s], (c / kStages) & 1)) break;
+        for (int q = 0; q < 2; ++q) {                  // 32 keys of each warpgroup's
+          if (!wait(sh.s_full[q], c & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int k = 4 * (e >> 1) + 2 * q + (e & 1);
+                umma_f16_ts(tmem + kColX, tmem + col_s(part, k), dk + (k >> 2) * (kTile >> 4) + 2 * (k & 3), kN64,
+                            q || part || e);
+              }
+            if (q == 1) umma_commit(smem_u32(&sh.x_done));
+          }
+          __syncwarp();
+        }
+        if (!ok || !wait(sh.y_free, (c & 1) ^ 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_f16_ts(tmem + kColY, tmem + col_s(part, k), dk + ((kHalfTile + (k >> 2) * kTile) >> 4) + 2 * (k & 3),
+                          kN64, part || k);
+        }
+        __syncwarp();
+        for (int q = 0; q < 2; ++q) {                  // 16 tokens of each warpgroup's
+          if (!wait(sh.r_full[q], c & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int t = 0; t < 2 - a; ++t)
+#pragma unroll
+                for (int k = q; k < 4; k += 2)
+                  umma_f16_ts(tmem + kColU, tmem + col_r(a, k), dt + t * (kTile >> 4) + 2 * k, kN64, q || a || t || k > 1);
+            if (q == 1) umma_commit(smem_u32(&sh.u_done));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int t = 0; t < 2 - a; ++t)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_f16_ts(tmem + kColO, tmem + col_r(a, k), dt + ((kHalfTile + t * kTile) >> 4) + 2 * k, kN64, a || t || k);
+          umma_commit(smem_u32(&sh.o_done));
+        }
+        __syncwarp();
+        for (int q = 0; q < 2; ++q) {
+          if (!wait(sh.p_full[q], c & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = q; k < 4; k += 2)           // 16 tokens a step: 16 rows of 128 bytes
+                umma_f16_ts(tmem + kColNew, tmem + col_u(part, k), dn + 128 * k, kKeys, q || part || k > 1);
+            if (q == 1) {
+              umma_commit(smem_u32(&sh.new_done));
+              umma_commit(smem_u32(&sh.empty[s]));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
       }
-      __syncwarp();
+      if (!ok) {   // products in flight end before tensor memory is given back
+        const int none = 0;
+        if (elect_one()) umma_commit(smem_u32(&sh.drained));
+        __syncwarp();
+        mbar_wait(smem_u32(&sh.drained), 0, &none);
+      }
+    } else if (warp == kMmaWarp + 1) {
+      // ---------------------------------------------- loads, a chunk ahead; values two
+      const int64_t key = tile_key(p.d.req, b, kShift);
+      int got = 0, values = 0;                         // chunks asked for
+      auto load_values = [&]() {
+        const int s = values % kValueStages;
+        if (values == chunks || !wait(sh.v_empty[s], ((values / kValueStages) & 1) ^ 1)) return;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(smem_u32(&sh.v_full[s]), kTile);
+          load_tile(stages + kValuesAt + s * kTile, kHalfTile, &tv, h, static_cast<int>(first) + values * kChunk,
+                    smem_u32(&sh.v_full[s]));
+        }
+        __syncwarp();
+        ++values;
+      };
+      load_values();
+      while (ok && got < chunks) {
+        const int s = got % kStages;
+        if (!wait(sh.empty[s], ((got / kStages) & 1) ^ 1)) break;
+        if (elect_one()) {
+          const uint32_t dst = stages + s * kStageBytes, bar = smem_u32(&sh.full[s]);
+          mbar_arrive_expect_tx(bar, kKq + kBlob);
+          bulk_load(dst, kq_at(p, key + got, h / p.d.group), kKq, bar);
+          bulk_load(dst + kBlobAt, blob_at(p, key + got, h), kBlob, bar);
+        }
+        __syncwarp();
+        ++got;
+        load_values();
+      }
+      if (!ok) {   // what was issued lands before the block ends
+        const int none = 0;
+        for (int d = got < kStages ? 0 : got - kStages; d < got; ++d)
+          mbar_wait(smem_u32(&sh.full[d % kStages]), (d / kStages) & 1, &none);
+        for (int d = values < kValueStages ? 0 : values - kValueStages; d < values; ++d)
+          mbar_wait(smem_u32(&sh.v_full[d % kValueStages]), (d / kValueStages) & 1, &none);
+      }
     }
-    if (!ok) {   // what was issued lands before the block ends
-      const int none = 0;
-      for (int d = c < kStages ? 0 : c - kStages; d < c; ++d)
-        mbar_wait(smem_u32(&sh.full[d % kStages]), (d / kStages) & 1, &none);
-    }
-  } else if (warp == kRowWarps) {
-    // ------------------------------------------------ products
-    constexpr uint32_t kN64 = idesc_bf16(128, 64), kKeys = idesc_bf16(128, 128) | (1u << 16);
+  } else if (warp >= kRowWarps) {
+    // ------------------------------------------------ rows of out: a value a thread, 64 tokens
+    warpgroup_reg_dealloc<96>();
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const bool odd = lane & 1;
     for (int c = 0; c < chunks; ++c) {
       const int s = c % kStages;
-      const uint32_t at = stages + s * kStageBytes;
-      const uint64_t dk = smem_desc_sw128(at), dq = smem_desc_sw128(at + kTile), dt = smem_desc_sw128(at + 3 * kTile);
-      const uint64_t dn = smem_desc_sw128_mn(at, kHalfTile);
-      if (!wait(sh.full[s], (c / kStages) & 1) || !wait(sh.s_full, c & 1)) break;
+      const float* scalars = reinterpret_cast<const float*>(base + s * kStageBytes + kBlobAt + kScalars);
+      if (!wait(sh.full[s], (c / kStages) & 1) || !wait(sh.o_done, c & 1)) break;
       tc_fence_after();
-      if (elect_one()) {
+      const float back = p.d.scale / sh.power[c & 1][r];
+      uint32_t v[32];
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
+      for (int g = 0; g < 2; ++g) {
+        float q[32], o[32];
+        tmem_ld32(mine + kColY + 32 * g, q);
+        tmem_ld32(mine + kColO + 32 * g, o);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16_ts(tmem + kColX, tmem + col_s(part, k), dk + (k >> 2) * (kHalfTile >> 4) + 2 * (k & 3), kN64,
-                         part || k);
-        umma_commit(smem_u32(&sh.x_done));
-#pragma unroll
-        for (int part = 0; part < 2; ++part)           // out is rounded to BF16: two parts, 2^-16
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16_ts(tmem + kColY, tmem + col_s(part, k), dq + (k >> 2) * (kHalfTile >> 4) + 2 * (k & 3), kN64,
-                         part || k);
+        for (int j = 0; j < 32; j += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(scalars + kQuery + 32 * g + j);
+          constexpr float t = 1.0f / kTScale;
+          v[16 * g + j / 2] = pack_bf16x2(fmaf(f.x, q[j], o[j] * t) * back, fmaf(f.y, q[j + 1], o[j + 1] * t) * back);
+        }
       }
-      __syncwarp();
-      if (!wait(sh.r_full, c & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
+      tc_fence_before();
+      tell_bar(sh.y_free);
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+      // two values of one token make a word: even lanes have the pair's even tokens, odd ones the odd
+      const uint32_t at = stages + kOutAt + (odd ? kOutPitch : 0) + (r & ~1) * 2;
 #pragma unroll
-        for (int a = 0; a < 3; ++a)                    // parts of r and of T, down to 2^-24 of the product
-#pragma unroll
-          for (int t = 0; t < 3 - a; ++t)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16_ts(tmem + kColU, tmem + col_r(a, k), dt + t * (kPart >> 4) + 2 * k, kN64, a || t || k);
-        umma_commit(smem_u32(&sh.u_done));
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int t = 0; t < 2 - a; ++t)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16_ts(tmem + kColO, tmem + col_r(a, k), dt + (3 + t) * (kPart >> 4) + 2 * k, kN64, a || t || k);
-        umma_commit(smem_u32(&sh.o_done));
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t w = __shfl_xor_sync(0xffffffffu, v[j], 1);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 2 * j * kOutPitch),
+                     "r"(odd ? __byte_perm(w, v[j], 0x7632) : __byte_perm(v[j], w, 0x5410))
+                     : "memory");
       }
-      __syncwarp();
-      if (!wait(sh.p_full, c & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
+      tell_bar(sh.out_full);
+      if (!wait(sh.out_full, 0)) break;
+      // a row of 256 bytes to 16 lanes
+      const int n = c == chunks - 1 ? tail : kChunk;
+      __nv_bfloat16* out = p.d.out + (first + static_cast<int64_t>(c) * kChunk) * p.d.ot + h * p.d.oh + (lane & 15) * 8;
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)                  // 16 tokens a step: 16 rows of 128 bytes
-            umma_bf16_ts(tmem + kColNew, tmem + col_u(part, k), dn + 128 * k, kKeys, part || k);
-        umma_commit(smem_u32(&sh.new_done));
-        umma_commit(smem_u32(&sh.empty[s]));
+      for (int e = 0; e < 8; ++e) {
+        const int t = 8 * e + 2 * (warp & 3) + (lane >> 4);
+        const uint4 w = lds128(stages + kOutAt + t * kOutPitch + (lane & 15) * 16);
+        if (t < n) *reinterpret_cast<uint4*>(out + t * p.d.ot) = w;
       }
-      __syncwarp();
-    }
-    if (!ok) {   // products in flight end before tensor memory is given back
-      const int none = 0;
-      if (elect_one()) umma_commit(smem_u32(&sh.drained));
-      __syncwarp();
-      mbar_wait(smem_u32(&sh.drained), 0, &none);
+      tell_bar(sh.out_full);                           // the tile may be written again
+      if (!wait(sh.out_full, 1)) break;
     }
   } else {
     // ------------------------------------------------ rows of S
+    warpgroup_reg_alloc<176>();
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int64_t from = slot_of(p.d.req, p.d.req.slots_in, b), to = slot_of(p.d.req, p.d.req.slots_out, b);
     const int64_t in_head = h * p.d.s_head + r * kD + 64 * wg;
-    float S[64];
+    float S[64], most = 0.0f;                          // S is the row times `power`
     if (from >= 0) {
       const float4* src = reinterpret_cast<const float4*>(p.d.state + from * p.d.s_slot + in_head);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const float4 f = src[k];
         S[4 * k] = f.x, S[4 * k + 1] = f.y, S[4 * k + 2] = f.z, S[4 * k + 3] = f.w;
+        most = fmaxf(most, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 64; ++k) S[k] = 0.0f;
     }
-    // S cut into its parts, and the word to the products' warp. The last chunk's rows past the
-    // request are the next one's: zeros, before they meet weights of 0.
-    auto hand_over = [&](int c) {
+    uint32_t values[16], top = 0;                      // the next chunk's: 32 tokens' BF16, two a word; the largest
+    auto load_values = [&](int c, int g) {             // 16 of its tokens
+      const int s = c % kValueStages, left = (c == chunks - 1 ? tail : kChunk) - 32 * wg;
+      if (!wait(sh.v_full[s], (c / kValueStages) & 1)) return;
+      const uint8_t* col = base + kValuesAt + s * kTile + (r >> 6) * kHalfTile + 32 * wg * 128;
+      if (g == 0) top = 0;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hi[16], mid[16], lo[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          split3(make_float2(S[32 * half + 2 * k], S[32 * half + 2 * k + 1]), hi[k], mid[k], lo[k]);
-        tmem_st16(mine + col_s(0, 4 * wg + 2 * half), hi);
-        tmem_st16(mine + col_s(1, 4 * wg + 2 * half), mid);
-        tmem_st16(mine + col_s(2, 4 * wg + 2 * half), lo);
+      for (int e = 0; e < 16; e += 2) {
+        const int j = 16 * g + e;
+        const uint32_t v0 = *reinterpret_cast<const uint16_t*>(col + j * 128 + (((r & 63) * 2) ^ ((j & 7) << 4)));
+        const uint32_t v1 = *reinterpret_cast<const uint16_t*>(col + (j + 1) * 128 + (((r & 63) * 2) ^ (((j + 1) & 7) << 4)));
+        uint32_t v = v0 | (v1 << 16);
+        if (left < 32) v = j >= left ? 0u : j + 1 >= left ? v0 : v;
+        values[j / 2] = v;
+        top = max_abs_bf16x2(top, v);
       }
-      tmem_wait_st();
-      if (c == chunks - 1 && tail < kChunk) {
-        if (!wait(sh.full[c % kStages], (c / kStages) & 1)) return;
-        const uint32_t at = stages + (c % kStages) * kStageBytes;
-        for (int v = tid; v < (kChunk - tail) * 16; v += 32 * kRowWarps) {
-          const int row = tail + (v >> 4);
-          sts128(at + ((v >> 3) & 1) * kHalfTile + row * 128 + ((v & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
-        }
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.s_full));
+      if (g == 1) tell_bar(sh.v_empty[s]);
     };
-    hand_over(0);
+    // The larger of the row's two halves' offers.
+    auto tell = [&](int turn, float offer) {
+      sh.most[turn & 1][wg][r] = offer;
+      tell_bar(sh.told);
+      if (!wait(sh.told, turn & 1)) return offer;
+      return fmaxf(offer, sh.most[turn & 1][wg ^ 1][r]);
+    };
+    uint32_t largest = 0;                              // of the parts of S, as F16 pairs
+    auto hand_over = [&](int q) {                      // 32 keys
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        split2(make_float2(S[32 * q + 2 * k], S[32 * q + 2 * k + 1]), hi[k], lo[k]);
+        largest = max_abs_f16x2(q || k ? largest : 0u, hi[k]);
+      }
+      tmem_st16(mine + col_s(0, 4 * wg + 2 * q), hi);
+      tmem_st16(mine + col_s(1, 4 * wg + 2 * q), lo);
+      tmem_wait_st();
+      tc_fence_before();
+      tell_bar(sh.s_full[q]);
+    };
+    load_values(0, 0);
+    if (ok) load_values(0, 1);
+    const float first_most = ok ? tell(0, fmaxf(most, max_bf16x2(top))) : 0.0f;
+    float power = first_most > 0.0f ? power_for(first_most, 2) : 1.0f;
+#pragma unroll
+    for (int k = 0; k < 64; ++k) S[k] *= power;
+    if (ok) hand_over(0), hand_over(1);
     for (int c = 0; ok && c < chunks; ++c) {
       const int s = c % kStages;
-      uint8_t* const at = base + s * kStageBytes;
-      const float* scalars = reinterpret_cast<const float*>(at + 3 * kTile + kScalars);
-      const int left = c == chunks - 1 ? tail : kChunk;
+      const bool more = c + 1 < chunks;
+      const float* scalars = reinterpret_cast<const float*>(base + s * kStageBytes + kBlobAt + kScalars);
+      // while S meets K: this chunk's values, and half of the next one's
+      if (wg == 0) sh.power[c & 1][r] = power;
       if (!wait(sh.full[s], (c / kStages) & 1)) break;
-      // column r of the values' tile, in rows of 128 bytes with the swizzle
-      const uint8_t* vcol = at + 2 * kTile + (r >> 6) * kHalfTile;
-      const uint32_t vbyte = (r & 63) * 2;
+      float y[32];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 be = *reinterpret_cast<const float4*>(scalars + kBeta + 32 * wg + j);
+        y[j] = __uint_as_float(values[j / 2] << 16) * (be.x * power);
+        y[j + 1] = __uint_as_float(values[j / 2] & 0xFFFF0000u) * (be.y * power);
+        y[j + 2] = __uint_as_float(values[j / 2 + 1] << 16) * (be.z * power);
+        y[j + 3] = __uint_as_float(values[j / 2 + 1] & 0xFFFF0000u) * (be.w * power);
+      }
+      if (more) load_values(c + 1, 0);
       if (!wait(sh.x_done, c & 1)) break;
       tc_fence_after();
       {
         float x[32];
         tmem_ld32(mine + kColX + 32 * wg, x);
-        uint32_t hi[16], mid[16], lo[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const int t = 32 * wg + j;
-          const float2 be = *reinterpret_cast<const float2*>(scalars + kBeta + t);
-          const float2 kf = *reinterpret_cast<const float2*>(scalars + kKey + t);
-          const uint16_t v0 = *reinterpret_cast<const uint16_t*>(vcol + t * 128 + (vbyte ^ ((t & 7) << 4)));
-          const uint16_t v1 = *reinterpret_cast<const uint16_t*>(vcol + (t + 1) * 128 + (vbyte ^ (((t + 1) & 7) << 4)));
-          float2 y = __fmul2_rn(make_float2(bf16_bits_to_f32(v0), bf16_bits_to_f32(v1)), be);
-          y = __ffma2_rn(make_float2(-x[j], -x[j + 1]), kf, y);
-          if (t >= left) y.x = 0.0f;
-          if (t + 1 >= left) y.y = 0.0f;
-          split3(y, hi[j / 2], mid[j / 2], lo[j / 2]);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const int j = 16 * q + e;
+            const float4 kf = *reinterpret_cast<const float4*>(scalars + kKey + 32 * wg + j);
+            split2(make_float2(fmaf(-kf.x, x[j], y[j]), fmaf(-kf.y, x[j + 1], y[j + 1])), hi[e / 2], lo[e / 2]);
+            split2(make_float2(fmaf(-kf.z, x[j + 2], y[j + 2]), fmaf(-kf.w, x[j + 3], y[j + 3])), hi[e / 2 + 1], lo[e / 2 + 1]);
+          }
+          tmem_st8(mine + col_r(0, 2 * wg + q), hi);
+          tmem_st8(mine + col_r(1, 2 * wg + q), lo);
+          tmem_wait_st();
+          tc_fence_before();
+          tell_bar(sh.r_full[q]);
         }
-        tmem_st16(mine + col_r(0, 2 * wg), hi);
-        tmem_st16(mine + col_r(1, 2 * wg), mid);
-        tmem_st16(mine + col_r(2, 2 * wg), lo);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.r_full));
+      }
+      // while r meets T: the other half of the next chunk's values
+      const float gamma = scalars[kGammaC];
+      float offer = gamma * max_f16x2(largest);
+      if (more) {
+        load_values(c + 1, 1);
+        offer = fmaxf(offer, max_bf16x2(top) * power);
       }
       if (!wait(sh.u_done, c & 1)) break;
       tc_fence_after();
       {
         float u[32];
+        uint32_t m = 0;
         tmem_ld32(mine + kColU + 32 * wg, u);
-        uint32_t hi[16], mid[16], lo[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float2 f = *reinterpret_cast<const float2*>(scalars + kUpdate + 32 * wg + j);
-          split3(__fmul2_rn(make_float2(u[j], u[j + 1]), f), hi[j / 2], mid[j / 2], lo[j / 2]);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const int j = 16 * q + e;
+            const float4 f = *reinterpret_cast<const float4*>(scalars + kUpdate + 32 * wg + j);
+            split2(make_float2(u[j] * f.x, u[j + 1] * f.y), hi[e / 2], lo[e / 2]);
+            split2(make_float2(u[j + 2] * f.z, u[j + 3] * f.w), hi[e / 2 + 1], lo[e / 2 + 1]);
+            m = max_abs_f16x2(max_abs_f16x2(m, hi[e / 2]), hi[e / 2 + 1]);
+          }
+          tmem_st8(mine + col_u(0, 2 * wg + q), hi);
+          tmem_st8(mine + col_u(1, 2 * wg + q), lo);
+          tmem_wait_st();
+          tc_fence_before();
+          tell_bar(sh.p_full[q]);
         }
-        tmem_st16(mine + col_u(0, 2 * wg), hi);
-        tmem_st16(mine + col_u(1, 2 * wg), mid);
-        tmem_st16(mine + col_u(2, 2 * wg), lo);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full));
+        offer = fmaxf(offer, max_f16x2(m));
       }
-      const float gamma = scalars[kGammaC];
-      if (!wait(sh.o_done, c & 1)) break;
-      tc_fence_after();
-      {
-        float y[32], o[32];
-        tmem_ld32(mine + kColY + 32 * wg, y);
-        tmem_ld32(mine + kColO + 32 * wg, o);
-        __nv_bfloat16* out = p.d.out + (first + static_cast<int64_t>(c) * kChunk + 32 * wg) * p.d.ot + h * p.d.oh + r;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (32 * wg + j < left) out[j * p.d.ot] = __float2bfloat16_rn(fmaf(scalars[kQuery + 32 * wg + j], y[j], o[j]));
-      }
-      __syncwarp();
+      // while u meets K: the row's power of two
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+      offer = tell(c + 1, offer);
+      float step = 1.0f;
+      if (offer > 0.0f && !(offer >= 0x1p-3f && offer < 0x1p6f)) {
+        step = fminf(fmaxf(power_for(offer / power, 2) / power, 0x1p-100f), 0x1p100f);
+        power *= step;
+      }
+      const bool rescale = __any_sync(0xffffffffu, step != 1.0f);
+      const float keep = gamma * step;
       if (!wait(sh.new_done, c & 1)) break;
       tc_fence_after();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int q = 0; q < 2; ++q) {
         float d[32];
-        tmem_ld32(mine + kColNew + 64 * wg + 32 * half, d);
+        tmem_ld32(mine + kColNew + 64 * wg + 32 * q, d);
+        if (rescale) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) S[32 * half + k] = fmaf(gamma, S[32 * half + k], d[k]);
+          for (int k = 0; k < 32; ++k) d[k] *= step;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) S[32 * q + k] = fmaf(keep, S[32 * q + k], d[k]);
       }
-      if (c + 1 < chunks) hand_over(c + 1);
+      if (more) hand_over(0), hand_over(1);
     }
     if (ok && to >= 0) {
+      const float back = 1.0f / power;
       float4* dst = reinterpret_cast<float4*>(p.d.state + to * p.d.s_slot + in_head);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) dst[k] = make_float4(S[4 * k], S[4 * k + 1], S[4 * k + 2], S[4 * k + 3]);
+      for (int k = 0; k < 16; ++k)
+        dst[k] = make_float4(S[4 * k] * back, S[4 * k + 1] * back, S[4 * k + 2] * back, S[4 * k + 3] * back);
     }
   }
   if (!ok) {
@@ -703,7 +1104,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kRowWarps) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -724,9 +1125,11 @@ bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
 }  // namespace
 
-size_t delta_rule_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q_len, int64_t, int64_t v_heads) {
+size_t delta_rule_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q_len, int64_t qk_heads,
+                                  int64_t v_heads) {
   if (max_q_len <= kStepTokens) return 0;
-  return static_cast<size_t>(chunk_slots(batch, tokens)) * static_cast<size_t>(v_heads) * kBlob;
+  return static_cast<size_t>(chunk_slots(batch, tokens)) *
+         (static_cast<size_t>(qk_heads) * kKq + static_cast<size_t>(v_heads) * kBlob);
 }
 
 int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
@@ -794,12 +1197,21 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   if (rc == BFP8_OK) rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_prepare_kernel), kPrepSmem);
   if (rc == BFP8_OK) rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_walk_kernel), kWalkSmem);
   if (rc != BFP8_OK) return rc;
-  const ChunkParams cp{p, static_cast<uint8_t*>(a.workspace)};
-  rc = launch_dependent(delta_prepare_kernel, dim3(static_cast<unsigned>(chunk_slots(a.batch, a.tokens) * a.v_heads)),
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc != BFP8_OK) return rc;
+  // Value heads of one key head share a block, which norms and multiplies their rows once, where
+  // there are blocks enough for that: three to an SM.
+  ChunkParams cp{p, static_cast<uint8_t*>(a.workspace), static_cast<int32_t>(a.qk_heads), 0, 0};
+  const int64_t apart = (a.tokens / kChunk + a.batch) * a.v_heads;
+  cp.per_block = apart <= 3 * sms ? 1 : p.group < kGroup ? p.group : kGroup;
+  cp.subgroups = (p.group + cp.per_block - 1) / cp.per_block;
+  rc = launch_dependent(delta_prepare_kernel,
+                        dim3(static_cast<unsigned>(chunk_slots(a.batch, a.tokens) * a.qk_heads * cp.subgroups)),
                         kPrepThreads, kPrepSmem, st, tq, tk, cp);
   if (rc != BFP8_OK) return rc;
   return launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(a.batch * a.v_heads)), kWalkThreads, kWalkSmem,
-                          st, tq, tk, tv, cp);
+                          st, tv, cp);
 }
 
 int delta_read_clear_error() {
