@@ -168,7 +168,7 @@ constexpr int kHalfTile = kChunk * 128;                // 64 rows of 128 bytes
 constexpr int kTile = 2 * kHalfTile;                   // 128 such rows: K over Q of 64 columns, or T over P T
 constexpr int kKq = 2 * kTile;                         // both halves of the columns
 constexpr int kScalars = 2 * kTile;                    // of a blob: T over P T, the parts, then
-// beta, beta Gamma ck, Gamma cq, (Gamma_C / Gamma) ck 2^-12 of each token, and Gamma_C
+// beta, -beta Gamma ck, Gamma cq 2^12, (Gamma_C / Gamma) ck 2^-12 of each token, and Gamma_C
 constexpr int kBeta = 0, kKey = 64, kQuery = 128, kUpdate = 192, kGammaC = 256;
 constexpr int kBlob = kScalars + 1152;
 constexpr float kTScale = 4096.0f;
@@ -197,11 +197,16 @@ BFP8_DEV uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// x minus an F16, exactly what rounding left.
+BFP8_DEV float minus_f16(float x, uint16_t h) {
+  float r;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(r) : "h"(h), "h"(static_cast<uint16_t>(0xBC00)), "f"(x));
+  return r;
+}
 // A pair's two F16 parts.
 BFP8_DEV void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = pack_f16x2(x.x, x.y);
-  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  lo = pack_f16x2(x.x - h.x, x.y - h.y);
+  lo = pack_f16x2(minus_f16(x.x, static_cast<uint16_t>(hi)), minus_f16(x.y, static_cast<uint16_t>(hi >> 16)));
 }
 // The larger size, of each half of a pair.
 BFP8_DEV uint32_t max_abs_f16x2(uint32_t m, uint32_t v) {
@@ -579,8 +584,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
       if (tid < kChunk) {
         const float beta = sh.beta[g][tid], gamma = sh.gamma[g][tid], ck = sh.factor[tid];
         scalars[kBeta + tid] = beta;
-        scalars[kKey + tid] = beta * gamma * ck;
-        scalars[kQuery + tid] = gamma * sh.factor[kChunk + tid];
+        scalars[kKey + tid] = -beta * gamma * ck;
+        scalars[kQuery + tid] = gamma * sh.factor[kChunk + tid] * kTScale;
         scalars[kUpdate + tid] = sh.rest[g][tid] * ck * (1.0f / kTScale);
         if (tid == kChunk - 1) scalars[kGammaC] = gamma;
       }
@@ -658,8 +663,8 @@ constexpr int kRowWarps = 8, kOutWarps = 4;
 constexpr int kWalkThreads = 32 * (kRowWarps + kOutWarps + 4);   // and a warp of products and one of loads
 constexpr int kBlobAt = kKq;
 constexpr int kStageBytes = kBlobAt + (kBlob + 1023) / 1024 * 1024;
-constexpr int kStages = 2, kValueStages = 3;           // values are looked at a chunk ahead
-constexpr int kValuesAt = kStages * kStageBytes, kOutAt = kValuesAt + kValueStages * kTile;
+constexpr int kStages = 2;
+constexpr int kValuesAt = kStages * kStageBytes, kTurnedAt = kValuesAt + 2 * kTile, kOutAt = kTurnedAt + 2 * kTile;
 constexpr int kOutPitch = 320;                         // of 64 rows of 128 BF16: two rows' banks apart
 constexpr int kWalkSharedAt = kOutAt + kChunk * kOutPitch;
 // Columns of tensor memory. 16 keys or tokens of one part take 8. The parts of S lie where u K
@@ -684,7 +689,7 @@ BFP8_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
 struct WalkShared {
   float most[2][2][kD];                                // what each half of a row offers for its power of two
   float power[2][kD];                                  // a chunk's, for its rows of out
-  uint64_t full[kStages], empty[kStages], v_full[kValueStages], v_empty[kValueStages];
+  uint64_t full[kStages], empty[kStages], v_full[2], v_empty[2], turned[2], taken[2];
   uint64_t s_full[2], x_done, r_full[2], u_done, p_full[2], o_done, y_free, new_done, told, out_full, drained;
   uint32_t tmem;
   int abort_flag;
@@ -712,9 +717,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       mbar_init(smem_u32(&sh.full[s]), 1);
       mbar_init(smem_u32(&sh.empty[s]), kRowWarps + kOutWarps + 1);
     }
-    for (int s = 0; s < kValueStages; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sh.v_full[s]), 1);
-      mbar_init(smem_u32(&sh.v_empty[s]), kRowWarps);
+      mbar_init(smem_u32(&sh.v_empty[s]), 2);
+      mbar_init(smem_u32(&sh.turned[s]), 2);
+      mbar_init(smem_u32(&sh.taken[s]), kRowWarps);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(smem_u32(&sh.s_full[q]), kRowWarps);
@@ -744,7 +751,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   const volatile int* abort_flag = &sh.abort_flag;
   bool ok = true;
   auto wait = [&](uint64_t& bar, uint32_t parity) {
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag));
+    ok = ok && __all_sync(0xffffffffu, warp < kRowWarps || warp == kMmaWarp
+                                           ? mbar_wait(smem_u32(&bar), parity, abort_flag)
+                                           : mbar_wait_sleep(smem_u32(&bar), parity, abort_flag));
     return ok;
   };
   auto tell_bar = [&](uint64_t& bar) {                 // one arrival a warp
@@ -845,8 +854,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       const int64_t key = tile_key(p.d.req, b, kShift);
       int got = 0, values = 0;                         // chunks asked for
       auto load_values = [&]() {
-        const int s = values % kValueStages;
-        if (values == chunks || !wait(sh.v_empty[s], ((values / kValueStages) & 1) ^ 1)) return;
+        const int s = values % 2;
+        if (values == chunks || !wait(sh.v_empty[s], ((values / 2) & 1) ^ 1)) return;
         if (elect_one()) {
           mbar_arrive_expect_tx(smem_u32(&sh.v_full[s]), kTile);
           load_tile(stages + kValuesAt + s * kTile, kHalfTile, &tv, h, static_cast<int>(first) + values * kChunk,
@@ -873,13 +882,38 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         const int none = 0;
         for (int d = got < kStages ? 0 : got - kStages; d < got; ++d)
           mbar_wait(smem_u32(&sh.full[d % kStages]), (d / kStages) & 1, &none);
-        for (int d = values < kValueStages ? 0 : values - kValueStages; d < values; ++d)
-          mbar_wait(smem_u32(&sh.v_full[d % kValueStages]), (d / kValueStages) & 1, &none);
+        for (int d = values < 2 ? 0 : values - 2; d < values; ++d)
+          mbar_wait(smem_u32(&sh.v_full[d % 2]), (d / 2) & 1, &none);
+      }
+    } else {
+      // ---------------------------------------------- values turned: of each value its tokens, two a word
+      const int half = warp - kMmaWarp - 2;            // of the values
+      for (int c = 0; c < chunks; ++c) {
+        if (!wait(sh.v_full[c & 1], (c >> 1) & 1) || !wait(sh.taken[c & 1], ((c >> 1) & 1) ^ 1)) break;
+        // a lane's row of the four 8 x 8 pieces that the warp turns at once: 32 tokens of 8 values
+        const uint32_t src = stages + kValuesAt + (c & 1) * kTile + half * kHalfTile + lane * 128;
+        const uint32_t dst = stages + kTurnedAt + (c & 1) * kTile + (64 * half + (lane >> 2)) * 128 + (lane & 3) * 4;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            uint32_t w[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(src + 32 * g * 128 + ((v ^ (lane & 7)) << 4))
+                         : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + 8 * v * 128 + (((4 * g + e) ^ (lane >> 2)) << 4)), "r"(w[e])
+                           : "memory");
+          }
+        tell_bar(sh.turned[c & 1]);
+        if (lane == 0) mbar_arrive(smem_u32(&sh.v_empty[c & 1]));
       }
     }
   } else if (warp >= kRowWarps) {
     // ------------------------------------------------ rows of out: a value a thread, 64 tokens
-    warpgroup_reg_dealloc<96>();
+    warpgroup_reg_dealloc<112>();
     const int r = (warp & 3) * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool odd = lane & 1;
@@ -888,7 +922,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       const float* scalars = reinterpret_cast<const float*>(base + s * kStageBytes + kBlobAt + kScalars);
       if (!wait(sh.full[s], (c / kStages) & 1) || !wait(sh.o_done, c & 1)) break;
       tc_fence_after();
-      const float back = p.d.scale / sh.power[c & 1][r];
+      const float back = p.d.scale * (1.0f / kTScale) / sh.power[c & 1][r];
+      const float2 back2 = make_float2(back, back);
       uint32_t v[32];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -898,8 +933,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
           const float2 f = *reinterpret_cast<const float2*>(scalars + kQuery + 32 * g + j);
-          constexpr float t = 1.0f / kTScale;
-          v[16 * g + j / 2] = pack_bf16x2(fmaf(f.x, q[j], o[j] * t) * back, fmaf(f.y, q[j + 1], o[j + 1] * t) * back);
+          const float2 w = __fmul2_rn(__ffma2_rn(f, make_float2(q[j], q[j + 1]), make_float2(o[j], o[j + 1])), back2);
+          v[16 * g + j / 2] = pack_bf16x2(w.x, w.y);
         }
       }
       tc_fence_before();
@@ -930,7 +965,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     }
   } else {
     // ------------------------------------------------ rows of S
-    warpgroup_reg_alloc<176>();
+    warpgroup_reg_alloc<168>();
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int64_t from = slot_of(p.d.req, p.d.req.slots_in, b), to = slot_of(p.d.req, p.d.req.slots_out, b);
@@ -949,29 +984,24 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       for (int k = 0; k < 64; ++k) S[k] = 0.0f;
     }
     uint32_t values[16], top = 0;                      // the next chunk's: 32 tokens' BF16, two a word; the largest
-    auto load_values = [&](int c, int g) {             // 16 of its tokens
-      const int s = c % kValueStages, left = (c == chunks - 1 ? tail : kChunk) - 32 * wg;
-      if (!wait(sh.v_full[s], (c / kValueStages) & 1)) return;
-      const uint8_t* col = base + kValuesAt + s * kTile + (r >> 6) * kHalfTile + 32 * wg * 128;
-      if (g == 0) top = 0;
+    auto load_values = [&](int c) {
+      const int left = (c == chunks - 1 ? tail : kChunk) - 32 * wg;
+      if (!wait(sh.turned[c & 1], (c >> 1) & 1)) return;
+      const uint32_t row = stages + kTurnedAt + (c & 1) * kTile + r * 128;
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const int j = 16 * g + e;
-        const uint32_t v0 = *reinterpret_cast<const uint16_t*>(col + j * 128 + (((r & 63) * 2) ^ ((j & 7) << 4)));
-        const uint32_t v1 = *reinterpret_cast<const uint16_t*>(col + (j + 1) * 128 + (((r & 63) * 2) ^ (((j + 1) & 7) << 4)));
-        uint32_t v = v0 | (v1 << 16);
-        if (left < 32) v = j >= left ? 0u : j + 1 >= left ? v0 : v;
-        values[j / 2] = v;
-        top = max_abs_bf16x2(top, v);
+      for (int v = 0; v < 4; ++v) {
+        const uint4 w = lds128(row + (((4 * wg + v) ^ (r & 7)) << 4));
+        values[4 * v] = w.x, values[4 * v + 1] = w.y, values[4 * v + 2] = w.z, values[4 * v + 3] = w.w;
       }
-      if (g == 1) tell_bar(sh.v_empty[s]);
-    };
-    // The larger of the row's two halves' offers.
-    auto tell = [&](int turn, float offer) {
-      sh.most[turn & 1][wg][r] = offer;
-      tell_bar(sh.told);
-      if (!wait(sh.told, turn & 1)) return offer;
-      return fmaxf(offer, sh.most[turn & 1][wg ^ 1][r]);
+      tell_bar(sh.taken[c & 1]);
+      if (left < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+          values[j / 2] = j >= left ? 0u : j + 1 >= left ? values[j / 2] & 0xFFFFu : values[j / 2];
+      }
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = max_abs_bf16x2(top, values[j]);
     };
     uint32_t largest = 0;                              // of the parts of S, as F16 pairs
     auto hand_over = [&](int q) {                      // 32 keys
@@ -987,9 +1017,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       tc_fence_before();
       tell_bar(sh.s_full[q]);
     };
-    load_values(0, 0);
-    if (ok) load_values(0, 1);
-    const float first_most = ok ? tell(0, fmaxf(most, max_bf16x2(top))) : 0.0f;
+    load_values(0);
+    most = fmaxf(most, max_bf16x2(top));
+    sh.most[1][wg][r] = most;
+    if (ok) {
+      tell_bar(sh.told);
+      wait(sh.told, 0);
+    }
+    const float first_most = fmaxf(most, sh.most[1][wg ^ 1][r]);
     float power = first_most > 0.0f ? power_for(first_most, 2) : 1.0f;
 #pragma unroll
     for (int k = 0; k < 64; ++k) S[k] *= power;
@@ -998,19 +1033,21 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       const int s = c % kStages;
       const bool more = c + 1 < chunks;
       const float* scalars = reinterpret_cast<const float*>(base + s * kStageBytes + kBlobAt + kScalars);
-      // while S meets K: this chunk's values, and half of the next one's
+      // while S meets K: this chunk's values
       if (wg == 0) sh.power[c & 1][r] = power;
       if (!wait(sh.full[s], (c / kStages) & 1)) break;
-      float y[32];
+      float2 y[16];
+      const float2 power2 = make_float2(power, power);
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         const float4 be = *reinterpret_cast<const float4*>(scalars + kBeta + 32 * wg + j);
-        y[j] = __uint_as_float(values[j / 2] << 16) * (be.x * power);
-        y[j + 1] = __uint_as_float(values[j / 2] & 0xFFFF0000u) * (be.y * power);
-        y[j + 2] = __uint_as_float(values[j / 2 + 1] << 16) * (be.z * power);
-        y[j + 3] = __uint_as_float(values[j / 2 + 1] & 0xFFFF0000u) * (be.w * power);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = values[j / 2 + e];
+          y[j / 2 + e] = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)),
+                                    __fmul2_rn(e ? make_float2(be.z, be.w) : make_float2(be.x, be.y), power2));
+        }
       }
-      if (more) load_values(c + 1, 0);
       if (!wait(sh.x_done, c & 1)) break;
       tc_fence_after();
       {
@@ -1023,8 +1060,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           for (int e = 0; e < 16; e += 4) {
             const int j = 16 * q + e;
             const float4 kf = *reinterpret_cast<const float4*>(scalars + kKey + 32 * wg + j);
-            split2(make_float2(fmaf(-kf.x, x[j], y[j]), fmaf(-kf.y, x[j + 1], y[j + 1])), hi[e / 2], lo[e / 2]);
-            split2(make_float2(fmaf(-kf.z, x[j + 2], y[j + 2]), fmaf(-kf.w, x[j + 3], y[j + 3])), hi[e / 2 + 1], lo[e / 2 + 1]);
+            split2(__ffma2_rn(make_float2(kf.x, kf.y), make_float2(x[j], x[j + 1]), y[j / 2]), hi[e / 2], lo[e / 2]);
+            split2(__ffma2_rn(make_float2(kf.z, kf.w), make_float2(x[j + 2], x[j + 3]), y[j / 2 + 1]), hi[e / 2 + 1],
+                   lo[e / 2 + 1]);
           }
           tmem_st8(mine + col_r(0, 2 * wg + q), hi);
           tmem_st8(mine + col_r(1, 2 * wg + q), lo);
@@ -1033,11 +1071,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           tell_bar(sh.r_full[q]);
         }
       }
-      // while r meets T: the other half of the next chunk's values
+      // while r meets T: the next chunk's values
       const float gamma = scalars[kGammaC];
       float offer = gamma * max_f16x2(largest);
       if (more) {
-        load_values(c + 1, 1);
+        load_values(c + 1);
         offer = fmaxf(offer, max_bf16x2(top) * power);
       }
       if (!wait(sh.u_done, c & 1)) break;
@@ -1053,30 +1091,29 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           for (int e = 0; e < 16; e += 4) {
             const int j = 16 * q + e;
             const float4 f = *reinterpret_cast<const float4*>(scalars + kUpdate + 32 * wg + j);
-            split2(make_float2(u[j] * f.x, u[j + 1] * f.y), hi[e / 2], lo[e / 2]);
-            split2(make_float2(u[j + 2] * f.z, u[j + 3] * f.w), hi[e / 2 + 1], lo[e / 2 + 1]);
+            split2(__fmul2_rn(make_float2(u[j], u[j + 1]), make_float2(f.x, f.y)), hi[e / 2], lo[e / 2]);
+            split2(__fmul2_rn(make_float2(u[j + 2], u[j + 3]), make_float2(f.z, f.w)), hi[e / 2 + 1], lo[e / 2 + 1]);
             m = max_abs_f16x2(max_abs_f16x2(m, hi[e / 2]), hi[e / 2 + 1]);
           }
           tmem_st8(mine + col_u(0, 2 * wg + q), hi);
           tmem_st8(mine + col_u(1, 2 * wg + q), lo);
+          if (q == 1) sh.most[c & 1][wg][r] = offer = fmaxf(offer, max_f16x2(m));   // read behind the product
           tmem_wait_st();
           tc_fence_before();
           tell_bar(sh.p_full[q]);
         }
-        offer = fmaxf(offer, max_f16x2(m));
       }
-      // while u meets K: the row's power of two
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
-      offer = tell(c + 1, offer);
+      if (!wait(sh.new_done, c & 1) || !wait(sh.p_full[1], c & 1)) break;   // (the second for the other half's offer)
+      tc_fence_after();
+      offer = fmaxf(offer, sh.most[c & 1][wg ^ 1][r]);
       float step = 1.0f;
       if (offer > 0.0f && !(offer >= 0x1p-3f && offer < 0x1p6f)) {
         step = fminf(fmaxf(power_for(offer / power, 2) / power, 0x1p-100f), 0x1p100f);
         power *= step;
       }
       const bool rescale = __any_sync(0xffffffffu, step != 1.0f);
-      const float keep = gamma * step;
-      if (!wait(sh.new_done, c & 1)) break;
-      tc_fence_after();
+      const float2 keep = make_float2(gamma * step, gamma * step);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float d[32];
@@ -1086,7 +1123,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           for (int k = 0; k < 32; ++k) d[k] *= step;
         }
 #pragma unroll
-        for (int k = 0; k < 32; ++k) S[32 * q + k] = fmaf(keep, S[32 * q + k], d[k]);
+        for (int k = 0; k < 32; k += 2) {
+          const float2 f = __ffma2_rn(keep, make_float2(S[32 * q + k], S[32 * q + k + 1]), make_float2(d[k], d[k + 1]));
+          S[32 * q + k] = f.x, S[32 * q + k + 1] = f.y;
+        }
       }
       if (more) hand_over(0), hand_over(1);
     }
