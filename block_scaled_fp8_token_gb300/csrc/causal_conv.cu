@@ -22,10 +22,10 @@ struct ConvParams {
   __nv_bfloat16* state;
   int64_t ldx, ldo, lds_slot, lds_row;
   Requests req;
-  int32_t channels, w_f32, silu, tile_shift;
+  int32_t channels, w_f32, tile_shift;
 };
 
-// n consecutive weights from `at` on, n a multiple of 8, widened.
+// N consecutive weights from `at` on, N a multiple of 8, widened.
 template <int N>
 BFP8_DEV void load_weights(const void* w, int32_t f32, int64_t at, float (&v)[N]) {
   if (f32) {
@@ -46,13 +46,19 @@ BFP8_DEV void load_weights(const void* w, int32_t f32, int64_t at, float (&v)[N]
     }
   }
 }
+BFP8_DEV void widen4x2(const uint4& r, float2 (&v)[4]) {
+  float f[8];
+  widen8(r, f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
 
 // A block takes 1024 channels of one tile of a request's tokens; a thread walks down its 8
-// channels with the last W - 1 inputs in registers. The thread of a request's first tile
-// also moves the state: it alone reads the old rows, before it writes the new ones, so one
-// slot may be both.
-template <int W>
-__global__ void __launch_bounds__(kConvThreads) causal_conv_kernel(const ConvParams p) {
+// channels with the last W - 1 inputs in registers, four rows at a time with the next four
+// asked for. The thread of a request's first tile also moves the state: it alone reads the old
+// rows, before it writes the new ones, so one slot may be both.
+template <int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads, 4) causal_conv_kernel(const ConvParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int b = find_request(p.req, blockIdx.y, p.tile_shift);
@@ -66,67 +72,90 @@ __global__ void __launch_bounds__(kConvThreads) causal_conv_kernel(const ConvPar
   const int64_t left = end - t0, most = int64_t{1} << p.tile_shift;
   const int n = static_cast<int>(left < most ? left : most);
 
-  float w[8 * W], bias[8] = {};
-  load_weights(p.weight, p.w_f32, static_cast<int64_t>(c) * W, w);
-  if (p.bias) load_weights(p.bias, p.w_f32, c, bias);
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const __nv_bfloat16* x = p.x + t0 * p.ldx + c;
-  uint4 past[W - 1];   // inputs t0 - (W - 1) .. t0 - 1
-  if (tile > 0) {
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      past[j] = __ldg(reinterpret_cast<const uint4*>(x + (j - (W - 1)) * p.ldx));
-  } else {
-    const int64_t from = slot_of(p.req, p.req.slots_in, b), to = slot_of(p.req, p.req.slots_out, b);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      past[j] = from < 0 ? zero
-                         : *reinterpret_cast<const uint4*>(p.state + from * p.lds_slot + j * p.lds_row + c);
-    if (to >= 0) {
-      const int64_t len = end - first;
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) {
-        uint4 v = zero;
-        if (len + j >= W - 1) {
-          v = __ldg(reinterpret_cast<const uint4*>(x + (len + j - (W - 1)) * p.ldx));
-        } else {
-#pragma unroll
-          for (int i = 0; i < W - 1; ++i)   // a short request: row len + j of the old state
-            if (i == len + j) v = past[i];
-        }
-        *reinterpret_cast<uint4*>(p.state + to * p.lds_slot + j * p.lds_row + c) = v;
-      }
-    }
-  }
-  float h[W - 1][8];
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) widen8(past[j], h[j]);
-  __nv_bfloat16* out = p.out + t0 * p.ldo + c;
   constexpr int U = 4;
-  for (int t = 0; t < n; t += U) {
-    uint4 raw[U];
+  const __nv_bfloat16* x = p.x + t0 * p.ldx + c;
+  auto row = [&](int64_t t) { return __ldg(reinterpret_cast<const uint4*>(x + t * p.ldx)); };
+  uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < n) raw[u] = __ldg(reinterpret_cast<const uint4*>(x + (t + u) * p.ldx));
+  for (int u = 0; u < U; ++u)
+    if (u < n) raw[u] = row(u);
+  float2 w[W][4], h[W - 1][4], bias[4];
+  {
+    float flat[8 * W], flat_bias[8] = {};
+    load_weights(p.weight, p.w_f32, static_cast<int64_t>(c) * W, flat);
+    if (p.bias) load_weights(p.bias, p.w_f32, c, flat_bias);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t + u >= n) break;
-      float v[8], y[8];
-      widen8(raw[u], v);
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = bias[e];
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) y[e] = fmaf(w[e * W + j], h[j][e], y[e]);
-        y[e] = fmaf(w[e * W + W - 1], v[e], y[e]);
-        if (p.silu) y[e] = silu(y[e]);
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
-        h[W - 2][e] = v[e];
-      }
-      *reinterpret_cast<uint4*>(out + (t + u) * p.ldo) = pack8(y);
+      for (int j = 0; j < W; ++j) w[j][e] = make_float2(flat[2 * e * W + j], flat[(2 * e + 1) * W + j]);
+      bias[e] = make_float2(flat_bias[2 * e], flat_bias[2 * e + 1]);
     }
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 past[W - 1];   // inputs t0 - (W - 1) .. t0 - 1
+    if (tile > 0) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) past[j] = row(j - (W - 1));
+    } else {
+      const int64_t from = slot_of(p.req, p.req.slots_in, b), to = slot_of(p.req, p.req.slots_out, b);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        past[j] = from < 0 ? zero
+                           : *reinterpret_cast<const uint4*>(p.state + from * p.lds_slot + j * p.lds_row + c);
+      if (to >= 0) {
+        const int64_t len = end - first;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          uint4 v = zero;
+          if (len + j >= W - 1) {
+            v = row(len + j - (W - 1));
+          } else {
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)   // a short request: row len + j of the old state
+              if (i == len + j) v = past[i];
+          }
+          *reinterpret_cast<uint4*>(p.state + to * p.lds_slot + j * p.lds_row + c) = v;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) widen4x2(past[j], h[j]);
   }
+  __nv_bfloat16* out = p.out + t0 * p.ldo + c;
+  auto step = [&](const uint4& r) {
+    float2 v[4], y[4];
+    widen4x2(r, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = bias[e];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) y[e] = __ffma2_rn(w[j][e], h[j][e], y[e]);
+      y[e] = __ffma2_rn(w[W - 1][e], v[e], y[e]);
+      if (SILU) y[e] = __fmul2_rn(y[e], make_float2(sigmoid(y[e].x), sigmoid(y[e].y)));
+#pragma unroll
+      for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
+      h[W - 2][e] = v[e];
+    }
+    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                                                pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+    out += p.ldo;
+  };
+  int t = 0;
+  for (; t + 2 * U <= n; t += U) {
+    uint4 now[U];
+    x += U * p.ldx;
+#pragma unroll
+    for (int u = 0; u < U; ++u) now[u] = raw[u], raw[u] = row(u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(now[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (t + u < n) step(raw[u]);
+  t += U;
+  x += U * p.ldx;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (t + u < n) step(row(u));
 }
 
 bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -171,15 +200,15 @@ int launch_causal_conv(const bfp8_causal_conv_args& a, void* stream) {
   p.req = {a.q_offsets, a.slots_in, a.slots_out, a.tokens, a.n_slots, static_cast<int32_t>(a.batch)};
   p.channels = static_cast<int32_t>(a.channels);
   p.w_f32 = a.w_dtype == BFP8_DT_F32;
-  p.silu = a.silu != 0;
   p.tile_shift = shift;
   const dim3 grid(static_cast<unsigned>((a.channels / 8 + kConvThreads - 1) / kConvThreads),
                   static_cast<unsigned>(tiles));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, kConvThreads, 0, st, p); };
   switch (a.width) {
-    case 2: return launch_dependent(causal_conv_kernel<2>, grid, kConvThreads, 0, st, p);
-    case 3: return launch_dependent(causal_conv_kernel<3>, grid, kConvThreads, 0, st, p);
-    default: return launch_dependent(causal_conv_kernel<4>, grid, kConvThreads, 0, st, p);
+    case 2: return a.silu ? go(causal_conv_kernel<2, true>) : go(causal_conv_kernel<2, false>);
+    case 3: return a.silu ? go(causal_conv_kernel<3, true>) : go(causal_conv_kernel<3, false>);
+    default: return a.silu ? go(causal_conv_kernel<4, true>) : go(causal_conv_kernel<4, false>);
   }
 }
 

@@ -15,7 +15,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kGatedThreads = 256;
+constexpr int kGatedThreads = 256, kGatedAhead = 4;   // tokens whose loads a warp has under way
 
 struct GatedParams {
   const __nv_bfloat16* x;
@@ -24,67 +24,119 @@ struct GatedParams {
   __nv_bfloat16* out;
   uint8_t* q;
   float* s;
-  int64_t xt, xh, zt, zh, ot, oh, ldq, ssm, sskb, items;
+  int64_t xt, xh, zt, zh, ot, oh, ldq, ssm, sskb, tokens, warps;
   int32_t cols, segs, w_f32, is_sigmoid;
   float eps, w_offset;
 };
 
-// A warp takes 256 columns of one token, 8 a lane: a head of DIM columns is DIM / 8
-// consecutive lanes, a group of 128 columns 16, so both reductions stay in the warp.
+// A warp takes 256 columns, 8 a lane, of one token after the other: a head of DIM columns is
+// DIM / 8 consecutive lanes, a group of 128 columns 16, so both reductions stay in the warp,
+// and the weights stay in registers. A lane copies its 16 bytes of the next tokens to places of
+// its own in shared memory, four ahead, and waits for nobody else.
 template <int DIM>
-__global__ void __launch_bounds__(kGatedThreads) gated_norm_kernel(const GatedParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kGatedThreads / 32) + (threadIdx.x >> 5);
-  if (item >= p.items) return;
-  const int64_t row = item / p.segs;
+__global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const GatedParams p) {
+  __shared__ alignas(16) uint4 ring[kGatedAhead][2][kGatedThreads];
   const int lane = threadIdx.x & 31;
-  const int c = (static_cast<int>(item - row * p.segs) * 32 + lane) * 8;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * (kGatedThreads / 32) + (threadIdx.x >> 5);
+  const int64_t step = p.warps / p.segs;               // tokens between a warp's: p.warps is a multiple of segs
+  const int c = (static_cast<int>(at % p.segs) * 32 + lane) * 8;
   const bool in = c < p.cols;
   const int head = c / DIM, d = c % DIM;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const uint4 xr = in ? *reinterpret_cast<const uint4*>(p.x + row * p.xt + head * p.xh + d) : zero;
-  const uint4 zr = in ? *reinterpret_cast<const uint4*>(p.z + row * p.zt + head * p.zh + d) : zero;
-  float y[8], z[8];
-  widen8(xr, y);
-  widen8(zr, z);
+  pdl_wait();
+  pdl_launch_dependents();
+  int64_t row = at / p.segs;
+  if (at >= p.warps || row >= p.tokens) return;
+  const __nv_bfloat16* px = p.x + row * p.xt + head * p.xh + d;
+  const __nv_bfloat16* pz = p.z + row * p.zt + head * p.zh + d;
+  __nv_bfloat16* po = p.out + row * p.ot + head * p.oh + d;
+  uint8_t* pq = p.q + row * p.ldq + c;
+  float* ps = p.s + row * p.ssm + (c >> 7) * p.sskb;
+  int64_t asked = row;
+  const uint32_t place = smem_u32(&ring[0][0][threadIdx.x]);
+  if (!in) {                                           // lanes past the last column take zeros for ever
+#pragma unroll
+    for (int s = 0; s < kGatedAhead; ++s) ring[s][0][threadIdx.x] = ring[s][1][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  auto ask = [&](int s) {
+    if (in && asked < p.tokens) {
+      cp_async16(place + s * static_cast<uint32_t>(sizeof(ring[0])), px);
+      cp_async16(place + s * static_cast<uint32_t>(sizeof(ring[0])) + static_cast<uint32_t>(sizeof(ring[0][0])), pz);
+    }
+    cp_async_commit();
+    asked += step, px += step * p.xt, pz += step * p.zt;
+  };
+#pragma unroll
+  for (int s = 0; s < kGatedAhead; ++s) ask(s);
+  float2 w[4];
   if (p.w) {
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-    for (int o = DIM / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(fmaf(ss, 1.0f / DIM, p.eps));
-    float w[8];
     if (p.w_f32) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d + 4));
-      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d));
+      const float4 g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d + 4));
+      w[0] = make_float2(f.x, f.y), w[1] = make_float2(f.z, f.w), w[2] = make_float2(g.x, g.y), w[3] = make_float2(g.z, g.w);
     } else {
-      widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w) + d)), w);
+      float f[8];
+      widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w) + d)), f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = make_float2(f[2 * e], f[2 * e + 1]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= r * (w[e] + p.w_offset);
+    for (int e = 0; e < 4; ++e) w[e].x += p.w_offset, w[e].y += p.w_offset;
   }
-  float am = 0.0f;
+  for (int s = 0; row < p.tokens; s = (s + 1) % kGatedAhead, row += step) {
+    float x[8], z[8];
+    cp_async_wait_group<kGatedAhead - 1>();
+    widen8(lds128(place + s * static_cast<uint32_t>(sizeof(ring[0]))), x);
+    widen8(lds128(place + s * static_cast<uint32_t>(sizeof(ring[0])) + static_cast<uint32_t>(sizeof(ring[0][0]))), z);
+    ask(s);
+    float2 y[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    y[e] *= p.is_sigmoid ? sigmoid(z[e]) : silu(z[e]);
-    am = fmaxf(am, fabsf(y[e]));
+    for (int e = 0; e < 4; ++e) y[e] = make_float2(x[2 * e], x[2 * e + 1]);
+    if (p.w) {
+      float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
+      float ss = s2.x + s2.y;
+#pragma unroll
+      for (int o = DIM / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(fmaf(ss, 1.0f / DIM, p.eps));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], __fmul2_rn(w[e], make_float2(r, r)));
+    }
+    float am = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = z[2 * e], b = z[2 * e + 1];
+      float2 g = make_float2(sigmoid(a), sigmoid(b));
+      if (!p.is_sigmoid) g = __fmul2_rn(g, make_float2(a, b));
+      y[e] = __fmul2_rn(y[e], g);
+      am = fmaxf(am, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
+    }
+    if (p.out && in)
+      *reinterpret_cast<uint4*>(po) =
+          make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
+                     pack_bf16x2(y[3].x, y[3].y));
+    if (p.q) {
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      // am / 448 rounded (its remainder is exact), and 1 / s within 2^-23
+      am = fmaxf(am, 1e-10f);
+      float sc = am * (1.0f / 448.0f);
+      if (am <= 3.0e38f) sc = fmaf(fmaf(-448.0f, sc, am), 1.0f / 448.0f, sc);
+      float inv = rcp_approx(sc);
+      if (am <= 3.0e38f) inv = fmaf(fmaf(-sc, inv, 1.0f), inv, inv);
+      if (in) {
+        if ((lane & 15) == 0) *ps = sc;
+        uint32_t cw[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = __fmul2_rn(y[2 * j], make_float2(inv, inv)), g = __fmul2_rn(y[2 * j + 1], make_float2(inv, inv));
+          cw[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(f.x, f.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(g.x, g.y)) << 16);
+        }
+        *reinterpret_cast<uint2*>(pq) = make_uint2(cw[0], cw[1]);
+      }
+    }
+    po += step * p.ot, pq += step * p.ldq, ps += step * p.ssm;
   }
-  if (p.out && in) *reinterpret_cast<uint4*>(p.out + row * p.ot + head * p.oh + d) = pack8(y);
-  if (!p.q) return;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  const float sc = __fdiv_rn(fmaxf(am, 1e-10f), 448.0f), inv = __frcp_rn(sc);
-  if (!in) return;
-  if ((lane & 15) == 0) p.s[row * p.ssm + (c >> 7) * p.sskb] = sc;
-  uint32_t cw[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    cw[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(y[4 * j] * inv, y[4 * j + 1] * inv)) |
-            (static_cast<uint32_t>(f32x2_to_e4m3x2(y[4 * j + 2] * inv, y[4 * j + 3] * inv)) << 16);
-  *reinterpret_cast<uint2*>(p.q + row * p.ldq + c) = make_uint2(cw[0], cw[1]);
 }
 
 bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -130,12 +182,20 @@ int launch_gated_norm(const bfp8_gated_norm_args& a, void* stream) {
   p.ldq = a.ldq, p.ssm = a.s_stride_m, p.sskb = a.s_stride_kb;
   p.cols = static_cast<int32_t>(cols);
   p.segs = static_cast<int32_t>((cols + 255) / 256);
-  p.items = a.tokens * p.segs;
   p.w_f32 = a.w_dtype == BFP8_DT_F32;
   p.is_sigmoid = a.gate_act == BFP8_ACT_SIGMOID;
   p.eps = a.eps;
   p.w_offset = a.weight_offset;
-  const int64_t blocks = (p.items + kGatedThreads / 32 - 1) / (kGatedThreads / 32);
+  p.tokens = a.tokens;
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc != BFP8_OK) return rc;
+  // a warp to each 256 columns of a token, down to what fills the GPU once
+  constexpr int kPer = kGatedThreads / 32, kFit = 96;  // warps of a block, and of an SM
+  int64_t rows = (int64_t{sms} * kFit + p.segs - 1) / p.segs;
+  rows = rows < a.tokens ? rows : a.tokens;
+  p.warps = rows * p.segs;
+  const int64_t blocks = (p.warps + kPer - 1) / kPer;
   if (blocks > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(blocks));

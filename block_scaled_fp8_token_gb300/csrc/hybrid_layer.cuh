@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attention_layer.cuh"
+#include "act_math.cuh"
 #include "hybrid_layer.h"
 
 namespace bfp8 {
@@ -27,12 +28,21 @@ BFP8_DEV uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// 1 / (1 + e^-x), relative error below (4 + 1.2 max(0, -x)) 2^-23: the approximate exponential's
-// is 2 + 1.16 |x| units, and counts in full where e^-x outweighs the 1. That is under 2^-16
-// down to x = -88, below which e^-x overflows and the result is 0: for results that BF16 or
-// E4M3 rounds (2^-8, 2^-4).
-BFP8_DEV float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
-BFP8_DEV float silu(float x) { return x * sigmoid(x); }
+// 16 bytes from global to shared memory past the registers. A thread's groups complete in
+// order; what a thread copied itself it may read after its own wait.
+BFP8_DEV void cp_async16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+BFP8_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+BFP8_DEV void cp_async_wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// 1 / (1 + e^-x), relative error below (4 + 1.2 max(0, -x)) 2^-23: 2^x's approximation is
+// within 2 units, its argument's product with log2 e adds 1.16 |x|, and both count in full
+// where e^-x outweighs the 1; the reciprocal adds 1. That is under 2^-16 down to x = -87, below
+// which e^-x overflows (or its reciprocal is subnormal) and the result is 0: for results that
+// BF16 or E4M3 rounds (2^-8, 2^-4).
+BFP8_DEV float sigmoid(float x) { return rcp_approx(1.0f + ex2_approx(x * -1.4426950408889634f)); }
 
 // The requests of a step lie one behind another: request b has the tokens
 // [offsets[b], offsets[b + 1]), within [0, T] whatever the array holds.

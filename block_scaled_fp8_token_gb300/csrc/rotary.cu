@@ -19,7 +19,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRotaryThreads = 256;
+constexpr int kRotaryThreads = 256, kRotaryAhead = 4;   // groups of heads whose loads a warp has under way
 
 struct RotaryTensor {
   const __nv_bfloat16* x;
@@ -33,7 +33,7 @@ struct RotaryParams {
   const int32_t* positions;
   const float* inv_freq;
   int64_t ldp, tokens;
-  int32_t axes, half, split, w_f32, interleaved;
+  int32_t axes, half, block_tokens, blocks, w_f32, interleaved;
   int32_t end[4];          // sections: of one behind another the ends; in turns, the lengths
   float eps, w_offset, factor;
 };
@@ -61,116 +61,152 @@ BFP8_DEV uint64_t turns_of(float f) {
   return bits >> 31 ? 0 - r : r;
 }
 
-template <int DIM>
-BFP8_DEV void load_norm_weight(const RotaryParams& p, const void* w, int d, float (&v)[8]) {
-  if (p.w_f32) {
-    const float* f = static_cast<const float*>(w) + d;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __ldg(f + e);
-  } else {
-    widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + d)), v);
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] += p.w_offset;
+BFP8_DEV float norm_weight(const RotaryParams& p, const void* w, int d) {
+  const float v = p.w_f32 ? __ldg(static_cast<const float*>(w) + d)
+                          : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + d));
+  return v + p.w_offset;
 }
 
-// A warp takes 256 / DIM heads of one token at a time, 8 columns a lane, and `split` warps
-// share a token's heads. Its angles' sines and cosines are formed once and serve all of the
-// warp's heads. The partner of a lane's columns is in the lane half / 8 away.
+// A warp takes 256 / DIM heads of one token at a time, 8 columns a lane. A block has one token
+// or several; its sines and cosines are formed once, an angle a thread, and with the norm's
+// weights they make two factors a column that serve all of a token's heads:
+//   out = r (x cw + partner sw),   r the head's norm factor.
+// A column's partner is in the lane half / 8 away, or next to it in the same word.
 template <int DIM, bool ADJACENT>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryParams p) {
-  __shared__ uint64_t turns[DIM / 2];
-  __shared__ uint8_t axis[DIM / 2];
+__global__ void __launch_bounds__(kRotaryThreads, 4) rotary_kernel(const RotaryParams p) {
+  constexpr int kWarps = kRotaryThreads / 32;
+  __shared__ float2 turned_by[kWarps][DIM / 2];    // cosine and sine of each token's pairs
+  __shared__ alignas(16) float weight[2][DIM];
+  __shared__ alignas(16) uint4 ring[kRotaryAhead][kRotaryThreads];
   pdl_wait();
   pdl_launch_dependents();
-  for (int i = threadIdx.x; i < p.half; i += kRotaryThreads) {
-    turns[i] = turns_of(__ldg(p.inv_freq + i));
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t block = blockIdx.x / p.blocks;     // of tokens; p.blocks > 1 blocks share one token
+  const int per = kWarps / p.block_tokens;         // warps of a token in this block
+  const int mine = (tid >> 5) / per;               // the warp's token among the block's
+  const int64_t t = block * p.block_tokens + mine;
+  const int split = per * p.blocks, first = (tid >> 5) % per * p.blocks + static_cast<int>(blockIdx.x % p.blocks);
+  constexpr int kLanes = DIM / 8;                  // of one head
+  const int d = (lane % kLanes) * 8, half = p.half;
+  const int64_t step = static_cast<int64_t>(split) * (32 / kLanes);
+  const uint32_t place = smem_u32(&ring[0][tid]);
+  // groups are dealt on from the queries' to the keys'
+  const int keys = (first + split - p.t[0].groups % split) % split;
+  const __nv_bfloat16* x = nullptr;
+  int asked = 0;
+  auto ask = [&](const RotaryTensor& q, int s) {   // a lane copies its own columns of a head
+    if (asked < q.heads) cp_async16(place + s * static_cast<uint32_t>(sizeof(ring[0])), x);
+    cp_async_commit();
+    asked += static_cast<int>(step), x += step * q.xh;
+  };
+  auto begin = [&](const RotaryTensor& q, int g) {
+    asked = g * (32 / kLanes) + lane / kLanes;
+    x = q.x + t * q.xt + asked * q.xh + d;
+#pragma unroll
+    for (int s = 0; s < kRotaryAhead; ++s) ask(q, s);
+  };
+  const bool queries = first < p.t[0].groups;
+  if (t < p.tokens && queries) begin(p.t[0], first);   // under way while the angles are formed
+  for (int i = tid; i < p.block_tokens * p.half; i += kRotaryThreads) {
+    const int k = i / p.half, pair = i - k * p.half;
+    if (block * p.block_tokens + k >= p.tokens) break;
     int a = 0;
     if (p.interleaved) {
-      a = i % p.axes;
-      if (i / p.axes >= p.end[a]) a = 0;
+      a = pair % p.axes;
+      if (pair / p.axes >= p.end[a]) a = 0;
     } else {
-      while (a + 1 < p.axes && i >= p.end[a]) ++a;
+      while (a + 1 < p.axes && pair >= p.end[a]) ++a;
     }
-    axis[i] = static_cast<uint8_t>(a);
+    const float f = __ldg(p.inv_freq + pair);
+    const uint64_t phase = static_cast<uint32_t>(__ldg(p.positions + a * p.ldp + block * p.block_tokens + k)) * turns_of(f);
+    float2 cs;
+    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &cs.y, &cs.x);
+    if (!(fabsf(f) < 0x1p32f)) cs.x = cs.y = __int_as_float(0x7FFFFFFF);
+    turned_by[k][pair] = make_float2(cs.x * p.factor, cs.y * p.factor);
+  }
+  for (int i = tid; i < 2 * DIM; i += kRotaryThreads) {
+    const void* w = i < DIM ? p.t[0].w : p.t[1].w;
+    if (w) weight[i / DIM][i % DIM] = norm_weight(p, w, i % DIM);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRotaryThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = item / p.split;
   if (t >= p.tokens) return;
-  int32_t pos[4] = {};
-  for (int a = 0; a < p.axes; ++a) {
-    pos[a] = __ldg(p.positions + a * p.ldp + t);
-    if (pos[a] < 0) return;                        // a row of no request
-  }
-  constexpr int kLanes = DIM / 8;                  // of one head
-  constexpr int N = ADJACENT ? 4 : 8;              // angles a lane needs
-  const int d = (lane % kLanes) * 8, half = p.half;
-  const bool turned = d < 2 * half;
-  const bool second = !ADJACENT && d >= half;
-  const int partner = (lane & ~(kLanes - 1)) + (((second ? d - half : d + half) & (DIM - 1)) >> 3);
-  float cs[N], sn[N];
-  if (turned) {
-    const int first = ADJACENT ? d / 2 : second ? d - half : d;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int a = axis[first + j];
-      const uint32_t at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-      const uint64_t phase = at * turns[first + j];
-      const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-      sincospif(x, &sn[j], &cs[j]);
-      const float f = __ldg(p.inv_freq + first + j);
-      if (!(fabsf(f) < 0x1p32f)) sn[j] = cs[j] = __int_as_float(0x7FFFFFFF);
-      cs[j] *= p.factor;
-      sn[j] *= second ? p.factor : -p.factor;      // what the partner is multiplied by
+  for (int a = 0; a < p.axes; ++a)
+    if (__ldg(p.positions + a * p.ldp + t) < 0) {  // a row of no request
+      cp_async_wait_group<0>();
+      return;
     }
-  }
-  const int all = p.t[0].groups + p.t[1].groups;
-  for (int g = static_cast<int>(item - t * p.split); g < all; g += p.split) {
-    const bool key = g >= p.t[0].groups;
-    const RotaryTensor& q = key ? p.t[1] : p.t[0];
-    const int head = (key ? g - p.t[0].groups : g) * (32 / kLanes) + lane / kLanes;
-    const bool in = head < q.heads;
-    const uint4 raw = in ? *reinterpret_cast<const uint4*>(q.x + t * q.xt + head * q.xh + d)
-                         : make_uint4(0u, 0u, 0u, 0u);
-    float x[8], other[8];
-    widen8(raw, x);
-    if (!ADJACENT) {
-      const uint4 r = make_uint4(__shfl_sync(0xffffffffu, raw.x, partner), __shfl_sync(0xffffffffu, raw.y, partner),
-                                 __shfl_sync(0xffffffffu, raw.z, partner), __shfl_sync(0xffffffffu, raw.w, partner));
-      widen8(r, other);
+  const bool turned = d < 2 * half, second = !ADJACENT && d >= half;
+  const int partner = turned ? (lane & ~(kLanes - 1)) + ((second ? d - half : d + half) >> 3) : lane;
+
+  auto walk = [&](const RotaryTensor& q, int g, const float2 (&cw)[4], const float2 (&sw)[4]) {
+    int head = g * (32 / kLanes) + lane / kLanes;
+    __nv_bfloat16* out = q.out + t * q.ot + head * q.oh + d;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int s = 0; g < q.groups; g += split, out += step * q.oh, head += static_cast<int>(step), s = (s + 1) % kRotaryAhead) {
+      const bool in = head < q.heads;
+      cp_async_wait_group<kRotaryAhead - 1>();
+      const uint4 raw = in ? lds128(place + s * static_cast<uint32_t>(sizeof(ring[0]))) : zero;
+      ask(q, s);
+      uint4 other;
+      if (ADJACENT) {
+        other = make_uint4(__byte_perm(raw.x, 0u, 0x1032), __byte_perm(raw.y, 0u, 0x1032), __byte_perm(raw.z, 0u, 0x1032),
+                           __byte_perm(raw.w, 0u, 0x1032));
+      } else {
+        other = make_uint4(__shfl_sync(0xffffffffu, raw.x, partner), __shfl_sync(0xffffffffu, raw.y, partner),
+                           __shfl_sync(0xffffffffu, raw.z, partner), __shfl_sync(0xffffffffu, raw.w, partner));
+      }
+      if (!turned) other = zero;                   // an infinity there stays one
+      const uint32_t xw[4] = {raw.x, raw.y, raw.z, raw.w}, ow[4] = {other.x, other.y, other.z, other.w};
+      float2 y[4];
+      float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = make_float2(__uint_as_float(xw[e] << 16), __uint_as_float(xw[e] & 0xFFFF0000u));
+        const float2 b = make_float2(__uint_as_float(ow[e] << 16), __uint_as_float(ow[e] & 0xFFFF0000u));
+        if (q.w) s2 = __ffma2_rn(a, a, s2);
+        y[e] = __ffma2_rn(a, cw[e], __fmul2_rn(b, sw[e]));
+      }
+      if (q.w) {
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(fmaf(ss, 1.0f / DIM, p.eps));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], make_float2(r, r));
+      }
+      if (in)
+        *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                                                    pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
     }
-    if (q.w) {
-      float ss = 0.0f;
+  };
+
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const RotaryTensor& q = k ? p.t[1] : p.t[0];
+    const int g = k ? keys : first;
+    if (g >= q.groups) continue;
+    if (k) {
+      cp_async_wait_group<0>();                    // the places are free: what the queries asked for has come
+      begin(q, g);
+    }
+    float c[8], s[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(fmaf(ss, 1.0f / DIM, p.eps));
-      float w[8];
-      load_norm_weight<DIM>(p, q.w, d, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
-      if (!ADJACENT) {
-        load_norm_weight<DIM>(p, q.w, (partner % kLanes) * 8, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) other[e] *= r * w[e];
+    for (int e = 0; e < 8; ++e) {
+      c[e] = 1.0f, s[e] = 0.0f;
+      if (turned) {
+        const float2 cs = turned_by[mine][ADJACENT ? (d + e) >> 1 : second ? d + e - half : d + e];
+        c[e] = cs.x;
+        s[e] = (ADJACENT ? e & 1 : second) ? cs.y : -cs.y;
+      }
+      if (q.w) {
+        c[e] *= weight[k][d + e];
+        if (turned) s[e] *= weight[k][ADJACENT ? (d + e) ^ 1 : second ? d + e - half : d + e + half];
       }
     }
-    if (turned) {
+    float2 cw[4], sw[4];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (ADJACENT) {
-          const float a = x[2 * j], b = x[2 * j + 1];
-          x[2 * j] = fmaf(b, sn[j], a * cs[j]);    // sn holds -sin
-          x[2 * j + 1] = fmaf(-a, sn[j], b * cs[j]);
-        } else {
-          x[j] = fmaf(other[j], sn[j], x[j] * cs[j]);
-        }
-      }
-    }
-    if (in) *reinterpret_cast<uint4*>(q.out + t * q.ot + head * q.oh + d) = pack8(x);
+    for (int e = 0; e < 4; ++e) cw[e] = make_float2(c[2 * e], c[2 * e + 1]), sw[e] = make_float2(s[2 * e], s[2 * e + 1]);
+    walk(q, g, cw, sw);
   }
 }
 
@@ -237,11 +273,15 @@ int launch_rotary(const bfp8_rotary_args& a, void* stream) {
   p.eps = a.eps;
   p.w_offset = a.weight_offset;
   p.factor = a.factor;
-  // few tokens: as many warps share one as fill the GPU, down to a warp a group of heads
-  const int64_t groups = p.t[0].groups + p.t[1].groups;
-  int64_t split = (int64_t{sms} * 32 + a.tokens - 1) / a.tokens;
-  p.split = static_cast<int32_t>(split < groups ? split : groups);
-  const int64_t warps = a.tokens * p.split, blocks = (warps + kRotaryThreads / 32 - 1) / (kRotaryThreads / 32);
+  // A token's angles are formed by each block that has it: eight tokens to a block, fewer where
+  // that leaves SMs without four blocks, and several blocks to a token of many heads where one
+  // each does.
+  const int64_t groups = p.t[0].groups + p.t[1].groups, want = sms;
+  p.block_tokens = a.tokens >= 8 * want ? 8 : a.tokens >= 4 * want ? 4 : a.tokens >= 2 * want ? 2 : 1;
+  int64_t share = (want + a.tokens - 1) / a.tokens;
+  const int64_t most = (groups + kRotaryThreads / 32 - 1) / (kRotaryThreads / 32);
+  p.blocks = static_cast<int32_t>(p.block_tokens > 1 ? 1 : share < most ? share : most);
+  const int64_t blocks = (a.tokens + p.block_tokens - 1) / p.block_tokens * p.blocks;
   if (blocks > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
