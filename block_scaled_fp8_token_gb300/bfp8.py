@@ -1007,6 +1007,13 @@ _GATED_NORM = struct.Struct("P2qP2qPiiffP2qPqP4qi0q")  # bfp8_gated_norm_args
 _ROTARY = struct.Struct("P2qP2qP2qP2qPq3Pifff3q9i0q")  # bfp8_rotary_args
 BFP8_ACT_SILU, BFP8_ACT_SIGMOID = 0, 1
 
+# The calls below first try what their arguments nearly always are: one expression looks at
+# types, shapes and inner strides, and the library itself refuses memory that is not the current
+# device's. Where either says no, the call goes through the helpers, piece by piece, which put
+# the strides of lone dimensions right, or say what is wrong. A call that the library refuses
+# has done nothing.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
 
 def _slots(state, slots_in, slots_out, B: int, dev: int) -> tuple[int, int, int]:
     """The pool's slots, and the addresses of the two slot arrays."""
@@ -1039,8 +1046,25 @@ def bfp8_causal_conv(x, weight, out, q_offsets, state=None, slots_in=None, slots
     """The short depthwise convolution of x [T, C] with weight [C, width] over each
     request's tokens; state [slots, width - 1, C] holds the inputs ahead of them."""
     dev = _device()
-    T, C = x.shape
+    T, C = shape = x.shape
     B, W = q_offsets.shape[0] - 1, weight.shape[1]
+    if (state is not None and slots_in is not None and slots_out is not None
+            and weight.shape == (C, W) and out.shape == shape
+            and state.shape[1:] == (W - 1, C) and slots_in.shape == slots_out.shape == (B,)
+            and x.dtype is out.dtype is state.dtype is _BF16
+            and q_offsets.dtype is slots_in.dtype is slots_out.dtype is _I32
+            and (bias is None or (bias.shape == (C,) and bias.dtype is weight.dtype
+                                  and bias.is_contiguous()))
+            and weight.is_contiguous() and q_offsets.is_contiguous()
+            and slots_in.is_contiguous() and slots_out.is_contiguous()):
+        (xt, xc), (ot, oc), (st, sr, sc) = x.stride(), out.stride(), state.stride()
+        if xc == oc == sc == 1 and _lib.bfp8_causal_conv(_CAUSAL_CONV.pack(
+                x.data_ptr(), xt, out.data_ptr(), ot, weight.data_ptr(),
+                0 if bias is None else bias.data_ptr(),
+                _WEIGHT_CODES.get(weight.dtype, BFP8_DT_NONE), W, silu, state.data_ptr(), st, sr,
+                state.shape[0], slots_in.data_ptr(), slots_out.data_ptr(), q_offsets.data_ptr(), B,
+                T, C), _raw_stream(stream, dev)) == BFP8_OK:
+            return
     if state is None:
         at = (0, 0, 0)
     else:
@@ -1077,8 +1101,32 @@ def bfp8_delta_rule(q, k, v, a, b, a_log, dt_bias, state, slots_in, slots_out, q
     gates' inputs a, b [T, v heads]; state [slots, v heads, 128, 128] is float32, a row a
     value and a column a key. scale defaults to 1 / sqrt(128)."""
     dev = _device()
-    T, hk, D = q.shape
-    hv, B = v.shape[1], q_offsets.shape[0] - 1
+    T, hk, D = qk = q.shape
+    vo, B = v.shape, q_offsets.shape[0] - 1
+    hv = vo[1]
+    if scale is None:
+        scale = D ** -0.5
+    if (state is not None and slots_in is not None and slots_out is not None
+            and k.shape == qk and vo == out.shape == (T, hv, D) and a.shape == b.shape == (T, hv)
+            and a_log.shape == dt_bias.shape == (hv,) and state.shape[1:] == (hv, D, D)
+            and slots_in.shape == slots_out.shape == (B,)
+            and q.dtype is k.dtype is v.dtype is out.dtype is a.dtype is b.dtype is _BF16
+            and a_log.dtype is dt_bias.dtype is state.dtype is _F32
+            and q_offsets.dtype is slots_in.dtype is slots_out.dtype is _I32
+            and a_log.is_contiguous() and dt_bias.is_contiguous() and q_offsets.is_contiguous()
+            and slots_in.is_contiguous() and slots_out.is_contiguous()):
+        (qt, qh, qd), (kt, kh, kd), (vt, vh, vd) = q.stride(), k.stride(), v.stride()
+        (ot, oh, od), (ss, sh, sv, sk) = out.stride(), state.stride()
+        (at, ah), (bt, bh) = a.stride(), b.stride()
+        wsp, wsb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+        if (qd == kd == vd == od == ah == bh == sk == 1 and sv == D
+                and _lib.bfp8_delta_rule(_DELTA_RULE.pack(
+                    q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, a.data_ptr(),
+                    at, b.data_ptr(), bt, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(),
+                    ss, sh, state.shape[0], slots_in.data_ptr(), slots_out.data_ptr(),
+                    q_offsets.data_ptr(), out.data_ptr(), ot, oh, B, T, max_q_len, hk, hv, D,
+                    scale, eps, wsp, wsb), _raw_stream(stream, dev)) == BFP8_OK):
+            return
     if state is None:
         at = (0, 0, 0)
     else:
@@ -1101,7 +1149,7 @@ def bfp8_delta_rule(q, k, v, a, b, a_log, dt_bias, state, slots_in, slots_out, q
         _vec(dt_bias, "dt_bias", "f32", hv, dev), *at,
         *_slots(state, slots_in, slots_out, B, dev),
         _vec(q_offsets, "q_offsets", "i32", B + 1, dev), *_head_rows(out, "out", T, hv, D, dev),
-        B, T, max_q_len, hk, hv, D, D ** -0.5 if scale is None else scale, eps,
+        B, T, max_q_len, hk, hv, D, scale, eps,
         *((0, 0) if workspace is None else _ws(workspace)))
     _check(_lib.bfp8_delta_rule(args, _raw_stream(stream, dev)), "bfp8_delta_rule")
 
@@ -1112,7 +1160,25 @@ def bfp8_gated_norm(x, gate, weight, out=None, *, q=None, scales=None, eps: floa
     """The heads x [T, heads, 64, 128 or 256] normed (weight None: not), times SiLU (or the
     sigmoid) of gate, to BF16 (out) and / or 1x128 codes (q [T, heads * width], scales)."""
     dev = _device()
-    T, H, D = x.shape
+    T, H, D = shape = x.shape
+    if (gate.shape == shape and x.dtype is gate.dtype is _BF16
+            and (weight is None or (weight.shape == (D,) and weight.is_contiguous()))
+            and (out is None or (out.shape == shape and out.dtype is _BF16))
+            and (q is None or (q.shape == (T, H * D) and q.dtype in _KINDS["e4m3"]
+                               and scales is not None and scales.shape == (T, -(-H * D // 128))
+                               and scales.dtype is _F32 and s_stride_m is s_stride_kb is None))):
+        (xt, xh, xd), (zt, zh, zd) = x.stride(), gate.stride()
+        ot, oh, od = (0, 0, 1) if out is None else out.stride()
+        (qt, qc), (sm, sk) = ((0, 1), (0, 0)) if q is None else (q.stride(), scales.stride())
+        if xd == zd == od == qc == 1 and _lib.bfp8_gated_norm(_GATED_NORM.pack(
+                x.data_ptr(), xt, xh, gate.data_ptr(), zt, zh,
+                0 if weight is None else weight.data_ptr(),
+                _WEIGHT_CODES.get(None if weight is None else weight.dtype, BFP8_DT_NONE),
+                BFP8_ACT_SIGMOID if sigmoid else BFP8_ACT_SILU, eps, weight_offset,
+                0 if out is None else out.data_ptr(), ot, oh, 0 if q is None else q.data_ptr(), qt,
+                0 if q is None else scales.data_ptr(), sm, sk, T, H, D),
+                _raw_stream(stream, dev)) == BFP8_OK:
+            return
     scales_at = (0, 0, 0)
     if q is not None:
         if scales is None:
@@ -1144,8 +1210,32 @@ def bfp8_rotary(q, k, positions, inv_freq, q_out=None, k_out=None, *, sections=N
     unless q_out and k_out are given, behind the heads' norms where q_weight and k_weight
     are. positions is [T], or [axes, T] with sections pairs of columns to each axis."""
     dev = _device()
-    T, _, D = q.shape
+    T, H, D = shape = q.shape
     half = inv_freq.shape[0]
+    if k is not None and positions.dim() == (1 if sections is None else 2):
+        K = k.shape[1]
+        qo, ko = q if q_out is None else q_out, k if k_out is None else k_out
+        parts = (half,) if sections is None else tuple(sections)
+        axes = len(parts)
+        if (k.shape == ko.shape == (T, K, D) and qo.shape == shape and axes <= 4
+                and positions.shape == ((T,) if sections is None else (axes, T))
+                and q.dtype is k.dtype is qo.dtype is ko.dtype is _BF16
+                and positions.dtype is _I32 and inv_freq.dtype is _F32 and inv_freq.is_contiguous()
+                and (q_weight is None or (q_weight.shape == (D,) and q_weight.is_contiguous()))
+                and (k_weight is None or (k_weight.shape == (D,) and k_weight.is_contiguous()
+                                          and (q_weight is None or q_weight.dtype is k_weight.dtype)))):
+            (qt, qh, qd), (kt, kh, kd), pt = q.stride(), k.stride(), positions.stride()
+            (qot, qoh, qod), (kot, koh, kod) = qo.stride(), ko.stride()
+            w = k_weight if q_weight is None else q_weight
+            if qd == kd == qod == kod == pt[-1] == 1 and _lib.bfp8_rotary(_ROTARY.pack(
+                    q.data_ptr(), qt, qh, qo.data_ptr(), qot, qoh, k.data_ptr(), kt, kh,
+                    ko.data_ptr(), kot, koh, positions.data_ptr(), pt[0], inv_freq.data_ptr(),
+                    0 if q_weight is None else q_weight.data_ptr(),
+                    0 if k_weight is None else k_weight.data_ptr(),
+                    _WEIGHT_CODES.get(None if w is None else w.dtype, BFP8_DT_NONE), eps,
+                    weight_offset, factor, T, H, K, D, 2 * half, axes, *parts, *(0,) * (4 - axes),
+                    interleaved, adjacent), _raw_stream(stream, dev)) == BFP8_OK:
+                return
     axes, pos = (1, (_vec(positions, "positions", "i32", T, dev), T)) if positions.dim() == 1 else \
         (positions.shape[0], _matrix(positions, "positions", "i32", (positions.shape[0], T), dev))
     parts = [half] if sections is None else list(sections)
