@@ -64,14 +64,14 @@ constexpr int kStepWarps = 4;
 // One token after the other: a warp holds 8 of a head's 128 rows of S, four columns a lane,
 // and needs no other warp. Both products with the old state are summed at once, as
 // S_new q' = alpha S q' + u (k' . q').
-__global__ void __launch_bounds__(32 * kStepWarps) delta_step_kernel(const DeltaParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  constexpr int kParts = kD / (8 * kStepWarps);
+// A block of WARPS warps, number `block`.
+template <int WARPS>
+BFP8_DEV void delta_steps(const DeltaParams& p, int64_t block) {
+  constexpr int kParts = kD / (8 * WARPS);
   const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x / kParts;
+  const int64_t item = block / kParts;
   const int b = static_cast<int>(item / p.v_heads), h = static_cast<int>(item - int64_t{b} * p.v_heads);
-  const int row0 = (static_cast<int>(blockIdx.x % kParts) * kStepWarps + (threadIdx.x >> 5)) * 8;
+  const int row0 = (static_cast<int>(block % kParts) * WARPS + (threadIdx.x >> 5)) * 8;
   const int64_t first = first_token(p.req, b);
   int64_t n = first_token(p.req, b + 1) - first;
   n = n < p.max_len ? n : p.max_len;
@@ -139,6 +139,11 @@ __global__ void __launch_bounds__(32 * kStepWarps) delta_step_kernel(const Delta
     for (int r = 0; r < 8; ++r) *reinterpret_cast<float4*>(s + r * kD) = S[r];
   }
 }
+__global__ void __launch_bounds__(32 * kStepWarps) delta_step_kernel(const DeltaParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  delta_steps<kStepWarps>(p, blockIdx.x);
+}
 
 // ------------------------------------------------------------------ chunks of 64 tokens
 //
@@ -180,6 +185,7 @@ __device__ int g_delta_err;
 struct ChunkParams {
   DeltaParams d;
   uint8_t* ws;
+  uint32_t chunk_blocks;                               // of the first kernel
   int32_t qk_heads, subgroups, per_block;              // value heads a block of the first kernel takes
 };
 BFP8_DEV int64_t slot_bytes(const ChunkParams& p) {
@@ -340,7 +346,8 @@ BFP8_DEV float4 negate(float4 v) { return make_float4(-v.x, -v.y, -v.z, -v.w); }
 // and the Q rows with the K rows leaves row i of K K^T and of Q K^T in a lane of tensor memory;
 // two threads share a lane's columns. (1 + A)^-1 is formed by blocks of 16: the diagonal ones
 // column by column, then each lower one as -T_b A_ba T_a, of 16 rows and of 32. P T is a
-// product on the tensor cores again.
+// product on the tensor cores again. The grid's last blocks take the step's short requests, a
+// token after the other, which so run beside the long ones' chunks.
 __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __grid_constant__ CUtensorMap tq,
                                                                      const __grid_constant__ CUtensorMap tk,
                                                                      const ChunkParams p) {
@@ -350,8 +357,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
   const uint32_t kq = smem_u32(base), blob = kq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const int hk = blockIdx.x % p.qk_heads, sub = blockIdx.x / p.qk_heads % p.subgroups;
-  const int64_t slot = blockIdx.x / (p.qk_heads * p.subgroups);
+  if (blockIdx.x >= p.chunk_blocks) {
+    pdl_launch_dependents();
+    delta_steps<kPrepThreads / 32>(p.d, blockIdx.x - p.chunk_blocks);
+    return;
+  }
+  const int block = static_cast<int>(blockIdx.x);
+  const int hk = block % p.qk_heads, sub = block / p.qk_heads % p.subgroups;
+  const int64_t slot = block / (p.qk_heads * p.subgroups);
   const int h0 = hk * p.d.group + sub * p.per_block, heads = min(p.per_block, p.d.group - sub * p.per_block);
   const int b = find_request(p.d.req, slot, kShift);
   if (b < 0) return;
@@ -1150,8 +1163,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   }
 }
 
-// A request of up to this many new tokens takes them one after the other.
-constexpr int64_t kStepTokens = 16;
+// Where no request has more new tokens than this, each takes them one after the other. One
+// request of 48 heads: 20 / 24 / 32 tokens 17 / 20 / 25 us against 21 us by a chunk; 64 requests
+// of 16 / 24 tokens 310 / 453 us against 343 / 346 us.
+constexpr int64_t kStepTokens = 20;
+// Beside longer ones, which run the chunks' kernels anyway, up to this many do: requests of 1 to
+// 141 tokens (12, of 48 heads) take 52, 60 and 60 us with 8, 16 and 20.
+constexpr int64_t kStepTokensBeside = 8;
 
 int64_t chunk_slots(int64_t batch, int64_t tokens) { return (tokens >> kShift) + batch; }
 
@@ -1198,7 +1216,7 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   const size_t need = delta_rule_workspace_bytes(a.batch, a.tokens, a.max_q_len, a.qk_heads, a.v_heads);
   if (need && (!a.workspace || a.ws_bytes < need)) return BFP8_ERR_INVALID_ARG;
   if (need && (reinterpret_cast<uintptr_t>(a.workspace) % 256 ||
-               chunk_slots(a.batch, a.tokens) * a.v_heads > 0x7FFFFFFF))
+               chunk_slots(a.batch, a.tokens) * a.v_heads > 0x5FFFFFFF))   // a grid, beside 2^29 blocks of steps
     return BFP8_ERR_UNSUPPORTED;
   int rc = check_device_ptrs({a.q_bf16, a.k_bf16, a.v_bf16, a.a_bf16, a.b_bf16, a.a_log, a.dt_bias, a.state,
                               a.out_bf16, a.q_offsets, a.slots_in, a.slots_out, need ? a.workspace : nullptr});
@@ -1225,11 +1243,12 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   p.group = static_cast<int32_t>(a.v_heads / a.qk_heads);
   p.scale = a.scale;
   p.eps = a.eps;
-  p.step_len = kStepTokens;
+  p.step_len = need ? kStepTokensBeside : kStepTokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned blocks = static_cast<unsigned>(a.batch * a.v_heads * (kD / (8 * kStepWarps)));
-  rc = launch_dependent(delta_step_kernel, dim3(blocks), 32 * kStepWarps, 0, st, p);
-  if (rc != BFP8_OK || !need) return rc;
+  if (!need)
+    return launch_dependent(delta_step_kernel,
+                            dim3(static_cast<unsigned>(a.batch * a.v_heads * (kD / (8 * kStepWarps)))), 32 * kStepWarps,
+                            0, st, p);
   CUtensorMap tq, tk, tv;
   rc = tile_map(&tq, a.q_bf16, a.qk_heads, a.tokens, a.q_stride_head, a.q_stride_token);
   if (rc == BFP8_OK) rc = tile_map(&tk, a.k_bf16, a.qk_heads, a.tokens, a.k_stride_head, a.k_stride_token);
@@ -1240,14 +1259,16 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   int sms = 0;
   rc = sm_count(&sms);
   if (rc != BFP8_OK) return rc;
-  // Value heads of one key head share a block, which norms and multiplies their rows once, where
-  // there are blocks enough for that: three to an SM.
-  ChunkParams cp{p, static_cast<uint8_t*>(a.workspace), static_cast<int32_t>(a.qk_heads), 0, 0};
+  // Value heads of one key head share a block, which norms and multiplies their rows once (14,000
+  // of its 24,500 clocks for one head), unless the blocks of one head each fit the GPU at once,
+  // three to an SM. (Requests of 1 to 141 tokens, 48 heads on 16: 52 us shared, 57 us apart.)
+  ChunkParams cp{p, static_cast<uint8_t*>(a.workspace), 0, static_cast<int32_t>(a.qk_heads), 0, 0};
   const int64_t apart = (a.tokens / kChunk + a.batch) * a.v_heads;
   cp.per_block = apart <= 3 * sms ? 1 : p.group < kGroup ? p.group : kGroup;
   cp.subgroups = (p.group + cp.per_block - 1) / cp.per_block;
+  cp.chunk_blocks = static_cast<uint32_t>(chunk_slots(a.batch, a.tokens) * a.qk_heads * cp.subgroups);
   rc = launch_dependent(delta_prepare_kernel,
-                        dim3(static_cast<unsigned>(chunk_slots(a.batch, a.tokens) * a.qk_heads * cp.subgroups)),
+                        dim3(cp.chunk_blocks + static_cast<unsigned>(a.batch * a.v_heads * (kD / (8 * (kPrepThreads / 32))))),
                         kPrepThreads, kPrepSmem, st, tq, tk, cp);
   if (rc != BFP8_OK) return rc;
   return launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(a.batch * a.v_heads)), kWalkThreads, kWalkSmem,
