@@ -571,10 +571,11 @@ int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream) {
 
 size_t bfp8_delta_rule_workspace(int64_t batch, int64_t tokens, int64_t max_q_len,
                                  int64_t qk_heads, int64_t v_heads) {
+  int sms = 0;
   if (batch <= 0 || tokens <= 0 || max_q_len <= 0 || qk_heads <= 0 || v_heads <= 0 ||
-      v_heads % qk_heads)
+      v_heads % qk_heads || sm_count(&sms) != BFP8_OK)
     return 0;
-  return delta_rule_workspace_bytes(batch, tokens, max_q_len, qk_heads, v_heads);
+  return delta_rule_workspace_bytes(batch, tokens, max_q_len, qk_heads, v_heads, sms);
 }
 
 int bfp8_delta_rule(const bfp8_delta_rule_args* args, void* stream) {

@@ -185,6 +185,9 @@ __device__ int g_delta_err;
 struct ChunkParams {
   DeltaParams d;
   uint8_t* ws;
+  float* ends;                                         // of each head's segments but the last: the state behind it
+  float* maps;                                         // ... and what it makes of the state ahead of it
+  int32_t segments, segment_chunks, second_walk;
   uint32_t chunk_blocks;                               // of the first kernel
   int32_t qk_heads, subgroups, per_block;              // value heads a block of the first kernel takes
 };
@@ -699,6 +702,14 @@ BFP8_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
                : "memory");
 }
 
+//
+// Few heads' long prompts leave most SMs idle, so their chunks are walked in segments, all at
+// once. What a segment makes of the state ahead of it is S -> S M + N, row by row of S: a walk
+// from zeros leaves N, and one from the identity, without values, M. The first walk takes the
+// first segment of each head (from the state itself, with its rows of out), and N and M of the
+// others but the last; the states between the segments are then S M + N one behind another; and
+// the second walk takes the other segments from those. That is two segments' time in place of
+// the whole prompt's.
 struct WalkShared {
   float most[2][2][kD];                                // what each half of a row offers for its power of two
   float power[2][kD];                                  // a chunk's, for its rows of out
@@ -718,17 +729,29 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kMmaWarp = kRowWarps + kOutWarps;
   pdl_wait();
-  const int h = blockIdx.x % p.d.v_heads, b = blockIdx.x / p.d.v_heads;
+  const int pairs = p.d.req.batch * p.d.v_heads, pair = blockIdx.x % pairs, job = blockIdx.x / pairs;
+  const int h = pair % p.d.v_heads, b = pair / p.d.v_heads;
+  // the first walk's jobs: N of the segments ahead of the last (the first one's with its rows of
+  // out), then M of those behind the first; the second's: the segments behind the first
+  const bool map = !p.second_walk && p.segments > 1 && job >= p.segments - 1;
+  const int segment = p.second_walk ? job + 1 : map ? job - (p.segments - 2) : job;
+  const bool rows_out = p.second_walk || segment == 0;
   int64_t first;
-  const int64_t len = chunked_len(p.d, b, first);
-  if (len == 0) return;
+  int64_t len = chunked_len(p.d, b, first);
+  const int64_t segment_tokens = static_cast<int64_t>(p.segment_chunks) << kShift;
+  if (len <= segment * segment_tokens) return;
+  const bool last = len <= (segment + 1) * segment_tokens;
+  if (last && !rows_out) return;
+  first += segment * segment_tokens;
+  len = last ? len - segment * segment_tokens : segment_tokens;
+  float* const between = p.ends + (static_cast<int64_t>(pair) * (p.segments - 1) + segment) * (kD * kD);
   const int chunks = static_cast<int>((len + kChunk - 1) >> kShift);
   const int tail = static_cast<int>(len - (static_cast<int64_t>(chunks - 1) << kShift));
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh.full[s]), 1);
-      mbar_init(smem_u32(&sh.empty[s]), kRowWarps + kOutWarps + 1);
+      mbar_init(smem_u32(&sh.empty[s]), kRowWarps + (rows_out ? kOutWarps : 0) + 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sh.v_full[s]), 1);
@@ -800,9 +823,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           }
           __syncwarp();
         }
-        if (!ok || !wait(sh.y_free, (c & 1) ^ 1)) break;
+        if (!ok || (rows_out && !wait(sh.y_free, (c & 1) ^ 1))) break;
         tc_fence_after();
-        if (elect_one()) {
+        if (rows_out && elect_one()) {
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -827,7 +850,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           __syncwarp();
         }
         if (!ok) break;
-        if (elect_one()) {
+        if (rows_out && elect_one()) {
 #pragma unroll
           for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -864,8 +887,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       }
     } else if (warp == kMmaWarp + 1) {
       // ---------------------------------------------- loads, a chunk ahead; values two
-      const int64_t key = tile_key(p.d.req, b, kShift);
-      int got = 0, values = 0;                         // chunks asked for
+      const int64_t key = tile_key(p.d.req, b, kShift) + static_cast<int64_t>(segment) * p.segment_chunks;
+      int got = 0, values = map ? chunks : 0;          // chunks asked for; a map has no values
       auto load_values = [&]() {
         const int s = values % 2;
         if (values == chunks || !wait(sh.v_empty[s], ((values / 2) & 1) ^ 1)) return;
@@ -895,13 +918,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         const int none = 0;
         for (int d = got < kStages ? 0 : got - kStages; d < got; ++d)
           mbar_wait(smem_u32(&sh.full[d % kStages]), (d / kStages) & 1, &none);
-        for (int d = values < 2 ? 0 : values - 2; d < values; ++d)
+        for (int d = values < 2 ? 0 : values - 2; !map && d < values; ++d)
           mbar_wait(smem_u32(&sh.v_full[d % 2]), (d / 2) & 1, &none);
       }
     } else {
       // ---------------------------------------------- values turned: of each value its tokens, two a word
       const int half = warp - kMmaWarp - 2;            // of the values
-      for (int c = 0; c < chunks; ++c) {
+      for (int c = 0; !map && c < chunks; ++c) {
         if (!wait(sh.v_full[c & 1], (c >> 1) & 1) || !wait(sh.taken[c & 1], ((c >> 1) & 1) ^ 1)) break;
         // a lane's row of the four 8 x 8 pieces that the warp turns at once: 32 tokens of 8 values
         const uint32_t src = stages + kValuesAt + (c & 1) * kTile + half * kHalfTile + lane * 128;
@@ -930,7 +953,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     const int r = (warp & 3) * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool odd = lane & 1;
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; rows_out && c < chunks; ++c) {
       const int s = c % kStages;
       const float* scalars = reinterpret_cast<const float*>(base + s * kStageBytes + kBlobAt + kScalars);
       if (!wait(sh.full[s], (c / kStages) & 1) || !wait(sh.o_done, c & 1)) break;
@@ -981,11 +1004,25 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     warpgroup_reg_alloc<168>();
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const int64_t from = slot_of(p.d.req, p.d.req.slots_in, b), to = slot_of(p.d.req, p.d.req.slots_out, b);
-    const int64_t in_head = h * p.d.s_head + r * kD + 64 * wg;
+    // where S comes from and goes to: the request's slots, or between the segments
+    const float* from = nullptr;
+    float* to = nullptr;
+    const int64_t in_row = r * kD + 64 * wg;
+    if (segment == 0) {
+      const int64_t slot = slot_of(p.d.req, p.d.req.slots_in, b);
+      if (slot >= 0) from = p.d.state + slot * p.d.s_slot + h * p.d.s_head + in_row;
+    } else if (p.second_walk) {
+      from = between - kD * kD + in_row;
+    }
+    if (last) {
+      const int64_t slot = slot_of(p.d.req, p.d.req.slots_out, b);
+      if (slot >= 0) to = p.d.state + slot * p.d.s_slot + h * p.d.s_head + in_row;
+    } else if (!p.second_walk) {
+      to = (map ? p.maps + (between - p.ends) : between) + in_row;
+    }
     float S[64], most = 0.0f;                          // S is the row times `power`
-    if (from >= 0) {
-      const float4* src = reinterpret_cast<const float4*>(p.d.state + from * p.d.s_slot + in_head);
+    if (from) {
+      const float4* src = reinterpret_cast<const float4*>(from);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const float4 f = src[k];
@@ -994,11 +1031,17 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) S[k] = 0.0f;
+      for (int k = 0; k < 64; ++k) S[k] = map && r == 64 * wg + k ? 1.0f : 0.0f;
+      if (map) most = 1.0f;
     }
     uint32_t values[16], top = 0;                      // the next chunk's: 32 tokens' BF16, two a word; the largest
     auto load_values = [&](int c) {
       const int left = (c == chunks - 1 ? tail : kChunk) - 32 * wg;
+      if (map) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) values[j] = 0u;
+        return;
+      }
       if (!wait(sh.turned[c & 1], (c >> 1) & 1)) return;
       const uint32_t row = stages + kTurnedAt + (c & 1) * kTile + r * 128;
 #pragma unroll
@@ -1143,9 +1186,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       }
       if (more) hand_over(0), hand_over(1);
     }
-    if (ok && to >= 0) {
+    if (ok && to) {
       const float back = 1.0f / power;
-      float4* dst = reinterpret_cast<float4*>(p.d.state + to * p.d.s_slot + in_head);
+      float4* dst = reinterpret_cast<float4*>(to);
 #pragma unroll
       for (int k = 0; k < 16; ++k)
         dst[k] = make_float4(S[4 * k] * back, S[4 * k + 1] * back, S[4 * k + 2] * back, S[4 * k + 3] * back);
@@ -1161,6 +1204,65 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// The states between a head's segments, one behind another: the end of each but the first is its
+// N and becomes S M + N. A warp has a row of S; the maps' rows come from L2, 16 at a time.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkParams p) {
+  __shared__ float4 S[kJoinThreads / 32][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kRows = kJoinThreads / 32, kParts = kD / kRows;
+  const int pair = blockIdx.x / kParts, b = pair / p.d.v_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t first;
+  const int64_t len = chunked_len(p.d, b, first), segment_tokens = static_cast<int64_t>(p.segment_chunks) << kShift;
+  const int64_t at = static_cast<int64_t>(pair) * (p.segments - 1) * (kD * kD);
+  const int row = (blockIdx.x % kParts) * kRows + warp;
+  float* const ends = p.ends + at + row * kD + 4 * lane;
+  const float* const maps = p.maps + at + 4 * lane;
+  float4 s = *reinterpret_cast<const float4*>(ends);
+  for (int g = 1; len > (g + 1) * segment_tokens; ++g) {
+    S[warp][lane] = s;
+    __syncwarp();
+    float4 sum = *reinterpret_cast<const float4*>(ends + g * (kD * kD));
+    const float* map = maps + static_cast<int64_t>(g) * (kD * kD);
+    for (int l = 0; l < kD; l += 16) {
+      float4 m[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m[e] = __ldg(reinterpret_cast<const float4*>(map + (l + e) * kD));
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 c4 = S[warp][(l + e) / 4];
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum.x = fmaf(c[i], m[e + i].x, sum.x), sum.y = fmaf(c[i], m[e + i].y, sum.y);
+          sum.z = fmaf(c[i], m[e + i].z, sum.z), sum.w = fmaf(c[i], m[e + i].w, sum.w);
+        }
+      }
+    }
+    __syncwarp();
+    s = sum;
+    *reinterpret_cast<float4*>(ends + g * (kD * kD)) = s;
+  }
+}
+
+// How many segments the longest request's chunks are walked in: the count with the least time,
+// in tenths of a microsecond, of those whose first walk fits the GPU at once (one block an SM).
+// A chunk takes 2.5 us; a join 3 us; the two launches and the blocks' beginnings 18 us.
+constexpr int kMostSegments = 16;
+int64_t longest_chunks(int64_t tokens, int64_t max_q_len) {
+  return ((max_q_len < tokens ? max_q_len : tokens) + kChunk - 1) / kChunk;
+}
+int segment_count(int64_t chunks, int64_t pairs, int sms) {
+  int best = 1;
+  int64_t least = 25 * chunks;
+  for (int n = 3; n <= kMostSegments && pairs * (2 * n - 3) <= sms; ++n) {
+    const int64_t time = 2 * 25 * ((chunks + n - 1) / n) + 30 * (n - 2) + 180;
+    if (time < least) least = time, best = n;
+  }
+  return best;
 }
 
 // Where no request has more new tokens than this, each takes them one after the other. One
@@ -1183,11 +1285,21 @@ bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
 }  // namespace
 
+// The chunks' part of the workspace, and behind it the states between segments: as a first walk
+// of n segments has 2 n - 3 blocks a head and at most one an SM, an end and a map for each SM
+// hold them.
+size_t chunk_bytes(int64_t batch, int64_t tokens, int64_t qk_heads, int64_t v_heads) {
+  const size_t n = static_cast<size_t>(chunk_slots(batch, tokens)) *
+                   (static_cast<size_t>(qk_heads) * kKq + static_cast<size_t>(v_heads) * kBlob);
+  return (n + 255) / 256 * 256;
+}
 size_t delta_rule_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q_len, int64_t qk_heads,
-                                  int64_t v_heads) {
+                                  int64_t v_heads, int sms) {
   if (max_q_len <= kStepTokens) return 0;
-  return static_cast<size_t>(chunk_slots(batch, tokens)) *
-         (static_cast<size_t>(qk_heads) * kKq + static_cast<size_t>(v_heads) * kBlob);
+  const size_t between = segment_count(longest_chunks(tokens, max_q_len), 1, sms) > 1
+                             ? static_cast<size_t>(sms) * 2 * kD * kD * sizeof(float)
+                             : 0;
+  return chunk_bytes(batch, tokens, qk_heads, v_heads) + between;
 }
 
 int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
@@ -1213,12 +1325,16 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
       off16(a.q_bf16) || off16(a.k_bf16) || off16(a.v_bf16) || off16(a.out_bf16) || off16(a.state) ||
       (a.state && (a.state_stride_slot % 4 || a.state_stride_head % 4)))
     return BFP8_ERR_UNSUPPORTED;
-  const size_t need = delta_rule_workspace_bytes(a.batch, a.tokens, a.max_q_len, a.qk_heads, a.v_heads);
+  int sms = 0;
+  int rc = BFP8_OK;
+  if (a.max_q_len > kStepTokens) rc = sm_count(&sms);
+  if (rc != BFP8_OK) return rc;
+  const size_t need = delta_rule_workspace_bytes(a.batch, a.tokens, a.max_q_len, a.qk_heads, a.v_heads, sms);
   if (need && (!a.workspace || a.ws_bytes < need)) return BFP8_ERR_INVALID_ARG;
   if (need && (reinterpret_cast<uintptr_t>(a.workspace) % 256 ||
                chunk_slots(a.batch, a.tokens) * a.v_heads > 0x5FFFFFFF))   // a grid, beside 2^29 blocks of steps
     return BFP8_ERR_UNSUPPORTED;
-  int rc = check_device_ptrs({a.q_bf16, a.k_bf16, a.v_bf16, a.a_bf16, a.b_bf16, a.a_log, a.dt_bias, a.state,
+  rc = check_device_ptrs({a.q_bf16, a.k_bf16, a.v_bf16, a.a_bf16, a.b_bf16, a.a_log, a.dt_bias, a.state,
                               a.out_bf16, a.q_offsets, a.slots_in, a.slots_out, need ? a.workspace : nullptr});
   if (rc != BFP8_OK) return rc;
   DeltaParams p{};
@@ -1256,13 +1372,13 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   if (rc == BFP8_OK) rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_prepare_kernel), kPrepSmem);
   if (rc == BFP8_OK) rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_walk_kernel), kWalkSmem);
   if (rc != BFP8_OK) return rc;
-  int sms = 0;
-  rc = sm_count(&sms);
-  if (rc != BFP8_OK) return rc;
   // Value heads of one key head share a block, which norms and multiplies their rows once (14,000
   // of its 24,500 clocks for one head), unless the blocks of one head each fit the GPU at once,
   // three to an SM. (Requests of 1 to 141 tokens, 48 heads on 16: 52 us shared, 57 us apart.)
-  ChunkParams cp{p, static_cast<uint8_t*>(a.workspace), 0, static_cast<int32_t>(a.qk_heads), 0, 0};
+  ChunkParams cp{};
+  cp.d = p;
+  cp.ws = static_cast<uint8_t*>(a.workspace);
+  cp.qk_heads = static_cast<int32_t>(a.qk_heads);
   const int64_t apart = (a.tokens / kChunk + a.batch) * a.v_heads;
   cp.per_block = apart <= 3 * sms ? 1 : p.group < kGroup ? p.group : kGroup;
   cp.subgroups = (p.group + cp.per_block - 1) / cp.per_block;
@@ -1271,8 +1387,19 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
                         dim3(cp.chunk_blocks + static_cast<unsigned>(a.batch * a.v_heads * (kD / (8 * (kPrepThreads / 32))))),
                         kPrepThreads, kPrepSmem, st, tq, tk, cp);
   if (rc != BFP8_OK) return rc;
-  return launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(a.batch * a.v_heads)), kWalkThreads, kWalkSmem,
-                          st, tv, cp);
+  const int64_t chunks = longest_chunks(a.tokens, a.max_q_len), pairs = a.batch * a.v_heads;
+  cp.segments = segment_count(chunks, pairs, sms);
+  cp.segment_chunks = static_cast<int32_t>((chunks + cp.segments - 1) / cp.segments);
+  cp.ends = reinterpret_cast<float*>(cp.ws + chunk_bytes(a.batch, a.tokens, a.qk_heads, a.v_heads));
+  cp.maps = cp.ends + static_cast<int64_t>(sms) * kD * kD;
+  const int jobs = cp.segments > 1 ? 2 * cp.segments - 3 : 1;
+  rc = launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * jobs)), kWalkThreads, kWalkSmem, st, tv, cp);
+  if (rc != BFP8_OK || cp.segments == 1) return rc;
+  rc = launch_dependent(delta_join_kernel, dim3(static_cast<unsigned>(pairs * (kD / (kJoinThreads / 32)))), kJoinThreads, 0, st, cp);
+  if (rc != BFP8_OK) return rc;
+  cp.second_walk = 1;
+  return launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * (cp.segments - 1))), kWalkThreads,
+                          kWalkSmem, st, tv, cp);
 }
 
 int delta_read_clear_error() {

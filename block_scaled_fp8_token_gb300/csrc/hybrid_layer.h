@@ -9,7 +9,7 @@ namespace bfp8 {
 
 int launch_causal_conv(const bfp8_causal_conv_args& args, void* stream);
 size_t delta_rule_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q_len,
-                                  int64_t qk_heads, int64_t v_heads);
+                                  int64_t qk_heads, int64_t v_heads, int sms);
 int launch_delta_rule(const bfp8_delta_rule_args& args, void* stream);
 // The device error word of the delta rule's kernels, as those of the projections.
 int delta_read_clear_error();

@@ -72,6 +72,37 @@ def test_prompts_match_oracle(bfp8, cuda_device, lens, hk, hv):
     _check(t, lens, _run(bfp8, t, lens))
 
 
+@pytest.mark.parametrize("lens,hk,hv", [([3000], 1, 1), ([2049], 1, 2), ([2500, 7, 40, 1300], 2, 2), ([1500, 1501], 1, 4),
+                                        ([64 * 27 + 1, 64 * 30, 0, 64 * 9], 1, 1)], ids=str)
+@pytest.mark.parametrize("decay", [1e-3, 1.0])
+def test_long_prompts_match_oracle(bfp8, cuda_device, lens, hk, hv, decay):
+    """Prompts of few heads, whose chunks are walked in segments at once and joined; short ones beside them."""
+    t = delta_inputs(cuda_device, lens, hk, hv, 19 * hv + sum(lens), extra=1, decay=decay)
+    _check(t, lens, _run(bfp8, t, lens))
+
+
+def test_long_prompts_in_one_slot_and_replayed(bfp8, cuda_device):
+    """Read from and left in the same slot; captured, and replayed with lengths that end in other segments."""
+    dev = cuda_device
+    T = 2400
+    t = delta_inputs(dev, [T], 1, 1, 23)
+    t["slots_in"] = t["slots_out"]
+    ws = torch.empty(bfp8.bfp8_delta_rule_workspace(1, T, T, 1, 1), dtype=torch.uint8, device=dev)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        bfp8.bfp8_delta_rule(*(t[k] for k in NAMES), T, workspace=ws)
+    for n in (T, 900, 64, 12, 2239, 0):
+        t["q_offsets"].copy_(offsets(dev, [n]))
+        t["out"].fill_(float("nan"))
+        before = t["state"].clone()
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(t, [n], before)
+
+
 @pytest.mark.parametrize("decay", [1e-6, 40.0])
 def test_heads_that_keep_all_and_heads_that_forget_at_once(bfp8, cuda_device, decay):
     lens = [150, 70]
