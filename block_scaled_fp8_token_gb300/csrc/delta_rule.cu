@@ -1207,45 +1207,70 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
 }
 
 // The states between a head's segments, one behind another: the end of each but the first is its
-// N and becomes S M + N. A warp has a row of S; the maps' rows come from L2, 16 at a time.
-constexpr int kJoinThreads = 256;
+// N and becomes S M + N. A warp has two rows of S; a block copies a map at a time to shared
+// memory, the next one while it multiplies where there is a next one.
+constexpr int kJoinThreads = 256, kJoinRows = 2 * kJoinThreads / 32, kMapBytes = kD * kD * 4;
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkParams p) {
-  __shared__ float4 S[kJoinThreads / 32][32];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(16) float2 S[kD][kJoinThreads / 32];   // of a key, each warp's two rows
+  __shared__ uint64_t full[2];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = (smem_u32(smem_raw) + 127) & ~127u;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&full[0]), 1);
+    mbar_init(smem_u32(&full[1]), 1);
+    abort_flag = 0;
+    mbar_fence_init();
+  }
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kRows = kJoinThreads / 32, kParts = kD / kRows;
-  const int pair = blockIdx.x / kParts, b = pair / p.d.v_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kParts = kD / kJoinRows;
+  const int pair = blockIdx.x / kParts, b = pair / p.d.v_heads;
   int64_t first;
   const int64_t len = chunked_len(p.d, b, first), segment_tokens = static_cast<int64_t>(p.segment_chunks) << kShift;
+  const int n = static_cast<int>((len + segment_tokens - 1) / segment_tokens);   // segments; maps 1 .. n - 2
+  if (n <= 2) return;
   const int64_t at = static_cast<int64_t>(pair) * (p.segments - 1) * (kD * kD);
-  const int row = (blockIdx.x % kParts) * kRows + warp;
+  const int row = (blockIdx.x % kParts) * kJoinRows + 2 * warp;
   float* const ends = p.ends + at + row * kD + 4 * lane;
-  const float* const maps = p.maps + at + 4 * lane;
-  float4 s = *reinterpret_cast<const float4*>(ends);
-  for (int g = 1; len > (g + 1) * segment_tokens; ++g) {
-    S[warp][lane] = s;
+  const int ahead = p.segments > 3 ? 2 : 1;            // maps that the shared memory holds
+  auto ask = [&](int g) {
+    if (threadIdx.x != 0 || g > n - 2) return;
+    const uint32_t bar = smem_u32(&full[(g - 1) % ahead]);
+    mbar_arrive_expect_tx(bar, kMapBytes);
+    bulk_load(ring + (g - 1) % ahead * kMapBytes, p.maps + at + static_cast<int64_t>(g) * (kD * kD), kMapBytes, bar);
+  };
+  __syncthreads();
+  for (int g = 1; g <= ahead; ++g) ask(g);
+  float4 s[2] = {*reinterpret_cast<const float4*>(ends), *reinterpret_cast<const float4*>(ends + kD)};
+  bool ok = true;
+  for (int g = 1; ok && g <= n - 2; ++g) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      S[4 * lane + e][warp] = e == 0   ? make_float2(s[0].x, s[1].x)
+                              : e == 1 ? make_float2(s[0].y, s[1].y)
+                              : e == 2 ? make_float2(s[0].z, s[1].z)
+                                       : make_float2(s[0].w, s[1].w);
     __syncwarp();
-    float4 sum = *reinterpret_cast<const float4*>(ends + g * (kD * kD));
-    const float* map = maps + static_cast<int64_t>(g) * (kD * kD);
-    for (int l = 0; l < kD; l += 16) {
-      float4 m[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) m[e] = __ldg(reinterpret_cast<const float4*>(map + (l + e) * kD));
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const float4 c4 = S[warp][(l + e) / 4];
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum.x = fmaf(c[i], m[e + i].x, sum.x), sum.y = fmaf(c[i], m[e + i].y, sum.y);
-          sum.z = fmaf(c[i], m[e + i].z, sum.z), sum.w = fmaf(c[i], m[e + i].w, sum.w);
-        }
-      }
+    float* const end = ends + g * (kD * kD);
+    s[0] = *reinterpret_cast<const float4*>(end), s[1] = *reinterpret_cast<const float4*>(end + kD);
+    ok = __syncthreads_and(mbar_wait(smem_u32(&full[(g - 1) % ahead]), (g - 1) / ahead & 1, &abort_flag));
+    if (!ok) break;
+    const uint32_t map = ring + (g - 1) % ahead * kMapBytes + lane * 16;
+#pragma unroll 8
+    for (int l = 0; l < kD; ++l) {
+      const uint4 w = lds128(map + l * (kD * 4));
+      const float4 m = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+      const float2 c = S[l][warp];
+      s[0].x = fmaf(c.x, m.x, s[0].x), s[0].y = fmaf(c.x, m.y, s[0].y), s[0].z = fmaf(c.x, m.z, s[0].z), s[0].w = fmaf(c.x, m.w, s[0].w);
+      s[1].x = fmaf(c.y, m.x, s[1].x), s[1].y = fmaf(c.y, m.y, s[1].y), s[1].z = fmaf(c.y, m.z, s[1].z), s[1].w = fmaf(c.y, m.w, s[1].w);
     }
-    __syncwarp();
-    s = sum;
-    *reinterpret_cast<float4*>(ends + g * (kD * kD)) = s;
+    *reinterpret_cast<float4*>(end) = s[0], *reinterpret_cast<float4*>(end + kD) = s[1];
+    __syncthreads();                                   // the map's place is free
+    ask(g + ahead);
   }
+  if (!ok && threadIdx.x == 0) atomicExch(&g_delta_err, static_cast<int>(BFP8_ERR_TIMEOUT));
 }
 
 // How many segments the longest request's chunks are walked in: the count with the least time,
@@ -1395,7 +1420,11 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   const int jobs = cp.segments > 1 ? 2 * cp.segments - 3 : 1;
   rc = launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * jobs)), kWalkThreads, kWalkSmem, st, tv, cp);
   if (rc != BFP8_OK || cp.segments == 1) return rc;
-  rc = launch_dependent(delta_join_kernel, dim3(static_cast<unsigned>(pairs * (kD / (kJoinThreads / 32)))), kJoinThreads, 0, st, cp);
+  const int join_smem = (cp.segments > 3 ? 2 : 1) * kMapBytes + 128;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_join_kernel), 2 * kMapBytes + 128);
+  if (rc == BFP8_OK)
+    rc = launch_dependent(delta_join_kernel, dim3(static_cast<unsigned>(pairs * (kD / kJoinRows))), kJoinThreads,
+                          join_smem, st, cp);
   if (rc != BFP8_OK) return rc;
   cp.second_walk = 1;
   return launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * (cp.segments - 1))), kWalkThreads,
