@@ -2,7 +2,7 @@
 lengths in one ragged step, then a token per request and step.
 
     kv_plan -> residual_norm (pre-norm + 1x128 quant) -> linear_w8a8 (QKV)
-    -> rotary embedding (plain torch) -> kv_append -> kv_attention
+    -> rotary -> kv_append -> kv_attention
     -> act_quant_group -> linear_w8a8 (output)
     -> residual_norm (post-norm, residual sum, pre-norm, quant)
     -> linear_w8a8_silu_quant (gate/up) -> linear_w8a8 (down)
@@ -32,14 +32,6 @@ def fp8_weight(n, k, gen, dev):
     s = torch.empty(-(-n // 128), -(-k // 128), dtype=torch.float32, device=dev)
     bfp8.bfp8_quantize_weight_block(w, q, s)
     return q, s
-
-
-def rotate(x, positions, base=1e6):
-    """Rotary embedding of [T, heads, D] in place, halves paired."""
-    f = positions.clamp(min=0).double()[:, None] * base ** (-torch.arange(0, D, 2, device=x.device).double() / D)
-    cos, sin = f.cos().float()[:, None], f.sin().float()[:, None]
-    a, b = x[..., : D // 2].float(), x[..., D // 2:].float()
-    x.copy_(torch.cat((a * cos - b * sin, b * cos + a * sin), -1))
 
 
 class PagePool:
@@ -89,6 +81,7 @@ class DecoderLayer:
         self.gate_up = fp8_weight(2 * inter, hidden, gen, dev)
         self.down = fp8_weight(hidden, inter, gen, dev)
         self.norms = [(1 + 0.1 * torch.randn(hidden, generator=gen, device=dev)).to(torch.bfloat16) for _ in range(5)]
+        self.inv_freq = (1e6 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().to(dev)
 
     def __call__(self, x, pool, step):
         """x [T, hidden], the residual stream, is updated; returns what the next
@@ -114,8 +107,7 @@ class DecoderLayer:
         bfp8.bfp8_residual_norm(None, x, q=a[0], scales=a[1], w_pre=pre_attn)
         qkv = linear(a, self.qkv, sum(self.members), self.members).view(T, -1, D)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
-        rotate(q, step["positions"])
-        rotate(k, step["positions"])
+        bfp8.bfp8_rotary(q, k, step["positions"], self.inv_freq)
         cache = (pool.k, pool.v, pool.k_exp, pool.v_exp)
         bfp8.bfp8_kv_append(k, v, step["slots"], *cache)
         out = bf16(T, self.heads, D)
