@@ -1129,10 +1129,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       }
       // while r meets T: the next chunk's values
       const float gamma = scalars[kGammaC];
-      float offer = gamma * max_f16x2(largest);
+      const float back = 1.0f / power;                 // offers are sizes as they are, not as they are held
+      float offer = gamma * max_f16x2(largest) * back;
       if (more) {
         load_values(c + 1);
-        offer = fmaxf(offer, max_bf16x2(top) * power);
+        offer = fmaxf(offer, max_bf16x2(top));
       }
       if (!wait(sh.u_done, c & 1)) break;
       tc_fence_after();
@@ -1153,7 +1154,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
           }
           tmem_st8(mine + col_u(0, 2 * wg + q), hi);
           tmem_st8(mine + col_u(1, 2 * wg + q), lo);
-          if (q == 1) sh.most[c & 1][wg][r] = offer = fmaxf(offer, max_f16x2(m));   // read behind the product
+          if (q == 1) sh.most[c & 1][wg][r] = offer = fmaxf(offer, max_f16x2(m) * back);   // read behind the product
           tmem_wait_st();
           tc_fence_before();
           tell_bar(sh.p_full[q]);
@@ -1163,24 +1164,29 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       if (!wait(sh.new_done, c & 1) || !wait(sh.p_full[1], c & 1)) break;   // (the second for the other half's offer)
       tc_fence_after();
       offer = fmaxf(offer, sh.most[c & 1][wg ^ 1][r]);
-      float step = 1.0f;
-      if (offer > 0.0f && !(offer >= 0x1p-3f && offer < 0x1p6f)) {
-        step = fminf(fmaxf(power_for(offer / power, 2) / power, 0x1p-100f), 0x1p100f);
-        power *= step;
+      // two factors, each a power of two that a float holds, where the power changes by up to 2^250
+      float step[2] = {1.0f, 1.0f};
+      const float held = offer * power;
+      if (offer > 0.0f && !(held >= 0x1p-3f && held < 0x1p6f)) {
+        const float next = power_for(offer, 2);
+        const int e = static_cast<int>(__float_as_uint(next) >> 23) - static_cast<int>(__float_as_uint(power) >> 23);
+        step[0] = __uint_as_float(static_cast<uint32_t>(127 + (e >> 1)) << 23);
+        step[1] = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
+        power = next;
       }
-      const bool rescale = __any_sync(0xffffffffu, step != 1.0f);
-      const float2 keep = make_float2(gamma * step, gamma * step);
+      const bool rescale = __any_sync(0xffffffffu, step[0] != 1.0f || step[1] != 1.0f);
+      const float2 keep = make_float2(gamma, gamma);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float d[32];
         tmem_ld32(mine + kColNew + 64 * wg + 32 * q, d);
-        if (rescale) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) d[k] *= step;
-        }
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          const float2 f = __ffma2_rn(keep, make_float2(S[32 * q + k], S[32 * q + k + 1]), make_float2(d[k], d[k + 1]));
+          float2 f = __ffma2_rn(keep, make_float2(S[32 * q + k], S[32 * q + k + 1]), make_float2(d[k], d[k + 1]));
+          if (rescale) {
+            f.x = f.x * step[0] * step[1];
+            f.y = f.y * step[0] * step[1];
+          }
           S[32 * q + k] = f.x, S[32 * q + k + 1] = f.y;
         }
       }
