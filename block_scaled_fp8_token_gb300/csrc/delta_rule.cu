@@ -6,7 +6,8 @@
 //   k' = k rsqrt(|k|^2 + eps),  q' = scale q rsqrt(|q|^2 + eps)
 //   u = beta (v - alpha S k'),  S <- alpha S + u k'^T,  out = S q'
 //
-// in FP32; only out is rounded, once, to BF16.
+// State, sums and gates are FP32 and out is rounded once to BF16; what the chunks' products round
+// beside is said there.
 #include "hybrid_layer.cuh"
 
 namespace bfp8 {
@@ -63,7 +64,9 @@ constexpr int kStepWarps = 4;
 
 // One token after the other: a warp holds 8 of a head's 128 rows of S, four columns a lane,
 // and needs no other warp. Both products with the old state are summed at once, as
-// S_new q' = alpha S q' + u (k' . q').
+// S_new q' = alpha S q' + u (k' . q'). Bound by HBM, the state's 64 KB read and written a head:
+// 64 single tokens of 48 heads move 405 MB in 63 us, 6.4 TB/s; three drafted tokens of 17 requests
+// of 32 heads, 73 MB, take 16 us, where each token adds 0.7 us of reductions one behind another.
 // A block of WARPS warps, number `block`.
 template <int WARPS>
 BFP8_DEV void delta_steps(const DeltaParams& p, int64_t block) {
@@ -350,7 +353,12 @@ BFP8_DEV float4 negate(float4 v) { return make_float4(-v.x, -v.y, -v.z, -v.w); }
 // two threads share a lane's columns. (1 + A)^-1 is formed by blocks of 16: the diagonal ones
 // column by column, then each lower one as -T_b A_ba T_a, of 16 rows and of 32. P T is a
 // product on the tensor cores again. The grid's last blocks take the step's short requests, a
-// token after the other, which so run beside the long ones' chunks.
+// token after the other, which so run beside the long ones' chunks (as its first blocks they kept
+// the chunks waiting: 81 us against 60 for 12 requests of 1 to 141 tokens and 48 heads).
+//
+// Bound by latency: a block passes a dozen barriers, and three to an SM issue in 42% of the clocks.
+// 129 chunks of 16 key and 32 value heads take 102 us (138 with a thread a row solving against A
+// from registers, whose unrolled code stalled on instruction fetches; 214 with one block an SM).
 __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __grid_constant__ CUtensorMap tq,
                                                                      const __grid_constant__ CUtensorMap tk,
                                                                      const ChunkParams p) {
@@ -667,14 +675,26 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
 // and 32 - 63.
 //
 // A row's power of two brings the larger of its state's and its values' entries near 2^2. With
-// all of them below 2^6, no u and no S of the chunk reaches 2^13 (|u| <= |v| + |S|, and |S| grows
-// by |v| a token at most), and with the largest above 2^-3, the rests' 2^-25 is 2^-22 of it. It
-// is looked at once a chunk: Gamma_C times the state's largest at the chunk's begin, the largest
-// update, and the next chunk's values stand for what the next chunk meets.
+// all of them below 2^6, neither u nor S reaches 2^14 in the chunk: a row's length grows by |v| a
+// token at most, |S| <= sqrt(128) 2^6 + 64 2^6, and |u| <= |v| + |S|. With the largest above 2^-3,
+// the rests' 2^-25 is 2^-22 of it. It is looked at once a chunk: Gamma_C times the state's largest
+// at the chunk's begin, the largest update, and the next chunk's values stand for what the next
+// chunk meets. So where a head forgets within a chunk, what comes after keeps 2^-22 of what was
+// forgotten there, not of itself.
 //
 // What the chain of three products does not need runs beside it: S0 Q^T and the out rows of
-// T behind the products that the chain waits for, and the out rows' arithmetic in a third
-// warpgroup. Each product begins on the first half of its operand while the second is cut.
+// T behind the products that the chain waits for, the out rows' arithmetic in a third warpgroup,
+// the values' turning (a row of S wants a value's tokens side by side) in two warps. Each product
+// begins on the first half of its operand while the second is cut.
+//
+// Bound by the chain: 4,750 clocks a chunk and block, 2.5 us, one block an SM. The products the
+// chain waits for are 1,410 of them at the tensor cores' rate (64 columns of 128 lanes by 16 take
+// 32 clocks, 128 take 64); reading, cutting and handing over r, u and S are 500, 540 and 1,400,
+// and each hand-over between threads and tensor cores costs 200 to 300 of waiting. On the way,
+// 8192 tokens of 32 heads: 4.7 us a chunk with three BF16 parts a value (the cuts' masks and
+// permutes run at half rate), 3.1 with two F16 parts, 2.5 with the out rows aside and the values
+// turned. Sixteen warps of rows instead of eight: 2.9 us. Out rows by bulk copies of 256 bytes: 80
+// clocks of the issuing warp each, which then was the bound.
 constexpr int kRowWarps = 8, kOutWarps = 4;
 constexpr int kWalkThreads = 32 * (kRowWarps + kOutWarps + 4);   // and a warp of products and one of loads
 constexpr int kBlobAt = kKq;

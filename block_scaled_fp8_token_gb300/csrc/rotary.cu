@@ -6,7 +6,10 @@
 //   (a, b) <- factor * (a cos - b sin, b cos + a sin)   for the pair (a, b) number i
 //
 // Pair i is (x[i], x[i + rotary_dim / 2]), or (x[2i], x[2i + 1]) where `adjacent`; columns
-// from rotary_dim on are not turned. Bound by HBM: a row is read once and written once.
+// from rotary_dim on are not turned. Bound by HBM: a row is read once and written once. 8192
+// tokens of 18 normed heads of 256, 151 MB, take 30 us, 5.0 TB/s (54 with the angles formed by
+// every lane and one head's loads under way; 38 with the angles shared, 30 with four heads'
+// loads); 8000 tokens of 72 heads of 128, 295 MB, 50 us. Few tokens: 2.6 us for one, 3.6 for 64.
 //
 // The angle of a position in the millions leaves a float32 no digits, so it is counted in
 // turns: inv_freq / (2 pi) as a 64-bit binary fraction, times the position modulo 2^64,
@@ -274,8 +277,8 @@ int launch_rotary(const bfp8_rotary_args& a, void* stream) {
   p.w_offset = a.weight_offset;
   p.factor = a.factor;
   // A token's angles are formed by each block that has it: eight tokens to a block, fewer where
-  // that leaves SMs without four blocks, and several blocks to a token of many heads where one
-  // each does.
+  // that leaves SMs without a block, and several blocks to a token where one each does. (A block
+  // an SM, two, four: 949 tokens of 72 heads 8.5, 9.6, 10.9 us; 64 tokens 3.7, 4.2, 4.2.)
   const int64_t groups = p.t[0].groups + p.t[1].groups, want = sms;
   p.block_tokens = a.tokens >= 8 * want ? 8 : a.tokens >= 4 * want ? 4 : a.tokens >= 2 * want ? 2 : 1;
   int64_t share = (want + a.tokens - 1) / a.tokens;

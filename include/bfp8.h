@@ -746,7 +746,11 @@ int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream);
  *   k' = k * rsqrt(|k|^2 + eps),  q' = scale * q * rsqrt(|q|^2 + eps)
  *   u = beta * (v - alpha * S k'),  S <- alpha * S + u k'^T,  out = S q'
  * State, sums and gates are float32; out is rounded to BF16 once. One ragged call
- * serves single tokens, drafted ones, and prompts.
+ * serves single tokens, drafted ones, and prompts. max_q_len and a request's own
+ * length choose between two ways for it: a token after the other (up to 20 tokens; up
+ * to 8 where max_q_len is larger), or by chunks of 64, whose products carry a row of S,
+ * and the values that meet it, to 2^-22 of the largest among them in a chunk. Long
+ * prompts of few heads are walked in segments at once.
  *   q, k, v, out  [tokens, heads, 128] BF16, 16-byte aligned, token and head strides
  *               in elements, multiples of 8, for example columns of the convolution's
  *               output. out must not overlap the inputs.
@@ -755,7 +759,8 @@ int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream);
  *   workspace   at least bfp8_delta_rule_workspace() bytes, 256-byte aligned, contents
  *               free (may be NULL where that is 0); calls sharing it must not overlap
  * A NaN or an infinity among a token's inputs reaches its request's outputs from there
- * on, and its state. Nothing synchronises with the host, results do not depend on what
+ * on, and its state; by chunks it may reach the outputs of up to 63 tokens ahead of it
+ * too. Nothing synchronises with the host, results do not depend on what
  * else runs, and a step can be captured in a CUDA graph. tokens == 0, batch == 0 or
  * max_q_len == 0 is a no-op. Errors: INVALID_ARG (null pointers, negative sizes, v_heads
  * not a multiple of qk_heads, strides below a row, slots without a state, workspace
