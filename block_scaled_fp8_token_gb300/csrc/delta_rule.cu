@@ -60,92 +60,124 @@ BFP8_DEV float warp_sum8(float (&v)[8], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-constexpr int kStepWarps = 4;
+constexpr int kStepWarps = 4, kMostSteps = 32;         // of a block; tokens of a request
+template <int WARPS>
+struct StepShared {
+  alignas(16) uint2 k[kMostSteps][32];                 // raw rows
+  uint2 q[kMostSteps][32];
+  alignas(16) __nv_bfloat16 v[kMostSteps][8 * WARPS];  // of the block's values
+  float alpha[kMostSteps], beta[kMostSteps], kn[kMostSteps], qn[kMostSteps], kq[kMostSteps];
+};
 
 // One token after the other: a warp holds 8 of a head's 128 rows of S, four columns a lane,
-// and needs no other warp. Both products with the old state are summed at once, as
-// S_new q' = alpha S q' + u (k' . q'). Bound by HBM, the state's 64 KB read and written a head:
-// 64 single tokens of 48 heads move 405 MB in 63 us, 6.4 TB/s; three drafted tokens of 17 requests
-// of 32 heads, 73 MB, take 16 us, where each token adds 0.7 us of reductions one behind another.
-// A block of WARPS warps, number `block`.
+// and in the loop needs no other warp. Both products with the old state are summed at once, as
+// S_new q' = alpha S q' + u (k' . q'), with the raw key and query, whose factors go behind the
+// sums. The tokens' rows and what of them needs no state (gates, factors, k' . q') are in shared
+// memory before the first token's turn, so that a turn is one reduction, u's way back to the
+// lanes and the update. A block of WARPS warps, number `block`.
+//
+// Bound by HBM, the state's 64 KB read and written a head: 64 single tokens of 48 heads move 405
+// MB in 62 us, 6.5 TB/s.
 template <int WARPS>
-BFP8_DEV void delta_steps(const DeltaParams& p, int64_t block) {
+BFP8_DEV void delta_steps(const DeltaParams& p, int64_t block, StepShared<WARPS>& sh) {
   constexpr int kParts = kD / (8 * WARPS);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t item = block / kParts;
   const int b = static_cast<int>(item / p.v_heads), h = static_cast<int>(item - int64_t{b} * p.v_heads);
-  const int row0 = (static_cast<int>(block % kParts) * WARPS + (threadIdx.x >> 5)) * 8;
+  const int block_row = static_cast<int>(block % kParts) * (8 * WARPS), row0 = block_row + warp * 8;
   const int64_t first = first_token(p.req, b);
-  int64_t n = first_token(p.req, b + 1) - first;
-  n = n < p.max_len ? n : p.max_len;
-  if (n <= 0 || n > p.step_len) return;
+  int64_t len = first_token(p.req, b + 1) - first;
+  len = len < p.max_len ? len : p.max_len;
+  if (len <= 0 || len > p.step_len) return;
+  const int n = static_cast<int>(len);
   const int64_t from = slot_of(p.req, p.req.slots_in, b), to = slot_of(p.req, p.req.slots_out, b);
   const int64_t in_head = h * p.s_head + row0 * kD + lane * 4;
-  float4 S[8];
+  const int hk = h / p.group;
+  const __nv_bfloat16* qp = p.q + first * p.qt + hk * p.qh;
+  const __nv_bfloat16* kp = p.k + first * p.kt + hk * p.kh;
+  const __nv_bfloat16* vp = p.v + first * p.vt + h * p.vh + block_row;
+  for (int t = warp; t < n; t += WARPS) {
+    const bool key = lane < 16;
+    cp_async16(smem_u32(key ? &sh.k[t][2 * lane] : &sh.q[t][2 * (lane - 16)]),
+               (key ? kp + t * p.kt : qp + t * p.qt) + 8 * (lane & 15));
+  }
+  for (int i = threadIdx.x; i < n * WARPS; i += 32 * WARPS)
+    cp_async16(smem_u32(&sh.v[i / WARPS][8 * (i % WARPS)]), vp + (i / WARPS) * p.vt + 8 * (i % WARPS));
+  cp_async_commit();
+  float2 S[8][2];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) S[r][0] = S[r][1] = make_float2(0.0f, 0.0f);
   if (from >= 0) {
     const float* s = p.state + from * p.s_slot + in_head;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) S[r] = *reinterpret_cast<const float4*>(s + r * kD);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) S[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  }
-  const float rate = expf(__ldg(p.a_log + h)), dt_bias = __ldg(p.dt_bias + h);
-  const int hk = h / p.group;
-  const __nv_bfloat16* qp = p.q + first * p.qt + hk * p.qh + lane * 4;
-  const __nv_bfloat16* kp = p.k + first * p.kt + hk * p.kh + lane * 4;
-  const __nv_bfloat16* vp = p.v + first * p.vt + h * p.vh + row0 + (lane >> 2);
-  const __nv_bfloat16* ap = p.a + first * p.at + h;
-  const __nv_bfloat16* bp = p.b + first * p.bt + h;
-  __nv_bfloat16* op = p.out + first * p.ot + h * p.oh + row0 + (lane >> 2);
-  uint2 kr = *reinterpret_cast<const uint2*>(kp), qr = *reinterpret_cast<const uint2*>(qp);
-  __nv_bfloat16 vr = *vp, ar = *ap, br = *bp;
-  for (int64_t t = 0; t < n; ++t) {
-    float k[4] = {__uint_as_float(kr.x << 16), __uint_as_float(kr.x & 0xFFFF0000u),
-                  __uint_as_float(kr.y << 16), __uint_as_float(kr.y & 0xFFFF0000u)};
-    float q[4] = {__uint_as_float(qr.x << 16), __uint_as_float(qr.x & 0xFFFF0000u),
-                  __uint_as_float(qr.y << 16), __uint_as_float(qr.y & 0xFFFF0000u)};
-    const float v = __bfloat162float(vr);
-    const float alpha = expf(log_decay(__bfloat162float(ar), dt_bias, rate)), beta = beta_of(__bfloat162float(br));
-    if (t + 1 < n) {   // the next token's inputs, a token ahead of their use
-      kp += p.kt, qp += p.qt, vp += p.vt, ap += p.at, bp += p.bt;
-      kr = *reinterpret_cast<const uint2*>(kp), qr = *reinterpret_cast<const uint2*>(qp);
-      vr = *vp, ar = *ap, br = *bp;
+    for (int r = 0; r < 8; ++r) {
+      const float4 f = *reinterpret_cast<const float4*>(s + r * kD);
+      S[r][0] = make_float2(f.x, f.y), S[r][1] = make_float2(f.z, f.w);
     }
-    const float kn = rsqrtf(warp_sum(fmaf(k[0], k[0], fmaf(k[1], k[1], fmaf(k[2], k[2], k[3] * k[3])))) + p.eps);
-    const float qn = rsqrtf(warp_sum(fmaf(q[0], q[0], fmaf(q[1], q[1], fmaf(q[2], q[2], q[3] * q[3])))) + p.eps) * p.scale;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) k[e] *= kn, q[e] *= qn;
-    const float kq = warp_sum(fmaf(k[0], q[0], fmaf(k[1], q[1], fmaf(k[2], q[2], k[3] * q[3]))));
+  }
+  if (warp == WARPS - 1 && lane < n) {
+    const float a = __bfloat162float(p.a[(first + lane) * p.at + h]), g = __bfloat162float(p.b[(first + lane) * p.bt + h]);
+    sh.alpha[lane] = expf(log_decay(a, __ldg(p.dt_bias + h), expf(__ldg(p.a_log + h))));
+    sh.beta[lane] = beta_of(g);
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  auto four = [](uint2 w, float2& lo, float2& hi) {
+    lo = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
+    hi = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+  };
+  for (int t = warp; t < n; t += WARPS) {
+    float2 k01, k23, q01, q23;
+    four(sh.k[t][lane], k01, k23);
+    four(sh.q[t][lane], q01, q23);
+    const float2 kk = __ffma2_rn(k01, k01, __fmul2_rn(k23, k23)), qq = __ffma2_rn(q01, q01, __fmul2_rn(q23, q23));
+    const float2 kq = __ffma2_rn(k01, q01, __fmul2_rn(k23, q23));
+    const float kn = rsqrtf(warp_sum(kk.x + kk.y) + p.eps), qn = rsqrtf(warp_sum(qq.x + qq.y) + p.eps) * p.scale;
+    const float both = warp_sum(kq.x + kq.y);
+    if (lane == 0) sh.kn[t] = kn, sh.qn[t] = qn, sh.kq[t] = both * kn * qn;
+  }
+  __syncthreads();
+  __nv_bfloat16* op = p.out + first * p.ot + h * p.oh + row0 + (lane >> 2);
+  for (int t = 0; t < n; ++t) {
+    float2 k01, k23, q01, q23;
+    four(sh.k[t][lane], k01, k23);
+    four(sh.q[t][lane], q01, q23);
+    const float v = __bfloat162float(sh.v[t][8 * warp + (lane >> 2)]);
+    const float alpha = sh.alpha[t], kn = sh.kn[t];
     float sk[8], sq[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      sk[r] = fmaf(S[r].x, k[0], fmaf(S[r].y, k[1], fmaf(S[r].z, k[2], S[r].w * k[3])));
-      sq[r] = fmaf(S[r].x, q[0], fmaf(S[r].y, q[1], fmaf(S[r].z, q[2], S[r].w * q[3])));
+      const float2 a = __ffma2_rn(S[r][0], k01, __fmul2_rn(S[r][1], k23));
+      const float2 c = __ffma2_rn(S[r][0], q01, __fmul2_rn(S[r][1], q23));
+      sk[r] = a.x + a.y;
+      sq[r] = c.x + c.y;
     }
     const float Sk = warp_sum8(sk, lane), Sq = warp_sum8(sq, lane);
-    const float u = beta * fmaf(-alpha, Sk, v);
-    if ((lane & 3) == 0) *op = __float2bfloat16_rn(fmaf(alpha, Sq, u * kq));
+    const float u = sh.beta[t] * fmaf(-alpha * kn, Sk, v);
+    if ((lane & 3) == 0) *op = __float2bfloat16_rn(fmaf(alpha * sh.qn[t], Sq, u * sh.kq[t]));
     op += p.ot;
+    const float uk = u * kn;
+    const float2 alpha2 = make_float2(alpha, alpha);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const float ur = __shfl_sync(0xffffffffu, u, 4 * r);
-      S[r].x = fmaf(alpha, S[r].x, ur * k[0]);
-      S[r].y = fmaf(alpha, S[r].y, ur * k[1]);
-      S[r].z = fmaf(alpha, S[r].z, ur * k[2]);
-      S[r].w = fmaf(alpha, S[r].w, ur * k[3]);
+      const float ur = __shfl_sync(0xffffffffu, uk, 4 * r);
+      const float2 u2 = make_float2(ur, ur);
+      S[r][0] = __ffma2_rn(u2, k01, __fmul2_rn(alpha2, S[r][0]));
+      S[r][1] = __ffma2_rn(u2, k23, __fmul2_rn(alpha2, S[r][1]));
     }
   }
   if (to >= 0) {
     float* s = p.state + to * p.s_slot + in_head;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) *reinterpret_cast<float4*>(s + r * kD) = S[r];
+    for (int r = 0; r < 8; ++r)
+      *reinterpret_cast<float4*>(s + r * kD) = make_float4(S[r][0].x, S[r][0].y, S[r][1].x, S[r][1].y);
   }
 }
 __global__ void __launch_bounds__(32 * kStepWarps) delta_step_kernel(const DeltaParams p) {
+  __shared__ StepShared<kStepWarps> sh;
   pdl_wait();
   pdl_launch_dependents();
-  delta_steps<kStepWarps>(p, blockIdx.x);
+  delta_steps<kStepWarps>(p, blockIdx.x, sh);
 }
 
 // ------------------------------------------------------------------ chunks of 64 tokens
@@ -288,6 +320,7 @@ struct PrepShared {
 };
 constexpr int kPrepSharedAt = (kBlob + 1023) / 1024 * 1024;   // the blob takes the K and Q rows' place
 constexpr int kPrepSmem = 1024 + kPrepSharedAt + static_cast<int>(sizeof(PrepShared));
+static_assert(sizeof(StepShared<kPrepThreads / 32>) <= kPrepSharedAt, "the steps' rows fit the blob's place");
 
 // Running products over the warp, of 32 values from the first to each lane's.
 BFP8_DEV float scan_product(float v, int lane) {
@@ -370,7 +403,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
   pdl_wait();
   if (blockIdx.x >= p.chunk_blocks) {
     pdl_launch_dependents();
-    delta_steps<kPrepThreads / 32>(p.d, blockIdx.x - p.chunk_blocks);
+    delta_steps<kPrepThreads / 32>(p.d, blockIdx.x - p.chunk_blocks,
+                                   *reinterpret_cast<StepShared<kPrepThreads / 32>*>(base));
     return;
   }
   const int block = static_cast<int>(blockIdx.x);
@@ -1316,13 +1350,14 @@ int segment_count(int64_t chunks, int64_t pairs, int sms) {
   return best;
 }
 
-// Where no request has more new tokens than this, each takes them one after the other. One
-// request of 48 heads: 20 / 24 / 32 tokens 17 / 20 / 25 us against 21 us by a chunk; 64 requests
-// of 16 / 24 tokens 310 / 453 us against 343 / 346 us.
-constexpr int64_t kStepTokens = 20;
+// Where no request has more new tokens than this, each takes them one after the other. Of 48
+// heads, 24 / 32 tokens against one chunk of the chunks' kernels: one request 12 / 15 and 21 us,
+// 16 requests 82 / 107 and 107, 64 requests 302 / 395 and 346.
+constexpr int64_t kStepTokens = 28;
 // Beside longer ones, which run the chunks' kernels anyway, up to this many do: requests of 1 to
-// 141 tokens (12, of 48 heads) take 52, 60 and 60 us with 8, 16 and 20.
-constexpr int64_t kStepTokensBeside = 8;
+// 141 tokens (12, of 48 heads) take 53.8, 52.4, 53.9 and 53.9 us with 8, 12, 16 and 24.
+constexpr int64_t kStepTokensBeside = 12;
+static_assert(kStepTokens <= kMostSteps, "a request's steps fit shared memory");
 
 int64_t chunk_slots(int64_t batch, int64_t tokens) { return (tokens >> kShift) + batch; }
 

@@ -54,8 +54,8 @@ def _check(t, lens, before, scale=128 ** -0.5, eps=1e-6, c=512):
     assert np.all(off <= tol_state), float(np.max(off / (tol_state + 1e-30)))
 
 
-STEPS = [[1], [1] * 9, [3, 3, 3], [2, 0, 1, 4, 7, 0, 5]]
-PROMPTS = [[64], [65], [63], [128, 1, 64], [40, 0, 100, 1, 17, 33], [200], [15, 16, 17, 31, 32, 33], [1, 130, 3, 66]]
+STEPS = [[1], [1] * 9, [3, 3, 3], [2, 0, 1, 4, 7, 0, 5], [28, 5, 27]]
+PROMPTS = [[64], [65], [29], [12, 13, 30], [63], [128, 1, 64], [40, 0, 100, 1, 17, 33], [200], [15, 16, 17, 31, 32, 33], [1, 130, 3, 66]]
 
 
 @pytest.mark.parametrize("lens", STEPS, ids=str)
