@@ -400,6 +400,10 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
   PrepShared& sh = *reinterpret_cast<PrepShared*>(base + kPrepSharedAt);
   const uint32_t kq = smem_u32(base), blob = kq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tq);
+  }
   pdl_wait();
   if (blockIdx.x >= p.chunk_blocks) {
     pdl_launch_dependents();
@@ -782,7 +786,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   const uint32_t stages = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kMmaWarp = kRowWarps + kOutWarps;
-  pdl_wait();
+  // The kernel ahead (the chunks' first one, or the join) waited for what came before it ahead of
+  // letting this one begin: lengths, values and the requests' states are there already. What it
+  // writes itself, the loads' warp waits for, and the rows' where they begin from a join's state.
+  if (tid == 0) tma_prefetch_desc(&tv);
   const int pairs = p.d.req.batch * p.d.v_heads, pair = blockIdx.x % pairs, job = blockIdx.x / pairs;
   const int h = pair % p.d.v_heads, b = pair / p.d.v_heads;
   // the first walk's jobs: N of the segments ahead of the last (the first one's with its rows of
@@ -793,9 +800,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   int64_t first;
   int64_t len = chunked_len(p.d, b, first);
   const int64_t segment_tokens = static_cast<int64_t>(p.segment_chunks) << kShift;
-  if (len <= segment * segment_tokens) return;
   const bool last = len <= (segment + 1) * segment_tokens;
-  if (last && !rows_out) return;
+  if (len <= segment * segment_tokens || (last && !rows_out)) {
+    pdl_wait();                                        // nothing behind this grid runs ahead of the one before it
+    return;
+  }
   first += segment * segment_tokens;
   len = last ? len - segment * segment_tokens : segment_tokens;
   float* const between = p.ends + (static_cast<int64_t>(pair) * (p.segments - 1) + segment) * (kD * kD);
@@ -955,6 +964,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         ++values;
       };
       load_values();
+      pdl_wait();
       while (ok && got < chunks) {
         const int s = got % kStages;
         if (!wait(sh.empty[s], ((got / kStages) & 1) ^ 1)) break;
@@ -1066,6 +1076,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       const int64_t slot = slot_of(p.d.req, p.d.req.slots_in, b);
       if (slot >= 0) from = p.d.state + slot * p.d.s_slot + h * p.d.s_head + in_row;
     } else if (p.second_walk) {
+      pdl_wait();
       from = between - kD * kD + in_row;
     }
     if (last) {
