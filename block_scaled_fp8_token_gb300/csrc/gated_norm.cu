@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const Gate
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float a = z[2 * e], b = z[2 * e + 1];
-      float2 g = make_float2(sigmoid(a), sigmoid(b));
+      float2 g = make_float2(sigmoid_bf16(a), sigmoid_bf16(b));
       if (!p.is_sigmoid) g = __fmul2_rn(g, make_float2(a, b));
       y[e] = __fmul2_rn(y[e], g);
       am = fmaxf(am, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));

@@ -44,6 +44,13 @@ BFP8_DEV void cp_async_wait_group() { asm volatile("cp.async.wait_group %0;" ::"
 // BF16 or E4M3 rounds (2^-8, 2^-4).
 BFP8_DEV float sigmoid(float x) { return rcp_approx(1.0f + ex2_approx(x * -1.4426950408889634f)); }
 
+// The same of a BF16 x, within 4 2^-23 and as much again where e^-x outweighs the 1: x times the
+// upper 16 bits of log2 e is exact, and the rest of the exponent is put right to first order.
+BFP8_DEV float sigmoid_bf16(float x) {
+  const float e = ex2_approx(x * kNegLog2eHi);
+  return rcp_approx(1.0f + fmaf(e, x * kNegLog2eLoLn2, e));
+}
+
 // The requests of a step lie one behind another: request b has the tokens
 // [offsets[b], offsets[b + 1]), within [0, T] whatever the array holds.
 struct Requests {
