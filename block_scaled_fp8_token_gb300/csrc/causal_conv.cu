@@ -5,10 +5,10 @@
 //
 // Inputs ahead of a request's first token come from its slot of the state, and the last
 // W - 1 inputs go there. Bound by HBM: a row is read once and written once. 11,600 rows of 8192
-// channels, 380 MB, take 69 us, 5.5 TB/s, with 40% of the issue slots; four channels a thread
-// with twice the warps took 93 us (a row's addresses and predicates for half the work), eight
-// without the next rows under way 84. A single token of 64 requests: 4.2 us of latency, two
-// rounds of loads (which request, then its rows).
+// channels, 380 MB, take 63 us, 6.0 TB/s; with the next four rows under way in registers 69 us,
+// without any 84, and with four channels a thread and twice the warps 93 (a row's addresses and
+// predicates for half the work). A single token of 64 requests: 3.8 us of latency, two rounds of
+// loads (which request, then its rows).
 #include "hybrid_layer.cuh"
 
 namespace bfp8 {
@@ -17,6 +17,7 @@ namespace {
 using namespace dev;
 
 constexpr int kConvThreads = 128;   // 8 channels each
+constexpr int kConvAhead = 8;       // rows that a thread has under way
 
 struct ConvParams {
   const __nv_bfloat16* x;
@@ -58,9 +59,10 @@ BFP8_DEV void widen4x2(const uint4& r, float2 (&v)[4]) {
 }
 
 // A block takes 1024 channels of one tile of a request's tokens; a thread walks down its 8
-// channels with the last W - 1 inputs in registers, four rows at a time with the next four
-// asked for. The thread of a request's first tile also moves the state: it alone reads the old
-// rows, before it writes the new ones, so one slot may be both.
+// channels with the last W - 1 inputs in registers. It copies its 16 bytes of the next eight rows
+// to places of its own in shared memory and waits for nobody else. The thread of a request's
+// first tile also moves the state: it alone reads the old rows, before it writes the new ones, so
+// one slot may be both.
 template <int W, bool SILU>
 __global__ void __launch_bounds__(kConvThreads, 4) causal_conv_kernel(const ConvParams p) {
   pdl_wait();
@@ -76,13 +78,20 @@ __global__ void __launch_bounds__(kConvThreads, 4) causal_conv_kernel(const Conv
   const int64_t left = end - t0, most = int64_t{1} << p.tile_shift;
   const int n = static_cast<int>(left < most ? left : most);
 
-  constexpr int U = 4;
+  __shared__ alignas(16) uint4 ring[kConvAhead][kConvThreads];   // a thread's own places
+  const uint32_t place = smem_u32(&ring[0][threadIdx.x]);
+  constexpr uint32_t kRow = sizeof(ring[0]);
   const __nv_bfloat16* x = p.x + t0 * p.ldx + c;
-  auto row = [&](int64_t t) { return __ldg(reinterpret_cast<const uint4*>(x + t * p.ldx)); };
-  uint4 raw[U];
+  const __nv_bfloat16* next = x;
+  int asked = 0;
+  auto ask = [&](int s) {
+    if (asked < n) cp_async16(place + s * kRow, next);
+    cp_async_commit();
+    ++asked, next += p.ldx;
+  };
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (u < n) raw[u] = row(u);
+  for (int s = 0; s < kConvAhead; ++s) ask(s);
+  auto row = [&](int64_t t) { return __ldg(reinterpret_cast<const uint4*>(x + t * p.ldx)); };
   float2 w[W][4], h[W - 1][4], bias[4];
   {
     float flat[8 * W], flat_bias[8] = {};
@@ -143,23 +152,17 @@ __global__ void __launch_bounds__(kConvThreads, 4) causal_conv_kernel(const Conv
                                                 pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
     out += p.ldo;
   };
-  int t = 0;
-  for (; t + 2 * U <= n; t += U) {
-    uint4 now[U];
-    x += U * p.ldx;
+  for (int t = 0; t < n; t += kConvAhead) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = raw[u], raw[u] = row(u);
-#pragma unroll
-    for (int u = 0; u < U; ++u) step(now[u]);
+    for (int s = 0; s < kConvAhead; ++s) {
+      if (t + s >= n) break;
+      cp_async_wait_group<kConvAhead - 1>();
+      const uint4 r = lds128(place + s * kRow);
+      ask(s);
+      step(r);
+    }
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (t + u < n) step(raw[u]);
-  t += U;
-  x += U * p.ldx;
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (t + u < n) step(row(u));
+  cp_async_wait_group<0>();
 }
 
 bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -183,7 +186,8 @@ int launch_causal_conv(const bfp8_causal_conv_args& a, void* stream) {
       off16(a.weight) || off16(a.bias) || off16(a.state_bf16) ||
       (a.state_bf16 && (a.state_stride_slot % 8 || a.state_stride_row % 8)))
     return BFP8_ERR_UNSUPPORTED;
-  // the grid's second dimension holds 65535 tiles
+  // Tiles of 32 tokens (16, 32, 64, 128 for 11,600 rows: 70, 63, 64, 76 us), or as many more as
+  // keep them within the grid's second dimension.
   int shift = 5;
   while ((a.tokens >> shift) + a.batch > 65535 && shift < 30) ++shift;
   const int64_t tiles = (a.tokens >> shift) + a.batch;
