@@ -343,43 +343,49 @@ BFP8_DEV float scan_product_behind(float v, int lane) {
   return r;
 }
 
-// out (rows x 32 of a 4-column piece a thread) = sign * X (rows x N) Y (N x 32), all in shared
-// memory with pitch kPitch.
-template <int N>
-BFP8_DEV float4 product4(const float* x, const float* y) {
-  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// A warp's 16 x 8 piece of X (16 x K) Y (K x 8), all FP32 in shared memory with pitch kPitch: lane
+// l has columns 2 (l % 4) and one more of rows l / 4 and l / 4 + 8. The operands are cut into two
+// F16 parts; none exceeds 32 (a row of A by a column of T1), so that 2^8 of them stay in range,
+// and the rests' smallest step is 2^-33. (On CUDA cores the two products of the 32-row block took
+// 2,400 clocks, most of them reading shared memory; so they take 700. tcgen05 has no shape
+// this small.)
+template <int K>
+BFP8_DEV void small_product(const float* x, const float* y, int lane, float (&c)[4]) {
+  constexpr float kUp = 256.0f;
+  const int g = lane >> 2, t = lane & 3;
+  c[0] = c[1] = c[2] = c[3] = 0.0f;
 #pragma unroll
-  for (int l = 0; l < N; l += 4) {
-    const float4 a = *reinterpret_cast<const float4*>(x + l);
-    const float c[4] = {a.x, a.y, a.z, a.w};
+  for (int k = 0; k < K; k += 16) {
+    uint32_t a[2][4], b[2][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 b = *reinterpret_cast<const float4*>(y + (l + e) * kPitch);
-      s.x = fmaf(c[e], b.x, s.x), s.y = fmaf(c[e], b.y, s.y), s.z = fmaf(c[e], b.z, s.z), s.w = fmaf(c[e], b.w, s.w);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = *reinterpret_cast<const float2*>(x + (g + 8 * (i & 1)) * kPitch + k + 2 * t + 8 * (i >> 1));
+      split2(make_float2(f.x * kUp, f.y * kUp), a[0][i], a[1][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* f = y + (k + 2 * t + 8 * i) * kPitch + g;
+      split2(make_float2(f[0] * kUp, f[kPitch] * kUp), b[0][i], b[1][i]);
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {                      // rests by rests left out
+      const uint32_t(&u)[4] = a[p >> 1];
+      const uint32_t(&v)[2] = b[p & 1];
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+          : "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(v[0]), "r"(v[1]));
     }
   }
-  return s;
-}
-// Two rows of it.
-template <int N>
-BFP8_DEV void product2x4(const float* x, const float* y, float4 (&s)[2]) {
-  s[0] = s[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int l = 0; l < N; l += 4) {
-    const float4 a[2] = {*reinterpret_cast<const float4*>(x + l), *reinterpret_cast<const float4*>(x + kPitch + l)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 b = *reinterpret_cast<const float4*>(y + (l + e) * kPitch);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float c = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
-        s[i].x = fmaf(c, b.x, s[i].x), s[i].y = fmaf(c, b.y, s[i].y);
-        s[i].z = fmaf(c, b.z, s[i].z), s[i].w = fmaf(c, b.w, s[i].w);
-      }
-    }
-  }
+  for (int i = 0; i < 4; ++i) c[i] *= 1.0f / (kUp * kUp);
 }
-BFP8_DEV float4 negate(float4 v) { return make_float4(-v.x, -v.y, -v.z, -v.w); }
+// A piece written with a sign.
+BFP8_DEV void store_piece(float* at, int lane, const float (&c)[4], float sign) {
+  float* const p = at + (lane >> 2) * kPitch + 2 * (lane & 3);
+  *reinterpret_cast<float2*>(p) = make_float2(sign * c[0], sign * c[1]);
+  *reinterpret_cast<float2*>(p + 8 * kPitch) = make_float2(sign * c[2], sign * c[3]);
+}
 
 // T and P T of one chunk, for up to four value heads of one key head. One product of the K rows
 // and the Q rows with the K rows leaves row i of K K^T and of Q K^T in a lane of tensor memory;
@@ -598,33 +604,31 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
       for (int r = 0; r < 16; ++r) sh.A[(at + r) * kPitch + at + j] = t[r];
     }
     __syncthreads();
+    float c[4];
     {
-      // the two lower blocks of 16 rows, next to the diagonal: 2 x 16 x 4 pieces of 4 columns
-      const int pair = (tid >> 6) & 1, r = (tid >> 2) & 15, c4 = (tid & 3) * 4, a0 = 32 * pair, b0 = a0 + 16;
-      if (tid < 128)
-        *reinterpret_cast<float4*>(sh.Z + (16 * pair + r) * kPitch + c4) =
-            product4<16>(sh.A + (b0 + r) * kPitch + a0, sh.A + a0 * kPitch + a0 + c4);
+      // the two lower blocks of 16 rows, next to the diagonal: four warps, half of one each
+      const int a0 = 32 * (warp >> 1), b0 = a0 + 16, n0 = 8 * (warp & 1);
+      float* const z = sh.Z + 16 * (warp >> 1) * kPitch + n0;
+      if (warp < 4) {
+        small_product<16>(sh.A + b0 * kPitch + a0, sh.A + a0 * kPitch + a0 + n0, lane, c);
+        store_piece(z, lane, c, 1.0f);
+      }
       __syncthreads();
-      if (tid < 128)
-        *reinterpret_cast<float4*>(sh.A + (b0 + r) * kPitch + a0 + c4) =
-            negate(product4<16>(sh.A + (b0 + r) * kPitch + b0, sh.Z + 16 * pair * kPitch + c4));
+      if (warp < 4) {
+        small_product<16>(sh.A + b0 * kPitch + b0, z, lane, c);
+        store_piece(sh.A + b0 * kPitch + a0 + n0, lane, c, -1.0f);
+      }
     }
     __syncthreads();
     {
-      // the lower block of 32 rows: two rows of four columns a thread, of half of the threads
-      const int r = 2 * (tid >> 3), c4 = (tid & 7) * 4;
-      float4 s[2];
-      if (tid < 128) {
-        product2x4<32>(sh.A + (32 + r) * kPitch, sh.A + c4, s);
-        *reinterpret_cast<float4*>(sh.Z + r * kPitch + c4) = s[0];
-        *reinterpret_cast<float4*>(sh.Z + (r + 1) * kPitch + c4) = s[1];
-      }
+      // the lower block of 32 rows: 16 x 8 of it a warp
+      const int r0 = 32 + 16 * (warp >> 2), n0 = 8 * (warp & 3);
+      float* const z = sh.Z + 16 * (warp >> 2) * kPitch + n0;
+      small_product<32>(sh.A + r0 * kPitch, sh.A + n0, lane, c);
+      store_piece(z, lane, c, 1.0f);
       __syncthreads();
-      if (tid < 128) {
-        product2x4<32>(sh.A + (32 + r) * kPitch + 32, sh.Z + c4, s);
-        *reinterpret_cast<float4*>(sh.A + (32 + r) * kPitch + c4) = negate(s[0]);
-        *reinterpret_cast<float4*>(sh.A + (33 + r) * kPitch + c4) = negate(s[1]);
-      }
+      small_product<32>(sh.A + r0 * kPitch + 32, sh.Z + n0, lane, c);
+      store_piece(sh.A + r0 * kPitch + n0, lane, c, -1.0f);
     }
     __syncthreads();
     {
