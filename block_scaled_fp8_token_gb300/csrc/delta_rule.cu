@@ -311,8 +311,8 @@ constexpr int kGroup = 4;                              // value heads a block ta
 struct PrepShared {
   alignas(16) float A[kChunk * kPitch];                // A, zeros from its diagonal on; then block by block T
   float Z[32 * kPitch];
-  float alpha[kGroup][kChunk], beta[kGroup][kChunk], gamma[kGroup][kChunk], rest[kGroup][kChunk];
-  float upper[kGroup][kChunk];                         // alpha_32 .. alpha_i
+  // each token's gates, and the products of alphas from its half's first to it, and behind it
+  float alpha[kGroup][kChunk], beta[kGroup][kChunk], within[kGroup][kChunk], behind[kGroup][kChunk];
   float factor[2 * kChunk], squares[2][2 * kChunk], largest[2][2 * kChunk];
   uint64_t full, gram, product;
   uint32_t tmem;
@@ -446,18 +446,17 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
     tmem_alloc(smem_u32(&sh.tmem), 128);
     tmem_relinquish();
   }
-  // the gates' inputs, of a value head a warp: asked for here, used while the rows' product runs
-  const int gate = warp - 1;
-  uint16_t ga[2] = {}, gb[2] = {};
+  // the gates' inputs, of half of a value head's tokens a warp: asked for here, used while the
+  // rows' product runs
+  const int gate = warp >> 1, token = lane + 32 * (warp & 1);
+  uint16_t ga = 0, gb = 0;
   float rate = 0.0f, dt_bias = 0.0f;
-  if (gate >= 0 && gate < heads) {
+  if (gate < heads) {
     rate = __ldg(p.d.a_log + h0 + gate), dt_bias = __ldg(p.d.dt_bias + h0 + gate);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (lane + 32 * e < n) {
-        ga[e] = *reinterpret_cast<const uint16_t*>(p.d.a + (t0 + lane + 32 * e) * p.d.at + h0 + gate);
-        gb[e] = *reinterpret_cast<const uint16_t*>(p.d.b + (t0 + lane + 32 * e) * p.d.bt + h0 + gate);
-      }
+    if (token < n) {
+      ga = *reinterpret_cast<const uint16_t*>(p.d.a + (t0 + token) * p.d.at + h0 + gate);
+      gb = *reinterpret_cast<const uint16_t*>(p.d.b + (t0 + token) * p.d.bt + h0 + gate);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -521,24 +520,13 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
     }
   }
   __syncwarp();
-  if (gate >= 0 && gate < heads) {
-    rate = expf(rate);
-    float alpha[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int t = lane + 32 * e;
-      alpha[e] = t < n ? expf(log_decay(bf16_bits_to_f32(ga[e]), dt_bias, rate)) : 1.0f;
-      sh.alpha[gate][t] = alpha[e];
-      sh.beta[gate][t] = t < n ? beta_of(bf16_bits_to_f32(gb[e])) : 0.0f;
-    }
-    const float g0 = scan_product(alpha[0], lane), g1 = scan_product(alpha[1], lane);
-    const float all0 = __shfl_sync(0xffffffffu, g0, 31), all1 = __shfl_sync(0xffffffffu, g1, 31);
-    sh.gamma[gate][lane] = g0;
-    sh.gamma[gate][lane + 32] = all0 * g1;
-    sh.rest[gate][lane] = scan_product_behind(alpha[0], lane) * all1;
-    sh.rest[gate][lane + 32] = scan_product_behind(alpha[1], lane);
-    sh.upper[gate][lane] = 1.0f;
-    sh.upper[gate][lane + 32] = g1;
+  if (gate < heads) {
+    const float alpha = token < n ? expf(log_decay(bf16_bits_to_f32(ga), dt_bias, expf(rate))) : 1.0f;
+    const float product = scan_product(alpha, lane);
+    sh.alpha[gate][token] = alpha;
+    sh.beta[gate][token] = token < n ? beta_of(bf16_bits_to_f32(gb)) : 0.0f;
+    sh.within[gate][token] = product;                  // of its half of the chunk
+    sh.behind[gate][token] = scan_product_behind(alpha, lane);
   }
   ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.gram), 0, &sh.abort_flag));
   if (warp == 0) bulk_wait_read_all();                 // the K and Q rows have left shared memory
@@ -556,7 +544,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
       float w[32];
       tmem_ld32(tmem + lanes + 32 * half, w);
       const float c = sh.factor[row], f0 = query ? c * 64.0f : c * sh.beta[g][i];
-      float ratio = half == 0 ? sh.upper[g][i] : 1.0f;   // Gamma_i / Gamma_j
+      float ratio = half == 0 && i >= 32 ? sh.within[g][i] : 1.0f;   // Gamma_i / Gamma_j
 #pragma unroll
       for (int jj = 31; jj >= 0; --jj) {
         const int j = 32 * half + jj;
@@ -648,11 +636,13 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
       }
       float* scalars = reinterpret_cast<float*>(base + kScalars);
       if (tid < kChunk) {
-        const float beta = sh.beta[g][tid], gamma = sh.gamma[g][tid], ck = sh.factor[tid];
+        const float beta = sh.beta[g][tid], ck = sh.factor[tid];
+        const float gamma = (tid >= 32 ? sh.within[g][31] : 1.0f) * sh.within[g][tid];
+        const float rest = sh.behind[g][tid] * (tid >= 32 ? 1.0f : sh.within[g][kChunk - 1]);
         scalars[kBeta + tid] = beta;
         scalars[kKey + tid] = -beta * gamma * ck;
         scalars[kQuery + tid] = gamma * sh.factor[kChunk + tid] * kTScale;
-        scalars[kUpdate + tid] = sh.rest[g][tid] * ck * (1.0f / kTScale);
+        scalars[kUpdate + tid] = rest * ck * (1.0f / kTScale);
         if (tid == kChunk - 1) scalars[kGammaC] = gamma;
       }
       fence_proxy_async_smem();
