@@ -735,6 +735,11 @@ constexpr int kStages = 2;
 constexpr int kValuesAt = kStages * kStageBytes, kTurnedAt = kValuesAt + 2 * kTile, kOutAt = kTurnedAt + 2 * kTile;
 constexpr int kOutPitch = 320;                         // of 64 rows of 128 BF16: two rows' banks apart
 constexpr int kWalkSharedAt = kOutAt + kChunk * kOutPitch;
+// A state on its way from and to memory, in a stage's place: 16 lanes copy 256 bytes of a row, and
+// a lane's own row lies across the banks from its neighbours'. (Lanes that read their own rows
+// from memory, 512 bytes apart, took 11,000 clocks for them.)
+constexpr int kRowPitch = 528;
+static_assert(kD * kRowPitch <= kStageBytes, "a state fits a stage's place");
 // Columns of tensor memory. 16 keys or tokens of one part take 8. The parts of S lie where u K
 // comes (read before they are written anew), those of r where S K^T came, those of u where u
 // came; each warpgroup overwrites only columns that it alone has read.
@@ -766,7 +771,7 @@ struct WalkShared {
   float most[2][2][kD];                                // what each half of a row offers for its power of two
   float power[2][kD];                                  // a chunk's, for its rows of out
   uint64_t full[kStages], empty[kStages], v_full[2], v_empty[2], turned[2], taken[2];
-  uint64_t s_full[2], x_done, r_full[2], u_done, p_full[2], o_done, y_free, new_done, told, out_full, drained;
+  uint64_t s_full[2], x_done, r_full[2], u_done, p_full[2], o_done, y_free, new_done, told, out_full, begun, drained;
   uint32_t tmem;
   int abort_flag;
 };
@@ -822,6 +827,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       mbar_init(smem_u32(&sh.p_full[q]), kRowWarps);
     }
     mbar_init(smem_u32(&sh.told), kRowWarps);
+    mbar_init(smem_u32(&sh.begun), kRowWarps);
     mbar_init(smem_u32(&sh.y_free), kOutWarps);
     mbar_init(smem_u32(&sh.out_full), kOutWarps);
     mbar_init(smem_u32(&sh.x_done), 1);
@@ -961,6 +967,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       pdl_wait();
       while (ok && got < chunks) {
         const int s = got % kStages;
+        if (got == 1 && !wait(sh.begun, 0)) break;     // the state that came through this stage's place is held
         if (!wait(sh.empty[s], ((got / kStages) & 1) ^ 1)) break;
         if (elect_one()) {
           const uint32_t dst = stages + s * kStageBytes, bar = smem_u32(&sh.full[s]);
@@ -1065,7 +1072,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     // where S comes from and goes to: the request's slots, or between the segments
     const float* from = nullptr;
     float* to = nullptr;
-    const int64_t in_row = r * kD + 64 * wg;
+    const int64_t in_row = (r - lane) * kD + 64 * wg + (lane >> 4) * kD + 4 * (lane & 15);   // of two rows a copy
     if (segment == 0) {
       const int64_t slot = slot_of(p.d.req, p.d.req.slots_in, b);
       if (slot >= 0) from = p.d.state + slot * p.d.s_slot + h * p.d.s_head + in_row;
@@ -1079,20 +1086,29 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     } else if (!p.second_walk) {
       to = (map ? p.maps + (between - p.ends) : between) + in_row;
     }
+    const uint32_t own = r * kRowPitch + 256 * wg;     // the thread's piece of its row, and where it copies
+    const uint32_t copy = (r - lane + (lane >> 4)) * kRowPitch + 256 * wg + 16 * (lane & 15);
     float S[64], most = 0.0f;                          // S is the row times `power`
     if (from) {
-      const float4* src = reinterpret_cast<const float4*>(from);
+      const uint32_t at = stages + kStageBytes;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) cp_async16(at + copy + 2 * k * kRowPitch, from + 2 * k * kD);
+      cp_async_wait_all();
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float4 f = src[k];
+        const uint4 w = lds128(at + own + 16 * k);
+        const float4 f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
         S[4 * k] = f.x, S[4 * k + 1] = f.y, S[4 * k + 2] = f.z, S[4 * k + 3] = f.w;
         most = fmaxf(most, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
       }
+      fence_proxy_async_smem();                        // read, before a load writes there
     } else {
 #pragma unroll
       for (int k = 0; k < 64; ++k) S[k] = map && r == 64 * wg + k ? 1.0f : 0.0f;
       if (map) most = 1.0f;
     }
+    tell_bar(sh.begun);
     uint32_t values[16], top = 0;                      // the next chunk's: 32 tokens' BF16, two a word; the largest
     auto load_values = [&](int c) {
       const int left = (c == chunks - 1 ? tail : kChunk) - 32 * wg;
@@ -1252,11 +1268,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       if (more) hand_over(0), hand_over(1);
     }
     if (ok && to) {
+      // through the place of the stage that the last chunk does not have
+      const uint32_t at = stages + (chunks % kStages) * kStageBytes;
       const float back = 1.0f / power;
-      float4* dst = reinterpret_cast<float4*>(to);
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        dst[k] = make_float4(S[4 * k] * back, S[4 * k + 1] * back, S[4 * k + 2] * back, S[4 * k + 3] * back);
+        sts128(at + own + 16 * k, make_uint4(__float_as_uint(S[4 * k] * back), __float_as_uint(S[4 * k + 1] * back),
+                                             __float_as_uint(S[4 * k + 2] * back), __float_as_uint(S[4 * k + 3] * back)));
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint4 w = lds128(at + copy + 2 * k * kRowPitch);
+        *reinterpret_cast<uint4*>(to + 2 * k * kD) = w;
+      }
     }
   }
   if (!ok) {
