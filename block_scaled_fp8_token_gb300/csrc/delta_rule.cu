@@ -223,6 +223,7 @@ struct ChunkParams {
   float* ends;                                         // of each head's segments but the last: the state behind it
   float* maps;                                         // ... and what it makes of the state ahead of it
   int32_t segments, segment_chunks, second_walk;
+  int32_t lead;                                        // the first segment is 1 + lead of the others' chunks long
   uint32_t chunk_blocks;                               // of the first kernel
   int32_t qk_heads, subgroups, per_block;              // value heads a block of the first kernel takes
 };
@@ -719,14 +720,20 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
 // the values' turning (a row of S wants a value's tokens side by side) in two warps. Each product
 // begins on the first half of its operand while the second is cut.
 //
-// Bound by the chain: 4,750 clocks a chunk and block, 2.5 us, one block an SM. The products the
+// Bound by the chain: 4,550 clocks a chunk and block, 2.4 us, one block an SM. The products the
 // chain waits for are 1,410 of them at the tensor cores' rate (64 columns of 128 lanes by 16 take
-// 32 clocks, 128 take 64); reading, cutting and handing over r, u and S are 500, 540 and 1,400,
+// 32 clocks, 128 take 64); reading, cutting and handing over r, u and S are 500, 540 and 1,200,
 // and each hand-over between threads and tensor cores costs 200 to 300 of waiting. On the way,
 // 8192 tokens of 32 heads: 4.7 us a chunk with three BF16 parts a value (the cuts' masks and
 // permutes run at half rate), 3.1 with two F16 parts, 2.5 with the out rows aside and the values
 // turned. Sixteen warps of rows instead of eight: 2.9 us. Out rows by bulk copies of 256 bytes: 80
 // clocks of the issuing warp each, which then was the bound.
+//
+// The sixteen warps' code does not fit what is fetched fast, and the SMs share what feeds it: with
+// the loops below unrolled, 128 blocks that write rows of out took 3.4 us a chunk where 64 took 2.7
+// (2.3 of 10 waiting warps without an instruction, against 0.4). So what the chain does not wait
+// for is rolled (rows of out by 16 tokens, S0 Q^T, T's rows of out, the turning), and a change of a row's power
+// stands apart: 2.85 and 2.55. The chain's own products rolled too cost it 150 clocks each.
 constexpr int kRowWarps = 8, kOutWarps = 4;
 constexpr int kWalkThreads = 32 * (kRowWarps + kOutWarps + 4);   // and a warp of products and one of loads
 constexpr int kBlobAt = kKq;
@@ -765,8 +772,9 @@ BFP8_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
 // from zeros leaves N, and one from the identity, without values, M. The first walk takes the
 // first segment of each head (from the state itself, with its rows of out), and N and M of the
 // others but the last; the states between the segments are then S M + N one behind another; and
-// the second walk takes the other segments from those. That is two segments' time in place of
-// the whole prompt's.
+// the second walk takes the other segments from those. Where the N and M do not all find an SM
+// beside the first segments, they come in waves of shorter segments, and the first ones are as
+// long as the waves. That is two segments' time, or a wave more, in place of the whole prompt's.
 struct WalkShared {
   float most[2][2][kD];                                // what each half of a row offers for its power of two
   float power[2][kD];                                  // a chunk's, for its rows of out
@@ -791,21 +799,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
   if (tid == 0) tma_prefetch_desc(&tv);
   const int pairs = p.d.req.batch * p.d.v_heads, pair = blockIdx.x % pairs, job = blockIdx.x / pairs;
   const int h = pair % p.d.v_heads, b = pair / p.d.v_heads;
-  // the first walk's jobs: N of the segments ahead of the last (the first one's with its rows of
-  // out), then M of those behind the first; the second's: the segments behind the first
-  const bool map = !p.second_walk && p.segments > 1 && job >= p.segments - 1;
-  const int segment = p.second_walk ? job + 1 : map ? job - (p.segments - 2) : job;
+  // the first walk's jobs: the first segment with its rows of out, then N and M of each other but
+  // the last (which so read the same chunks at about a time); the second's: the others
+  const bool map = !p.second_walk && job && !(job & 1);
+  const int segment = p.second_walk ? job + 1 : (job + 1) >> 1;
   const bool rows_out = p.second_walk || segment == 0;
   int64_t first;
   int64_t len = chunked_len(p.d, b, first);
   const int64_t segment_tokens = static_cast<int64_t>(p.segment_chunks) << kShift;
-  const bool last = len <= (segment + 1) * segment_tokens;
-  if (len <= segment * segment_tokens || (last && !rows_out)) {
+  const int begin = segment ? segment + p.lead : 0;    // in segments' lengths
+  const bool last = len <= (segment + p.lead + 1) * segment_tokens;
+  if (len <= begin * segment_tokens || (last && !rows_out)) {
     pdl_wait();                                        // nothing behind this grid runs ahead of the one before it
     return;
   }
-  first += segment * segment_tokens;
-  len = last ? len - segment * segment_tokens : segment_tokens;
+  first += begin * segment_tokens;
+  len = last ? len - begin * segment_tokens : (segment + p.lead + 1 - begin) * segment_tokens;
   float* const between = p.ends + (static_cast<int64_t>(pair) * (p.segments - 1) + segment) * (kD * kD);
   const int chunks = static_cast<int>((len + kChunk - 1) >> kShift);
   const int tail = static_cast<int>(len - (static_cast<int64_t>(chunks - 1) << kShift));
@@ -870,6 +879,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         const uint32_t at = stages + s * kStageBytes;
         const uint64_t dk = smem_desc_sw128(at), dt = smem_desc_sw128(at + kBlobAt), dn = smem_desc_sw128_mn(at, kTile);
         if (!wait(sh.full[s], (c / kStages) & 1)) break;
+#pragma unroll
         for (int q = 0; q < 2; ++q) {                  // 32 keys of each warpgroup's
           if (!wait(sh.s_full[q], c & 1)) break;
           tc_fence_after();
@@ -889,14 +899,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         if (!ok || (rows_out && !wait(sh.y_free, (c & 1) ^ 1))) break;
         tc_fence_after();
         if (rows_out && elect_one()) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_f16_ts(tmem + kColY, tmem + col_s(part, k), dk + ((kHalfTile + (k >> 2) * kTile) >> 4) + 2 * (k & 3),
-                          kN64, part || k);
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ts(tmem + kColY, tmem + col_s(i >> 1, 4 * (i & 1) + k),
+                          dk + ((kHalfTile + (i & 1) * kTile) >> 4) + 2 * k, kN64, i || k);
         }
         __syncwarp();
+#pragma unroll
         for (int q = 0; q < 2; ++q) {                  // 16 tokens of each warpgroup's
           if (!wait(sh.r_full[q], c & 1)) break;
           tc_fence_after();
@@ -906,24 +917,27 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
 #pragma unroll
               for (int t = 0; t < 2 - a; ++t)
 #pragma unroll
-                for (int k = q; k < 4; k += 2)
-                  umma_f16_ts(tmem + kColU, tmem + col_r(a, k), dt + t * (kTile >> 4) + 2 * k, kN64, q || a || t || k > 1);
+                for (int e = 0; e < 2; ++e) {
+                  const int k = q + 2 * e;
+                  umma_f16_ts(tmem + kColU, tmem + col_r(a, k), dt + t * (kTile >> 4) + 2 * k, kN64, q || a || t || e);
+                }
             if (q == 1) umma_commit(smem_u32(&sh.u_done));
           }
           __syncwarp();
         }
         if (!ok) break;
         if (rows_out && elect_one()) {
+#pragma unroll 1
+          for (int i = 0; i < 3; ++i) {
+            const int a = i >> 1, t = i & 1;
 #pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int t = 0; t < 2 - a; ++t)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_f16_ts(tmem + kColO, tmem + col_r(a, k), dt + ((kHalfTile + t * kTile) >> 4) + 2 * k, kN64, a || t || k);
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ts(tmem + kColO, tmem + col_r(a, k), dt + ((kHalfTile + t * kTile) >> 4) + 2 * k, kN64, i || k);
+          }
           umma_commit(smem_u32(&sh.o_done));
         }
         __syncwarp();
+#pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (!wait(sh.p_full[q], c & 1)) break;
           tc_fence_after();
@@ -931,8 +945,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int k = q; k < 4; k += 2)           // 16 tokens a step: 16 rows of 128 bytes
-                umma_f16_ts(tmem + kColNew, tmem + col_u(part, k), dn + 128 * k, kKeys, q || part || k > 1);
+              for (int e = 0; e < 2; ++e) {            // 16 tokens a step: 16 rows of 128 bytes
+                const int k = q + 2 * e;
+                umma_f16_ts(tmem + kColNew, tmem + col_u(part, k), dn + 128 * k, kKeys, q || part || e);
+              }
             if (q == 1) {
               umma_commit(smem_u32(&sh.new_done));
               umma_commit(smem_u32(&sh.empty[s]));
@@ -950,7 +966,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       }
     } else if (warp == kMmaWarp + 1) {
       // ---------------------------------------------- loads, a chunk ahead; values two
-      const int64_t key = tile_key(p.d.req, b, kShift) + static_cast<int64_t>(segment) * p.segment_chunks;
+      const int64_t key = tile_key(p.d.req, b, kShift) + static_cast<int64_t>(begin) * p.segment_chunks;
       int got = 0, values = map ? chunks : 0;          // chunks asked for; a map has no values
       auto load_values = [&]() {
         const int s = values % 2;
@@ -994,9 +1010,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         // a lane's row of the four 8 x 8 pieces that the warp turns at once: 32 tokens of 8 values
         const uint32_t src = stages + kValuesAt + (c & 1) * kTile + half * kHalfTile + lane * 128;
         const uint32_t dst = stages + kTurnedAt + (c & 1) * kTile + (64 * half + (lane >> 2)) * 128 + (lane & 3) * 4;
-#pragma unroll
+#pragma unroll 1
         for (int g = 0; g < 2; ++g)
-#pragma unroll
+#pragma unroll 2
           for (int v = 0; v < 8; ++v) {
             uint32_t w[4];
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -1025,37 +1041,39 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       tc_fence_after();
       const float back = p.d.scale * (1.0f / kTScale) / sh.power[c & 1][r];
       const float2 back2 = make_float2(back, back);
-      uint32_t v[32];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float q[32], o[32];
-        tmem_ld32(mine + kColY + 32 * g, q);
-        tmem_ld32(mine + kColO + 32 * g, o);
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float2 f = *reinterpret_cast<const float2*>(scalars + kQuery + 32 * g + j);
-          const float2 w = __fmul2_rn(__ffma2_rn(f, make_float2(q[j], q[j + 1]), make_float2(o[j], o[j + 1])), back2);
-          v[16 * g + j / 2] = pack_bf16x2(w.x, w.y);
-        }
-      }
-      tc_fence_before();
-      tell_bar(sh.y_free);
-      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
       // two values of one token make a word: even lanes have the pair's even tokens, odd ones the odd
       const uint32_t at = stages + kOutAt + (odd ? kOutPitch : 0) + (r & ~1) * 2;
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        uint32_t q[16], o[16], v[8];
+        tmem_ld16(mine + kColY + 16 * g, q);
+        tmem_ld16(mine + kColO + 16 * g, o);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t w = __shfl_xor_sync(0xffffffffu, v[j], 1);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 2 * j * kOutPitch),
-                     "r"(odd ? __byte_perm(w, v[j], 0x7632) : __byte_perm(v[j], w, 0x5410))
-                     : "memory");
+        for (int j = 0; j < 16; j += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(scalars + kQuery + 16 * g + j);
+          const float2 w = __fmul2_rn(__ffma2_rn(f, make_float2(__uint_as_float(q[j]), __uint_as_float(q[j + 1])),
+                                                 make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1]))), back2);
+          v[j / 2] = pack_bf16x2(w.x, w.y);
+        }
+        if (g == 3) {
+          tc_fence_before();
+          tell_bar(sh.y_free);
+          if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w = __shfl_xor_sync(0xffffffffu, v[j], 1);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + (16 * g + 2 * j) * kOutPitch),
+                       "r"(odd ? __byte_perm(w, v[j], 0x7632) : __byte_perm(v[j], w, 0x5410))
+                       : "memory");
+        }
       }
       tell_bar(sh.out_full);
       if (!wait(sh.out_full, 0)) break;
       // a row of 256 bytes to 16 lanes
       const int n = c == chunks - 1 ? tail : kChunk;
       __nv_bfloat16* out = p.d.out + (first + static_cast<int64_t>(c) * kChunk) * p.d.ot + h * p.d.oh + (lane & 15) * 8;
-#pragma unroll
+#pragma unroll 4
       for (int e = 0; e < 8; ++e) {
         const int t = 8 * e + 2 * (warp & 3) + (lane >> 4);
         const uint4 w = lds128(stages + kOutAt + t * kOutPitch + (lane & 15) * 16);
@@ -1159,8 +1177,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     float power = first_most > 0.0f ? power_for(first_most, 2) : 1.0f;
 #pragma unroll
     for (int k = 0; k < 64; ++k) S[k] *= power;
-    if (ok) hand_over(0), hand_over(1);
     for (int c = 0; ok && c < chunks; ++c) {
+      hand_over(0);
+      hand_over(1);
       const int s = c % kStages;
       const bool more = c + 1 < chunks;
       const float* scalars = reinterpret_cast<const float*>(base + s * kStageBytes + kBlobAt + kScalars);
@@ -1249,7 +1268,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         step[1] = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
         power = next;
       }
-      const bool rescale = __any_sync(0xffffffffu, step[0] != 1.0f || step[1] != 1.0f);
       const float2 keep = make_float2(gamma, gamma);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -1257,15 +1275,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         tmem_ld32(mine + kColNew + 64 * wg + 32 * q, d);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          float2 f = __ffma2_rn(keep, make_float2(S[32 * q + k], S[32 * q + k + 1]), make_float2(d[k], d[k + 1]));
-          if (rescale) {
-            f.x = f.x * step[0] * step[1];
-            f.y = f.y * step[0] * step[1];
-          }
+          const float2 f = __ffma2_rn(keep, make_float2(S[32 * q + k], S[32 * q + k + 1]), make_float2(d[k], d[k + 1]));
           S[32 * q + k] = f.x, S[32 * q + k + 1] = f.y;
         }
       }
-      if (more) hand_over(0), hand_over(1);
+      if (__any_sync(0xffffffffu, step[0] != 1.0f || step[1] != 1.0f)) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) S[k] = S[k] * step[0] * step[1];
+      }
     }
     if (ok && to) {
       // through the place of the stage that the last chunk does not have
@@ -1296,12 +1313,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
 }
 
 // The states between a head's segments, one behind another: the end of each but the first is its
-// N and becomes S M + N. A warp has two rows of S; a block copies a map at a time to shared
+// N and becomes S M + N. A warp has four rows of S; a block copies a map at a time to shared
 // memory, the next one while it multiplies where there is a next one.
-constexpr int kJoinThreads = 256, kJoinRows = 2 * kJoinThreads / 32, kMapBytes = kD * kD * 4;
+constexpr int kJoinThreads = 256, kJoinRows = 4 * kJoinThreads / 32, kMapBytes = kD * kD * 4;
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(16) float2 S[kD][kJoinThreads / 32];   // of a key, each warp's two rows
+  __shared__ float4 S[kD][kJoinThreads / 32];          // of a key, each warp's rows
   __shared__ uint64_t full[2];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1318,10 +1335,10 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkPar
   const int pair = blockIdx.x / kParts, b = pair / p.d.v_heads;
   int64_t first;
   const int64_t len = chunked_len(p.d, b, first), segment_tokens = static_cast<int64_t>(p.segment_chunks) << kShift;
-  const int n = static_cast<int>((len + segment_tokens - 1) / segment_tokens);   // segments; maps 1 .. n - 2
+  const int n = static_cast<int>((len + segment_tokens - 1) / segment_tokens) - p.lead;   // segments; maps 1 .. n - 2
   if (n <= 2) return;
   const int64_t at = static_cast<int64_t>(pair) * (p.segments - 1) * (kD * kD);
-  const int row = (blockIdx.x % kParts) * kJoinRows + 2 * warp;
+  const int row = (blockIdx.x % kParts) * kJoinRows + 4 * warp;
   float* const ends = p.ends + at + row * kD + 4 * lane;
   const int ahead = p.segments > 3 ? 2 : 1;            // maps that the shared memory holds
   auto ask = [&](int g) {
@@ -1332,18 +1349,19 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkPar
   };
   __syncthreads();
   for (int g = 1; g <= ahead; ++g) ask(g);
-  float4 s[2] = {*reinterpret_cast<const float4*>(ends), *reinterpret_cast<const float4*>(ends + kD)};
+  float4 s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const float4*>(ends + i * kD);
   bool ok = true;
   for (int g = 1; ok && g <= n - 2; ++g) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      S[4 * lane + e][warp] = e == 0   ? make_float2(s[0].x, s[1].x)
-                              : e == 1 ? make_float2(s[0].y, s[1].y)
-                              : e == 2 ? make_float2(s[0].z, s[1].z)
-                                       : make_float2(s[0].w, s[1].w);
+    S[4 * lane][warp] = make_float4(s[0].x, s[1].x, s[2].x, s[3].x);
+    S[4 * lane + 1][warp] = make_float4(s[0].y, s[1].y, s[2].y, s[3].y);
+    S[4 * lane + 2][warp] = make_float4(s[0].z, s[1].z, s[2].z, s[3].z);
+    S[4 * lane + 3][warp] = make_float4(s[0].w, s[1].w, s[2].w, s[3].w);
     __syncwarp();
     float* const end = ends + g * (kD * kD);
-    s[0] = *reinterpret_cast<const float4*>(end), s[1] = *reinterpret_cast<const float4*>(end + kD);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const float4*>(end + i * kD);
     ok = __syncthreads_and(mbar_wait(smem_u32(&full[(g - 1) % ahead]), (g - 1) / ahead & 1, &abort_flag));
     if (!ok) break;
     const uint32_t map = ring + (g - 1) % ahead * kMapBytes + lane * 16;
@@ -1351,40 +1369,52 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkPar
     for (int l = 0; l < kD; ++l) {
       const uint4 w = lds128(map + l * (kD * 4));
       const float4 m = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-      const float2 c = S[l][warp];
-      s[0].x = fmaf(c.x, m.x, s[0].x), s[0].y = fmaf(c.x, m.y, s[0].y), s[0].z = fmaf(c.x, m.z, s[0].z), s[0].w = fmaf(c.x, m.w, s[0].w);
-      s[1].x = fmaf(c.y, m.x, s[1].x), s[1].y = fmaf(c.y, m.y, s[1].y), s[1].z = fmaf(c.y, m.z, s[1].z), s[1].w = fmaf(c.y, m.w, s[1].w);
+      const float4 c = S[l][warp];
+      const float row[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[i].x = fmaf(row[i], m.x, s[i].x), s[i].y = fmaf(row[i], m.y, s[i].y), s[i].z = fmaf(row[i], m.z, s[i].z),
+        s[i].w = fmaf(row[i], m.w, s[i].w);
     }
-    *reinterpret_cast<float4*>(end) = s[0], *reinterpret_cast<float4*>(end + kD) = s[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(end + i * kD) = s[i];
     __syncthreads();                                   // the map's place is free
     ask(g + ahead);
   }
   if (!ok && threadIdx.x == 0) atomicExch(&g_delta_err, static_cast<int>(BFP8_ERR_TIMEOUT));
 }
 
-// How many segments the longest request's chunks are walked in: the count with the least time,
-// in tenths of a microsecond, of those whose first walk fits the GPU at once (one block an SM).
-// A chunk takes 2.5 us; a join 3 us; the two launches and the blocks' beginnings 18 us.
-constexpr int kMostSegments = 16;
 int64_t longest_chunks(int64_t tokens, int64_t max_q_len) {
   return ((max_q_len < tokens ? max_q_len : tokens) + kChunk - 1) / kChunk;
 }
-int segment_count(int64_t chunks, int64_t pairs, int sms) {
-  int best = 1;
+
+// How the longest request's chunks are walked in segments: the count with the least time, in
+// tenths of a microsecond. A chunk takes 2.5 us; a join 4.5 us; the two launches and the blocks'
+// beginnings 18 us, and 5 us those of a further wave, of the first walk or the second.
+constexpr int kMostSegments = 16, kMostWaves = 4;
+struct Split {
+  int segments, lead;
+};
+Split split_walk(int64_t chunks, int64_t pairs, int sms) {
+  Split best{1, 0};
   int64_t least = 25 * chunks;
-  for (int n = 3; n <= kMostSegments && pairs * (2 * n - 3) <= sms; ++n) {
-    const int64_t time = 2 * 25 * ((chunks + n - 1) / n) + 30 * (n - 2) + 180;
-    if (time < least) least = time, best = n;
+  for (int n = 3; n <= kMostSegments && pairs < sms; ++n) {
+    const int64_t beside = sms - pairs, waves = (2 * pairs * (n - 2) + beside - 1) / beside;
+    if (waves > kMostWaves) break;
+    const int64_t all = waves + (pairs * (n - 1) + sms - 1) / sms;
+    const int64_t time = 25 * all * ((chunks + n + waves - 2) / (n + waves - 1)) + 45 * (n - 2) + 50 * (all - 2) + 180;
+    if (time < least) least = time, best = {n, static_cast<int>(waves - 1)};
   }
   return best;
 }
 
 // Where no request has more new tokens than this, each takes them one after the other. Of 48
-// heads, 24 / 32 tokens against one chunk of the chunks' kernels: one request 12 / 15 and 21 us,
-// 16 requests 82 / 107 and 107, 64 requests 302 / 395 and 346.
-constexpr int64_t kStepTokens = 28;
+// heads, 16 / 24 / 32 tokens one after the other against the chunks' kernels: one request 9.0,
+// 11.9, 14.9 and 14.6 us; 4 requests 21, 29, 38 and 27; 16 requests 57, 82, 107 and 82; 64 requests
+// 206, 302, 395 and 268. They meet between 20 and 24 but for few heads, which lose 3 us.
+constexpr int64_t kStepTokens = 20;
 // Beside longer ones, which run the chunks' kernels anyway, up to this many do: requests of 1 to
-// 141 tokens (12, of 48 heads) take 53.8, 52.4, 53.9 and 53.9 us with 8, 12, 16 and 24.
+// 141 tokens (12, of 48 heads) take 49.2, 47.5, 47.8, 47.3 and 50.2 us with 2, 4, 8, 12 and 20.
 constexpr int64_t kStepTokensBeside = 12;
 static_assert(kStepTokens <= kMostSteps, "a request's steps fit shared memory");
 
@@ -1400,9 +1430,9 @@ bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
 }  // namespace
 
-// The chunks' part of the workspace, and behind it the states between segments: as a first walk
-// of n segments has 2 n - 3 blocks a head and at most one an SM, an end and a map for each SM
-// hold them.
+// The chunks' part of the workspace, and behind it the states between segments: n - 1 ends and
+// maps a head. As 2 (n - 2) blocks a head fit the waves that the SMs beside the first segments
+// take, they are fewer than half the waves' for each SM.
 size_t chunk_bytes(int64_t batch, int64_t tokens, int64_t qk_heads, int64_t v_heads) {
   const size_t n = static_cast<size_t>(chunk_slots(batch, tokens)) *
                    (static_cast<size_t>(qk_heads) * kKq + static_cast<size_t>(v_heads) * kBlob);
@@ -1411,8 +1441,8 @@ size_t chunk_bytes(int64_t batch, int64_t tokens, int64_t qk_heads, int64_t v_he
 size_t delta_rule_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q_len, int64_t qk_heads,
                                   int64_t v_heads, int sms) {
   if (max_q_len <= kStepTokens) return 0;
-  const size_t between = segment_count(longest_chunks(tokens, max_q_len), 1, sms) > 1
-                             ? static_cast<size_t>(sms) * 2 * kD * kD * sizeof(float)
+  const size_t between = split_walk(longest_chunks(tokens, max_q_len), 1, sms).segments > 1
+                             ? static_cast<size_t>(sms) * kMostWaves * kD * kD * sizeof(float)
                              : 0;
   return chunk_bytes(batch, tokens, qk_heads, v_heads) + between;
 }
@@ -1503,10 +1533,12 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
                         kPrepThreads, kPrepSmem, st, tq, tk, cp);
   if (rc != BFP8_OK) return rc;
   const int64_t chunks = longest_chunks(a.tokens, a.max_q_len), pairs = a.batch * a.v_heads;
-  cp.segments = segment_count(chunks, pairs, sms);
-  cp.segment_chunks = static_cast<int32_t>((chunks + cp.segments - 1) / cp.segments);
+  const Split split = split_walk(chunks, pairs, sms);
+  cp.segments = split.segments;
+  cp.lead = split.lead;
+  cp.segment_chunks = static_cast<int32_t>((chunks + cp.segments + cp.lead - 1) / (cp.segments + cp.lead));
   cp.ends = reinterpret_cast<float*>(cp.ws + chunk_bytes(a.batch, a.tokens, a.qk_heads, a.v_heads));
-  cp.maps = cp.ends + static_cast<int64_t>(sms) * kD * kD;
+  cp.maps = cp.ends + static_cast<int64_t>(sms) * (kMostWaves / 2) * kD * kD;
   const int jobs = cp.segments > 1 ? 2 * cp.segments - 3 : 1;
   rc = launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * jobs)), kWalkThreads, kWalkSmem, st, tv, cp);
   if (rc != BFP8_OK || cp.segments == 1) return rc;

@@ -747,7 +747,7 @@ int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream);
  *   u = beta * (v - alpha * S k'),  S <- alpha * S + u k'^T,  out = S q'
  * State, sums and gates are float32; out is rounded to BF16 once. One ragged call
  * serves single tokens, drafted ones, and prompts. max_q_len and a request's own
- * length choose between two ways for it: a token after the other (up to 28 tokens; up
+ * length choose between two ways for it: a token after the other (up to 20 tokens; up
  * to 12 where max_q_len is larger), or by chunks of 64, whose products carry a row of S,
  * and the values that meet it, to 2^-22 of the largest among them in a chunk. Long
  * prompts of few heads (batch * v_heads) are walked in segments at once.

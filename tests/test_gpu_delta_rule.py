@@ -4,9 +4,9 @@ Tolerances. One token adds to a row of the state an error of at most c (1 + |g|)
 gate's logarithm is a handful of rounded steps (alpha's error is 8 |g| 2^-24 and the exponential's), key and query
 are normed within 16 2^-24, a product with the state sums 128 terms in chains and trees of at most 16 roundings, and
 beta, u and the update are 8 more; c = 64 counts each twice. Requests of many tokens go through chunks of 64, whose
-sums run over 64 to 128 terms in the tensor cores (each truncated to FP32, 2^-23) with operands split into three
-BF16 parts (2^-24), three such products one behind another, and the decay of a chunk in place of a token's: c = 512
-counts 128 terms of 2^-23 twice. The oracle's `grown` carries such errors through the recurrence, which lengthens
+sums run over 64 to 128 terms in the tensor cores (each truncated to FP32, 2^-23) with operands split into two F16
+parts (2^-22), three such products one behind another, and the decay of a chunk in place of a token's: c = 512 counts
+128 terms of 2^-23 twice, and the operands' three times 4 2^-24 within that. The oracle's `grown` carries such errors through the recurrence, which lengthens
 none; the output adds the product with the query (|q'| = scale) and half a BF16 step, 2^-8.
 """
 
@@ -78,6 +78,13 @@ def test_prompts_match_oracle(bfp8, cuda_device, lens, hk, hv):
 def test_long_prompts_match_oracle(bfp8, cuda_device, lens, hk, hv, decay):
     """Prompts of few heads, whose chunks are walked in segments at once and joined; short ones beside them."""
     t = delta_inputs(cuda_device, lens, hk, hv, 19 * hv + sum(lens), extra=1, decay=decay)
+    _check(t, lens, _run(bfp8, t, lens))
+
+
+@pytest.mark.parametrize("lens,hk,hv", [([64 * 36 - 5], 16, 64), ([64 * 35 + 1], 9, 72), ([64 * 50, 64 * 11 + 3], 2, 20), ([3300], 4, 40)], ids=str)
+def test_long_prompts_of_many_heads_match_oracle(bfp8, cuda_device, lens, hk, hv):
+    """Segments that come in waves, the first one longer than the others; one request ends inside its first."""
+    t = delta_inputs(cuda_device, lens, hk, hv, 29 * hv + sum(lens), extra=1, decay=0.1)
     _check(t, lens, _run(bfp8, t, lens))
 
 
