@@ -307,20 +307,20 @@ BFP8_DEV void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32
 }
 
 constexpr int kPrepThreads = 256;
-constexpr int kPitch = 68;                             // floats of a row of A, T or Z
+constexpr int kPitch = 68, kPitchZ = 36;               // floats of a row of A or T, and of Z
 constexpr int kGroup = 4;                              // value heads a block takes, at most
 struct PrepShared {
   alignas(16) float A[kChunk * kPitch];                // A, zeros from its diagonal on; then block by block T
-  float Z[32 * kPitch];
   // each token's gates, and the products of alphas from its half's first to it, and behind it
   float alpha[kGroup][kChunk], beta[kGroup][kChunk], within[kGroup][kChunk], behind[kGroup][kChunk];
-  float factor[2 * kChunk], squares[2][2 * kChunk], largest[2][2 * kChunk];
+  float factor[2 * kChunk];
   uint64_t full, gram, product;
   uint32_t tmem;
   int abort_flag;
 };
-constexpr int kPrepSharedAt = (kBlob + 1023) / 1024 * 1024;   // the blob takes the K and Q rows' place
-constexpr int kPrepSmem = 1024 + kPrepSharedAt + static_cast<int>(sizeof(PrepShared));
+constexpr int kPrepSharedAt = (kBlob + 15) / 16 * 16;   // the blob takes the K and Q rows' place
+constexpr int kPrepSmem = kPrepSharedAt + static_cast<int>(sizeof(PrepShared));
+static_assert(4 * (kPrepSmem + 1024) <= 228 * 1024 && 32 * kPitchZ * 4 <= kHalfTile, "four blocks an SM; Z in T's place");
 static_assert(sizeof(StepShared<kPrepThreads / 32>) <= kPrepSharedAt, "the steps' rows fit the blob's place");
 
 // Running products over the warp, of 32 values from the first to each lane's.
@@ -344,13 +344,13 @@ BFP8_DEV float scan_product_behind(float v, int lane) {
   return r;
 }
 
-// A warp's 16 x 8 piece of X (16 x K) Y (K x 8), all FP32 in shared memory with pitch kPitch: lane
+// A warp's 16 x 8 piece of X (16 x K) Y (K x 8), all FP32 in shared memory, Y with rows PY apart: lane
 // l has columns 2 (l % 4) and one more of rows l / 4 and l / 4 + 8. The operands are cut into two
 // F16 parts; none exceeds 32 (a row of A by a column of T1), so that 2^8 of them stay in range,
 // and the rests' smallest step is 2^-33. (On CUDA cores the two products of the 32-row block took
 // 2,400 clocks, most of them reading shared memory; so they take 700. tcgen05 has no shape
 // this small.)
-template <int K>
+template <int K, int PY = kPitch>
 BFP8_DEV void small_product(const float* x, const float* y, int lane, float (&c)[4]) {
   constexpr float kUp = 256.0f;
   const int g = lane >> 2, t = lane & 3;
@@ -365,8 +365,8 @@ BFP8_DEV void small_product(const float* x, const float* y, int lane, float (&c)
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float* f = y + (k + 2 * t + 8 * i) * kPitch + g;
-      split2(make_float2(f[0] * kUp, f[kPitch] * kUp), b[0][i], b[1][i]);
+      const float* f = y + (k + 2 * t + 8 * i) * PY + g;
+      split2(make_float2(f[0] * kUp, f[PY] * kUp), b[0][i], b[1][i]);
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p) {                      // rests by rests left out
@@ -382,10 +382,11 @@ BFP8_DEV void small_product(const float* x, const float* y, int lane, float (&c)
   for (int i = 0; i < 4; ++i) c[i] *= 1.0f / (kUp * kUp);
 }
 // A piece written with a sign.
+template <int P = kPitch>
 BFP8_DEV void store_piece(float* at, int lane, const float (&c)[4], float sign) {
-  float* const p = at + (lane >> 2) * kPitch + 2 * (lane & 3);
+  float* const p = at + (lane >> 2) * P + 2 * (lane & 3);
   *reinterpret_cast<float2*>(p) = make_float2(sign * c[0], sign * c[1]);
-  *reinterpret_cast<float2*>(p + 8 * kPitch) = make_float2(sign * c[2], sign * c[3]);
+  *reinterpret_cast<float2*>(p + 8 * P) = make_float2(sign * c[2], sign * c[3]);
 }
 
 // T and P T of one chunk, for up to four value heads of one key head. One product of the K rows
@@ -396,14 +397,15 @@ BFP8_DEV void store_piece(float* at, int lane, const float (&c)[4], float sign) 
 // token after the other, which so run beside the long ones' chunks (as its first blocks they kept
 // the chunks waiting: 81 us against 60 for 12 requests of 1 to 141 tokens and 48 heads).
 //
-// Bound by latency: a block passes a dozen barriers, and three to an SM issue in 42% of the clocks.
-// 129 chunks of 16 key and 32 value heads take 102 us (138 with a thread a row solving against A
-// from registers, whose unrolled code stalled on instruction fetches; 214 with one block an SM).
-__global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __grid_constant__ CUtensorMap tq,
+// Bound by latency: a block passes a dozen barriers, and four to an SM issue in 53% of the clocks.
+// 129 chunks of 16 key and 32 value heads take 88 us (94 with three to an SM, 214 with one; 138
+// with a thread a row solving against A from registers, whose unrolled code stalled on instruction
+// fetches).
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(const __grid_constant__ CUtensorMap tq,
                                                                      const __grid_constant__ CUtensorMap tk,
                                                                      const ChunkParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* const base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t prepare_smem[];
+  uint8_t* const base = prepare_smem;
   PrepShared& sh = *reinterpret_cast<PrepShared*>(base + kPrepSharedAt);
   const uint32_t kq = smem_u32(base), blob = kq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -484,13 +486,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
       m = max_abs_bf16x2(max_abs_bf16x2(m, raw[v].x), raw[v].y);
       m = max_abs_bf16x2(max_abs_bf16x2(m, raw[v].z), raw[v].w);
     }
-    sh.squares[half][row] = ss.x + ss.y;
-    sh.largest[half][row] = max_bf16x2(m);
+    float* const squares = sh.A;                       // of each half of a row, and the largest behind them
+    float* const largest = sh.A + 4 * kChunk;
+    squares[half * 2 * kChunk + row] = ss.x + ss.y;
+    largest[half * 2 * kChunk + row] = max_bf16x2(m);
     __syncthreads();
-    const float top = fmaxf(sh.largest[0][row], sh.largest[1][row]);
+    const float top = fmaxf(largest[row], largest[2 * kChunk + row]);
     const float to_one = top > 0.0f ? power_for(top, 0) : 1.0f;
     // rsqrt and the power taken back, in an order that does not overflow with it
-    const float c = i < n ? rsqrtf(sh.squares[0][row] + sh.squares[1][row] + p.d.eps) / to_one : 0.0f;
+    const float c = i < n ? rsqrtf(squares[row] + squares[2 * kChunk + row] + p.d.eps) / to_one : 0.0f;
     if (half == 0) sh.factor[row] = c;
     const float2 s2 = make_float2(to_one, to_one);
 #pragma unroll
@@ -594,17 +598,18 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
     }
     __syncthreads();
     float c[4];
+    float* const Z = reinterpret_cast<float*>(base);   // where T's parts will be
     {
       // the two lower blocks of 16 rows, next to the diagonal: four warps, half of one each
       const int a0 = 32 * (warp >> 1), b0 = a0 + 16, n0 = 8 * (warp & 1);
-      float* const z = sh.Z + 16 * (warp >> 1) * kPitch + n0;
+      float* const z = Z + 16 * (warp >> 1) * kPitchZ + n0;
       if (warp < 4) {
         small_product<16>(sh.A + b0 * kPitch + a0, sh.A + a0 * kPitch + a0 + n0, lane, c);
-        store_piece(z, lane, c, 1.0f);
+        store_piece<kPitchZ>(z, lane, c, 1.0f);
       }
       __syncthreads();
       if (warp < 4) {
-        small_product<16>(sh.A + b0 * kPitch + b0, z, lane, c);
+        small_product<16, kPitchZ>(sh.A + b0 * kPitch + b0, z, lane, c);
         store_piece(sh.A + b0 * kPitch + a0 + n0, lane, c, -1.0f);
       }
     }
@@ -612,11 +617,11 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const __
     {
       // the lower block of 32 rows: 16 x 8 of it a warp
       const int r0 = 32 + 16 * (warp >> 2), n0 = 8 * (warp & 3);
-      float* const z = sh.Z + 16 * (warp >> 2) * kPitch + n0;
+      float* const z = Z + 16 * (warp >> 2) * kPitchZ + n0;
       small_product<32>(sh.A + r0 * kPitch, sh.A + n0, lane, c);
-      store_piece(z, lane, c, 1.0f);
+      store_piece<kPitchZ>(z, lane, c, 1.0f);
       __syncthreads();
-      small_product<32>(sh.A + r0 * kPitch + 32, sh.Z + n0, lane, c);
+      small_product<32, kPitchZ>(sh.A + r0 * kPitch + 32, Z + n0, lane, c);
       store_piece(sh.A + r0 * kPitch + n0, lane, c, -1.0f);
     }
     __syncthreads();
@@ -1360,8 +1365,12 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkPar
     S[4 * lane + 3][warp] = make_float4(s[0].w, s[1].w, s[2].w, s[3].w);
     __syncwarp();
     float* const end = ends + g * (kD * kD);
+    float4 n4[4];                                      // N, added behind the product
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const float4*>(end + i * kD);
+    for (int i = 0; i < 4; ++i) {
+      s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      n4[i] = *reinterpret_cast<const float4*>(end + i * kD);
+    }
     ok = __syncthreads_and(mbar_wait(smem_u32(&full[(g - 1) % ahead]), (g - 1) / ahead & 1, &abort_flag));
     if (!ok) break;
     const uint32_t map = ring + (g - 1) % ahead * kMapBytes + lane * 16;
@@ -1372,12 +1381,18 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const ChunkPar
       const float4 c = S[l][warp];
       const float row[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s[i].x = fmaf(row[i], m.x, s[i].x), s[i].y = fmaf(row[i], m.y, s[i].y), s[i].z = fmaf(row[i], m.z, s[i].z),
-        s[i].w = fmaf(row[i], m.w, s[i].w);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = make_float2(row[i], row[i]);
+        const float2 lo = __ffma2_rn(f, make_float2(m.x, m.y), make_float2(s[i].x, s[i].y));
+        const float2 hi = __ffma2_rn(f, make_float2(m.z, m.w), make_float2(s[i].z, s[i].w));
+        s[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(end + i * kD) = s[i];
+    for (int i = 0; i < 4; ++i) {
+      s[i] = make_float4(s[i].x + n4[i].x, s[i].y + n4[i].y, s[i].z + n4[i].z, s[i].w + n4[i].w);
+      *reinterpret_cast<float4*>(end + i * kD) = s[i];
+    }
     __syncthreads();                                   // the map's place is free
     ask(g + ahead);
   }
@@ -1519,13 +1534,13 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   if (rc != BFP8_OK) return rc;
   // Value heads of one key head share a block, which norms and multiplies their rows once (14,000
   // of its 24,500 clocks for one head), unless the blocks of one head each fit the GPU at once,
-  // three to an SM. (Requests of 1 to 141 tokens, 48 heads on 16: 52 us shared, 57 us apart.)
+  // four to an SM. (4 requests of 128 tokens, 48 heads: 39 us apart, 42.7 shared. Requests of 1 to 141 tokens, 48 heads on 16: 52 us shared, 57 us apart.)
   ChunkParams cp{};
   cp.d = p;
   cp.ws = static_cast<uint8_t*>(a.workspace);
   cp.qk_heads = static_cast<int32_t>(a.qk_heads);
   const int64_t apart = (a.tokens / kChunk + a.batch) * a.v_heads;
-  cp.per_block = apart <= 3 * sms ? 1 : p.group < kGroup ? p.group : kGroup;
+  cp.per_block = apart <= 4 * sms ? 1 : p.group < kGroup ? p.group : kGroup;
   cp.subgroups = (p.group + cp.per_block - 1) / cp.per_block;
   cp.chunk_blocks = static_cast<uint32_t>(chunk_slots(a.batch, a.tokens) * a.qk_heads * cp.subgroups);
   rc = launch_dependent(delta_prepare_kernel,
