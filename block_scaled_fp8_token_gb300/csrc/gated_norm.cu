@@ -7,9 +7,10 @@
 //
 // act is SiLU or the sigmoid; without w there is no norm (the gate of a full-attention
 // layer's heads). Bound by HBM: x and z are read once, and the codes (a quarter of the
-// bytes) or the BF16 row written once. 8192 rows of 48 heads to codes, 253 MB, take 44 us, 5.8
-// TB/s; with one token's loads ahead in registers, 32 warps an SM had too few bytes under way
-// (55 us), and without any 67.
+// bytes) or the BF16 row written once. 8192 rows of 48 heads to codes, 253 MB, take 52 us, 4.9
+// TB/s, of which looking for codes that FP32 may miss and settling them is 7; with one token's
+// loads ahead in registers, 32 warps an SM had too few bytes under way (55 us in place of 44),
+// and without any 67.
 #include "hybrid_layer.cuh"
 
 namespace bfp8 {
@@ -31,13 +32,113 @@ struct GatedParams {
   float eps, w_offset;
 };
 
+// A code may hang on FP32's last bits: y / s within kNear units of its last place of the middle
+// between two codes, which lies where the 20 bits below a code's are 0x80000. (Of 78 million codes
+// none was off by more than 4 units. Below 2^-6 the middles lie elsewhere, and a step is 2^-9 of
+// 448.) Twelve bits up, so that two operations an entry find the nearest.
+constexpr int kNotes = 16;                             // of a warp
+constexpr uint32_t kNear = 8;
+BFP8_DEV uint32_t from_tie(float f) { return __float_as_uint(f) * 4096u - ((0x80000u - kNear) << 12); }
+
+// For those few, sums of two floats (by Knuth's and Dekker's error-free sums and products): entries
+// within 2^-32, so that no code but one in some 2^32 differs from exact arithmetic's.
+struct Two {
+  float hi, lo;
+};
+BFP8_DEV Two two_sum(float a, float b) {
+  const float s = a + b, c = s - a;
+  return {s, (a - (s - c)) + (b - c)};
+}
+BFP8_DEV Two two_times(Two a, Two b) {
+  const float h = a.hi * b.hi, l = fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi);
+  return {h + l, (h - (h + l)) + l};
+}
+BFP8_DEV Two two_over(Two a, Two b) {
+  const float r = rcp_approx(b.hi), q = a.hi * r, l = (fmaf(-q, b.hi, a.hi) + fmaf(-q, b.lo, a.lo)) * r;
+  return {q + l, (q - (q + l)) + l};
+}
+// 1 + e^-z for a BF16 z in [-60, 40], within 2^-32: e^r by its series, its terms from r^4 / 24 on in
+// one float, with r = -z - k ln 2 (Cody and Waite's reduction: ln 2 in pieces of 12 and 13 bits, exact
+// times k, and the rest).
+BFP8_DEV Two one_and_exp(float z) {
+  const float k = rintf(z * -1.4426950408889634f);
+  const Two a = two_sum(fmaf(-k, 0.693115234375f, -z), k * -3.1948089599609375e-5f);
+  const Two r = two_sum(a.hi, fmaf(k, 1.9046543e-9f, a.lo));
+  const float x = r.hi;
+  float s = 2.7557319e-7f;                             // 1 / 10!, 1 / 9!, ...
+  s = fmaf(s, x, 2.7557319e-6f), s = fmaf(s, x, 2.4801587e-5f), s = fmaf(s, x, 1.9841270e-4f);
+  s = fmaf(s, x, 1.3888889e-3f), s = fmaf(s, x, 8.3333333e-3f), s = fmaf(s, x, 4.1666667e-2f);
+  const Two r2 = two_times(r, r), r3 = two_times(r2, r);
+  const Two third = two_times(r3, {0.16666667f, -4.9670537e-9f});
+  const Two u = two_sum(third.hi, s * r2.hi * r2.hi), v = two_sum(0.5f * r2.hi, u.hi), w = two_sum(r.hi, v.hi);
+  const Two e = two_sum(1.0f, w.hi);
+  const float rest = e.lo + (w.lo + (v.lo + (u.lo + (third.lo + (0.5f * r2.lo + r.lo)))));
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(k)) << 23);
+  const Two d = two_sum(up * e.hi, 1.0f);
+  return two_sum(d.hi, fmaf(up, rest, d.lo));
+}
+// x * w * act(z) in column c of a row, with the head's factor where a group has two; NaN where it
+// leaves the range in which the products' errors are exact.
+template <int DIM>
+BFP8_DEV Two entry(const GatedParams& p, int64_t row, int c) {
+  const int head = c / DIM, d = c % DIM;
+  const __nv_bfloat16* const px = p.x + row * p.xt + head * p.xh;
+  const float x = __bfloat162float(px[d]), z = __bfloat162float(p.z[row * p.zt + head * p.zh + d]);
+  float w = 1.0f;
+  if (p.w) w = p.w_f32 ? static_cast<const float*>(p.w)[d] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.w)[d]);
+  Two y = {p.is_sigmoid ? x : x * z, 0.0f};            // exact: 16 bits
+  if (!(y.hi == 0.0f || (fabsf(y.hi) > 0x1p-60f && fabsf(y.hi) < 0x1p60f)) || !(z > -60.0f)) y.hi = NAN;
+  if (p.w) y = two_times(y, two_sum(w, p.w_offset));
+  y = two_over(y, one_and_exp(fminf(fmaxf(z, -60.0f), 40.0f)));
+  if (DIM < 128 && p.w) {
+    double ss = 0.0;
+#pragma unroll 1
+    for (int k = 0; k < DIM; k += 8) {
+      float f[8];
+      widen8(*reinterpret_cast<const uint4*>(px + k), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += static_cast<double>(f[e]) * f[e];
+    }
+    const double r = rsqrt(ss / DIM + p.eps);
+    y = two_times(y, {static_cast<float>(r), static_cast<float>(r - static_cast<float>(r))});
+  }
+  return y;
+}
+// The warp's doubtful codes settled, two lanes each: one has the code's column, the other that with
+// the largest entry of its group. A note is a row (x), a column of the warp's in bits 0 - 7 (y), and
+// from bit 8 on that of its group.
+template <int DIM>
+__device__ __noinline__ void settle(const GatedParams& p, const uint2* notes, int count, int c) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  const bool valid = (lane & 15) < count;
+  const uint2 note = valid ? notes[lane & 15] : make_uint2(0u, 0u);
+  c += note.y & 0xFF;
+  Two y = {1.0f, 0.0f};
+  if (valid) y = entry<DIM>(p, note.x, lane < 16 ? c : (c & ~127) + static_cast<int>(note.y >> 8));
+  const Two m = {__shfl_down_sync(0xffffffffu, y.hi, 16), __shfl_down_sync(0xffffffffu, y.lo, 16)};
+  y = two_times(two_over(y, m), {m.hi < 0.0f ? -448.0f : 448.0f, 0.0f});
+  if (valid && lane < 16 && fabsf(y.hi) < 449.0f) {    // not NaN
+    // towards zero, with what is cut off as an odd last bit: rounding that once more is exact
+    uint32_t bits = __float_as_uint(y.hi);
+    if (y.lo != 0.0f) bits = (bits - (((__float_as_uint(y.lo) ^ bits) >> 31) & 1u)) | 1u;
+    p.q[note.x * p.ldq + c] = static_cast<uint8_t>(f32x2_to_e4m3x2(__uint_as_float(bits), 0.0f));
+  }
+  __syncwarp();
+}
+
 // A warp takes 256 columns, 8 a lane, of one token after the other: a head of DIM columns is
 // DIM / 8 consecutive lanes, a group of 128 columns 16, so both reductions stay in the warp,
 // and the weights stay in registers. A lane copies its 16 bytes of the next tokens to places of
 // its own in shared memory, four ahead, and waits for nobody else.
-template <int DIM>
-__global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const GatedParams p) {
+//
+// Codes that FP32 may have missed are noted in shared memory and settled behind the warp's last row,
+// two lanes each (one in 60,000 is noted; a 17th stays as FP32 has it): a call inside the loop, though
+// never taken, cost the loop 14 of 62 us. A row that its own output overwrites (IN_PLACE) cannot wait.
+template <int DIM, bool IN_PLACE>
+__global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __grid_constant__ GatedParams p) {
   __shared__ alignas(16) uint4 ring[kGatedAhead][2][kGatedThreads];
+  __shared__ uint2 doubtful[kGatedThreads / 32 * kNotes];
   const int lane = threadIdx.x & 31;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * (kGatedThreads / 32) + (threadIdx.x >> 5);
   const int64_t step = p.warps / p.segs;               // tokens between a warp's: p.warps is a multiple of segs
@@ -84,6 +185,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const Gate
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e].x += p.w_offset, w[e].y += p.w_offset;
   }
+  int count = 0;
   for (int s = 0; row < p.tokens; s = (s + 1) % kGatedAhead, row += step) {
     float x[8], z[8];
     cp_async_wait_group<kGatedAhead - 1>();
@@ -113,10 +215,6 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const Gate
       y[e] = __fmul2_rn(y[e], g);
       am = fmaxf(am, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
     }
-    if (p.out && in)
-      *reinterpret_cast<uint4*>(po) =
-          make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
-                     pack_bf16x2(y[3].x, y[3].y));
     if (p.q) {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
@@ -126,19 +224,47 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const Gate
       if (am <= 3.0e38f) sc = fmaf(fmaf(-448.0f, sc, am), 1.0f / 448.0f, sc);
       float inv = rcp_approx(sc);
       if (am <= 3.0e38f) inv = fmaf(fmaf(-sc, inv, 1.0f), inv, inv);
+      uint2 cw;
+      uint32_t near = ~0u;
+      {
+        const float2 i2 = make_float2(inv, inv);
+        const float2 f0 = __fmul2_rn(y[0], i2), f1 = __fmul2_rn(y[1], i2), f2 = __fmul2_rn(y[2], i2), f3 = __fmul2_rn(y[3], i2);
+        cw.x = static_cast<uint32_t>(f32x2_to_e4m3x2(f0.x, f0.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(f1.x, f1.y)) << 16);
+        cw.y = static_cast<uint32_t>(f32x2_to_e4m3x2(f2.x, f2.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(f3.x, f3.y)) << 16);
+        near = min(min(min(from_tie(f0.x), from_tie(f0.y)), min(from_tie(f1.x), from_tie(f1.y))),
+                   min(min(from_tie(f2.x), from_tie(f2.y)), min(from_tie(f3.x), from_tie(f3.y))));
+      }
       if (in) {
         if ((lane & 15) == 0) *ps = sc;
-        uint32_t cw[2];
+        *reinterpret_cast<uint2*>(pq) = cw;
+      }
+      const bool near_one = near <= ((2 * kNear) << 12) && in && am > 1e-10f && am <= 3.0e38f;
+      if (__any_sync(0xffffffffu, near_one)) {
+        uint32_t top = 8;                            // the lane's column with its group's largest entry
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 f = __fmul2_rn(y[2 * j], make_float2(inv, inv)), g = __fmul2_rn(y[2 * j + 1], make_float2(inv, inv));
-          cw[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(f.x, f.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(g.x, g.y)) << 16);
+        for (int e = 3; e >= 0; --e) top = fabsf(y[e].x) == am ? 2 * e : fabsf(y[e].y) == am ? 2 * e + 1 : top;
+        const uint32_t tops = __ballot_sync(0xffffffffu, top < 8) & (lane < 16 ? 0xFFFFu : 0xFFFF0000u);
+        const int src = tops ? __ffs(tops) - 1 : lane;
+        top = 8 * (src & 15) + (__shfl_sync(0xffffffffu, top, src) & 7);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool one = near_one && from_tie((e & 1 ? y[e >> 1].y : y[e >> 1].x) * inv) <= ((2 * kNear) << 12);
+          const uint32_t ones = __ballot_sync(0xffffffffu, one);
+          const int at = count + __popc(ones & ((1u << lane) - 1));
+          if (one && at < kNotes)
+            doubtful[(threadIdx.x >> 5) * kNotes + at] = make_uint2(static_cast<uint32_t>(row), top << 8 | (8 * lane + e));
+          count += __popc(ones);
         }
-        *reinterpret_cast<uint2*>(pq) = make_uint2(cw[0], cw[1]);
+        if (IN_PLACE) settle<DIM>(p, doubtful + (threadIdx.x >> 5) * kNotes, count, c - 8 * lane), count = 0;
       }
     }
+    if (p.out && in)
+      *reinterpret_cast<uint4*>(po) =
+          make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
+                     pack_bf16x2(y[3].x, y[3].y));
     po += step * p.ot, pq += step * p.ldq, ps += step * p.ssm;
   }
+  if (!IN_PLACE && count) settle<DIM>(p, doubtful + (threadIdx.x >> 5) * kNotes, count, c - 8 * lane);
 }
 
 bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -193,8 +319,8 @@ int launch_gated_norm(const bfp8_gated_norm_args& a, void* stream) {
   rc = sm_count(&sms);
   if (rc != BFP8_OK) return rc;
   // A warp to each 256 columns of a token, up to 96 warps an SM, three times what is resident:
-  // later blocks fill in where earlier ones end (8192 x 48 heads: 51, 45, 44, 49 us with 32, 64,
-  // 128 and 256).
+  // later blocks fill in where earlier ones end (8192 x 48 heads, before codes were
+  // settled: 51, 45, 44, 49 us with 32, 64, 128 and 256).
   constexpr int kPer = kGatedThreads / 32, kFit = 96;  // warps of a block, and of an SM
   int64_t rows = (int64_t{sms} * kFit + p.segs - 1) / p.segs;
   rows = rows < a.tokens ? rows : a.tokens;
@@ -203,10 +329,14 @@ int launch_gated_norm(const bfp8_gated_norm_args& a, void* stream) {
   if (blocks > 0x7FFFFFFF) return BFP8_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(blocks));
+  const bool in_place = a.out_bf16 && a.q_e4m3 && (a.out_bf16 == a.x_bf16 || a.out_bf16 == a.gate_bf16);
+  auto launch = [&](auto kernel, auto kernel_in_place) {
+    return launch_dependent(in_place ? kernel_in_place : kernel, grid, kGatedThreads, 0, st, p);
+  };
   switch (a.head_dim) {
-    case 64: return launch_dependent(gated_norm_kernel<64>, grid, kGatedThreads, 0, st, p);
-    case 128: return launch_dependent(gated_norm_kernel<128>, grid, kGatedThreads, 0, st, p);
-    default: return launch_dependent(gated_norm_kernel<256>, grid, kGatedThreads, 0, st, p);
+    case 64: return launch(gated_norm_kernel<64, false>, gated_norm_kernel<64, true>);
+    case 128: return launch(gated_norm_kernel<128, false>, gated_norm_kernel<128, true>);
+    default: return launch(gated_norm_kernel<256, false>, gated_norm_kernel<256, true>);
   }
 }
 

@@ -804,8 +804,9 @@ int bfp8_delta_rule(const bfp8_delta_rule_args* args, void* stream);
  * projection, per token and head:
  *   y = (weight ? x * rsqrt(mean(x^2) + eps) * (weight + weight_offset) : x) * act(gate)
  *   out = bf16_rn(y); per 128 columns of a token's heads, one behind another,
- *   s = max(max|y|, 1e-10f) / 448, q = RNE_satfinite_e4m3(y / s)   (the quotient within 2^-21)
- * in float32: the quantizer takes y before it is rounded to BF16.
+ *   s = max(max|y|, 1e-10f) / 448, q = RNE_satfinite_e4m3(y / s)
+ * in float32: the quantizer takes y before it is rounded to BF16. Where the quotient's last
+ * bits would decide a code above 2^-6, it is formed once more to 2^-31.
  * tokens == 0 or heads == 0 is a no-op. Errors: INVALID_ARG (null x or gate, no
  * output, strides below a row, q without scales, gate_act, eps < 0), SCALE_DTYPE
  * (w_dtype), UNSUPPORTED (head width, rows that are not 16-byte aligned, codes' rows

@@ -72,6 +72,27 @@ def test_matches_oracle(bfp8, cuda_device, T, H, D, wt, sigmoid):
         assert all(torch.equal(lone[k], o[k]) for k in lone)
 
 
+@pytest.mark.parametrize("T,H,D,wt,sigmoid", [(8000, 16, 128, torch.float32, False), (3001, 33, 64, torch.float32, False),
+                                              (4000, 9, 256, torch.float32, True), (700, 40, 128, torch.float32, True)])
+def test_codes_are_those_of_exact_arithmetic(bfp8, cuda_device, T, H, D, wt, sigmoid):
+    """Where FP32's last bits would decide a code, sums of two floats do: entries within 2^-32, so a quotient within
+    2^-31 of the exact one. (One code in a million differs without. Below 2^-6 codes stay as FP32 has them.)"""
+    t, o = _inputs(cuda_device, T, H, D, 31 * T + D, wt), _outputs(cuda_device, T, H, D)
+    _run(bfp8, t, o, sigmoid=sigmoid, weight_offset=0.125)
+    y = HY.gated_norm(f64(t["x"]), f64(t["gate"]), f64(t["weight"]), 1e-6, 0.125, sigmoid).reshape(T, -1)
+    largest = np.maximum.reduceat(np.abs(y), np.arange(0, y.shape[1], 128), axis=1)
+    v = y / np.repeat(largest / 448, 128, axis=1)[:, :y.shape[1]]
+    lut = F.e4m3_decode_lut()
+    code, plain = lut[o["q"].cpu().numpy()], np.abs(v) > 2.0 ** -6 * 1.01
+    assert np.all((code >= lut[F.e4m3_encode_rne_sat(v - 2.0 ** -31 * np.abs(v))])[plain])
+    assert np.all((code <= lut[F.e4m3_encode_rne_sat(v + 2.0 ** -31 * np.abs(v))])[plain])
+    for name in ("x", "gate"):                       # the same codes where the row is overwritten by the output
+        held, again = t[name].clone(), _outputs(cuda_device, T, H, D)
+        _run(bfp8, t, dict(again, out=t[name]), sigmoid=sigmoid, weight_offset=0.125)
+        assert all(torch.equal(again[k], o[k]) for k in ("q", "scales")) and torch.equal(t[name], o["out"])
+        t[name].copy_(held)
+
+
 def test_strides_scales_of_either_order_and_in_place(bfp8, cuda_device):
     dev, T, H, D = cuda_device, 33, 6, 128
     t, o = _inputs(dev, T, H, D, 1), _outputs(dev, T, H, D)
