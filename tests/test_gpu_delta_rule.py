@@ -72,6 +72,12 @@ def test_prompts_match_oracle(bfp8, cuda_device, lens, hk, hv):
     _check(t, lens, _run(bfp8, t, lens))
 
 
+@pytest.mark.parametrize("lens,c", [([20, 1, 19], 64), ([21, 20, 12, 13], 512), ([20], 64), ([21], 512)], ids=str)
+def test_lengths_about_the_limit_of_steps(bfp8, cuda_device, lens, c):
+    t = delta_inputs(cuda_device, lens, 2, 6, 41 + sum(lens), extra=1)
+    _check(t, lens, _run(bfp8, t, lens), c=c)
+
+
 @pytest.mark.parametrize("lens,hk,hv", [([3000], 1, 1), ([2049], 1, 2), ([2500, 7, 40, 1300], 2, 2), ([1500, 1501], 1, 4),
                                         ([64 * 27 + 1, 64 * 30, 0, 64 * 9], 1, 1)], ids=str)
 @pytest.mark.parametrize("decay", [1e-3, 1.0])
