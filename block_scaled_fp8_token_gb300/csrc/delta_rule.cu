@@ -393,9 +393,10 @@ BFP8_DEV void store_piece(float* at, int lane, const float (&c)[4], float sign) 
 // and the Q rows with the K rows leaves row i of K K^T and of Q K^T in a lane of tensor memory;
 // two threads share a lane's columns. (1 + A)^-1 is formed by blocks of 16: the diagonal ones
 // column by column, then each lower one as -T_b A_ba T_a, of 16 rows and of 32. P T is a
-// product on the tensor cores again. The grid's last blocks take the step's short requests, a
-// token after the other, which so run beside the long ones' chunks (as its first blocks they kept
-// the chunks waiting: 81 us against 60 for 12 requests of 1 to 141 tokens and 48 heads).
+// product on the tensor cores again. The grid's last blocks, up to four an SM, take the step's short
+// requests, a token after the other, which so run beside the long ones' chunks (as its first
+// blocks they kept the chunks waiting: 81 us against 60 for 12 requests of 1 to 141 tokens and 48
+// heads; with a block for every part, 64 requests without a short one took 15 us of empty blocks).
 //
 // Bound by latency: a block passes a dozen barriers, and four to an SM issue in 53% of the clocks.
 // 129 chunks of 16 key and 32 value heads take 88 us (94 with three to an SM, 214 with one; 138
@@ -416,8 +417,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(const __
   pdl_wait();
   if (blockIdx.x >= p.chunk_blocks) {
     pdl_launch_dependents();
-    delta_steps<kPrepThreads / 32>(p.d, blockIdx.x - p.chunk_blocks,
-                                   *reinterpret_cast<StepShared<kPrepThreads / 32>*>(base));
+    constexpr int kWarps = kPrepThreads / 32;
+    const int64_t all = static_cast<int64_t>(p.d.req.batch) * p.d.v_heads * (kD / (8 * kWarps));
+    for (int64_t part = blockIdx.x - p.chunk_blocks; part < all; part += gridDim.x - p.chunk_blocks) {
+      delta_steps<kWarps>(p.d, part, *reinterpret_cast<StepShared<kWarps>*>(base));
+      __syncthreads();
+    }
     return;
   }
   const int block = static_cast<int>(blockIdx.x);
@@ -1543,9 +1548,10 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   cp.per_block = apart <= 4 * sms ? 1 : p.group < kGroup ? p.group : kGroup;
   cp.subgroups = (p.group + cp.per_block - 1) / cp.per_block;
   cp.chunk_blocks = static_cast<uint32_t>(chunk_slots(a.batch, a.tokens) * a.qk_heads * cp.subgroups);
-  rc = launch_dependent(delta_prepare_kernel,
-                        dim3(cp.chunk_blocks + static_cast<unsigned>(a.batch * a.v_heads * (kD / (8 * (kPrepThreads / 32))))),
-                        kPrepThreads, kPrepSmem, st, tq, tk, cp);
+  const int64_t step_parts = a.batch * a.v_heads * (kD / (8 * (kPrepThreads / 32)));
+  const int64_t step_blocks = step_parts < 4 * sms ? step_parts : 4 * sms;
+  rc = launch_dependent(delta_prepare_kernel, dim3(cp.chunk_blocks + static_cast<unsigned>(step_blocks)), kPrepThreads,
+                        kPrepSmem, st, tq, tk, cp);
   if (rc != BFP8_OK) return rc;
   const int64_t chunks = longest_chunks(a.tokens, a.max_q_len), pairs = a.batch * a.v_heads;
   const Split split = split_walk(chunks, pairs, sms);
