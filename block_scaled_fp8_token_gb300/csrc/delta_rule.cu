@@ -1539,7 +1539,8 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   if (rc != BFP8_OK) return rc;
   // Value heads of one key head share a block, which norms and multiplies their rows once (14,000
   // of its 24,500 clocks for one head), unless the blocks of one head each fit the GPU at once,
-  // four to an SM. (4 requests of 128 tokens, 48 heads: 39 us apart, 42.7 shared. Requests of 1 to 141 tokens, 48 heads on 16: 52 us shared, 57 us apart.)
+  // four to an SM. (4 requests of 128 tokens, 48 heads on 16: 43 us shared, 39 apart; 12 of 1 to
+  // 141 tokens 47 and 51; 64 of 128 tokens 354 and 418.)
   ChunkParams cp{};
   cp.d = p;
   cp.ws = static_cast<uint8_t*>(a.workspace);
