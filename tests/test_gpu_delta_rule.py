@@ -94,6 +94,13 @@ def test_long_prompts_of_many_heads_match_oracle(bfp8, cuda_device, lens, hk, hv
     _check(t, lens, _run(bfp8, t, lens))
 
 
+def test_many_requests_of_ragged_lengths(bfp8, cuda_device):
+    """More heads than SMs: blocks begin with the longest of each 32 requests."""
+    lens = [(37 * i * i + 11 * i) % 150 if i % 5 else 0 for i in range(67)]
+    t = delta_inputs(cuda_device, lens, 2, 4, 47, extra=2)
+    _check(t, lens, _run(bfp8, t, lens))
+
+
 def test_long_prompts_in_one_slot_and_replayed(bfp8, cuda_device):
     """Read from and left in the same slot; captured, and replayed with lengths that end in other segments."""
     dev = cuda_device
