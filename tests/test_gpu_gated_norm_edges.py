@@ -1,0 +1,48 @@
+"""bfp8_gated_norm at gates without an end."""
+
+import numpy as np
+import pytest
+import torch
+
+from hybrid_util import f64, nan_like
+from oracle import hybrid as HY
+from test_gpu_gated_norm import _inputs, _outputs, _run
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("wt", [torch.float32, None])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_gates_without_an_end(bfp8, cuda_device, D, wt, sigmoid):
+    """sigmoid(inf) is 1, SiLU(inf) infinite and sigmoid(-inf) 0; gates of +-3e38 are finite and count as far as that.
+    Of y the tolerance is that of any gate: tol = (36 + 2.4 max(0, -z)) 2^-24 |y|, and BF16's half step 2^-8."""
+    t, o = _inputs(cuda_device, 6, 2, D, D, wt), dict(out=nan_like((6, 2, D), cuda_device))
+    gates = [INF, -INF, 3.0e38, -3.0e38]
+    for row, z in enumerate(gates):
+        t["gate"][row, :, ::3] = z
+    t["gate"][4, 0, 5] = INF
+    _run(bfp8, t, o, sigmoid=sigmoid)
+    z = f64(t["gate"])
+    y = HY.gated_norm(f64(t["x"]), np.clip(z, -600, 600), f64(t["weight"]), 1e-6, 0.0, True)   # x times the sigmoid
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = y if sigmoid else np.where(z <= -3e38, np.where(np.isinf(z), np.nan, -0.0 * y), y * z)
+    got = f64(o["out"])
+    big = np.abs(want) > 3.39e38                     # BF16's end
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.isinf(got[np.isinf(want)]).all()
+    fine = np.isfinite(want) & ~big
+    tol = (36 + 2.4 * np.clip(-z, 0, 600)) * 2.0 ** -24 * np.abs(want) + 1e-37
+    assert np.all(np.abs(got[fine] - want[fine]) <= (tol + 2.0 ** -8 * (np.abs(want) + tol))[fine])
+    assert np.array_equal(np.sign(got[np.isinf(want)]), np.sign(want[np.isinf(want)]))
+
+
+def test_an_infinite_gate_among_codes(bfp8, cuda_device):
+    """The sigmoid of an infinite gate is 1, and its codes are those of a gate of 200, which is 1 too."""
+    t, o, far = _inputs(cuda_device, 5, 3, 128, 17), _outputs(cuda_device, 5, 3, 128), _outputs(cuda_device, 5, 3, 128)
+    t["gate"][1, 2], t["gate"][3, :, 7], t["gate"][4] = INF, INF, -INF
+    _run(bfp8, t, o, sigmoid=True)
+    t["gate"].copy_(torch.where(t["gate"] == INF, 200.0, t["gate"]))
+    _run(bfp8, t, far, sigmoid=True)
+    assert all(torch.equal(o[k], far[k]) for k in o)
+    assert not o["out"][4].any() and torch.isfinite(o["out"]).all()
