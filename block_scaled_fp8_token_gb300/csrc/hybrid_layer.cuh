@@ -45,13 +45,19 @@ BFP8_DEV void cp_async_wait_group() { asm volatile("cp.async.wait_group %0;" ::"
 BFP8_DEV float sigmoid(float x) { return rcp_approx(1.0f + ex2_approx(x * -1.4426950408889634f)); }
 
 // The same of two BF16 x, within 4 2^-23 and as much again where e^-x outweighs the 1: x times the
-// upper 16 bits of log2 e is exact, and the rest of the exponent is put right to first order. (Of an x
-// past 128, where e^-x is 0, by 128's rest: an infinite one times 0 would be NaN.)
+// upper 16 bits of log2 e is exact, and the rest of the exponent is put right to first order: 1 + x k,
+// as 1.5 - (0.5 - x k) within 2^-25, the latter kept in [0, 1] so that an infinite x meets no 0 of e^-x.
+BFP8_DEV float saturated_fma(float a, float b, float c) {
+  float r;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 BFP8_DEV float2 sigmoid_bf16(float2 x) {
   const float2 t = __fmul2_rn(x, make_float2(kNegLog2eHi, kNegLog2eHi));
-  const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y)), in = make_float2(fminf(x.x, 128.0f), fminf(x.y, 128.0f));
-  const float2 right = __ffma2_rn(e, __fmul2_rn(in, make_float2(kNegLog2eLoLn2, kNegLog2eLoLn2)), e);
-  const float2 d = __fadd2_rn(right, make_float2(1.0f, 1.0f));
+  const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+  const float2 rest = make_float2(saturated_fma(x.x, -kNegLog2eLoLn2, 0.5f), saturated_fma(x.y, -kNegLog2eLoLn2, 0.5f));
+  const float2 right = __ffma2_rn(rest, make_float2(-1.0f, -1.0f), make_float2(1.5f, 1.5f));
+  const float2 d = __ffma2_rn(e, right, make_float2(1.0f, 1.0f));
   return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
