@@ -38,31 +38,39 @@ struct GatedParams {
 // 448.) Twelve bits up, so that two operations an entry find the nearest.
 constexpr int kNotes = 16;                             // of a warp
 constexpr uint32_t kNear = 8;
+constexpr uint32_t kBothSides = (2 * kNear) << 12;
 BFP8_DEV uint32_t from_tie(float f) { return __float_as_uint(f) * 4096u - ((0x80000u - kNear) << 12); }
+BFP8_DEV bool is_near(float f) { return from_tie(f) <= kBothSides; }
 
 // For those few, sums of two floats (by Knuth's and Dekker's error-free sums and products): entries
 // within 2^-32, so that no code but one in some 2^32 differs from exact arithmetic's.
 struct Two {
   float hi, lo;
 };
+// (Each operation rounded on its own: a product that the compiler took into a sum would count its
+// rest twice.)
 BFP8_DEV Two two_sum(float a, float b) {
-  const float s = a + b, c = s - a;
-  return {s, (a - (s - c)) + (b - c)};
+  const float s = __fadd_rn(a, b), c = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, c)), __fsub_rn(b, c))};
+}
+BFP8_DEV Two two_parts(float h, float l) {
+  const float s = __fadd_rn(h, l);
+  return {s, __fadd_rn(__fsub_rn(h, s), l)};
 }
 BFP8_DEV Two two_times(Two a, Two b) {
-  const float h = a.hi * b.hi, l = fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi);
-  return {h + l, (h - (h + l)) + l};
+  const float h = __fmul_rn(a.hi, b.hi);
+  return two_parts(h, __fadd_rn(fmaf(a.hi, b.hi, -h), fmaf(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
 }
 BFP8_DEV Two two_over(Two a, Two b) {
-  const float r = rcp_approx(b.hi), q = a.hi * r, l = (fmaf(-q, b.hi, a.hi) + fmaf(-q, b.lo, a.lo)) * r;
-  return {q + l, (q - (q + l)) + l};
+  const float r = rcp_approx(b.hi), q = __fmul_rn(a.hi, r);
+  return two_parts(q, __fmul_rn(__fadd_rn(fmaf(-q, b.hi, a.hi), fmaf(-q, b.lo, a.lo)), r));
 }
 // 1 + e^-z for a BF16 z in [-60, 40], within 2^-32: e^r by its series, its terms from r^4 / 24 on in
 // one float, with r = -z - k ln 2 (Cody and Waite's reduction: ln 2 in pieces of 12 and 13 bits, exact
 // times k, and the rest).
 BFP8_DEV Two one_and_exp(float z) {
   const float k = rintf(z * -1.4426950408889634f);
-  const Two a = two_sum(fmaf(-k, 0.693115234375f, -z), k * -3.1948089599609375e-5f);
+  const Two a = two_sum(fmaf(-k, 0.693115234375f, -z), __fmul_rn(k, -3.1948089599609375e-5f));
   const Two r = two_sum(a.hi, fmaf(k, 1.9046543e-9f, a.lo));
   const float x = r.hi;
   float s = 2.7557319e-7f;                             // 1 / 10!, 1 / 9!, ...
@@ -70,11 +78,12 @@ BFP8_DEV Two one_and_exp(float z) {
   s = fmaf(s, x, 1.3888889e-3f), s = fmaf(s, x, 8.3333333e-3f), s = fmaf(s, x, 4.1666667e-2f);
   const Two r2 = two_times(r, r), r3 = two_times(r2, r);
   const Two third = two_times(r3, {0.16666667f, -4.9670537e-9f});
-  const Two u = two_sum(third.hi, s * r2.hi * r2.hi), v = two_sum(0.5f * r2.hi, u.hi), w = two_sum(r.hi, v.hi);
+  const Two u = two_sum(third.hi, __fmul_rn(__fmul_rn(s, r2.hi), r2.hi)), v = two_sum(__fmul_rn(0.5f, r2.hi), u.hi);
+  const Two w = two_sum(r.hi, v.hi);
   const Two e = two_sum(1.0f, w.hi);
   const float rest = e.lo + (w.lo + (v.lo + (u.lo + (third.lo + (0.5f * r2.lo + r.lo)))));
   const float up = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(k)) << 23);
-  const Two d = two_sum(up * e.hi, 1.0f);
+  const Two d = two_sum(__fmul_rn(up, e.hi), 1.0f);
   return two_sum(d.hi, fmaf(up, rest, d.lo));
 }
 // x * w * act(z) in column c of a row, with the head's factor where a group has two; NaN where it
@@ -104,6 +113,77 @@ BFP8_DEV Two entry(const GatedParams& p, int64_t row, int c) {
   }
   return y;
 }
+// 8 weights from column d of a head on, with their offset.
+BFP8_DEV void load_weights(const GatedParams& p, int d, float2 (&w)[4]) {
+  if (p.w_f32) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d));
+    const float4 g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d + 4));
+    w[0] = make_float2(f.x, f.y), w[1] = make_float2(f.z, f.w), w[2] = make_float2(g.x, g.y), w[3] = make_float2(g.z, g.w);
+  } else {
+    float f[8];
+    widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w) + d)), f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = make_float2(f[2 * e], f[2 * e + 1]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e].x += p.w_offset, w[e].y += p.w_offset;
+}
+// y of a lane's 8 columns of a row. The whole warp.
+template <int DIM>
+BFP8_DEV void row_values(const GatedParams& p, const uint4& xr, const uint4& zr, const float2 (&w)[4], float2 (&y)[4]) {
+  float x[8], z[8];
+  widen8(xr, x);
+  widen8(zr, z);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = make_float2(x[2 * e], x[2 * e + 1]);
+  if (p.w) {
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = DIM / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(fmaf(ss, 1.0f / DIM, p.eps));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], __fmul2_rn(w[e], make_float2(r, r)));
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 a = make_float2(z[2 * e], z[2 * e + 1]);
+    float2 g = sigmoid_bf16(a);
+    if (!p.is_sigmoid) g = __fmul2_rn(g, a);
+    y[e] = __fmul2_rn(y[e], g);
+  }
+}
+// The largest |y| of a lane's group, its scale, and 1 / scale.
+BFP8_DEV float group_scale(const float2 (&y)[4], float& sc, float& inv) {
+  float am = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) am = fmaxf(am, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+  // am / 448 rounded (its remainder is exact), and 1 / s within 2^-23
+  am = fmaxf(am, 1e-10f);
+  sc = am * (1.0f / 448.0f);
+  if (am <= 3.0e38f) sc = fmaf(fmaf(-448.0f, sc, am), 1.0f / 448.0f, sc);
+  inv = rcp_approx(sc);
+  if (am <= 3.0e38f) inv = fmaf(fmaf(-sc, inv, 1.0f), inv, inv);
+  return am;
+}
+BFP8_DEV void quotients(const float2 (&y)[4], float inv, float2 (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = __fmul2_rn(y[e], make_float2(inv, inv));
+}
+BFP8_DEV bool may_be_near(float am) { return am > 1e-10f && am <= 3.0e38f; }
+// The place of its largest entry in a lane's group, the first of equal ones. The whole warp.
+BFP8_DEV uint32_t group_top(const float2 (&y)[4], float am, int lane) {
+  uint32_t top = 8;
+#pragma unroll
+  for (int e = 3; e >= 0; --e) top = fabsf(y[e].x) == am ? 2 * e : fabsf(y[e].y) == am ? 2 * e + 1 : top;
+  const uint32_t tops = __ballot_sync(0xffffffffu, top < 8) & (lane < 16 ? 0xFFFFu : 0xFFFF0000u);
+  const int src = tops ? __ffs(tops) - 1 : lane;
+  return 8 * (src & 15) + (__shfl_sync(0xffffffffu, top, src) & 7);
+}
 // The warp's doubtful codes settled, two lanes each: one has the code's column, the other that with
 // the largest entry of its group. A note is a row (x), a column of the warp's in bits 0 - 7 (y), and
 // from bit 8 on that of its group.
@@ -127,13 +207,49 @@ __device__ __noinline__ void settle(const GatedParams& p, const uint2* notes, in
   __syncwarp();
 }
 
+// The same of rows `step` apart, each formed once more with the loop's own operations, for any number
+// of doubtful codes; c is the lane's column.
+template <int DIM>
+__device__ __noinline__ void settle_rows(const GatedParams& p, uint2* notes, int64_t row, int64_t end, int64_t step, int c) {
+  const int lane = threadIdx.x & 31, head = c / DIM, d = c % DIM;
+  const bool in = c < p.cols;
+  float2 w[4], y[4], f[4];
+  if (p.w) load_weights(p, d, w);
+  for (; row < end; row += step) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), z = x;
+    if (in) {
+      x = *reinterpret_cast<const uint4*>(p.x + row * p.xt + head * p.xh + d);
+      z = *reinterpret_cast<const uint4*>(p.z + row * p.zt + head * p.zh + d);
+    }
+    row_values<DIM>(p, x, z, w, y);
+    float sc, inv;
+    const float am = group_scale(y, sc, inv);
+    quotients(y, inv, f);
+    uint32_t near = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (in && may_be_near(am) && is_near(e & 1 ? f[e >> 1].y : f[e >> 1].x)) near |= 1u << e;
+    const uint32_t top = group_top(y, am, lane);
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t ones = __ballot_sync(0xffffffffu, near >> e & 1u);
+      for (int done = 0; done < __popc(ones); done += kNotes) {
+        const int at = __popc(ones & ((1u << lane) - 1)) - done;
+        if ((near >> e & 1u) && at >= 0 && at < kNotes) notes[at] = make_uint2(static_cast<uint32_t>(row), top << 8 | (8 * lane + e));
+        settle<DIM>(p, notes, __popc(ones) - done, c - 8 * lane);
+      }
+    }
+  }
+}
+
 // A warp takes 256 columns, 8 a lane, of one token after the other: a head of DIM columns is
 // DIM / 8 consecutive lanes, a group of 128 columns 16, so both reductions stay in the warp,
 // and the weights stay in registers. A lane copies its 16 bytes of the next tokens to places of
 // its own in shared memory, four ahead, and waits for nobody else.
 //
 // Codes that FP32 may have missed are noted in shared memory and settled behind the warp's last row,
-// two lanes each (one in 60,000 is noted; a 17th stays as FP32 has it): a call inside the loop, though
+// two lanes each (one in 60,000 is noted; where a warp has a 17th, all of its rows are looked through
+// again, so that a row's codes are its own, whatever is beside it): a call inside the loop, though
 // never taken, cost the loop 14 of 62 us. A row that its own output overwrites (IN_PLACE) cannot wait.
 template <int DIM, bool IN_PLACE>
 __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __grid_constant__ GatedParams p) {
@@ -171,91 +287,45 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __gr
 #pragma unroll
   for (int s = 0; s < kGatedAhead; ++s) ask(s);
   float2 w[4];
-  if (p.w) {
-    if (p.w_f32) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d));
-      const float4 g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + d + 4));
-      w[0] = make_float2(f.x, f.y), w[1] = make_float2(f.z, f.w), w[2] = make_float2(g.x, g.y), w[3] = make_float2(g.z, g.w);
-    } else {
-      float f[8];
-      widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w) + d)), f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = make_float2(f[2 * e], f[2 * e + 1]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e].x += p.w_offset, w[e].y += p.w_offset;
-  }
+  if (p.w) load_weights(p, d, w);
+  uint2* const notes = doubtful + (threadIdx.x >> 5) * kNotes;
   int count = 0;
   for (int s = 0; row < p.tokens; s = (s + 1) % kGatedAhead, row += step) {
-    float x[8], z[8];
     cp_async_wait_group<kGatedAhead - 1>();
-    widen8(lds128(place + s * static_cast<uint32_t>(sizeof(ring[0]))), x);
-    widen8(lds128(place + s * static_cast<uint32_t>(sizeof(ring[0])) + static_cast<uint32_t>(sizeof(ring[0][0]))), z);
+    const uint4 xr = lds128(place + s * static_cast<uint32_t>(sizeof(ring[0])));
+    const uint4 zr = lds128(place + s * static_cast<uint32_t>(sizeof(ring[0])) + static_cast<uint32_t>(sizeof(ring[0][0])));
     ask(s);
     float2 y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = make_float2(x[2 * e], x[2 * e + 1]);
-    if (p.w) {
-      float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
-      float ss = s2.x + s2.y;
-#pragma unroll
-      for (int o = DIM / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(fmaf(ss, 1.0f / DIM, p.eps));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], __fmul2_rn(w[e], make_float2(r, r)));
-    }
-    float am = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = make_float2(z[2 * e], z[2 * e + 1]);
-      float2 g = sigmoid_bf16(a);
-      if (!p.is_sigmoid) g = __fmul2_rn(g, a);
-      y[e] = __fmul2_rn(y[e], g);
-      am = fmaxf(am, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
-    }
+    row_values<DIM>(p, xr, zr, w, y);
     if (p.q) {
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-      // am / 448 rounded (its remainder is exact), and 1 / s within 2^-23
-      am = fmaxf(am, 1e-10f);
-      float sc = am * (1.0f / 448.0f);
-      if (am <= 3.0e38f) sc = fmaf(fmaf(-448.0f, sc, am), 1.0f / 448.0f, sc);
-      float inv = rcp_approx(sc);
-      if (am <= 3.0e38f) inv = fmaf(fmaf(-sc, inv, 1.0f), inv, inv);
+      float sc, inv;
+      const float am = group_scale(y, sc, inv);
+      float2 f[4];
+      quotients(y, inv, f);
       uint2 cw;
-      uint32_t near = ~0u;
-      {
-        const float2 i2 = make_float2(inv, inv);
-        const float2 f0 = __fmul2_rn(y[0], i2), f1 = __fmul2_rn(y[1], i2), f2 = __fmul2_rn(y[2], i2), f3 = __fmul2_rn(y[3], i2);
-        cw.x = static_cast<uint32_t>(f32x2_to_e4m3x2(f0.x, f0.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(f1.x, f1.y)) << 16);
-        cw.y = static_cast<uint32_t>(f32x2_to_e4m3x2(f2.x, f2.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(f3.x, f3.y)) << 16);
-        near = min(min(min(from_tie(f0.x), from_tie(f0.y)), min(from_tie(f1.x), from_tie(f1.y))),
-                   min(min(from_tie(f2.x), from_tie(f2.y)), min(from_tie(f3.x), from_tie(f3.y))));
-      }
+      cw.x = static_cast<uint32_t>(f32x2_to_e4m3x2(f[0].x, f[0].y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(f[1].x, f[1].y)) << 16);
+      cw.y = static_cast<uint32_t>(f32x2_to_e4m3x2(f[2].x, f[2].y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(f[3].x, f[3].y)) << 16);
+      const uint32_t near = min(min(min(from_tie(f[0].x), from_tie(f[0].y)), min(from_tie(f[1].x), from_tie(f[1].y))),
+                                min(min(from_tie(f[2].x), from_tie(f[2].y)), min(from_tie(f[3].x), from_tie(f[3].y))));
       if (in) {
         if ((lane & 15) == 0) *ps = sc;
         *reinterpret_cast<uint2*>(pq) = cw;
       }
-      const bool near_one = near <= ((2 * kNear) << 12) && in && am > 1e-10f && am <= 3.0e38f;
+      const bool near_one = near <= kBothSides && in && may_be_near(am);
       if (__any_sync(0xffffffffu, near_one)) {
-        uint32_t top = 8;                            // the lane's column with its group's largest entry
+        if (IN_PLACE) {
+          settle_rows<DIM>(p, notes, row, row + 1, 1, c);
+        } else {
+          const uint32_t top = group_top(y, am, lane);
 #pragma unroll
-        for (int e = 3; e >= 0; --e) top = fabsf(y[e].x) == am ? 2 * e : fabsf(y[e].y) == am ? 2 * e + 1 : top;
-        const uint32_t tops = __ballot_sync(0xffffffffu, top < 8) & (lane < 16 ? 0xFFFFu : 0xFFFF0000u);
-        const int src = tops ? __ffs(tops) - 1 : lane;
-        top = 8 * (src & 15) + (__shfl_sync(0xffffffffu, top, src) & 7);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool one = near_one && from_tie((e & 1 ? y[e >> 1].y : y[e >> 1].x) * inv) <= ((2 * kNear) << 12);
-          const uint32_t ones = __ballot_sync(0xffffffffu, one);
-          const int at = count + __popc(ones & ((1u << lane) - 1));
-          if (one && at < kNotes)
-            doubtful[(threadIdx.x >> 5) * kNotes + at] = make_uint2(static_cast<uint32_t>(row), top << 8 | (8 * lane + e));
-          count += __popc(ones);
+          for (int e = 0; e < 8; ++e) {
+            const bool one = near_one && is_near(e & 1 ? f[e >> 1].y : f[e >> 1].x);
+            const uint32_t ones = __ballot_sync(0xffffffffu, one);
+            const int at = count + __popc(ones & ((1u << lane) - 1));
+            if (one && at < kNotes) notes[at] = make_uint2(static_cast<uint32_t>(row), top << 8 | (8 * lane + e));
+            count += __popc(ones);
+          }
         }
-        if (IN_PLACE) settle<DIM>(p, doubtful + (threadIdx.x >> 5) * kNotes, count, c - 8 * lane), count = 0;
       }
     }
     if (p.out && in)
@@ -264,7 +334,9 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __gr
                      pack_bf16x2(y[3].x, y[3].y));
     po += step * p.ot, pq += step * p.ldq, ps += step * p.ssm;
   }
-  if (!IN_PLACE && count) settle<DIM>(p, doubtful + (threadIdx.x >> 5) * kNotes, count, c - 8 * lane);
+  if (IN_PLACE || count == 0) return;
+  if (count <= kNotes) settle<DIM>(p, notes, count, c - 8 * lane);
+  else settle_rows<DIM>(p, notes, at / p.segs, p.tokens, step, c);
 }
 
 bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }

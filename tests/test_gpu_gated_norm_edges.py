@@ -1,4 +1,4 @@
-"""bfp8_gated_norm at gates without an end."""
+"""bfp8_gated_norm at gates without an end, and for the same row in other calls."""
 
 import numpy as np
 import pytest
@@ -46,3 +46,43 @@ def test_an_infinite_gate_among_codes(bfp8, cuda_device):
     _run(bfp8, t, far, sigmoid=True)
     assert all(torch.equal(o[k], far[k]) for k in o)
     assert not o["out"][4].any() and torch.isfinite(o["out"]).all()
+
+
+def _tied_rows(T, H, D, largest, seed):
+    """BF16 rows whose groups of 128 columns have `largest` as their largest entry, and beside it every entry above
+    2^-6 of a code's step that lies in the middle between two codes at a largest of 1.75: 448 / 1.75 is 2^8."""
+    g = np.random.default_rng(seed)
+    ties = [(1 + (2 * m + 1) / 16) * 2.0 ** e for e in range(-14, 1) for m in range(8)]
+    ties = [v for v in ties if v < 1.75]
+    x = np.empty((T, H * D))
+    for row in x:
+        for at in range(0, H * D, 128):
+            n = min(128, H * D - at)
+            group = np.concatenate([[1.75], g.permutation(ties)[:n - 1], g.uniform(0.01, 1.7, max(0, n - 1 - len(ties)))])
+            row[at:at + n] = g.permutation(group) * g.choice([-1.0, 1.0], n)
+    return torch.tensor(x * (largest / 1.75)).to(torch.bfloat16).view(T, H, D)
+
+
+@pytest.mark.parametrize("gate", [1.296875, -2.453125])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_row_has_the_same_codes_in_any_call(bfp8, cuda_device, D, gate):
+    """Rows full of codes that FP32's last bits decide: alone, next to others, 8192 of them, and over their own input."""
+    dev, H = cuda_device, 6144 // D
+    row = torch.cat([_tied_rows(1, H, D, 1.75, D), _inputs("cpu", 1, H, D, 5 + D)["x"]]).to(dev)
+    calls = []
+    for order in ([0], [1, 0], [0] * 40 + [1] * 3 + [0], [0] * 8192):
+        t = dict(x=row[order].contiguous(), weight=None)
+        t["gate"] = torch.full_like(t["x"], gate)
+        o = _outputs(dev, len(order), H, D)
+        _run(bfp8, t, o)
+        calls.append((order, o))
+        over = dict(_outputs(dev, len(order), H, D), out=t["x"])
+        _run(bfp8, t, over)
+        calls.append((order, over))
+    want = {0: calls[0][1], 1: {k: v[:1] for k, v in calls[2][1].items()}}
+    for order, o in calls:
+        at = torch.tensor(order, device=dev)
+        for r in set(order):
+            for k in ("q", "scales"):
+                assert (o[k][at == r] == want[r][k]).all(), (order[:3], len(order), k)
+            assert torch.equal(o["out"][at == r][-1:], want[r]["out"])
