@@ -43,7 +43,8 @@ BFP8_DEV uint32_t from_tie(float f) { return __float_as_uint(f) * 4096u - ((0x80
 BFP8_DEV bool is_near(float f) { return from_tie(f) <= kBothSides; }
 
 // For those few, sums of two floats (by Knuth's and Dekker's error-free sums and products): entries
-// within 2^-32, so that no code but one in some 2^32 differs from exact arithmetic's.
+// within 2^-32, so that of codes whose quotient is not the middle itself none but one in some 2^32
+// differs from exact arithmetic's.
 struct Two {
   float hi, lo;
 };
@@ -184,6 +185,19 @@ BFP8_DEV uint32_t group_top(const float2 (&y)[4], float am, int lane) {
   const int src = tops ? __ffs(tops) - 1 : lane;
   return 8 * (src & 15) + (__shfl_sync(0xffffffffu, top, src) & 7);
 }
+// The code of y. A quotient that is the middle itself goes to the even code: entries with one gate and
+// one weight have their bits of x alone, and one in 16 of those can be such a tie. Their divisors by
+// the gate are the same, so that a quotient is within 2^-42 (three divisions of 2^-44 and four products
+// of 2^-47), and what is within 2^-40 of the middle counts as it: of others that is one in some 2^36.
+BFP8_DEV uint8_t settled_code(Two y) {
+  const uint32_t middle = (__float_as_uint(y.hi) & 0xFFF00000u) | 0x80000u;
+  const float m = __uint_as_float(middle);
+  // towards zero, with what is cut off as an odd last bit: rounding that once more is exact
+  uint32_t bits = __float_as_uint(y.hi);
+  if (y.lo != 0.0f) bits = (bits - (((__float_as_uint(y.lo) ^ bits) >> 31) & 1u)) | 1u;
+  if (fabsf((y.hi - m) + y.lo) <= 0x1p-40f * fabsf(m)) bits = middle;
+  return static_cast<uint8_t>(f32x2_to_e4m3x2(__uint_as_float(bits), 0.0f));
+}
 // The warp's doubtful codes settled, two lanes each: one has the code's column, the other that with
 // the largest entry of its group. A note is a row (x), a column of the warp's in bits 0 - 7 (y), and
 // from bit 8 on that of its group.
@@ -198,12 +212,8 @@ __device__ __noinline__ void settle(const GatedParams& p, const uint2* notes, in
   if (valid) y = entry<DIM>(p, note.x, lane < 16 ? c : (c & ~127) + static_cast<int>(note.y >> 8));
   const Two m = {__shfl_down_sync(0xffffffffu, y.hi, 16), __shfl_down_sync(0xffffffffu, y.lo, 16)};
   y = two_times(two_over(y, m), {m.hi < 0.0f ? -448.0f : 448.0f, 0.0f});
-  if (valid && lane < 16 && fabsf(y.hi) < 449.0f) {    // not NaN
-    // towards zero, with what is cut off as an odd last bit: rounding that once more is exact
-    uint32_t bits = __float_as_uint(y.hi);
-    if (y.lo != 0.0f) bits = (bits - (((__float_as_uint(y.lo) ^ bits) >> 31) & 1u)) | 1u;
-    p.q[note.x * p.ldq + c] = static_cast<uint8_t>(f32x2_to_e4m3x2(__uint_as_float(bits), 0.0f));
-  }
+  if (valid && lane < 16 && fabsf(y.hi) < 449.0f)      // not NaN
+    p.q[note.x * p.ldq + c] = settled_code(y);
   __syncwarp();
 }
 

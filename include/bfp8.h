@@ -806,7 +806,9 @@ int bfp8_delta_rule(const bfp8_delta_rule_args* args, void* stream);
  *   out = bf16_rn(y); per 128 columns of a token's heads, one behind another,
  *   s = max(max|y|, 1e-10f) / 448, q = RNE_satfinite_e4m3(y / s)
  * in float32: the quantizer takes y before it is rounded to BF16. Where the quotient's last
- * bits would decide a code above 2^-6, it is formed once more to 2^-31.
+ * bits would decide a code above 2^-6, it is formed once more to 2^-31, and one in the middle
+ * between two codes goes to the even one (unless x, for SiLU x gate, leaves 2^-60 .. 2^60, or the
+ * gate lies below -60). A row's codes do not depend on the rows beside it.
  * tokens == 0 or heads == 0 is a no-op. Errors: INVALID_ARG (null x or gate, no
  * output, strides below a row, q without scales, gate_act, eps < 0), SCALE_DTYPE
  * (w_dtype), UNSUPPORTED (head width, rows that are not 16-byte aligned, codes' rows

@@ -1,10 +1,12 @@
-"""bfp8_gated_norm at gates without an end, and for the same row in other calls."""
+"""bfp8_gated_norm at gates without an end, for the same row in other calls, and at quotients that are exactly the middle
+between two codes."""
 
 import numpy as np
 import pytest
 import torch
 
 from hybrid_util import f64, nan_like
+from oracle import formats as F
 from oracle import hybrid as HY
 from test_gpu_gated_norm import _inputs, _outputs, _run
 
@@ -86,3 +88,27 @@ def test_a_row_has_the_same_codes_in_any_call(bfp8, cuda_device, D, gate):
             for k in ("q", "scales"):
                 assert (o[k][at == r] == want[r][k]).all(), (order[:3], len(order), k)
             assert torch.equal(o["out"][at == r][-1:], want[r]["out"])
+@pytest.mark.parametrize("T,H,D", [(1, 1, 128), (3, 4, 64), (40, 3, 128), (9, 5, 256)])
+@pytest.mark.parametrize("largest", [1.75, 1.75 * 2.0 ** -9, 1.0, 1.75 * 2.0 ** 20])
+@pytest.mark.parametrize("gate,sigmoid", [(0.0, True), (40.0, True), (1.296875, False), (-2.453125, False)])
+@pytest.mark.parametrize("weight", [None, 0.75, 1.0])
+def test_quotients_in_the_middle_go_to_the_even_code(bfp8, cuda_device, T, H, D, largest, gate, sigmoid, weight):
+    """One gate and one weight for a whole row: they cancel from y / max|y|, whose middles are then those of 448 x / max|x|,
+    which float64 has without rounding (8 bits by 9, over 1 or 7 / 4). A norm cancels within a head; of heads of 64 there are
+    two to a group, so there without."""
+    if weight is not None and D == 64:
+        return
+    dev = cuda_device
+    x = _tied_rows(T, H, D, largest, 3 * T + D)
+    if largest == 1.0:                               # where the middles are 3 / 2 of powers of two: 448 is 7 / 4 of one
+        x.view(T, -1)[:, 1::5] = 1.5 * torch.exp2(-1 - torch.arange(H * D)[1::5] % 12).to(torch.bfloat16)
+        x.view(T, -1)[:, ::128] = 1.0
+    t = dict(x=x.to(dev), gate=torch.full_like(x, gate).to(dev), weight=None if weight is None else torch.full((D,), weight, device=dev))
+    o = _outputs(dev, T, H, D)
+    _run(bfp8, t, o, sigmoid=sigmoid)
+    flat = f64(t["x"]).reshape(T, -1)
+    top = np.repeat(np.maximum.reduceat(np.abs(flat), np.arange(0, H * D, 128), axis=1), 128, axis=1)[:, :H * D]
+    quotient = 448 * flat / top
+    want = F.e4m3_encode_rne_sat(quotient if gate > 0 or sigmoid else -quotient)
+    plain = np.abs(quotient) > 2.0 ** -6 * 1.01
+    assert np.array_equal(o["q"].cpu().numpy()[plain], want[plain])
