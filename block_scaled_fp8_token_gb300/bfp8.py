@@ -28,6 +28,7 @@ _lib = ctypes.CDLL(os.fspath(_LIB_PATH))
 
 # ---- enums (include/bfp8.h) ------------------------------------------------
 BFP8_OK = 0
+BFP8_ERR_CUDA = 14
 STATUS_NAMES = {
     0: "OK", 1: "INVALID_ARG", 2: "E5M2", 3: "NO_SCALE", 4: "ROW_SCALE",
     5: "AMBIGUOUS_SCALE", 6: "GRID_TRANSPOSED", 7: "GRID_SHAPE", 8: "SCALE_DTYPE",
@@ -1011,8 +1012,14 @@ BFP8_ACT_SILU, BFP8_ACT_SIGMOID = 0, 1
 # types, shapes and inner strides, and the library itself refuses memory that is not the current
 # device's. Where either says no, the call goes through the helpers, piece by piece, which put
 # the strides of lone dimensions right, or say what is wrong. A call that the library refuses
-# has done nothing.
+# has done nothing; one that ends in a CUDA error may have launched kernels, which have a state
+# on its way, and is not made again.
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _raise_cuda(status: int, name: str) -> None:
+    if status == BFP8_ERR_CUDA:
+        _check(status, name)
 
 
 def _slots(state, slots_in, slots_out, B: int, dev: int) -> tuple[int, int, int]:
@@ -1058,13 +1065,16 @@ def bfp8_causal_conv(x, weight, out, q_offsets, state=None, slots_in=None, slots
             and weight.is_contiguous() and q_offsets.is_contiguous()
             and slots_in.is_contiguous() and slots_out.is_contiguous()):
         (xt, xc), (ot, oc), (st, sr, sc) = x.stride(), out.stride(), state.stride()
-        if xc == oc == sc == 1 and _lib.bfp8_causal_conv(_CAUSAL_CONV.pack(
+        if xc == oc == sc == 1:
+            status = _lib.bfp8_causal_conv(_CAUSAL_CONV.pack(
                 x.data_ptr(), xt, out.data_ptr(), ot, weight.data_ptr(),
                 0 if bias is None else bias.data_ptr(),
                 _WEIGHT_CODES.get(weight.dtype, BFP8_DT_NONE), W, silu, state.data_ptr(), st, sr,
                 state.shape[0], slots_in.data_ptr(), slots_out.data_ptr(), q_offsets.data_ptr(), B,
-                T, C), _raw_stream(stream, dev)) == BFP8_OK:
-            return
+                T, C), _raw_stream(stream, dev))
+            if status == BFP8_OK:
+                return
+            _raise_cuda(status, "bfp8_causal_conv")
     if state is None:
         at = (0, 0, 0)
     else:
@@ -1119,14 +1129,16 @@ def bfp8_delta_rule(q, k, v, a, b, a_log, dt_bias, state, slots_in, slots_out, q
         (ot, oh, od), (ss, sh, sv, sk) = out.stride(), state.stride()
         (at, ah), (bt, bh) = a.stride(), b.stride()
         wsp, wsb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-        if (qd == kd == vd == od == ah == bh == sk == 1 and sv == D
-                and _lib.bfp8_delta_rule(_DELTA_RULE.pack(
-                    q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, a.data_ptr(),
-                    at, b.data_ptr(), bt, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(),
-                    ss, sh, state.shape[0], slots_in.data_ptr(), slots_out.data_ptr(),
-                    q_offsets.data_ptr(), out.data_ptr(), ot, oh, B, T, max_q_len, hk, hv, D,
-                    scale, eps, wsp, wsb), _raw_stream(stream, dev)) == BFP8_OK):
-            return
+        if qd == kd == vd == od == ah == bh == sk == 1 and sv == D:
+            status = _lib.bfp8_delta_rule(_DELTA_RULE.pack(
+                q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, a.data_ptr(),
+                at, b.data_ptr(), bt, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(),
+                ss, sh, state.shape[0], slots_in.data_ptr(), slots_out.data_ptr(),
+                q_offsets.data_ptr(), out.data_ptr(), ot, oh, B, T, max_q_len, hk, hv, D,
+                scale, eps, wsp, wsb), _raw_stream(stream, dev))
+            if status == BFP8_OK:
+                return
+            _raise_cuda(status, "bfp8_delta_rule")
     if state is None:
         at = (0, 0, 0)
     else:
@@ -1170,15 +1182,17 @@ def bfp8_gated_norm(x, gate, weight, out=None, *, q=None, scales=None, eps: floa
         (xt, xh, xd), (zt, zh, zd) = x.stride(), gate.stride()
         ot, oh, od = (0, 0, 1) if out is None else out.stride()
         (qt, qc), (sm, sk) = ((0, 1), (0, 0)) if q is None else (q.stride(), scales.stride())
-        if xd == zd == od == qc == 1 and _lib.bfp8_gated_norm(_GATED_NORM.pack(
+        if xd == zd == od == qc == 1:
+            status = _lib.bfp8_gated_norm(_GATED_NORM.pack(
                 x.data_ptr(), xt, xh, gate.data_ptr(), zt, zh,
                 0 if weight is None else weight.data_ptr(),
                 _WEIGHT_CODES.get(None if weight is None else weight.dtype, BFP8_DT_NONE),
                 BFP8_ACT_SIGMOID if sigmoid else BFP8_ACT_SILU, eps, weight_offset,
                 0 if out is None else out.data_ptr(), ot, oh, 0 if q is None else q.data_ptr(), qt,
-                0 if q is None else scales.data_ptr(), sm, sk, T, H, D),
-                _raw_stream(stream, dev)) == BFP8_OK:
-            return
+                0 if q is None else scales.data_ptr(), sm, sk, T, H, D), _raw_stream(stream, dev))
+            if status == BFP8_OK:
+                return
+            _raise_cuda(status, "bfp8_gated_norm")
     scales_at = (0, 0, 0)
     if q is not None:
         if scales is None:
@@ -1227,15 +1241,18 @@ def bfp8_rotary(q, k, positions, inv_freq, q_out=None, k_out=None, *, sections=N
             (qt, qh, qd), (kt, kh, kd), pt = q.stride(), k.stride(), positions.stride()
             (qot, qoh, qod), (kot, koh, kod) = qo.stride(), ko.stride()
             w = k_weight if q_weight is None else q_weight
-            if qd == kd == qod == kod == pt[-1] == 1 and _lib.bfp8_rotary(_ROTARY.pack(
+            if qd == kd == qod == kod == pt[-1] == 1:
+                status = _lib.bfp8_rotary(_ROTARY.pack(
                     q.data_ptr(), qt, qh, qo.data_ptr(), qot, qoh, k.data_ptr(), kt, kh,
                     ko.data_ptr(), kot, koh, positions.data_ptr(), pt[0], inv_freq.data_ptr(),
                     0 if q_weight is None else q_weight.data_ptr(),
                     0 if k_weight is None else k_weight.data_ptr(),
                     _WEIGHT_CODES.get(None if w is None else w.dtype, BFP8_DT_NONE), eps,
                     weight_offset, factor, T, H, K, D, 2 * half, axes, *parts, *(0,) * (4 - axes),
-                    interleaved, adjacent), _raw_stream(stream, dev)) == BFP8_OK:
-                return
+                    interleaved, adjacent), _raw_stream(stream, dev))
+                if status == BFP8_OK:
+                    return
+                _raise_cuda(status, "bfp8_rotary")
     axes, pos = (1, (_vec(positions, "positions", "i32", T, dev), T)) if positions.dim() == 1 else \
         (positions.shape[0], _matrix(positions, "positions", "i32", (positions.shape[0], T), dev))
     parts = [half] if sections is None else list(sections)

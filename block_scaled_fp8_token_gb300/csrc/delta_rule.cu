@@ -1565,6 +1565,10 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   if (rc == BFP8_OK) rc = tile_map(&tv, a.v_bf16, a.v_heads, a.tokens, a.v_stride_head, a.v_stride_token);
   if (rc == BFP8_OK) rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_prepare_kernel), kPrepSmem);
   if (rc == BFP8_OK) rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_walk_kernel), kWalkSmem);
+  const int64_t chunks = longest_chunks(a.tokens, a.max_q_len), pairs = a.batch * a.v_heads;
+  const Split split = split_walk(chunks, pairs, sms);
+  if (rc == BFP8_OK && split.segments > 1)             // whatever can fail does so ahead of the first launch
+    rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_join_kernel), 2 * kMapBytes + 128);
   if (rc != BFP8_OK) return rc;
   // Value heads of one key head share a block, which norms and multiplies their rows once (14,000
   // of its 24,500 clocks for one head), unless the blocks of one head each fit the GPU at once,
@@ -1583,8 +1587,6 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   rc = launch_dependent(delta_prepare_kernel, dim3(cp.chunk_blocks + static_cast<unsigned>(step_blocks)), kPrepThreads,
                         kPrepSmem, st, tq, tk, cp);
   if (rc != BFP8_OK) return rc;
-  const int64_t chunks = longest_chunks(a.tokens, a.max_q_len), pairs = a.batch * a.v_heads;
-  const Split split = split_walk(chunks, pairs, sms);
   cp.segments = split.segments;
   // More heads than SMs: the longest requests' blocks first, so that none of them begins last. (48
   // heads: 12 requests of 1 to 1300 tokens 220 -> 202 us, 24 of 1 to 1121 203 -> 188; 64 of 40
@@ -1598,10 +1600,8 @@ int launch_delta_rule(const bfp8_delta_rule_args& a, void* stream) {
   rc = launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * jobs)), kWalkThreads, kWalkSmem, st, tv, cp);
   if (rc != BFP8_OK || cp.segments == 1) return rc;
   const int join_smem = (cp.segments > 3 ? 2 : 1) * kMapBytes + 128;
-  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(delta_join_kernel), 2 * kMapBytes + 128);
-  if (rc == BFP8_OK)
-    rc = launch_dependent(delta_join_kernel, dim3(static_cast<unsigned>(pairs * (kD / kJoinRows))), kJoinThreads,
-                          join_smem, st, cp);
+  rc = launch_dependent(delta_join_kernel, dim3(static_cast<unsigned>(pairs * (kD / kJoinRows))), kJoinThreads,
+                        join_smem, st, cp);
   if (rc != BFP8_OK) return rc;
   cp.second_walk = 1;
   return launch_dependent(delta_walk_kernel, dim3(static_cast<unsigned>(pairs * (cp.segments - 1))), kWalkThreads,
