@@ -46,6 +46,11 @@ BFP8_DEV float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+BFP8_DEV float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 // Eight sums over the warp at once: sum r is left in lanes 4r .. 4r + 3.
 BFP8_DEV float warp_sum8(float (&v)[8], int lane) {
 #pragma unroll
@@ -718,10 +723,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(const __
 // warpgroups share the columns: keys 0 - 63 and 64 - 127 of S (kept in registers), tokens 0 - 31
 // and 32 - 63.
 //
-// A row's power of two brings the larger of its state's and its values' entries near 2^2. With
-// all of them below 2^6, neither u nor S reaches 2^14 in the chunk: a row's length grows by |v| a
-// token at most, |S| <= sqrt(128) 2^6 + 64 2^6, and |u| <= |v| + |S|. With the largest above 2^-3,
-// the rests' 2^-25 is 2^-22 of it. It is looked at once a chunk: Gamma_C times the state's largest
+// A row's power of two brings the larger of its state's entries and of what its values write near
+// 2^2: the chunk's largest beta times its largest |v|, as all that enters of a value is beta v. With
+// both below 2^6, neither u nor S reaches 2^14 in the chunk: a row's length grows by beta |v| a
+// token at most, |S| <= sqrt(128) 2^6 + 64 2^6, and |u| <= beta |v| + |S|. With the larger above 2^-3,
+// the rests' 2^-25 is 2^-22 of it. (With |v| for beta |v|, a state of writes with beta about e^-10
+// was right to 10 bits; looking for the largest beta takes 8192 tokens of 32 heads from 283.5 to 287
+// us.) It is looked at once a chunk: Gamma_C times the state's largest
 // at the chunk's begin, the largest update, and the next chunk's values stand for what the next
 // chunk meets. So where a head forgets within a chunk, what comes after keeps 2^-22 of what was
 // forgotten there, not of itself.
@@ -789,6 +797,7 @@ BFP8_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
 struct WalkShared {
   float most[2][2][kD];                                // what each half of a row offers for its power of two
   float power[2][kD];                                  // a chunk's, for its rows of out
+  float2 beta[2];                                      // of the chunk whose values are turned: the largest of each 32 tokens
   uint64_t full[kStages], empty[kStages], v_full[2], v_empty[2], turned[2], taken[2];
   uint64_t s_full[2], x_done, r_full[2], u_done, p_full[2], o_done, y_free, new_done, told, out_full, begun, drained;
   uint32_t tmem;
@@ -1046,7 +1055,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
     } else {
       // ---------------------------------------------- values turned: of each value its tokens, two a word
       const int half = warp - kMmaWarp - 2;            // of the values
+      // of tokens too: their gate b, whose largest has the largest beta
+      const uint16_t* gate = reinterpret_cast<const uint16_t*>(p.d.b) + (first + 32 * half + lane) * p.d.bt + h;
+      int left = static_cast<int>(len) - 32 * half - lane;
       for (int c = 0; !map && c < chunks; ++c) {
+        const float b = left > 0 ? bf16_bits_to_f32(__ldg(gate)) : -INFINITY;
+        gate += kChunk * p.d.bt, left -= kChunk;
         if (!wait(sh.v_full[c & 1], (c >> 1) & 1) || !wait(sh.taken[c & 1], ((c >> 1) & 1) ^ 1)) break;
         // a lane's row of the four 8 x 8 pieces that the warp turns at once: 32 tokens of 8 values
         const uint32_t src = stages + kValuesAt + (c & 1) * kTile + half * kHalfTile + lane * 128;
@@ -1065,6 +1079,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + 8 * v * 128 + (((4 * g + e) ^ (lane >> 2)) << 4)), "r"(w[e])
                            : "memory");
           }
+        const float beta = sigmoid(warp_max(b));
+        if (lane == 0) (half ? sh.beta[c & 1].y : sh.beta[c & 1].x) = beta;
         tell_bar(sh.turned[c & 1]);
         if (lane == 0) mbar_arrive(smem_u32(&sh.v_empty[c & 1]));
       }
@@ -1166,7 +1182,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       if (map) most = 1.0f;
     }
     tell_bar(sh.begun);
-    uint32_t values[16], top = 0;                      // the next chunk's: 32 tokens' BF16, two a word; the largest
+    uint32_t values[16];                               // the next chunk's: 32 tokens' BF16, two a word
+    float written = 0.0f;                              // their largest times the chunk's largest beta
     auto load_values = [&](int c) {
       const int left = (c == chunks - 1 ? tail : kChunk) - 32 * wg;
       if (map) {
@@ -1181,15 +1198,17 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
         const uint4 w = lds128(row + (((4 * wg + v) ^ (r & 7)) << 4));
         values[4 * v] = w.x, values[4 * v + 1] = w.y, values[4 * v + 2] = w.z, values[4 * v + 3] = w.w;
       }
+      const float2 beta = sh.beta[c & 1];
       tell_bar(sh.taken[c & 1]);
       if (left < 32) {
 #pragma unroll
         for (int j = 0; j < 32; j += 2)
           values[j / 2] = j >= left ? 0u : j + 1 >= left ? values[j / 2] & 0xFFFFu : values[j / 2];
       }
-      top = 0;
+      uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = max_abs_bf16x2(top, values[j]);
+      written = fmaxf(beta.x, beta.y) * max_bf16x2(top);
     };
     uint32_t largest = 0;                              // of the parts of S, as F16 pairs
     auto hand_over = [&](int q) {                      // 32 keys
@@ -1206,7 +1225,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       tell_bar(sh.s_full[q]);
     };
     load_values(0);
-    most = fmaxf(most, max_bf16x2(top));
+    most = fmaxf(most, written);
     sh.most[1][wg][r] = most;
     if (ok) {
       tell_bar(sh.told);
@@ -1266,7 +1285,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       float offer = gamma * max_f16x2(largest) * back;
       if (more) {
         load_values(c + 1);
-        offer = fmaxf(offer, max_bf16x2(top));
+        offer = fmaxf(offer, written);
       }
       if (!wait(sh.u_done, c & 1)) break;
       tc_fence_after();

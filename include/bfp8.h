@@ -749,7 +749,8 @@ int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream);
  * serves single tokens, drafted ones, and prompts. max_q_len and a request's own
  * length choose between two ways for it: a token after the other (up to 20 tokens; up
  * to 12 where max_q_len is larger), or by chunks of 64, whose products carry a row of S,
- * and the values that meet it, to 2^-22 of the largest among them in a chunk. Long
+ * and what the values write into it (the chunk's largest beta times its largest |v|), to
+ * 2^-22 of the larger of them in a chunk. Long
  * prompts of few heads (batch * v_heads) are walked in segments at once.
  *   q, k, v, out  [tokens, heads, 128] BF16, 16-byte aligned, token and head strides
  *               in elements, multiples of 8, for example columns of the convolution's
