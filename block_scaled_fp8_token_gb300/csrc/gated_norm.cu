@@ -376,6 +376,11 @@ int launch_gated_norm(const bfp8_gated_norm_args& a, void* stream) {
   if (off16(a.x_bf16) || off16(a.gate_bf16) || off16(a.weight) || off16(a.out_bf16) ||
       (a.q_e4m3 && (a.ldq % 8 || reinterpret_cast<uintptr_t>(a.q_e4m3) % 8)))
     return BFP8_ERR_UNSUPPORTED;
+  // over its own input, but laid out otherwise: rows would go before they are read
+  for (int i = 0; i < 2; ++i)
+    if (a.out_bf16 && a.out_bf16 == (i ? a.gate_bf16 : a.x_bf16) &&
+        ((a.tokens > 1 && strides[2 * i] != strides[4]) || (a.heads > 1 && strides[2 * i + 1] != strides[5])))
+      return BFP8_ERR_INVALID_ARG;
   int rc = check_device_ptrs({a.x_bf16, a.gate_bf16, a.weight, a.out_bf16, a.q_e4m3,
                               a.q_e4m3 ? a.scales : nullptr});
   if (rc != BFP8_OK) return rc;

@@ -249,6 +249,13 @@ int launch_rotary(const bfp8_rotary_args& a, void* stream) {
   if (off16(a.q_bf16) || off16(a.q_out_bf16) || off16(a.k_bf16) || off16(a.k_out_bf16) ||
       off16(a.q_weight) || off16(a.k_weight) || a.q_heads > (1 << 20) || a.k_heads > (1 << 20))
     return BFP8_ERR_UNSUPPORTED;
+  // over its own input, but laid out otherwise: rows would go before they are read
+  for (int i = 0; i < 2; ++i) {
+    const int64_t heads = i ? a.k_heads : a.q_heads, *s = strides[i];
+    if (heads > 0 && (i ? a.k_bf16 == a.k_out_bf16 : a.q_bf16 == a.q_out_bf16) &&
+        ((a.tokens > 1 && s[0] != s[2]) || (heads > 1 && s[1] != s[3])))
+      return BFP8_ERR_INVALID_ARG;
+  }
   int rc = check_device_ptrs({a.q_heads ? a.q_bf16 : nullptr, a.q_heads ? a.q_out_bf16 : nullptr,
                               a.k_heads ? a.k_bf16 : nullptr, a.k_heads ? a.k_out_bf16 : nullptr,
                               a.positions, a.inv_freq, a.q_weight, a.k_weight});

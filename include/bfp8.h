@@ -813,9 +813,9 @@ int bfp8_delta_rule(const bfp8_delta_rule_args* args, void* stream);
  * between two codes goes to the even one (unless x, for SiLU x gate, leaves 2^-60 .. 2^60, or the
  * gate lies below -60). A row's codes do not depend on the rows beside it.
  * tokens == 0 or heads == 0 is a no-op. Errors: INVALID_ARG (null x or gate, no
- * output, strides below a row, q without scales, gate_act, eps < 0), SCALE_DTYPE
- * (w_dtype), UNSUPPORTED (head width, rows that are not 16-byte aligned, codes' rows
- * that are not 8-byte aligned).
+ * output, strides below a row, out over x or the gate with other strides, q without
+ * scales, gate_act, eps < 0), SCALE_DTYPE (w_dtype), UNSUPPORTED (head width, rows that
+ * are not 16-byte aligned, codes' rows that are not 8-byte aligned).
  */
 enum bfp8_gate_act { BFP8_ACT_SILU = 0, BFP8_ACT_SIGMOID = 1 };
 
@@ -828,7 +828,8 @@ typedef struct {
   int32_t w_dtype;               /* BFP8_DT_BF16 or BFP8_DT_F32                  */
   int32_t gate_act;              /* enum bfp8_gate_act                           */
   float eps, weight_offset;
-  void* out_bf16;                /* may be x or gate itself; NULL: not written   */
+  void* out_bf16;                /* may be x or gate itself, of the same strides;
+                                    NULL: not written                            */
   int64_t out_stride_token, out_stride_head;
   void* q_e4m3;                  /* [tokens, heads * head_dim] E4M3, row stride ldq bytes; NULL: not written */
   int64_t ldq;
@@ -855,14 +856,15 @@ int bfp8_gated_norm(const bfp8_gated_norm_args* args, void* stream);
  * A token with a negative position on any axis is left alone: nothing of it is written.
  * inv_freq entries of 2^32 and more, and those that are not finite, give NaN.
  * tokens == 0 or no heads is a no-op. Errors: INVALID_ARG (null pointers, negative
- * sizes, sections that do not add up, strides below a row, eps < 0, factor not finite),
+ * sizes, sections that do not add up, strides below a row, an output over its input
+ * with other strides, eps < 0, factor not finite),
  * SCALE_DTYPE (w_dtype), UNSUPPORTED (head width, rotary_dim not a multiple of 16, rows
  * that are not 16-byte aligned).
  */
 typedef struct {
   const void* q_bf16;            /* [tokens, q_heads, head_dim]; strides in elements */
   int64_t q_stride_token, q_stride_head;
-  void* q_out_bf16;              /* may be q itself                              */
+  void* q_out_bf16;              /* may be q itself, of the same strides (and k) */
   int64_t q_out_stride_token, q_out_stride_head;
   const void* k_bf16;            /* [tokens, k_heads, head_dim]                  */
   int64_t k_stride_token, k_stride_head;
