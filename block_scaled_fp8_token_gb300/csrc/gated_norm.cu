@@ -216,7 +216,6 @@ __device__ __noinline__ void settle(const GatedParams& p, const uint2* notes, in
     p.q[note.x * p.ldq + c] = settled_code(y);
   __syncwarp();
 }
-
 // The same of rows `step` apart, each formed once more with the loop's own operations, for any number
 // of doubtful codes; c is the lane's column.
 template <int DIM>
@@ -260,11 +259,14 @@ __device__ __noinline__ void settle_rows(const GatedParams& p, uint2* notes, int
 // Codes that FP32 may have missed are noted in shared memory and settled behind the warp's last row,
 // two lanes each (one in 60,000 is noted; where a warp has a 17th, all of its rows are looked through
 // again, so that a row's codes are its own, whatever is beside it): a call inside the loop, though
-// never taken, cost the loop 14 of 62 us. A row that its own output overwrites (IN_PLACE) cannot wait.
+// never taken, cost the loop 14 of 62 us. A row that its own output overwrites (IN_PLACE) cannot wait,
+// and has room for as many notes as codes; with that call in the loop, three blocks an SM of 80 registers
+// each take 58 us (codes and rows), four of 64, which spill, 64.
 template <int DIM, bool IN_PLACE>
-__global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __grid_constant__ GatedParams p) {
+__global__ void __launch_bounds__(kGatedThreads, IN_PLACE ? 3 : 4) gated_norm_kernel(const __grid_constant__ GatedParams p) {
   __shared__ alignas(16) uint4 ring[kGatedAhead][2][kGatedThreads];
-  __shared__ uint2 doubtful[kGatedThreads / 32 * kNotes];
+  constexpr int kRoom = IN_PLACE ? 256 : kNotes;       // a row's codes, or a few of the warp's rows'
+  __shared__ uint2 doubtful[kGatedThreads / 32 * kRoom];
   const int lane = threadIdx.x & 31;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * (kGatedThreads / 32) + (threadIdx.x >> 5);
   const int64_t step = p.warps / p.segs;               // tokens between a warp's: p.warps is a multiple of segs
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __gr
   for (int s = 0; s < kGatedAhead; ++s) ask(s);
   float2 w[4];
   if (p.w) load_weights(p, d, w);
-  uint2* const notes = doubtful + (threadIdx.x >> 5) * kNotes;
+  uint2* const notes = doubtful + (threadIdx.x >> 5) * kRoom;
   int count = 0;
   for (int s = 0; row < p.tokens; s = (s + 1) % kGatedAhead, row += step) {
     cp_async_wait_group<kGatedAhead - 1>();
@@ -323,18 +325,22 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_norm_kernel(const __gr
       }
       const bool near_one = near <= kBothSides && in && may_be_near(am);
       if (__any_sync(0xffffffffu, near_one)) {
-        if (IN_PLACE) {
-          settle_rows<DIM>(p, notes, row, row + 1, 1, c);
-        } else {
-          const uint32_t top = group_top(y, am, lane);
+        const uint32_t top = group_top(y, am, lane);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const bool one = near_one && is_near(e & 1 ? f[e >> 1].y : f[e >> 1].x);
-            const uint32_t ones = __ballot_sync(0xffffffffu, one);
-            const int at = count + __popc(ones & ((1u << lane) - 1));
-            if (one && at < kNotes) notes[at] = make_uint2(static_cast<uint32_t>(row), top << 8 | (8 * lane + e));
-            count += __popc(ones);
-          }
+        for (int e = 0; e < 8; ++e) {
+          const bool one = near_one && is_near(e & 1 ? f[e >> 1].y : f[e >> 1].x);
+          const uint32_t ones = __ballot_sync(0xffffffffu, one);
+          const int at = count + __popc(ones & ((1u << lane) - 1));
+          if (one && at < kRoom) notes[at] = make_uint2(static_cast<uint32_t>(row), top << 8 | (8 * lane + e));
+          count += __popc(ones);
+        }
+        if (IN_PLACE) {
+          int done = 0;
+#pragma unroll 1
+          do {
+            settle<DIM>(p, notes + done, count - done, c - 8 * lane);
+          } while ((done += kNotes) < count);
+          count = 0;
         }
       }
     }
