@@ -65,7 +65,7 @@ BFP8_DEV float warp_sum8(float (&v)[8], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-constexpr int kStepWarps = 4, kMostSteps = 32;         // of a block; tokens of a request
+constexpr int kStepWarps = 4, kMostSteps = 32;         // of a block; tokens of a request, of which up to 20 come
 template <int WARPS>
 struct StepShared {
   alignas(16) uint2 k[kMostSteps][32];                 // raw rows
@@ -82,7 +82,8 @@ struct StepShared {
 // lanes and the update. A block of WARPS warps, number `block`.
 //
 // Bound by HBM, the state's 64 KB read and written a head: 64 single tokens of 48 heads move 405
-// MB in 62 us, 6.5 TB/s.
+// MB in 62 us, 6.5 TB/s. 17 requests of 3 tokens, 32 heads, take 17: at 65 registers seven blocks fit
+// an SM, and 2,176 are two waves and a tail of 48.
 template <int WARPS>
 BFP8_DEV void delta_steps(const DeltaParams& p, int64_t block, StepShared<WARPS>& sh) {
   constexpr int kParts = kD / (8 * WARPS);
@@ -404,7 +405,8 @@ BFP8_DEV void store_piece(float* at, int lane, const float (&c)[4], float sign) 
 // blocks they kept the chunks waiting: 81 us against 60 for 12 requests of 1 to 141 tokens and 48
 // heads; with a block for every part, 64 requests without a short one took 15 us of empty blocks).
 //
-// Bound by latency: a block passes a dozen barriers, and four to an SM issue in 53% of the clocks.
+// Bound by latency: a block passes a dozen barriers, and four to an SM, whose 64 registers spill 88
+// bytes a thread, issue in 53% of the clocks.
 // 129 chunks of 16 key and 32 value heads take 88 us (94 with three to an SM, 214 with one; 138
 // with a thread a row solving against A from registers, whose unrolled code stalled on instruction
 // fetches).
@@ -739,7 +741,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(const __
 // the values' turning (a row of S wants a value's tokens side by side) in two warps. Each product
 // begins on the first half of its operand while the second is cut.
 //
-// Bound by the chain: 4,550 clocks a chunk and block, 2.4 us, one block an SM. The products the
+// Bound by the chain: 4,600 clocks a chunk and block, 2.4 us, one block an SM. The products the
 // chain waits for are 1,410 of them at the tensor cores' rate (64 columns of 128 lanes by 16 take
 // 32 clocks, 128 take 64); reading, cutting and handing over r, u and S are 500, 540 and 1,200,
 // and each hand-over between threads and tensor cores costs 200 to 300 of waiting. On the way,
@@ -1482,7 +1484,8 @@ Split split_walk(int64_t chunks, int64_t pairs, int sms) {
 // 206, 302, 395 and 268. They meet between 20 and 24 but for few heads, which lose 3 us.
 constexpr int64_t kStepTokens = 20;
 // Beside longer ones, which run the chunks' kernels anyway, up to this many do: requests of 1 to
-// 141 tokens (12, of 48 heads) take 49.2, 47.5, 47.8, 47.3 and 50.2 us with 2, 4, 8, 12 and 20.
+// 141 tokens (12, of 48 heads) take 49.2, 47.5, 47.8, 47.3 and 50.2 us with 2, 4, 8, 12 and 20. (One
+// mix of lengths, in which 4, 8 and 12 are within its noise.)
 constexpr int64_t kStepTokensBeside = 12;
 static_assert(kStepTokens <= kMostSteps, "a request's steps fit shared memory");
 

@@ -7,8 +7,8 @@
 //
 // act is SiLU or the sigmoid; without w there is no norm (the gate of a full-attention
 // layer's heads). Bound by HBM: x and z are read once, and the codes (a quarter of the
-// bytes) or the BF16 row written once. 8192 rows of 48 heads to codes, 253 MB, take 50 us, 5.1
-// TB/s, of which looking for codes that FP32 may miss and settling them is 7; with one token's
+// bytes) or the BF16 row written once. 8192 rows of 48 heads to codes, 253 MB, take 51 us, 5.0
+// TB/s, of which looking for codes that FP32 may miss and settling them is 6.5; with one token's
 // loads ahead in registers, 32 warps an SM had too few bytes under way (55 us in place of 44),
 // and without any 67.
 #include "hybrid_layer.cuh"

@@ -10,6 +10,7 @@
 // tokens of 18 normed heads of 256, 151 MB, take 30 us, 5.0 TB/s (54 with the angles formed by
 // every lane and one head's loads under way; 38 with the angles shared, 30 with four heads'
 // loads); 8000 tokens of 72 heads of 128, 295 MB, 50 us. Few tokens: 2.6 us for one, 3.6 for 64.
+// At 64 registers each variant spills 8 bytes a thread, those of adjacent pairs 16 to 28.
 //
 // The angle of a position in the millions leaves a float32 no digits, so it is counted in
 // turns: inv_freq / (2 pi) as a 64-bit binary fraction, times the position modulo 2^64,
