@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(const __
 // both below 2^6, neither u nor S reaches 2^14 in the chunk: a row's length grows by beta |v| a
 // token at most, |S| <= sqrt(128) 2^6 + 64 2^6, and |u| <= beta |v| + |S|. With the larger above 2^-3,
 // the rests' 2^-25 is 2^-22 of it. (With |v| for beta |v|, a state of writes with beta about e^-10
-// was right to 10 bits; looking for the largest beta takes 8192 tokens of 32 heads from 283.5 to 287
+// was right to 10 bits; looking for the largest beta takes 8192 tokens of 32 heads from 283 to 286
 // us.) It is looked at once a chunk: Gamma_C times the state's largest
 // at the chunk's begin, the largest update, and the next chunk's values stand for what the next
 // chunk meets. So where a head forgets within a chunk, what comes after keeps 2^-22 of what was
@@ -1061,7 +1061,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
       const uint16_t* gate = reinterpret_cast<const uint16_t*>(p.d.b) + (first + 32 * half + lane) * p.d.bt + h;
       int left = static_cast<int>(len) - 32 * half - lane;
       for (int c = 0; !map && c < chunks; ++c) {
-        const float b = left > 0 ? bf16_bits_to_f32(__ldg(gate)) : -INFINITY;
+        const float b = left > 0 ? bf16_bits_to_f32(__ldcg(gate)) : -INFINITY;
         gate += kChunk * p.d.bt, left -= kChunk;
         if (!wait(sh.v_full[c & 1], (c >> 1) & 1) || !wait(sh.taken[c & 1], ((c >> 1) & 1) ^ 1)) break;
         // a lane's row of the four 8 x 8 pieces that the warp turns at once: 32 tokens of 8 values
@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_walk_kernel(const __gri
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + 8 * v * 128 + (((4 * g + e) ^ (lane >> 2)) << 4)), "r"(w[e])
                            : "memory");
           }
-        const float beta = sigmoid(warp_max(b));
+        const float beta = sigmoid(fmaxf(warp_max(b), -87.0f));   // e^-87 bounds what is subnormal below it
         if (lane == 0) (half ? sh.beta[c & 1].y : sh.beta[c & 1].x) = beta;
         tell_bar(sh.turned[c & 1]);
         if (lane == 0) mbar_arrive(smem_u32(&sh.v_empty[c & 1]));

@@ -749,11 +749,10 @@ int bfp8_causal_conv(const bfp8_causal_conv_args* args, void* stream);
  * serves single tokens, drafted ones, and prompts. max_q_len and a request's own
  * length choose between two ways for it: a token after the other (up to 20 tokens; up
  * to 12 where max_q_len is larger), or by chunks of 64, whose products carry a row of S,
- * and what the values write into it (the chunk's largest beta times its largest |v|), to
- * 2^-22 of the larger of them in a chunk. Long
- * prompts of few heads are walked in segments at once; how many goes by max_q_len and
- * batch * v_heads, every request of the call counted, and the last bits of such a prompt's
- * results with it.
+ * and what the values write into it (the chunk's largest beta, e^-87 at least, times its
+ * largest |v|), to 2^-22 of the larger of them in a chunk. Long prompts of few heads are
+ * walked in segments at once; how many goes by max_q_len and batch * v_heads, every
+ * request of the call counted, and the last bits of such a prompt's results with it.
  *   q, k, v, out  [tokens, heads, 128] BF16, 16-byte aligned, token and head strides
  *               in elements, multiples of 8, for example columns of the convolution's
  *               output. out must not overlap the inputs.

@@ -84,3 +84,19 @@ def test_write_gates_that_change_from_chunk_to_chunk(bfp8, cuda_device):
     t["a"][64 * 3:] += 2.0
     t["slots_in"].fill_(-1)
     _check_written(t, n, _run(bfp8, t, [n]), True)
+
+
+@pytest.mark.parametrize("b", [-88.0, -87.5, -89.0])
+def test_gates_whose_beta_is_subnormal(bfp8, cuda_device, b):
+    """beta is 6e-39 at b = -88 and 0 from -89 on; values of 2^100 write with it all the same, beside a smaller state."""
+    n = 100
+    t = delta_inputs(cuda_device, [n], 1, 2, 79, decay=0.01)
+    t["b"][:] = b
+    t["v"].copy_(t["v"].float() * 2.0 ** 100)
+    t["state"] *= 2.0 ** -100
+    before = _run(bfp8, t, [n])
+    if b > -89.0:
+        _check_written(t, n, before, True)
+    else:                                            # nothing is written: the state decays, near its own size
+        assert torch.isfinite(t["out"][:n]).all()
+        assert (t["state"][int(t["slots_out"][0])].abs() < 2.0 ** -96).all()
