@@ -85,9 +85,11 @@ int sm_count(int* out) {
   return BFP8_OK;
 }
 
-int check_launch() {
-  return cudaPeekAtLastError() == cudaSuccess ? BFP8_OK : BFP8_ERR_CUDA;
+int launch_status(cudaError_t e) {
+  cudaGetLastError();  // taken: a later call does not report it as its own
+  return e == cudaSuccess ? BFP8_OK : BFP8_ERR_CUDA;
 }
+int check_launch() { return launch_status(cudaGetLastError()); }
 
 int check_device_ptrs(std::initializer_list<const void*> ptrs) {
   int dev = 0;
@@ -108,8 +110,10 @@ int check_device_ptrs(std::initializer_list<const void*> ptrs) {
 int set_max_dynamic_smem(const void* kernel, int bytes) {
   // Cheap and idempotent; done on every launch so that every device is covered.
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess)
+      cudaSuccess) {
+    cudaGetLastError();
     return BFP8_ERR_CUDA;
+  }
   return BFP8_OK;
 }
 

@@ -24,8 +24,7 @@ int launch_dependent(Kernel kernel, dim3 grid, unsigned threads, size_t smem, cu
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return BFP8_ERR_CUDA;
-  return check_launch();
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 namespace dev {

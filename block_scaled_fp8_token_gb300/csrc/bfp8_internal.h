@@ -13,7 +13,9 @@ namespace bfp8 {
 
 // Multiprocessor count of the current device (cached per device).
 int sm_count(int* out);
-// Map the last launch error (if any) to a status.
+// A launch's error, or that of the launch just made, as a status. The error is taken from the
+// thread, so that no later call reports it as its own.
+int launch_status(cudaError_t e);
 int check_launch();
 // Every pointer a kernel or a tensor map will dereference must be device
 // memory of the current device (cudaMalloc, a stream-ordered pool, or the

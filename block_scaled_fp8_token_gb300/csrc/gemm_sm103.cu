@@ -1294,8 +1294,7 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, 
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, ty, p) != cudaSuccess) return BFP8_ERR_CUDA;
-  return check_launch();
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, ta, tb, ty, p));
 }
 
 bool aligned16(const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0; }

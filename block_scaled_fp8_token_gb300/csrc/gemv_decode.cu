@@ -161,7 +161,7 @@ int launch_pdl(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t s
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? BFP8_OK : BFP8_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // One CTA per K-block, 256 threads: thread t handles token t / 16 and the 8
@@ -617,8 +617,6 @@ int launch_kernels(const void* x, int64_t ldx, uint8_t* xtile, float* xinv, cons
                 : launch_pdl(gemv_split_tokens_kernel<false>, dim3(p.Kb), dim3(kSplitThreads), 0, st, xb, ldx,
                              p.M, p.K, xtile, xinv, p.counters, p.RT);
   if (rc != BFP8_OK) return rc;
-  rc = check_launch();
-  if (rc != BFP8_OK) return rc;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(gemv_kernel<false>), kSmemBytes);
   if (rc != BFP8_OK) return rc;
   cudaLaunchConfig_t cfg{};
@@ -631,8 +629,7 @@ int launch_kernels(const void* x, int64_t ldx, uint8_t* xtile, float* xinv, cons
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gemv_kernel<false>, tw, tx, p) != cudaSuccess) return BFP8_ERR_CUDA;
-  return check_launch();
+  return launch_status(cudaLaunchKernelEx(&cfg, gemv_kernel<false>, tw, tx, p));
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -757,8 +754,6 @@ int launch_gemv_w8a8(const void* q_a, const float* s_a, int64_t sa_sm, int64_t s
   if (clear_counters) {   // else the kernel before this one on the stream zeroed them
     rc = launch_pdl(gemv_clear_counters_kernel, dim3(1), dim3(256), 0, st, p.counters, p.RT);
     if (rc != BFP8_OK) return rc;
-    rc = check_launch();
-    if (rc != BFP8_OK) return rc;
   }
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(gemv_kernel<true>), kSmemBytes);
   if (rc != BFP8_OK) return rc;
@@ -772,8 +767,7 @@ int launch_gemv_w8a8(const void* q_a, const float* s_a, int64_t sa_sm, int64_t s
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gemv_kernel<true>, tw, tx, p) != cudaSuccess) return BFP8_ERR_CUDA;
-  return check_launch();
+  return launch_status(cudaLaunchKernelEx(&cfg, gemv_kernel<true>, tw, tx, p));
 }
 
 // ---------------------------------------------------------------------------

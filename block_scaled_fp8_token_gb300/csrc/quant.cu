@@ -378,7 +378,7 @@ int launch_dependent(Kernel kernel, unsigned blocks, cudaStream_t st, Args... ar
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? BFP8_OK : BFP8_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // Blocks of kThreads that one SM keeps resident for `kernel` (at least 1):
@@ -438,8 +438,7 @@ int act_quant_common(bool silu, const void* x, int64_t M, int64_t K, int64_t ld,
   else
     lrc = silu ? (full ? go(act_quant_kernel<true, true>) : go(act_quant_kernel<true, false>))
                : (full ? go(act_quant_kernel<false, true>) : go(act_quant_kernel<false, false>));
-  if (lrc != BFP8_OK) return lrc;
-  return check_launch();
+  return lrc;
 }
 
 }  // namespace
@@ -475,11 +474,9 @@ int launch_silu_mul(const void* gu, int64_t M, int64_t I, int64_t ld, void* h, i
   const int64_t want = (items + kThreads - 1) / kThreads;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const unsigned blocks = static_cast<unsigned>(want < cap ? want : cap);
-  rc = launch_dependent(silu_mul_kernel, blocks, static_cast<cudaStream_t>(stream),
-                        static_cast<const __nv_bfloat16*>(gu), M, I, ld,
-                        static_cast<__nv_bfloat16*>(h), ldh, vec);
-  if (rc != BFP8_OK) return rc;
-  return check_launch();
+  return launch_dependent(silu_mul_kernel, blocks, static_cast<cudaStream_t>(stream),
+                          static_cast<const __nv_bfloat16*>(gu), M, I, ld,
+                          static_cast<__nv_bfloat16*>(h), ldh, vec);
 }
 
 int launch_moe_gather_act_quant(const void* x, int64_t T, int64_t H, int64_t ldx,
@@ -509,12 +506,10 @@ int launch_moe_combine(const void* y, int64_t R, int64_t H, int64_t ldy, const i
   const int64_t want = (items + kThreads - 1) / kThreads;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const unsigned blocks = static_cast<unsigned>(want < cap ? want : cap);
-  rc = launch_dependent(moe_combine_kernel, blocks, static_cast<cudaStream_t>(stream),
-                        static_cast<const __nv_bfloat16*>(y), R, H, ldy, token_rows,
-                        token_weights, T, static_cast<int>(topk),
-                        static_cast<__nv_bfloat16*>(out), ldo, vec);
-  if (rc != BFP8_OK) return rc;
-  return check_launch();
+  return launch_dependent(moe_combine_kernel, blocks, static_cast<cudaStream_t>(stream),
+                          static_cast<const __nv_bfloat16*>(y), R, H, ldy, token_rows,
+                          token_weights, T, static_cast<int>(topk),
+                          static_cast<__nv_bfloat16*>(out), ldo, vec);
 }
 
 int launch_weight_quant(const float* w, int64_t N, int64_t K, int64_t ldw, void* q, int64_t ldq,
